@@ -240,6 +240,122 @@ rkv_status rkv_compress_noalloc(const rkv_params *p, const void *kv, const rkv_r
                                 const rkv_cache *cache, float *z_out, int32_t *dev_status,
                                 void *stream);
 
+/* ---- the dense cache of the full-attention layers -------------------------------------
+ * The layers that keep every token [RKV §2.4, §2.7 = Sec. IV-A, IV-C: full-attention
+ * layers hold 4-bit K and V and choose the index set of the sparse layers].  S sequences
+ * (of one or several layers; index s), N KV heads of D channels, T tokens of capacity.
+ *
+ * A block is 32 tokens (32 i .. 32 i + 31) of one sequence and KV head.  A finished block
+ * is held in `bits` bits; a group is one channel over the block's 32 tokens for keys, and
+ * 32 channels of one token for values:
+ *   step  = bf16((max - min) / (2^bits - 1))
+ *   code  = min(2^bits - 1, round((x - min) / step)), 0 where step is 0
+ *   value = bf16(min + code step)
+ * with each rounding taken once, from the exact number, to nearest with ties to even.
+ * min is an element of the group, so a constant group is exact.  A group that holds a
+ * NaN, an infinity or a magnitude of 2^126 or more reads as NaN.  The tokens of the last,
+ * unfinished block are held as bf16 rows in `tail` until their block is full.
+ *
+ * Every reader takes `len` (int32 [S], device): the tokens that sequence s holds, of which
+ * the first 32 floor(len / 32) are in finished blocks.  A length outside [0, T] sets
+ * RKV_ERR_INDEX and counts as 0.                                                        */
+typedef struct rkv_dense_params {
+    int32_t S;          /* sequences, >= 1                                               */
+    int32_t T;          /* capacity in tokens, >= 1                                      */
+    int32_t N, D;       /* KV heads, head dim (64, 128 or 256)                           */
+    int32_t bits;       /* 2 or 4                                                        */
+    int32_t reserved;   /* set to 0                                                      */
+} rkv_dense_params;
+
+/* Sizes of the three buffers: rkv_dense_sizes().  The layout inside is the library's:
+ *  codes: [S][N][T/32] records of D (8 bits + 4) bytes: key codes, value codes, value
+ *         extremes and steps, in the order in which the tensor cores take them
+ *  khdr:  [S][N][T/32][4 D bytes]: extremes and steps of the keys
+ *  tail:  bf16 [S][N][2 (K, V)][32][D]: the rows of the unfinished block               */
+typedef struct rkv_dense_cache {
+    void *codes;
+    void *khdr;
+    void *tail;
+} rkv_dense_cache;
+
+rkv_status rkv_dense_sizes(const rkv_dense_params *p, size_t *codes_bytes, size_t *khdr_bytes,
+                           size_t *tail_bytes);
+
+/* Writes rows kv[s][0 .. n_new[s]) as tokens pos[s] .. pos[s] + n_new[s] - 1 of sequence s.
+ * kv: [S][n][2 N D] in kv_dtype (RKV_F32 rows are rounded to bf16 first), K of all heads
+ * then V of all heads, as in rkv_compress; keys as the queries will meet them (rotated, if
+ * the model rotates).  Blocks that these rows finish are quantised; rows of the last,
+ * unfinished block go to the tail.  The tokens before pos[s] must have been written, and
+ * pos[s] must not lie before the start of the unfinished block.
+ * pos, n_new: int32 [S], device; n_new may be NULL: n rows for every sequence.  Where
+ * pos < 0, n_new is outside [0, n] or pos + n_new > T, RKV_ERR_INDEX is set and nothing of
+ * that sequence is written.  n may be 1 (a decode step) or any prompt length.            */
+rkv_status rkv_dense_write(const rkv_dense_params *p, const void *kv, int32_t kv_dtype, int32_t n,
+                           const int32_t *pos, const int32_t *n_new, const rkv_dense_cache *cache,
+                           int32_t *dev_status, void *stream);
+
+/* Reads tokens back: out_k[s][i], out_v[s][i] = K and V of token sel[s][i], bf16
+ * [S][n_sel][N D] (the layout that rkv_sparse_attention takes).  sel: int32 [S][n_sel] in
+ * any order; -1 is padding and yields zero rows; an entry < -1 or >= len[s] sets
+ * RKV_ERR_INDEX and yields zero rows.                                                   */
+rkv_status rkv_dense_read(const rkv_dense_params *p, const rkv_dense_cache *cache, const int32_t *len,
+                          const int32_t *sel, int32_t n_sel, void *out_k, void *out_v,
+                          int32_t *dev_status, void *stream);
+
+/* Selects finished blocks for one query token per sequence by an upper bound on its scores:
+ *   score[n][i] = max over the H/N query heads of KV head n of sum_d max(q_d lo_d, q_d hi_d)
+ * where lo_d and hi_d are the values of codes 0 and 2^bits - 1 of channel d in block i.
+ * lists = N: a list for each KV head; lists = 1: one list for all of them, by the largest
+ * score of any head.  A list holds the n_blocks finished blocks of highest score (all of
+ * them, where there are fewer), ascending, then -1; the first keep_first and the last
+ * keep_last finished blocks are always in it (keep_first + keep_last <= n_blocks).  The
+ * ranking is that of the exact scores, equal ones by the lower index; a NaN ranks above
+ * every number.
+ * q: bf16 [S][H][D]; blocks (output): int32 [S][lists][n_blocks].
+ * workspace: >= the bytes of rkv_block_select_workspace, 256-byte aligned.
+ * Requires H a multiple of N, H/N <= 8.                                                  */
+rkv_status rkv_block_select_workspace(const rkv_dense_params *p, int32_t lists, size_t *bytes);
+rkv_status rkv_block_select(const rkv_dense_params *p, int32_t H, const void *q,
+                            const rkv_dense_cache *cache, const int32_t *len, int32_t lists,
+                            int32_t n_blocks, int32_t keep_first, int32_t keep_last, int32_t *blocks,
+                            void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Attention of one token per sequence over the cache:
+ *   out[s][j] = softmax( q[s][j] K^T / sqrt(D) ) V   for each query head j < H
+ * (KV head floor(j / (H/N))) over the listed finished blocks (all of them where blocks is
+ * NULL) and the tokens of the unfinished block, which are always attended.  blocks: int32
+ * [S][lists][n_blocks], lists = 1 or N, as rkv_block_select writes it or any other list: -1
+ * is skipped; an entry < -1 or >= floor(len/32) sets RKV_ERR_INDEX and is skipped; a block
+ * listed twice enters twice.  A sequence with nothing to attend gives zeros.
+ * q: bf16 [S][H][D]; out: [S][H][D] in out_dtype (RKV_F32 or RKV_BF16).  Scores, softmax and
+ * sums in fp32; probabilities meet the values as bf16 hi + lo (relative error about 2^-16).
+ * workspace: >= the bytes of rkv_dense_attention_workspace(p, H, 1, n_blocks, blocks != NULL),
+ * 256-byte aligned.  Requires H a multiple of N, H/N <= 8.                               */
+rkv_status rkv_dense_attention_workspace(const rkv_dense_params *p, int32_t H, int32_t n_query,
+                                         int32_t n_blocks, int32_t listed, size_t *bytes);
+rkv_status rkv_dense_attention(const rkv_dense_params *p, int32_t H, const void *q,
+                               const rkv_dense_cache *cache, const int32_t *len, const int32_t *blocks,
+                               int32_t lists, int32_t n_blocks, void *out, int32_t out_dtype,
+                               void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                               void *stream);
+
+/* Attention for a tree of drafted tokens behind the cache: drafted token j of sequence s
+ * attends every token of the cache, itself, and the drafted tokens on its line of parents.
+ * parent: int32 [S][n_draft]; -1: the token follows the cached text; 0 .. j - 1: it follows
+ * that drafted token; -2: padding, its output rows are zero.  Any other value, and a parent
+ * that is padding, set RKV_ERR_INDEX and give zero rows for the tokens whose line holds it.
+ * draft_kv: bf16 [S][n_draft][2 N D], K then V, as for rkv_dense_write; the cache is not
+ * changed (accepted tokens are written with rkv_dense_write).  What lies in rows that a
+ * token does not see has no effect on it, NaN included.
+ * q: bf16 [S][n_draft][H][D]; out: [S][n_draft][H][D] in out_dtype.  1 <= n_draft <= 64.
+ * workspace: >= the bytes of rkv_dense_attention_workspace(p, H, n_draft, 0, 0), 256-byte
+ * aligned.  Requires H a multiple of N, H/N <= 8.                                        */
+rkv_status rkv_tree_attention(const rkv_dense_params *p, int32_t H, const void *q, int32_t n_draft,
+                              const int32_t *parent, const void *draft_kv,
+                              const rkv_dense_cache *cache, const int32_t *len, void *out,
+                              int32_t out_dtype, void *workspace, size_t workspace_bytes,
+                              int32_t *dev_status, void *stream);
+
 /* Diagnostics: per-kernel device time.  rkv_profile_enable(1) clears the record
  * and brackets every later kernel launch of the library with two CUDA events on
  * the launch stream; rkv_profile_enable(0) stops recording.  rkv_profile_collect

@@ -1,0 +1,614 @@
+// rkv_dense_attention.cu -- attention over the dense quantised cache, for one token per
+// sequence (all finished blocks, or listed ones) and for trees of drafted tokens.
+//
+// The R = n_query H/N query rows of a KV head share its blocks.  Two kernels:
+//   k_dense_split   the finished blocks.  A CTA has a run of blocks of one (sequence, KV
+//                   head) and 8 NT query rows; its warps take blocks in turn, each through
+//                   a ring of its own (cp.async.bulk, one record and one header a block),
+//                   so that no warp waits for another.  A record is already in operand
+//                   order: a lane reads 16 bytes of codes, turns pairs of them into bf16
+//                   (value = min + code step, the cache's own definition, exact), and
+//                   multiplies: scores^T = K q^T and out^T = V^T p^T, 16 x 8 x 16, so that
+//                   the 32 tokens (or 32 channels) fill the operand's rows and the few
+//                   query rows its columns.  Probabilities go from one product to the
+//                   other by movmatrix, as bf16 hi + lo.  Softmax: running maximum and sum
+//                   for each warp, in base 2.  No masks: a finished block is whole.
+//   k_dense_finish  one warp per query row: the bf16 rows of the unfinished block and the
+//                   drafted tokens that the row sees (fp32 on CUDA cores; a token that it
+//                   does not see is not touched), while the first kernel still runs, then
+//                   the merge of the splits.
+#include "rkv_dense.cuh"
+#include "umma.cuh"
+
+#include <math.h>
+
+namespace rkv {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kFinWarps = 8;
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                 "{%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t trans8x8(uint32_t a)
+{
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     um::smem_u32(dst)), "l"(src), "r"(bytes), "r"(um::smem_u32(bar)) : "memory");
+}
+
+template <int D, int BITS, int NT>
+struct SplitCfg {
+    static constexpr int kUnit = 4 * D * BITS, kRec = 2 * kUnit + 4 * D, kHdr = 4 * D;
+    static constexpr int kStage = kRec + kHdr;
+    // ring depth: about 80 KB in flight per CTA, two CTAs to an SM where registers allow
+    static constexpr int kStages = D == 256 ? 2 : (D == 128 ? (BITS == 4 ? 2 : 3) : 4);
+    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kRow = D + 4;                     // merge row, padded
+    static constexpr int kMerge = kWarps * 8 * NT * kRow * 4;
+    static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kQ = NT > 1 ? (D / 16) * NT * 32 * 8 : 0;   // q operands, lane order
+    static constexpr int kSmem = kBody + kQ + kWarps * kStages * 8;
+    static_assert(kStage % 16 == 0 && kSmem <= 227 * 1024, "shared memory of the split pass");
+};
+
+// Which finished block the i-th of a run is: the list's entry, or i itself.  -1: skip.
+__device__ __forceinline__ int block_at(const int32_t *list, int i, int have, int32_t *status)
+{
+    if (!list) return i;
+    const int b = __ldg(list + i);
+    if (b >= 0 && b < have) return b;
+    if (b != -1) set_status(status, RKV_ERR_INDEX);
+    return -1;
+}
+
+// Partials: sums [S N][splits][R][D] and {max, sum} [S N][splits][R] (max in base 2).
+template <int D, int BITS, int NT>
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 && D <= 128 ? 2 : 1)
+k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ codes,
+              const uint8_t *__restrict__ khdr, const int32_t *__restrict__ len, const int32_t *__restrict__ blocks,
+              int lists, int n_blocks, int T, int N, int G, int nq, int nb, int splits, int chunk, int tiles,
+              float scale_log2, float *__restrict__ part, float2 *__restrict__ ml, int32_t *status)
+{
+    using C = SplitCfg<D, BITS, NT>;
+    constexpr int kUnits = D / 16, kPer = 8 / BITS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float2 sml[kWarps][8 * NT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    int id = blockIdx.x;
+    const int split = id % splits;
+    id /= splits;
+    const int tile = id % tiles, sn = id / tiles, s = sn / N, n = sn % N;
+    const int R = nq * G, row0 = tile * 8 * NT;
+    uint8_t *ring = smem + warp * C::kStages * C::kStage;
+    uint64_t *bars = (uint64_t *)(smem + C::kBody + C::kQ) + warp * C::kStages;
+
+    const int have = dense_len(len, s, T, status) / kBlk;
+    const int32_t *list = blocks ? blocks + ((size_t)s * lists + (lists > 1 ? n : 0)) * n_blocks : nullptr;
+    const int total = list ? n_blocks : have;
+    const int i0 = split * chunk, i1 = min(total, i0 + chunk);
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (i0 >= i1) {
+        for (int r = threadIdx.x; r < 8 * NT && row0 + r < R; r += blockDim.x)
+            ml[((size_t)sn * splits + split) * R + row0 + r] = make_float2(-INFINITY, 0.0f);
+        return;
+    }
+    if (lane == 0) {
+        for (int i = 0; i < C::kStages; ++i) um::mbar_init(bars + i, 1);
+        um::fence_mbar_init();
+    }
+    __syncwarp();
+    // the warp's blocks: i0 + warp, + 8, ..., those that are to be skipped left out
+    int next = i0 + warp, issued = 0;
+    auto issue = [&]() {
+        int b = -1;
+        while (next < i1 && b < 0) {
+            b = block_at(list, next, have, status);
+            next += kWarps;
+        }
+        if (b < 0) return;
+        if (lane == 0) {
+            const int st = issued % C::kStages;
+            uint8_t *dst = ring + st * C::kStage;
+            const size_t rec = (size_t)sn * nb + b;
+            um::mbar_arrive_expect_tx(bars + st, C::kStage);
+            bulk_load(dst, codes + rec * C::kRec, C::kRec, bars + st);
+            bulk_load(dst + C::kRec, khdr + rec * C::kHdr, C::kHdr, bars + st);
+        }
+        ++issued;
+    };
+#pragma unroll 1
+    for (int i = 0; i < C::kStages; ++i) issue();
+
+    // query rows as the second operand: column g is row 8 nt + g, lane (g, c) holds channels
+    // 2c, 2c + 1 and 2c + 8, 2c + 9 of each unit
+    uint32_t qr[NT == 1 ? kUnits : 1][2];
+    const uint2 *qs = (const uint2 *)(smem + C::kBody);
+    auto q_row = [&](int r) -> const uint32_t * {
+        return (const uint32_t *)(q + (((size_t)s * nq + r / G) * N * G + n * G + r % G) * D);
+    };
+    if constexpr (NT == 1) {
+        const int r = row0 + g;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            qr[u][0] = r < R ? __ldg(q_row(r) + u * 8 + c) : 0u;
+            qr[u][1] = r < R ? __ldg(q_row(r) + u * 8 + 4 + c) : 0u;
+        }
+    } else {
+        for (int i = threadIdx.x; i < kUnits * NT * 32; i += blockDim.x) {
+            const int l = i & 31, nt = (i >> 5) % NT, u = (i >> 5) / NT, r = row0 + 8 * nt + (l >> 2);
+            uint2 v = make_uint2(0u, 0u);
+            if (r < R) v = make_uint2(__ldg(q_row(r) + u * 8 + (l & 3)), __ldg(q_row(r) + u * 8 + 4 + (l & 3)));
+            ((uint2 *)(smem + C::kBody))[i] = v;
+        }
+        __syncthreads();
+    }
+
+    float acc[NT][2 * (D / 32)][4], m_run[NT][2], l_run[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 2 * (D / 32); ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.0f;
+        m_run[nt][0] = m_run[nt][1] = -INFINITY;
+        l_run[nt][0] = l_run[nt][1] = 0.0f;
+    }
+    bool ok = true;
+    const int kslot = key_slot(g, c) * 16, vslot = value_slot(g, c) * 16;
+#pragma unroll 1
+    for (int k = 0; k < issued; ++k) {
+        const int st = k % C::kStages;
+        const bool landed = um::mbar_wait(bars + st, (uint32_t)(k / C::kStages) & 1u, kWaitCycles);
+        if (!__all_sync(0xffffffffu, landed)) {
+            ok = false;
+            break;
+        }
+        const uint8_t *kc = ring + st * C::kStage, *vc = kc + C::kUnit, *vh = vc + C::kUnit, *kh = kc + C::kRec;
+        // scores^T: 32 tokens x 8 NT rows
+        float sc[NT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[nt][m][e] = 0.0f;
+#pragma unroll
+        for (int u0 = 0; u0 < kUnits; u0 += kPer) {
+            const uint4 w4 = *(const uint4 *)(kc + (u0 / kPer) * 512 + kslot);
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) {
+                const int u = u0 + x;
+                const uint4 hd = *(const uint4 *)(kh + (u * 4 + c) * 16);
+                uint32_t a[2][4];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        a[m][i] = value_pair<BITS>(BITS == 4 ? w[(2 * x + m) & 3] : w[x & 3], BITS == 4 ? i : 4 * m + i,
+                                                   i < 2 ? hd.x : hd.z, i < 2 ? hd.y : hd.w);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    uint32_t b0, b1;
+                    if constexpr (NT == 1) {
+                        b0 = qr[u][0];
+                        b1 = qr[u][1];
+                    } else {
+                        const uint2 t = qs[(u * NT + nt) * 32 + lane];
+                        b0 = t.x;
+                        b1 = t.y;
+                    }
+                    mma16816(sc[nt][0], a[0], b0, b1);
+                    mma16816(sc[nt][1], a[1], b0, b1);
+                }
+            }
+        }
+        // softmax: rows 2c, 2c + 1 of each column tile; this lane's tokens are 16 m + g, + 8
+        uint32_t ph[NT][2][2], pl[NT][2][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float mx[2], al[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v = fmaxf(fmaxf(sc[nt][0][e], sc[nt][0][e + 2]), fmaxf(sc[nt][1][e], sc[nt][1][e + 2]));
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+                mx[e] = fmaxf(m_run[nt][e], v * scale_log2);
+                al[e] = ex2(m_run[nt][e] - (mx[e] == -INFINITY ? 0.0f : mx[e]));
+            }
+            if (__any_sync(0xffffffffu, mx[0] != m_run[nt][0] || mx[1] != m_run[nt][1])) {
+#pragma unroll
+                for (int i = 0; i < 2 * (D / 32); ++i) {
+                    acc[nt][i][0] *= al[0];
+                    acc[nt][i][1] *= al[1];
+                    acc[nt][i][2] *= al[0];
+                    acc[nt][i][3] *= al[1];
+                }
+                l_run[nt][0] *= al[0];
+                l_run[nt][1] *= al[1];
+                m_run[nt][0] = mx[0];
+                m_run[nt][1] = mx[1];
+            }
+            const float o0 = mx[0] == -INFINITY ? 0.0f : mx[0], o1 = mx[1] == -INFINITY ? 0.0f : mx[1];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float p0 = ex2(fmaf(sc[nt][m][2 * h], scale_log2, -o0));
+                    const float p1 = ex2(fmaf(sc[nt][m][2 * h + 1], scale_log2, -o1));
+                    l_run[nt][0] += p0;
+                    l_run[nt][1] += p1;
+                    const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - __low2float(hi), p1 - __high2float(hi));
+                    ph[nt][m][h] = trans8x8(as_u32(hi));
+                    pl[nt][m][h] = trans8x8(as_u32(lo));
+                }
+        }
+        // out^T: D channels x 8 NT rows
+#pragma unroll
+        for (int u0 = 0; u0 < kUnits; u0 += kPer) {
+            const uint4 w4 = *(const uint4 *)(vc + (u0 / kPer) * 512 + vslot);
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) {
+                const int u = u0 + x, ks = u & 1;
+                const uint4 hd = *(const uint4 *)(vh + (u * 4 + c) * 16);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    uint32_t a[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        a[i] = value_pair<BITS>(BITS == 4 ? w[(2 * x + m) & 3] : w[x & 3], BITS == 4 ? i : 4 * m + i,
+                                                i < 2 ? hd.x : hd.z, i < 2 ? hd.y : hd.w);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma16816(acc[nt][(u & ~1) + m], a, ph[nt][ks][0], ph[nt][ks][1]);
+                        mma16816(acc[nt][(u & ~1) + m], a, pl[nt][ks][0], pl[nt][ks][1]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        issue();
+    }
+    if (!ok && lane == 0) set_status(status, RKV_ERR_DEVICE_TIMEOUT);
+
+    // the lanes' sums, then the warps' partials through shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], o);
+            if (g == 0)
+                sml[warp][8 * nt + 2 * c + e] = make_float2(ok ? m_run[nt][e] : __uint_as_float(0x7fffffffu), l_run[nt][e]);
+        }
+    __syncthreads();                                       // every warp is done with its ring
+    float *rows = (float *)smem + (size_t)warp * 8 * NT * C::kRow;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2 * (D / 32); ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                rows[(8 * nt + 2 * c + (e & 1)) * C::kRow + 16 * i + g + 8 * (e >> 1)] = acc[nt][i][e];
+    __syncthreads();
+    const float *all = (const float *)smem;
+    for (int x = threadIdx.x; x < 8 * NT * (D / 4); x += blockDim.x) {
+        const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+        if (row0 + r >= R) break;
+        float m = -INFINITY;
+        bool bad = false;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            m = fmaxf(m, sml[w][r].x);
+            bad |= sml[w][r].x != sml[w][r].x;
+        }
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float l = 0.0f;
+        const float mu = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = ex2(sml[w][r].x - mu);
+            const float4 v = *(const float4 *)(all + ((size_t)w * 8 * NT + r) * C::kRow + d);
+            o.x = fmaf(v.x, f, o.x);
+            o.y = fmaf(v.y, f, o.y);
+            o.z = fmaf(v.z, f, o.z);
+            o.w = fmaf(v.w, f, o.w);
+            l = fmaf(sml[w][r].y, f, l);
+        }
+        const size_t at = ((size_t)sn * splits + split) * R + row0 + r;
+        *(float4 *)(part + at * D + d) = o;
+        if (d == 0) ml[at] = make_float2(bad ? __uint_as_float(0x7fffffffu) : m, l);
+    }
+}
+
+// One warp per query row.  Tokens that are not in finished blocks come in groups of 32
+// through shared memory: the unfinished block's rows, then drafted tokens 0..31, 32..63.
+template <int D>
+__global__ void __launch_bounds__(32 * kFinWarps)
+k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ tail,
+               const int32_t *__restrict__ len, const int32_t *__restrict__ parent,
+               const __nv_bfloat16 *__restrict__ draft, int T, int N, int G, int nq, int splits, int row_ctas,
+               float scale_log2, const float *__restrict__ part, const float2 *__restrict__ ml,
+               void *__restrict__ out, int out_bf16, int32_t *status)
+{
+    constexpr int kCh = D / 8, kPad = kCh + 1, kE = D / 32;   // 16-byte chunks of a row; channels of a lane
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint4 *ks = (uint4 *)smem, *vs = ks + kBlk * kPad;
+    __shared__ __align__(16) float qf[kFinWarps][D];
+    __shared__ int par[kMaxDraft];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sn = blockIdx.x / row_ctas, s = sn / N, n = sn % N;
+    const int R = nq * G, r = (blockIdx.x % row_ctas) * kFinWarps + warp;
+    const int length = dense_len(len, s, T, status);
+    const int rest = length % kBlk;
+    const bool live = r < R;
+    const int j = live ? r / G : 0;
+    const size_t row = (((size_t)s * nq + j) * N + n) * G + (live ? r % G : 0);
+    if (parent)
+        for (int i = threadIdx.x; i < nq; i += blockDim.x) par[i] = __ldg(parent + (size_t)s * nq + i);
+    if (live)
+        for (int i = lane; i < D / 2; i += 32) {
+            const uint32_t v = __ldg((const uint32_t *)(q + row * D) + i);
+            qf[warp][2 * i] = __uint_as_float(v << 16);
+            qf[warp][2 * i + 1] = __uint_as_float(v & 0xffff0000u);
+        }
+    __syncthreads();
+    // the drafted tokens that the row sees; parents come before their children, so that the
+    // way up ends
+    uint64_t sees = 0;
+    bool padding = !live;
+    if (parent && live) {
+        bool bad = false;
+        int p = j;
+        if (par[j] == -2) padding = true;
+        else
+            while (p >= 0) {
+                sees |= 1ull << p;
+                const int up = par[p];
+                if (up >= p || up < -1) { bad = true; break; }
+                p = up;
+            }
+        if (bad) {
+            padding = true;
+            if (lane == 0) set_status(status, RKV_ERR_INDEX);
+        }
+    }
+
+    float m = -INFINITY, l = 0.0f, acc[kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
+    const int groups = parent ? 1 + (nq + kBlk - 1) / kBlk : 1;
+    for (int grp = 0; grp < groups; ++grp) {
+        const int cnt = grp == 0 ? rest : min(kBlk, nq - (grp - 1) * kBlk);
+        if (cnt == 0) continue;
+        if (grp) __syncthreads();
+        for (int i = threadIdx.x; i < cnt * kCh; i += blockDim.x) {
+            const int t = i / kCh, ch = i % kCh;
+            const uint4 *kr, *vr;
+            if (grp == 0) {
+                kr = (const uint4 *)(tail + ((size_t)sn * 2 * kBlk + t) * D);
+                vr = kr + kBlk * kCh;
+            } else {
+                kr = (const uint4 *)(draft + (((size_t)s * nq + (grp - 1) * kBlk + t) * 2 * N + n) * D);
+                vr = kr + N * kCh;
+            }
+            ks[t * kPad + ch] = kr[ch];
+            vs[t * kPad + ch] = vr[ch];
+        }
+        __syncthreads();
+        uint32_t mask = 0u;
+        if (!padding)
+            mask = grp == 0 ? (1u << rest) - 1u : (uint32_t)(sees >> ((grp - 1) * kBlk));
+        if (mask == 0u) continue;                          // the same for the whole warp
+        // lane t scores token t of the group
+        float x = -INFINITY;
+        if ((mask >> lane) & 1u) {
+            float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll 4
+            for (int ch = 0; ch < kCh; ++ch) {
+                const uint4 kv = ks[lane * kPad + ch];
+                const float4 a = *(const float4 *)&qf[warp][8 * ch], b = *(const float4 *)&qf[warp][8 * ch + 4];
+                d0 = fmaf(a.x, __uint_as_float(kv.x << 16), d0);
+                d1 = fmaf(a.y, __uint_as_float(kv.x & 0xffff0000u), d1);
+                d0 = fmaf(a.z, __uint_as_float(kv.y << 16), d0);
+                d1 = fmaf(a.w, __uint_as_float(kv.y & 0xffff0000u), d1);
+                d0 = fmaf(b.x, __uint_as_float(kv.z << 16), d0);
+                d1 = fmaf(b.y, __uint_as_float(kv.z & 0xffff0000u), d1);
+                d0 = fmaf(b.z, __uint_as_float(kv.w << 16), d0);
+                d1 = fmaf(b.w, __uint_as_float(kv.w & 0xffff0000u), d1);
+            }
+            x = (d0 + d1) * scale_log2;
+        }
+        float mx = x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = fmaxf(mx, m);
+        const float mu = mx == -INFINITY ? 0.0f : mx;
+        const float al = ex2(m - mu), p = ex2(x - mu);
+        m = mx;
+        l *= al;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[e] *= al;
+        while (mask) {
+            const int t = __ffs(mask) - 1;
+            mask &= mask - 1u;
+            const float pt = __shfl_sync(0xffffffffu, p, t);
+            l += pt;
+            const uint32_t *v = (const uint32_t *)(vs + t * kPad) + lane * (kE / 2);
+#pragma unroll
+            for (int e = 0; e < kE / 2; ++e) {
+                acc[2 * e] = fmaf(pt, __uint_as_float(v[e] << 16), acc[2 * e]);
+                acc[2 * e + 1] = fmaf(pt, __uint_as_float(v[e] & 0xffff0000u), acc[2 * e + 1]);
+            }
+        }
+    }
+
+    // the splits' partials: launched as a programmatic dependent, this waits for them
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!live) return;
+    if (!padding) {
+        const float2 *mlr = ml + (size_t)sn * splits * R + r;
+        float mx = m;
+        bool bad = false;
+        for (int i = lane; i < splits; i += 32) {
+            const float v = mlr[(size_t)i * R].x;
+            bad |= v != v;
+            mx = fmaxf(mx, v);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mu = mx == -INFINITY ? 0.0f : mx;
+        const float al = ex2(m - mu);
+        l *= al;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[e] *= al;
+        const float *pr = part + ((size_t)sn * splits * R + r) * D + lane * kE;
+#pragma unroll 4
+        for (int i = 0; i < splits; ++i) {
+            const float2 v = mlr[(size_t)i * R];
+            if (v.x == -INFINITY) continue;                // nothing in this split
+            const float f = ex2(v.x - mu);
+            l = fmaf(v.y, f, l);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) acc[e] = fmaf(pr[(size_t)i * R * D + e], f, acc[e]);
+        }
+        if (__any_sync(0xffffffffu, bad)) l = __uint_as_float(0x7fffffffu);
+    }
+    // l is 0 only where the row sees nothing (the largest p is 1); NaN stays NaN
+    const bool none = padding || l == 0.0f;
+    const float inv = none ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) acc[e] = none ? 0.0f : acc[e] * inv;
+    if (out_bf16) {
+        uint32_t *o = (uint32_t *)((__nv_bfloat16 *)out + row * D) + lane * (kE / 2);
+#pragma unroll
+        for (int e = 0; e < kE / 2; ++e) o[e] = as_u32(__floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]));
+    } else {
+        float *o = (float *)out + row * D + lane * kE;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] = acc[e];
+    }
+}
+
+// How the finished blocks of a (sequence, KV head) are cut: `chunk` blocks for a CTA.  Fixed
+// sizes, so that long sequences take more CTAs than short ones.  Does not depend on the
+// device, so that the workspace's size and the order of the sums do not either.
+struct Plan { int tiles, nt, chunk, splits; };
+
+Plan plan_of(const DenseGeom &g, int H, int nq, int max_blocks)
+{
+    Plan p;
+    const int R = nq * (H / g.N);
+    p.nt = R <= 8 ? 1 : (R <= 16 || g.D == 256 ? 2 : 4);
+    p.tiles = (R + 8 * p.nt - 1) / (8 * p.nt);
+    constexpr int kTarget = 1024;                          // CTAs
+    const long long work = (long long)g.S * g.N * p.tiles * max_blocks;
+    long long chunk = (work + kTarget - 1) / kTarget;
+    chunk = (chunk + kWarps - 1) / kWarps * kWarps;
+    p.chunk = (int)(chunk < kWarps ? kWarps : chunk);
+    p.splits = max(1, (max_blocks + p.chunk - 1) / p.chunk);
+    return p;
+}
+
+template <int D, int BITS, int NT>
+cudaError_t run_split(const DenseGeom &g, const Plan &p, int H, const void *q, int nq, const rkv_dense_cache *c,
+                      const int32_t *len, const int32_t *blocks, int lists, int n_blocks, float scale_log2,
+                      float *part, float2 *ml, int32_t *status, cudaStream_t s)
+{
+    using C = SplitCfg<D, BITS, NT>;
+    static PerDevice<int> setup;
+    int unused = 0;
+    cudaError_t e = per_device(setup, unused, [](int &) {
+        return cudaFuncSetAttribute(k_dense_split<D, BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    });
+    if (e != cudaSuccess) return e;
+    ProfScope prof("dense_attention_split", s);
+    k_dense_split<D, BITS, NT><<<(unsigned)((size_t)g.S * g.N * p.tiles * p.splits), 32 * kWarps, C::kSmem, s>>>(
+        (const __nv_bfloat16 *)q, (const uint8_t *)c->codes, (const uint8_t *)c->khdr, len, blocks, lists, n_blocks,
+        g.T, g.N, H / g.N, nq, g.nb, p.splits, p.chunk, p.tiles, scale_log2, part, ml, status);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t run_finish(const DenseGeom &g, const Plan &p, int H, const void *q, int nq, const int32_t *parent,
+                       const void *draft, const rkv_dense_cache *c, const int32_t *len, float scale_log2,
+                       const float *part, const float2 *ml, void *out, int out_dtype, int32_t *status, cudaStream_t s)
+{
+    const int R = nq * (H / g.N), row_ctas = (R + kFinWarps - 1) / kFinWarps;
+    constexpr int kSmem = 2 * kBlk * (D / 8 + 1) * 16;
+    static_assert(kSmem + kFinWarps * D * 4 + kMaxDraft * 4 <= 48 * 1024, "shared memory of the last pass");
+    ProfScope prof("dense_attention_finish", s);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)((size_t)g.S * g.N * row_ctas), 1, 1);
+    cfg.blockDim = dim3(32 * kFinWarps, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k_dense_finish<D>, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)c->tail,
+                                       len, parent, (const __nv_bfloat16 *)draft, g.T, g.N, H / g.N, nq, p.splits,
+                                       row_ctas, scale_log2, part, ml, out, (int)(out_dtype == RKV_BF16), status);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq, int max_blocks)
+{
+    const Plan p = plan_of(g, H, nq, max_blocks);
+    const size_t rows = (size_t)g.S * g.N * p.splits * nq * (H / g.N);
+    return align256(rows * g.D * sizeof(float)) + align256(rows * sizeof(float2));
+}
+
+cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int nq, const int32_t *parent,
+                                   const void *draft, const rkv_dense_cache *cache, const int32_t *len,
+                                   const int32_t *blocks, int lists, int n_blocks, void *out, int out_dtype,
+                                   void *ws, int32_t *status, cudaStream_t s)
+{
+    const Plan p = plan_of(g, H, nq, blocks ? n_blocks : g.nb);
+    const size_t rows = (size_t)g.S * g.N * p.splits * nq * (H / g.N);
+    float *part = (float *)ws;
+    float2 *ml = (float2 *)((uint8_t *)ws + align256(rows * g.D * sizeof(float)));
+    const float scale_log2 = (float)(1.4426950408889634 / sqrt((double)g.D));
+    auto go = [&](auto bits, auto d) -> cudaError_t {
+        constexpr int B = decltype(bits)::value, D = decltype(d)::value;
+        cudaError_t e;
+        if (p.nt == 1)
+            e = run_split<D, B, 1>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
+        else if (p.nt == 2)
+            e = run_split<D, B, 2>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
+        else if constexpr (D < 256)
+            e = run_split<D, B, 4>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
+        else
+            e = cudaErrorInvalidValue;
+        if (e != cudaSuccess) return e;
+        return run_finish<D>(g, p, H, q, nq, parent, draft, cache, len, scale_log2, part, ml, out, out_dtype, status, s);
+    };
+    return dense_dispatch(g, go);
+}
+
+}  // namespace rkv

@@ -20,7 +20,10 @@ RKV_ERR_CUDA, RKV_ERR_INDEX, RKV_ERR_DEVICE_TIMEOUT, RKV_ERR_WORKSPACE = 4, 5, 6
 EXPORTED = ("rkv_n_ref", "rkv_query_sizes", "rkv_build_ref_pool", "rkv_compress",
             "rkv_gather_dequant", "rkv_restore_kv", "rkv_attention_workspace", "rkv_sparse_attention",
             "rkv_append_token", "rkv_compress_noalloc", "rkv_profile_enable", "rkv_profile_collect",
-            "rkv_debug_wait_fault", "rkv_status_string")
+            "rkv_debug_wait_fault", "rkv_status_string",
+            "rkv_dense_sizes", "rkv_dense_write", "rkv_dense_read", "rkv_block_select_workspace",
+            "rkv_block_select", "rkv_dense_attention_workspace", "rkv_dense_attention",
+            "rkv_tree_attention")
 _DTYPES = {"f32": RKV_F32, "bf16": RKV_BF16, "fp8": RKV_FP8_E4M3}
 
 
@@ -38,6 +41,14 @@ class rkv_ref_pool(ctypes.Structure):
 
 class rkv_cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "hdr", "ref_idx")]
+
+
+class rkv_dense_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("S", "T", "N", "D", "bits", "reserved")]
+
+
+class rkv_dense_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "khdr", "tail")]
 
 
 class RkvError(RuntimeError):
@@ -85,6 +96,18 @@ def lib():
         L.rkv_attention_workspace.restype = I32
         L.rkv_sparse_attention.argtypes = [P, I32, V, V, V, V, I32, V, V, ctypes.c_size_t, V]
         L.rkv_sparse_attention.restype = I32
+        DP, DC, Z = ctypes.POINTER(rkv_dense_params), ctypes.POINTER(rkv_dense_cache), ctypes.c_size_t
+        for name, args in (
+                ("rkv_dense_sizes", [DP, sz, sz, sz]),
+                ("rkv_dense_write", [DP, V, I32, I32, V, V, DC, V, V]),
+                ("rkv_dense_read", [DP, DC, V, V, I32, V, V, V, V]),
+                ("rkv_block_select_workspace", [DP, I32, sz]),
+                ("rkv_block_select", [DP, I32, V, DC, V, I32, I32, I32, I32, V, V, Z, V, V]),
+                ("rkv_dense_attention_workspace", [DP, I32, I32, I32, I32, sz]),
+                ("rkv_dense_attention", [DP, I32, V, DC, V, V, I32, I32, V, I32, V, Z, V, V]),
+                ("rkv_tree_attention", [DP, I32, V, I32, V, V, DC, V, V, I32, V, Z, V, V])):
+            f = getattr(L, name)
+            f.argtypes, f.restype = args, I32
         L.rkv_profile_enable.argtypes = [I32]
         L.rkv_profile_enable.restype = I32
         L.rkv_profile_collect.argtypes = [ctypes.c_char_p, I32, ctypes.POINTER(ctypes.c_float),
@@ -214,6 +237,82 @@ def rkv_sparse_attention(p: rkv_params, H: int, q, k_hat, v_hat, sel, n_sel: int
                                     int(workspace_bytes), _stream(stream))
     if st:
         raise RkvError(st, "rkv_sparse_attention")
+
+
+def make_dense_params(S, T, N, D, bits=4) -> rkv_dense_params:
+    return rkv_dense_params(S, T, N, D, bits, 0)
+
+
+def rkv_dense_sizes(p: rkv_dense_params):
+    """(codes, khdr, tail) bytes."""
+    a, b, c = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
+    st = lib().rkv_dense_sizes(ctypes.byref(p), ctypes.byref(a), ctypes.byref(b), ctypes.byref(c))
+    if st:
+        raise RkvError(st, "rkv_dense_sizes")
+    return a.value, b.value, c.value
+
+
+def rkv_dense_write(p: rkv_dense_params, kv, kv_dtype: int, n: int, pos, n_new, cache: rkv_dense_cache,
+                    dev_status, stream=None) -> None:
+    st = lib().rkv_dense_write(ctypes.byref(p), _ptr(kv), kv_dtype, n, _ptr(pos), _ptr(n_new),
+                               ctypes.byref(cache), _ptr(dev_status), _stream(stream))
+    if st:
+        raise RkvError(st, "rkv_dense_write")
+
+
+def rkv_dense_read(p: rkv_dense_params, cache: rkv_dense_cache, length, sel, n_sel: int, out_k, out_v,
+                   dev_status, stream=None) -> None:
+    st = lib().rkv_dense_read(ctypes.byref(p), ctypes.byref(cache), _ptr(length), _ptr(sel), n_sel,
+                              _ptr(out_k), _ptr(out_v), _ptr(dev_status), _stream(stream))
+    if st:
+        raise RkvError(st, "rkv_dense_read")
+
+
+def rkv_block_select_workspace(p: rkv_dense_params, lists: int) -> int:
+    b = ctypes.c_size_t()
+    st = lib().rkv_block_select_workspace(ctypes.byref(p), lists, ctypes.byref(b))
+    if st:
+        raise RkvError(st, "rkv_block_select_workspace")
+    return b.value
+
+
+def rkv_block_select(p: rkv_dense_params, H: int, q, cache: rkv_dense_cache, length, lists: int,
+                     n_blocks: int, keep_first: int, keep_last: int, blocks, workspace,
+                     workspace_bytes: int, dev_status, stream=None) -> None:
+    st = lib().rkv_block_select(ctypes.byref(p), H, _ptr(q), ctypes.byref(cache), _ptr(length), lists,
+                                n_blocks, keep_first, keep_last, _ptr(blocks), _ptr(workspace),
+                                workspace_bytes, _ptr(dev_status), _stream(stream))
+    if st:
+        raise RkvError(st, "rkv_block_select")
+
+
+def rkv_dense_attention_workspace(p: rkv_dense_params, H: int, n_query: int = 1, n_blocks: int = 0,
+                                  listed: bool = False) -> int:
+    b = ctypes.c_size_t()
+    st = lib().rkv_dense_attention_workspace(ctypes.byref(p), H, n_query, n_blocks, int(listed), ctypes.byref(b))
+    if st:
+        raise RkvError(st, "rkv_dense_attention_workspace")
+    return b.value
+
+
+def rkv_dense_attention(p: rkv_dense_params, H: int, q, cache: rkv_dense_cache, length, blocks, lists: int,
+                        n_blocks: int, out, out_dtype: int, workspace, workspace_bytes: int, dev_status,
+                        stream=None) -> None:
+    st = lib().rkv_dense_attention(ctypes.byref(p), H, _ptr(q), ctypes.byref(cache), _ptr(length),
+                                   _ptr(blocks), lists, n_blocks, _ptr(out), out_dtype, _ptr(workspace),
+                                   workspace_bytes, _ptr(dev_status), _stream(stream))
+    if st:
+        raise RkvError(st, "rkv_dense_attention")
+
+
+def rkv_tree_attention(p: rkv_dense_params, H: int, q, n_draft: int, parent, draft_kv,
+                       cache: rkv_dense_cache, length, out, out_dtype: int, workspace, workspace_bytes: int,
+                       dev_status, stream=None) -> None:
+    st = lib().rkv_tree_attention(ctypes.byref(p), H, _ptr(q), n_draft, _ptr(parent), _ptr(draft_kv),
+                                  ctypes.byref(cache), _ptr(length), _ptr(out), out_dtype, _ptr(workspace),
+                                  workspace_bytes, _ptr(dev_status), _stream(stream))
+    if st:
+        raise RkvError(st, "rkv_tree_attention")
 
 
 def rkv_debug_wait_fault(wait_cycles: int, skip_use: int) -> None:
@@ -354,3 +453,136 @@ class Buffers:
             if raw is not None and t is not None and not guard_intact(t, raw):
                 bad.append(name)
         return bad
+
+
+class DenseCache:
+    """The dense cache of one rkv_dense_params on one device: its three buffers, the device
+    status, and its operators with their tensors checked (type, shape, contiguity, device).
+    Scratch is taken from torch's allocator for each call, on the stream that the call runs on,
+    so that calls on several streams, and captured graphs, share none of it.  Calls that write
+    the cache and calls that read it are ordered by the caller, as for any tensor.
+    guard > 0 puts that many guard bytes behind every buffer, scratch included (test support)."""
+
+    def __init__(self, p: rkv_dense_params, device="cuda", guard: int = 0):
+        codes, khdr, tail = rkv_dense_sizes(p)
+        self.p = p
+        self.guard = guard
+        self._raw = {}
+        for name, n, fill in (("codes", codes, None), ("khdr", khdr, None), ("tail", tail, None), ("status", 16, 0)):
+            t, raw = guarded_empty((n,), torch.uint8, device, guard, fill)
+            setattr(self, name, t)
+            self._raw[name] = (t, raw)
+        self.status = self.status.view(torch.int32)
+        self.device = self.status.device
+        self.cache = rkv_dense_cache(_ptr(self.codes), _ptr(self.khdr), _ptr(self.tail))
+        self._sizes = {}
+
+    def _check(self, name, t, dtypes, shape):
+        if t.dtype not in dtypes:
+            raise ValueError("%s: %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
+        if tuple(t.shape) != shape:
+            raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
+        if not t.is_contiguous():
+            raise ValueError("%s is not contiguous" % name)
+        if t.device != self.device:
+            raise ValueError("%s is on %s, the cache on %s" % (name, t.device, self.device))
+
+    def _run(self, stream, key, query, call):
+        """Runs call(workspace, bytes) with the cache's device current and scratch of
+        query() bytes from the pool of the stream that the call runs on."""
+        need = self._sizes.get(key)
+        if need is None:
+            need = self._sizes[key] = query()
+        if stream is None and torch.cuda.current_device() == self.device.index:
+            return call(*self._scratch(need))
+        with torch.cuda.device(self.device):
+            if stream is None:
+                return call(*self._scratch(need))
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=self.device)
+            with torch.cuda.stream(stream):
+                return call(*self._scratch(need))
+
+    def _scratch(self, need):
+        if need == 0:
+            return None, 0
+        if not self.guard:
+            return torch.empty(need, dtype=torch.uint8, device=self.device), need
+        t, raw = guarded_empty((need,), torch.uint8, self.device, self.guard)
+        self._raw["scratch %d" % len(self._raw)] = (t, raw)
+        return t, need
+
+    def write(self, kv, pos, n_new=None, stream=None):
+        """kv [S][n][2ND] (bf16 or fp32) as tokens pos[s] .. of each sequence; n_new[s] of its n
+        rows (all of them where n_new is None)."""
+        p = self.p
+        n = kv.shape[1] if kv.dim() == 3 else -1
+        self._check("kv", kv, (torch.bfloat16, torch.float32), (p.S, n, 2 * p.N * p.D))
+        self._check("pos", pos, (torch.int32,), (p.S,))
+        if n_new is not None:
+            self._check("n_new", n_new, (torch.int32,), (p.S,))
+        dt = RKV_F32 if kv.dtype == torch.float32 else RKV_BF16
+        self._run(stream, None, lambda: 0, lambda ws, nb: rkv_dense_write(
+            p, kv, dt, n, pos, n_new, self.cache, self.status))
+
+    def read(self, length, sel, out_k, out_v, stream=None):
+        """K and V of tokens sel [S][n_sel] (-1: zero rows) to out_k, out_v bf16 [S][n_sel][ND]."""
+        p = self.p
+        n = sel.shape[1] if sel.dim() == 2 else -1
+        self._check("length", length, (torch.int32,), (p.S,))
+        self._check("sel", sel, (torch.int32,), (p.S, n))
+        self._check("out_k", out_k, (torch.bfloat16,), (p.S, n, p.N * p.D))
+        self._check("out_v", out_v, (torch.bfloat16,), (p.S, n, p.N * p.D))
+        self._run(stream, None, lambda: 0, lambda ws, nb: rkv_dense_read(
+            p, self.cache, length, sel, n, out_k, out_v, self.status))
+
+    def select(self, H: int, q, length, blocks, keep_first: int = 0, keep_last: int = 0, stream=None):
+        """The blocks [S][N or 1][n_blocks] (output) with the largest score bounds for q [S][H][D]."""
+        p = self.p
+        lists, n = (blocks.shape[1], blocks.shape[2]) if blocks.dim() == 3 else (-1, -1)
+        self._check("q", q, (torch.bfloat16,), (p.S, H, p.D))
+        self._check("length", length, (torch.int32,), (p.S,))
+        self._check("blocks", blocks, (torch.int32,), (p.S, lists, n))
+        self._run(stream, ("select", lists), lambda: rkv_block_select_workspace(p, lists),
+                  lambda ws, nb: rkv_block_select(p, H, q, self.cache, length, lists, n, keep_first, keep_last,
+                                                  blocks, ws, nb, self.status))
+
+    def attend(self, H: int, q, length, out, blocks=None, stream=None):
+        """out [S][H][D] (fp32 or bf16): attention of q [S][H][D] over the cache, or over the
+        listed blocks [S][N or 1][n_blocks] and the unfinished one."""
+        p = self.p
+        self._check("q", q, (torch.bfloat16,), (p.S, H, p.D))
+        self._check("length", length, (torch.int32,), (p.S,))
+        self._check("out", out, (torch.float32, torch.bfloat16), (p.S, H, p.D))
+        lists, n = 1, 0
+        if blocks is not None:
+            lists, n = (blocks.shape[1], blocks.shape[2]) if blocks.dim() == 3 else (-1, -1)
+            self._check("blocks", blocks, (torch.int32,), (p.S, lists, n))
+            if n < 1:
+                raise ValueError("blocks: an empty list")
+        dt = RKV_F32 if out.dtype == torch.float32 else RKV_BF16
+        self._run(stream, ("attend", H, 1, n), lambda: rkv_dense_attention_workspace(p, H, 1, n, blocks is not None),
+                  lambda ws, nb: rkv_dense_attention(p, H, q, self.cache, length, blocks, lists, n, out, dt, ws, nb,
+                                                     self.status))
+
+    def tree_attend(self, H: int, q, parent, draft_kv, length, out, stream=None):
+        """out [S][n][H][D] (fp32 or bf16): attention of the drafted tokens' q [S][n][H][D] over
+        the cache and their own line of parents; draft_kv bf16 [S][n][2ND], parent [S][n]."""
+        p = self.p
+        n = q.shape[1] if q.dim() == 4 else -1
+        self._check("q", q, (torch.bfloat16,), (p.S, n, H, p.D))
+        self._check("parent", parent, (torch.int32,), (p.S, n))
+        self._check("draft_kv", draft_kv, (torch.bfloat16,), (p.S, n, 2 * p.N * p.D))
+        self._check("length", length, (torch.int32,), (p.S,))
+        self._check("out", out, (torch.float32, torch.bfloat16), (p.S, n, H, p.D))
+        dt = RKV_F32 if out.dtype == torch.float32 else RKV_BF16
+        self._run(stream, ("attend", H, n, 0), lambda: rkv_dense_attention_workspace(p, H, n),
+                  lambda ws, nb: rkv_tree_attention(p, H, q, n, parent, draft_kv, self.cache, length, out, dt, ws,
+                                                    nb, self.status))
+
+    def device_status(self) -> int:
+        return int(self.status[0].item())
+
+    def guard_violations(self):
+        """Names of the buffers whose guard bytes changed (empty without guards)."""
+        return [k for k, (t, raw) in self._raw.items() if raw is not None and not guard_intact(t, raw)]
