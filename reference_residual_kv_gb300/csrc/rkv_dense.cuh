@@ -117,4 +117,10 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
                                    const int32_t *blocks, int lists, int n_blocks, void *out, int out_dtype,
                                    void *ws, int32_t *status, cudaStream_t s);
 
+// The finished blocks against many query rows (rkv_dense_tree.cu), D <= 128: two partials
+// for each of `splits` runs of `chunk` blocks.
+cudaError_t launch_dense_tree(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *cache,
+                              const int32_t *len, int splits, int chunk, float scale_log2, bool p_lo, float *part,
+                              float2 *ml, int32_t *status, cudaStream_t s);
+
 }  // namespace rkv

@@ -512,12 +512,25 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
 // How the finished blocks of a (sequence, KV head) are cut: `chunk` blocks for a CTA.  Fixed
 // sizes, so that long sequences take more CTAs than short ones.  Does not depend on the
 // device, so that the workspace's size and the order of the sums do not either.
-struct Plan { int tiles, nt, chunk, splits; };
+// `parts`: partials of a row.
+struct Plan { int tiles, nt, chunk, splits, parts; bool tree; };
 
 Plan plan_of(const DenseGeom &g, int H, int nq, int max_blocks)
 {
     Plan p;
     const int R = nq * (H / g.N);
+    p.tree = R > 32 && g.D <= 128;
+    if (p.tree) {
+        constexpr int kTarget = 304;                       // CTAs, one to an SM
+        const long long heads = (long long)g.S * g.N * ((R + 255) / 256);
+        long long chunk = (heads * max_blocks + kTarget - 1) / kTarget;
+        chunk = (chunk + 15) / 16 * 16;
+        p.nt = p.tiles = 0;
+        p.chunk = (int)(chunk < 32 ? 32 : chunk);
+        p.splits = max(1, (max_blocks + p.chunk - 1) / p.chunk);
+        p.parts = 2 * p.splits;
+        return p;
+    }
     p.nt = R <= 8 ? 1 : (R <= 16 || g.D == 256 ? 2 : 4);
     p.tiles = (R + 8 * p.nt - 1) / (8 * p.nt);
     constexpr int kTarget = 1024;                          // CTAs
@@ -525,7 +538,7 @@ Plan plan_of(const DenseGeom &g, int H, int nq, int max_blocks)
     long long chunk = (work + kTarget - 1) / kTarget;
     chunk = (chunk + kWarps - 1) / kWarps * kWarps;
     p.chunk = (int)(chunk < kWarps ? kWarps : chunk);
-    p.splits = max(1, (max_blocks + p.chunk - 1) / p.chunk);
+    p.parts = p.splits = max(1, (max_blocks + p.chunk - 1) / p.chunk);
     return p;
 }
 
@@ -568,7 +581,7 @@ cudaError_t run_finish(const DenseGeom &g, const Plan &p, int H, const void *q, 
     cfg.attrs = at;
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, k_dense_finish<D>, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)c->tail,
-                                       len, parent, (const __nv_bfloat16 *)draft, g.T, g.N, H / g.N, nq, p.splits,
+                                       len, parent, (const __nv_bfloat16 *)draft, g.T, g.N, H / g.N, nq, p.parts,
                                        row_ctas, scale_log2, part, ml, out, (int)(out_dtype == RKV_BF16), status);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
@@ -580,7 +593,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq, int max_blocks)
 {
     const Plan p = plan_of(g, H, nq, max_blocks);
-    const size_t rows = (size_t)g.S * g.N * p.splits * nq * (H / g.N);
+    const size_t rows = (size_t)g.S * g.N * p.parts * nq * (H / g.N);
     return align256(rows * g.D * sizeof(float)) + align256(rows * sizeof(float2));
 }
 
@@ -590,14 +603,17 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
                                    void *ws, int32_t *status, cudaStream_t s)
 {
     const Plan p = plan_of(g, H, nq, blocks ? n_blocks : g.nb);
-    const size_t rows = (size_t)g.S * g.N * p.splits * nq * (H / g.N);
+    const size_t rows = (size_t)g.S * g.N * p.parts * nq * (H / g.N);
     float *part = (float *)ws;
     float2 *ml = (float2 *)((uint8_t *)ws + align256(rows * g.D * sizeof(float)));
     const float scale_log2 = (float)(1.4426950408889634 / sqrt((double)g.D));
     auto go = [&](auto bits, auto d) -> cudaError_t {
         constexpr int B = decltype(bits)::value, D = decltype(d)::value;
         cudaError_t e;
-        if (p.nt == 1)
+        if (p.tree)
+            e = launch_dense_tree(g, H, q, nq, cache, len, p.splits, p.chunk, scale_log2, out_dtype == RKV_F32, part, ml,
+                                  status, s);
+        else if (p.nt == 1)
             e = run_split<D, B, 1>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
         else if (p.nt == 2)
             e = run_split<D, B, 2>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);

@@ -109,14 +109,16 @@ def select(q, ends, n_blocks, keep_first, keep_last, shared):
     return out
 
 
-def attend(q, k, v):
+def attend(q, k, v, p_err=2.0 ** -16):
     """softmax(q K^T / sqrt(D)) V for one row q [D] over k, v [n][D], and an error bound of a
     pass whose scores are fp32 sums of exact products: (out, bound).
       scores: D products added in fp32, each addition off by at most 2^-22 of the sum of the
       magnitudes so far (tensor cores may cut instead of round): |ds| <= D 2^-22 A / sqrt(D),
-      A = max_n sum |q k|; the exponent's argument adds 2^-23 |s|; probabilities as bf16
-      hi + lo are within 2^-16; sums of p and of p v in fp32: 2^-20 together.  A relative
-      error r of every p moves the output by at most 2 r sum(p |v|) / sum(p)."""
+      A = max_n sum |q k|; the exponent's argument adds 2^-23 |s|; sums of p and of p v in
+      fp32: 2^-20 together.  A relative error r of every p, in numerator and denominator,
+      moves the output by at most 2 r sum(p |v|) / sum(p).  The probabilities that meet the
+      values, but not their sum, are rounded further by p_err: 2^-16 as bf16 hi + lo, 2^-8
+      (half a step of bf16) as bf16; that moves the output by p_err sum(p |v|) / sum(p)."""
     D = q.shape[0]
     if len(k) == 0:
         return np.zeros(D), np.zeros(D)
@@ -124,8 +126,8 @@ def attend(q, k, v):
     p = np.exp(s - s.max())
     p /= p.sum()
     A = (np.abs(k) @ np.abs(q)).max() / math.sqrt(D)
-    r = D * 2.0 ** -22 * A + 2.0 ** -23 * np.abs(s).max() + 2.0 ** -16 + 2.0 ** -20
-    return p @ v, 2 * r * (p @ np.abs(v)) + 1e-30
+    r = D * 2.0 ** -22 * A + 2.0 ** -23 * np.abs(s).max() + 2.0 ** -20
+    return p @ v, (2 * r + p_err) * (p @ np.abs(v)) + 1e-30
 
 
 def line_of(parent, j):

@@ -327,7 +327,8 @@ def check_tree(case, q, parent, draft, got, bf16=False):
             for h in range(H):
                 kh = np.concatenate([K[:, h // G], draft[s, line, 0, h // G]])
                 vh = np.concatenate([V[:, h // G], draft[s, line, 1, h // G]])
-                want, tol = do.attend(q[s, j, h], kh, vh)
+                # many rows with bf16 outputs: probabilities in bf16 (include/rkv.h)
+                want, tol = do.attend(q[s, j, h], kh, vh, 2.0 ** -8 if bf16 and n * G > 32 and D <= 128 else 2.0 ** -16)
                 if bf16:
                     tol = tol + HALF_BF16 * np.abs(want)
                 assert np.all(np.abs(got[s, j, h] - want) <= tol), (s, j, h, np.abs(got[s, j, h] - want).max(), tol.min())
@@ -355,6 +356,23 @@ def test_tree_attention(D, bits, N, G, n):
     for dtype in (torch.float32, torch.bfloat16):
         got = tree_gpu(case, q, parent, draft, dtype)
         check_tree(case, q, parent, draft, got, dtype == torch.bfloat16)
+    case.done()
+
+
+@pytest.mark.parametrize("D,bits,G,n", [(128, 4, 4, 64), (128, 2, 5, 20), (64, 4, 8, 40), (64, 2, 3, 12), (128, 4, 8, 5)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_trees_over_long_caches(D, bits, G, n, dtype):
+    # many tiles and several runs of blocks; keys grow along the cache, so that the maximum of
+    # a row moves again and again (and by more than any fixed reference allows); the other
+    # sequence ends inside a tile
+    rng = np.random.default_rng(D * n)
+    rows = make_rows(rng, 2, 4500, 1, D)
+    rows[:, :, 0] = do.bf16(rows[:, :, 0] * (0.2 + 4.0 * np.arange(4500)[None, :, None, None] / 4500))
+    case = Case(rows, [4500, 2085], bits)
+    q = do.bf16(rng.normal(size=(2, n, G, D)) * 1.5)
+    draft = make_rows(rng, 2, n, 1, D)
+    parent = random_tree(rng, 2, n)
+    check_tree(case, q, parent, draft, tree_gpu(case, q, parent, draft, dtype), dtype == torch.bfloat16)
     case.done()
 
 
