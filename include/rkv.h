@@ -329,10 +329,9 @@ rkv_status rkv_block_select(const rkv_dense_params *p, int32_t H, const void *q,
  * listed twice enters twice.  A sequence with nothing to attend gives zeros.
  * q: bf16 [S][H][D]; out: [S][H][D] in out_dtype (RKV_F32 or RKV_BF16).  Scores, softmax and
  * sums in fp32; probabilities meet the values as bf16 hi + lo (relative error about 2^-16).
- * workspace: >= the bytes of rkv_dense_attention_workspace(p, H, 1, n_blocks, blocks != NULL),
- * 256-byte aligned.  Requires H a multiple of N, H/N <= 8.                               */
-rkv_status rkv_dense_attention_workspace(const rkv_dense_params *p, int32_t H, int32_t n_query,
-                                         int32_t n_blocks, int32_t listed, size_t *bytes);
+ * workspace: >= the bytes of rkv_dense_attention_workspace(p, H, 1), 256-byte
+ * aligned.  Requires H a multiple of N, H/N <= 8.                               */
+rkv_status rkv_dense_attention_workspace(const rkv_dense_params *p, int32_t H, int32_t n_query, size_t *bytes);
 rkv_status rkv_dense_attention(const rkv_dense_params *p, int32_t H, const void *q,
                                const rkv_dense_cache *cache, const int32_t *len, const int32_t *blocks,
                                int32_t lists, int32_t n_blocks, void *out, int32_t out_dtype,
@@ -350,7 +349,7 @@ rkv_status rkv_dense_attention(const rkv_dense_params *p, int32_t H, const void 
  * in rkv_dense_attention, except for more than 32 query rows to a KV head (n_draft H/N) of
  * D <= 128 with bf16 outputs: there as bf16 (2^-8 for each, half a step of the outputs).
  * q: bf16 [S][n_draft][H][D]; out: [S][n_draft][H][D] in out_dtype.  1 <= n_draft <= 64.
- * workspace: >= the bytes of rkv_dense_attention_workspace(p, H, n_draft, 0, 0), 256-byte
+ * workspace: >= the bytes of rkv_dense_attention_workspace(p, H, n_draft), 256-byte
  * aligned.  Requires H a multiple of N, H/N <= 8.                                        */
 rkv_status rkv_tree_attention(const rkv_dense_params *p, int32_t H, const void *q, int32_t n_draft,
                               const int32_t *parent, const void *draft_kv,

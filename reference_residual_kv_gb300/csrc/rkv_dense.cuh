@@ -68,8 +68,92 @@ __device__ __forceinline__ int dense_len(const int32_t *len, int s, int T, int32
 __device__ __forceinline__ int key_slot(int g, int c) { return 4 * g + c; }
 __device__ __forceinline__ int value_slot(int g, int c) { return 8 * c + ((g + 2 * c) & 7); }
 
-// {min} pair of columns half h (0: 2c, 2c + 1; 1: 2c + 8, 2c + 9) of a header
-__device__ __forceinline__ uint32_t hdr_min(const uint4 &hd, int h) { return h ? hd.z : hd.x; }
+// ---- how finished blocks are dealt out ---------------------------------------------------
+// The blocks to attend (of all sequences, for one KV head) are cut into runs of at most `chunk`
+// blocks of one sequence, numbered through; chunk follows from the lengths that the device
+// holds, so that a batch of uneven or short sequences fills the GPU as full ones do: it is
+// near the smallest that makes no more than `target` runs (or one for every sequence, where
+// there are more sequences than that).  So there are at most max(target, S) runs (the host's
+// grid and workspace).  Every lane of a warp takes part.
+struct DenseCut {
+    int target, unit, least;                 // wanted runs; chunk is a multiple of unit, at least `least`
+};
+struct DenseRun { int s, first, end, slot; };   // s < 0: none
+
+// blocks of sequence s: finished ones, or the entries of its list
+__device__ __forceinline__ int blocks_of(const int32_t *len, int s, int S, int T, int listed, int32_t *status)
+{
+    if (s >= S) return 0;
+    return listed ? listed : dense_len(len, s, T, status) / kBlk;
+}
+__device__ __forceinline__ int dense_chunk(const int32_t *len, int S, int T, int listed, const DenseCut &c,
+                                           int32_t *status)
+{
+    const int lane = threadIdx.x & 31;
+    long long all = 0;
+    int most = 0;
+    for (int s0 = 0; s0 < S; s0 += 32) {
+        const int n = blocks_of(len, s0 + lane, S, T, listed, status);
+        all += __reduce_add_sync(0xffffffffu, n);
+        most = max(most, __reduce_max_sync(0xffffffffu, n));
+    }
+    if (S >= c.target) return max(most, 1);
+    int chunk = max(c.least, (int)((all + c.target - 1) / c.target));
+    while (true) {
+        chunk = (chunk + c.unit - 1) / c.unit * c.unit;
+        if (chunk >= most) return chunk;                   // a run for every sequence: S < target
+        int runs = 0;
+        for (int s0 = 0; s0 < S; s0 += 32)
+            runs += __reduce_add_sync(0xffffffffu, (blocks_of(len, s0 + lane, S, T, listed, status) + chunk - 1) / chunk);
+        if (runs <= c.target) return chunk;
+        chunk += max(1, chunk >> 4);
+    }
+}
+// Inclusive sum over the lanes.
+__device__ __forceinline__ int lane_scan(int v)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    return v;
+}
+// Run number p.
+__device__ __forceinline__ DenseRun dense_run(const int32_t *len, int S, int T, int listed, const DenseCut &c, int p,
+                                              int32_t *status)
+{
+    const int chunk = dense_chunk(len, S, T, listed, c, status), lane = threadIdx.x & 31;
+    int base = 0;
+    for (int s0 = 0; s0 < S; s0 += 32) {
+        const int n = blocks_of(len, s0 + lane, S, T, listed, status), runs = (n + chunk - 1) / chunk;
+        const int upto = base + lane_scan(runs);
+        const uint32_t hit = __ballot_sync(0xffffffffu, p < upto);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            const int k = p - __shfl_sync(0xffffffffu, upto - runs, l);
+            return DenseRun{s0 + l, k * chunk, min(__shfl_sync(0xffffffffu, n, l), (k + 1) * chunk), p};
+        }
+        base = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return DenseRun{-1, 0, 0, 0};
+}
+// The runs of sequence s: first number in .first, one past the last in .end.
+__device__ __forceinline__ DenseRun dense_runs_of(const int32_t *len, int S, int T, int listed, const DenseCut &c, int s,
+                                                  int32_t *status)
+{
+    const int chunk = dense_chunk(len, S, T, listed, c, status), lane = threadIdx.x & 31;
+    int base = 0;
+    for (int s0 = 0; s0 <= s; s0 += 32) {
+        const int runs = (blocks_of(len, s0 + lane, S, T, listed, status) + chunk - 1) / chunk;
+        const int upto = base + lane_scan(runs);
+        if (s < s0 + 32)
+            return DenseRun{s, __shfl_sync(0xffffffffu, upto - runs, s - s0), __shfl_sync(0xffffffffu, upto, s - s0), 0};
+        base = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return DenseRun{s, 0, 0, 0};
+}
 
 // The two codes at pair j of a word as bf16: 128 + code is exact in 8 significant bits.
 template <int BITS>
@@ -110,17 +194,17 @@ cudaError_t launch_block_select(const DenseGeom &g, int H, const void *q, const 
                                 const int32_t *len, int lists, int n_blocks, int keep_first, int keep_last,
                                 int32_t *blocks, void *ws, int32_t *status, cudaStream_t s);
 
-size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq, int max_blocks);
+size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq);
 // blocks may be NULL (all finished blocks); parent and draft are NULL for one token (nq = 1)
 cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int nq, const int32_t *parent,
                                    const void *draft, const rkv_dense_cache *cache, const int32_t *len,
                                    const int32_t *blocks, int lists, int n_blocks, void *out, int out_dtype,
                                    void *ws, int32_t *status, cudaStream_t s);
 
-// The finished blocks against many query rows (rkv_dense_tree.cu), D <= 128: two partials
-// for each of `splits` runs of `chunk` blocks.
+// The finished blocks against many query rows (rkv_dense_tree.cu), D <= 128: two partials for
+// each run and KV head.
 cudaError_t launch_dense_tree(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *cache,
-                              const int32_t *len, int splits, int chunk, float scale_log2, bool p_lo, float *part,
+                              const int32_t *len, const DenseCut &cut, float scale_log2, bool p_lo, float *part,
                               float2 *ml, int32_t *status, cudaStream_t s);
 
 }  // namespace rkv

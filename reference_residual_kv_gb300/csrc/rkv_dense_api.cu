@@ -57,7 +57,7 @@ rkv_status check_attention_shape(const rkv_dense_params *p, int32_t H, int32_t n
     if (st != RKV_OK) return st;
     if (nq < 1 || nq > kMaxDraft || (listed && n_blocks < 1)) return RKV_ERR_INVALID_ARG;
     if ((long long)p->S * nq * H > (long long)INT_MAX ||
-        (listed && (long long)p->S * p->N * n_blocks > (long long)INT_MAX))
+        (listed && (long long)p->S * p->N * n_blocks > (1LL << 30)))
         return RKV_ERR_UNSUPPORTED;
     return RKV_OK;
 }
@@ -145,14 +145,13 @@ rkv_status rkv_block_select(const rkv_dense_params *p, int32_t H, const void *q,
                                     dev_status, (cudaStream_t)stream));
 }
 
-rkv_status rkv_dense_attention_workspace(const rkv_dense_params *p, int32_t H, int32_t n_query, int32_t n_blocks,
-                                         int32_t listed, size_t *bytes)
+rkv_status rkv_dense_attention_workspace(const rkv_dense_params *p, int32_t H, int32_t n_query, size_t *bytes)
 {
-    rkv_status st = check_attention_shape(p, H, n_query, n_blocks, listed);
+    rkv_status st = check_attention_shape(p, H, n_query, 0, 0);
     if (st != RKV_OK) return st;
     if (!bytes) return RKV_ERR_INVALID_ARG;
     const DenseGeom g = geom(p);
-    *bytes = dense_attention_workspace_bytes(g, H, n_query, listed ? n_blocks : g.nb);
+    *bytes = dense_attention_workspace_bytes(g, H, n_query);
     return RKV_OK;
 }
 
@@ -169,7 +168,7 @@ rkv_status rkv_dense_attention(const rkv_dense_params *p, int32_t H, const void 
     if ((st = check_dense_cache(cache, g)) != RKV_OK) return st;
     if (!q || !len || !out || !dev_status) return RKV_ERR_INVALID_ARG;
     if (!aligned16(q, len, blocks, out, dev_status)) return RKV_ERR_ALIGNMENT;
-    const size_t need = dense_attention_workspace_bytes(g, H, 1, blocks ? n_blocks : g.nb);
+    const size_t need = dense_attention_workspace_bytes(g, H, 1);
     if ((st = check_workspace(workspace, workspace_bytes, need)) != RKV_OK) return st;
     return done(launch_dense_attention(g, H, q, 1, nullptr, nullptr, cache, len, blocks, lists, n_blocks, out,
                                        out_dtype, workspace, dev_status, (cudaStream_t)stream));
@@ -187,7 +186,7 @@ rkv_status rkv_tree_attention(const rkv_dense_params *p, int32_t H, const void *
     if ((st = check_dense_cache(cache, g)) != RKV_OK) return st;
     if (!q || !parent || !draft_kv || !len || !out || !dev_status) return RKV_ERR_INVALID_ARG;
     if (!aligned16(q, parent, draft_kv, len, out, dev_status)) return RKV_ERR_ALIGNMENT;
-    const size_t need = dense_attention_workspace_bytes(g, H, n_draft, g.nb);
+    const size_t need = dense_attention_workspace_bytes(g, H, n_draft);
     if ((st = check_workspace(workspace, workspace_bytes, need)) != RKV_OK) return st;
     return done(launch_dense_attention(g, H, q, n_draft, parent, draft_kv, cache, len, nullptr, 1, 0, out, out_dtype,
                                        workspace, dev_status, (cudaStream_t)stream));

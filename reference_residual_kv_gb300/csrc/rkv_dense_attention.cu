@@ -13,10 +13,9 @@
 //                   query rows its columns.  Probabilities go from one product to the
 //                   other by movmatrix, as bf16 hi + lo.  Softmax: running maximum and sum
 //                   for each warp, in base 2.  No masks: a finished block is whole.
-//   k_dense_finish  one warp per query row: the bf16 rows of the unfinished block and the
-//                   drafted tokens that the row sees (fp32 on CUDA cores; a token that it
-//                   does not see is not touched), while the first kernel still runs, then
-//                   the merge of the splits.
+//   k_dense_finish  the bf16 rows of the unfinished block and the drafted tokens that a row
+//                   sees (the values of a token that it does not see are not touched), while
+//                   the first kernel still runs, then the merge of the runs' partials.
 #include "rkv_dense.cuh"
 #include "umma.cuh"
 
@@ -40,6 +39,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  "{%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ uint32_t trans8x8(uint32_t a)
 {
@@ -78,12 +82,12 @@ __device__ __forceinline__ int block_at(const int32_t *list, int i, int have, in
     return -1;
 }
 
-// Partials: sums [S N][splits][R][D] and {max, sum} [S N][splits][R] (max in base 2).
+// Partials: sums [run][N][R][D] and {max, sum} [run][N][R] (max in base 2).
 template <int D, int BITS, int NT>
 __global__ void __launch_bounds__(32 * kWarps, NT == 1 && D <= 128 ? 2 : 1)
 k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ codes,
               const uint8_t *__restrict__ khdr, const int32_t *__restrict__ len, const int32_t *__restrict__ blocks,
-              int lists, int n_blocks, int T, int N, int G, int nq, int nb, int splits, int chunk, int tiles,
+              int lists, int n_blocks, int S, int T, int N, int G, int nq, int nb, DenseCut cut, int tiles,
               float scale_log2, float *__restrict__ part, float2 *__restrict__ ml, int32_t *status)
 {
     using C = SplitCfg<D, BITS, NT>;
@@ -91,24 +95,17 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 sml[kWarps][8 * NT];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    int id = blockIdx.x;
-    const int split = id % splits;
-    id /= splits;
-    const int tile = id % tiles, sn = id / tiles, s = sn / N, n = sn % N;
+    // the row tiles of a run are neighbours, then its KV heads: they read the same blocks
+    const int tile = blockIdx.x % tiles, n = blockIdx.x / tiles % N;
+    const DenseRun run = dense_run(len, S, T, blocks ? n_blocks : 0, cut, blockIdx.x / tiles / N, status);
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (run.s < 0) return;
+    const int s = run.s, sn = s * N + n, i0 = run.first, i1 = run.end;
     const int R = nq * G, row0 = tile * 8 * NT;
     uint8_t *ring = smem + warp * C::kStages * C::kStage;
     uint64_t *bars = (uint64_t *)(smem + C::kBody + C::kQ) + warp * C::kStages;
-
-    const int have = dense_len(len, s, T, status) / kBlk;
+    const int have = blocks ? dense_len(len, s, T, status) / kBlk : 0;
     const int32_t *list = blocks ? blocks + ((size_t)s * lists + (lists > 1 ? n : 0)) * n_blocks : nullptr;
-    const int total = list ? n_blocks : have;
-    const int i0 = split * chunk, i1 = min(total, i0 + chunk);
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (i0 >= i1) {
-        for (int r = threadIdx.x; r < 8 * NT && row0 + r < R; r += blockDim.x)
-            ml[((size_t)sn * splits + split) * R + row0 + r] = make_float2(-INFINITY, 0.0f);
-        return;
-    }
     if (lane == 0) {
         for (int i = 0; i < C::kStages; ++i) um::mbar_init(bars + i, 1);
         um::fence_mbar_init();
@@ -334,44 +331,46 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
             o.w = fmaf(v.w, f, o.w);
             l = fmaf(sml[w][r].y, f, l);
         }
-        const size_t at = ((size_t)sn * splits + split) * R + row0 + r;
+        const size_t at = ((size_t)run.slot * N + n) * R + row0 + r;
         *(float4 *)(part + at * D + d) = o;
         if (d == 0) ml[at] = make_float2(bad ? __uint_as_float(0x7fffffffu) : m, l);
     }
 }
 
-// One warp per query row.  Tokens that are not in finished blocks come in groups of 32
-// through shared memory: the unfinished block's rows, then drafted tokens 0..31, 32..63.
+// The last pass: 8 / wpr query rows of a KV head per CTA, wpr warps for each.  Tokens that are
+// not in finished blocks come in groups of 32 through shared memory: the unfinished block's
+// rows, then drafted tokens 0..31, 32..63.  A group's scores for all rows are one product
+// (two warps, 16 tokens each); every row then takes its own, and adds p v for the tokens that
+// it sees alone.  The warps of a row deal tokens and partials among them.
 template <int D>
 __global__ void __launch_bounds__(32 * kFinWarps)
 k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ tail,
                const int32_t *__restrict__ len, const int32_t *__restrict__ parent,
-               const __nv_bfloat16 *__restrict__ draft, int T, int N, int G, int nq, int splits, int row_ctas,
-               float scale_log2, const float *__restrict__ part, const float2 *__restrict__ ml,
-               void *__restrict__ out, int out_bf16, int32_t *status)
+               const __nv_bfloat16 *__restrict__ draft, int S, int T, int N, int G, int nq, DenseCut cut, int listed,
+               int each, int wpr, int row_ctas, float scale_log2, const float *__restrict__ part,
+               const float2 *__restrict__ ml, void *__restrict__ out, int out_bf16, int32_t *status)
 {
     constexpr int kCh = D / 8, kPad = kCh + 1, kE = D / 32;   // 16-byte chunks of a row; channels of a lane
     extern __shared__ __align__(128) uint8_t smem[];
     uint4 *ks = (uint4 *)smem, *vs = ks + kBlk * kPad;
-    __shared__ __align__(16) float qf[kFinWarps][D];
+    __shared__ float sc[8][kBlk + 1];
+    __shared__ __align__(16) float part_s[kFinWarps][D + 4];
+    __shared__ float2 ml_s[kFinWarps];
     __shared__ int par[kMaxDraft];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sn = blockIdx.x / row_ctas, s = sn / N, n = sn % N;
-    const int R = nq * G, r = (blockIdx.x % row_ctas) * kFinWarps + warp;
+    const int R = nq * G, rpc = kFinWarps / wpr, r0 = (blockIdx.x % row_ctas) * rpc;
+    const int slot = warp / wpr, turn = warp % wpr, r = r0 + slot;
     const int length = dense_len(len, s, T, status);
     const int rest = length % kBlk;
     const bool live = r < R;
     const int j = live ? r / G : 0;
-    const size_t row = (((size_t)s * nq + j) * N + n) * G + (live ? r % G : 0);
-    if (parent)
+    auto row_of = [&](int x) { return (((size_t)s * nq + x / G) * N + n) * G + x % G; };
+    const int groups = parent ? 1 + (nq + kBlk - 1) / kBlk : 1;
+    if (parent) {
         for (int i = threadIdx.x; i < nq; i += blockDim.x) par[i] = __ldg(parent + (size_t)s * nq + i);
-    if (live)
-        for (int i = lane; i < D / 2; i += 32) {
-            const uint32_t v = __ldg((const uint32_t *)(q + row * D) + i);
-            qf[warp][2 * i] = __uint_as_float(v << 16);
-            qf[warp][2 * i + 1] = __uint_as_float(v & 0xffff0000u);
-        }
-    __syncthreads();
+        __syncthreads();
+    }
     // the drafted tokens that the row sees; parents come before their children, so that the
     // way up ends
     uint64_t sees = 0;
@@ -392,11 +391,23 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
             if (lane == 0) set_status(status, RKV_ERR_INDEX);
         }
     }
+    // warps 0 and 1: the rows as the second operand (columns behind the last row are zero)
+    uint32_t qr[D / 16][2];
+    if (warp < 2 && (rest || parent)) {
+        const int g = lane >> 2, c = lane & 3;
+        const bool there = g < rpc && r0 + g < R;
+        const uint32_t *src = (const uint32_t *)(q + row_of(there ? r0 + g : 0) * D);
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u) {
+            qr[u][0] = there ? __ldg(src + u * 8 + c) : 0u;
+            qr[u][1] = there ? __ldg(src + u * 8 + 4 + c) : 0u;
+        }
+    }
 
     float m = -INFINITY, l = 0.0f, acc[kE];
 #pragma unroll
     for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
-    const int groups = parent ? 1 + (nq + kBlk - 1) / kBlk : 1;
+#pragma unroll 1
     for (int grp = 0; grp < groups; ++grp) {
         const int cnt = grp == 0 ? rest : min(kBlk, nq - (grp - 1) * kBlk);
         if (cnt == 0) continue;
@@ -415,29 +426,33 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
             vs[t * kPad + ch] = vr[ch];
         }
         __syncthreads();
+        if (warp < 2) {
+            // tokens 16 warp ..: rows of the first operand (those behind cnt give scores that
+            // no row takes)
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const uint32_t at = um::smem_u32(ks + (16 * warp + 8 * ((lane >> 3) & 1) + (lane & 7)) * kPad + (lane >> 4));
+#pragma unroll
+            for (int u = 0; u < D / 16; ++u) {
+                uint32_t a[4];
+                ldmatrix4(a, at + u * 32);
+                mma16816(d, a, qr[u][0], qr[u][1]);
+            }
+            const int g = lane >> 2, c = lane & 3;
+            sc[2 * c][16 * warp + g] = d[0];
+            sc[2 * c + 1][16 * warp + g] = d[1];
+            sc[2 * c][16 * warp + g + 8] = d[2];
+            sc[2 * c + 1][16 * warp + g + 8] = d[3];
+        }
+        __syncthreads();
         uint32_t mask = 0u;
         if (!padding)
             mask = grp == 0 ? (1u << rest) - 1u : (uint32_t)(sees >> ((grp - 1) * kBlk));
+        // this warp's tokens of the row: bits turn, turn + wpr, ...
+        if (wpr == 2) mask &= 0x55555555u << turn;
+        else if (wpr == 4) mask &= 0x11111111u << turn;
+        else if (wpr == 8) mask &= 0x01010101u << turn;
         if (mask == 0u) continue;                          // the same for the whole warp
-        // lane t scores token t of the group
-        float x = -INFINITY;
-        if ((mask >> lane) & 1u) {
-            float d0 = 0.0f, d1 = 0.0f;
-#pragma unroll 4
-            for (int ch = 0; ch < kCh; ++ch) {
-                const uint4 kv = ks[lane * kPad + ch];
-                const float4 a = *(const float4 *)&qf[warp][8 * ch], b = *(const float4 *)&qf[warp][8 * ch + 4];
-                d0 = fmaf(a.x, __uint_as_float(kv.x << 16), d0);
-                d1 = fmaf(a.y, __uint_as_float(kv.x & 0xffff0000u), d1);
-                d0 = fmaf(a.z, __uint_as_float(kv.y << 16), d0);
-                d1 = fmaf(a.w, __uint_as_float(kv.y & 0xffff0000u), d1);
-                d0 = fmaf(b.x, __uint_as_float(kv.z << 16), d0);
-                d1 = fmaf(b.y, __uint_as_float(kv.z & 0xffff0000u), d1);
-                d0 = fmaf(b.z, __uint_as_float(kv.w << 16), d0);
-                d1 = fmaf(b.w, __uint_as_float(kv.w & 0xffff0000u), d1);
-            }
-            x = (d0 + d1) * scale_log2;
-        }
+        const float x = ((mask >> lane) & 1u) ? sc[slot][lane] * scale_log2 : -INFINITY;
         float mx = x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -445,14 +460,16 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
         const float mu = mx == -INFINITY ? 0.0f : mx;
         const float al = ex2(m - mu), p = ex2(x - mu);
         m = mx;
-        l *= al;
+        float ps = p;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
+        l = fmaf(l, al, ps);
 #pragma unroll
         for (int e = 0; e < kE; ++e) acc[e] *= al;
         while (mask) {
             const int t = __ffs(mask) - 1;
             mask &= mask - 1u;
             const float pt = __shfl_sync(0xffffffffu, p, t);
-            l += pt;
             const uint32_t *v = (const uint32_t *)(vs + t * kPad) + lane * (kE / 2);
 #pragma unroll
             for (int e = 0; e < kE / 2; ++e) {
@@ -461,84 +478,126 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
             }
         }
     }
+    const DenseRun runs = dense_runs_of(len, S, T, listed, cut, s, status);
 
-    // the splits' partials: launched as a programmatic dependent, this waits for them
+    // the finished blocks' partials: launched as a programmatic dependent, this waits for them
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!live) return;
+    bool bad = false;
     if (!padding) {
-        const float2 *mlr = ml + (size_t)sn * splits * R + r;
-        float mx = m;
-        bool bad = false;
-        for (int i = lane; i < splits; i += 32) {
-            const float v = mlr[(size_t)i * R].x;
-            bad |= v != v;
-            mx = fmaxf(mx, v);
-        }
+        // `each` partials for every run and KV head, this warp's every wpr-th; 32 at a time:
+        // their weights, a lane each, then their sums, those with nothing in them left out
+        const int parts = (runs.end - runs.first) * each;
+        auto part_at = [&](int i) {
+            return ((size_t)(runs.first + i / each) * N * each + (size_t)n * each + i % each) * R + r;
+        };
+        for (int i0 = turn; i0 < parts; i0 += 32 * wpr) {
+            const int mine = i0 + lane * wpr;
+            const float2 v = mine < parts ? ml[part_at(mine)] : make_float2(-INFINITY, 0.0f);
+            bad |= v.x != v.x;
+            float mx = v.x;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float mu = mx == -INFINITY ? 0.0f : mx;
-        const float al = ex2(m - mu);
-        l *= al;
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            mx = fmaxf(mx, m);
+            const float mu = mx == -INFINITY ? 0.0f : mx;
+            const float al = ex2(m - mu), f = ex2(v.x - mu);
+            m = mx;
+            float ls = v.y * f;
 #pragma unroll
-        for (int e = 0; e < kE; ++e) acc[e] *= al;
-        const float *pr = part + ((size_t)sn * splits * R + r) * D + lane * kE;
-#pragma unroll 4
-        for (int i = 0; i < splits; ++i) {
-            const float2 v = mlr[(size_t)i * R];
-            if (v.x == -INFINITY) continue;                // nothing in this split
-            const float f = ex2(v.x - mu);
-            l = fmaf(v.y, f, l);
+            for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+            l = fmaf(l, al, ls);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) acc[e] = fmaf(pr[(size_t)i * R * D + e], f, acc[e]);
+            for (int e = 0; e < kE; ++e) acc[e] *= al;
+            uint32_t todo = __ballot_sync(0xffffffffu, v.x > -INFINITY);
+            constexpr int kU = kE <= 4 ? 8 : 4;            // sums in flight
+            while (todo) {
+                float x[kU][kE], w[kU];
+#pragma unroll
+                for (int k = 0; k < kU; ++k) {
+                    const int i = todo ? __ffs(todo) - 1 : 0;
+                    w[k] = __shfl_sync(0xffffffffu, f, i);
+                    if (!todo) w[k] = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) x[k][e] = 0.0f;
+                    if (todo) {
+                        const float *pr = part + part_at(i0 + i * wpr) * D + lane * kE;
+#pragma unroll
+                        for (int e = 0; e < kE; ++e) x[k][e] = pr[e];
+                    }
+                    todo &= todo - 1u;
+                }
+#pragma unroll
+                for (int k = 0; k < kU; ++k)
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) acc[e] = fmaf(x[k][e], w[k], acc[e]);
+            }
         }
         if (__any_sync(0xffffffffu, bad)) l = __uint_as_float(0x7fffffffu);
     }
+    if (wpr > 1) {
+        // the warps of a row, in order
+#pragma unroll
+        for (int e = 0; e < kE; ++e) part_s[warp][lane * kE + e] = acc[e];
+        if (lane == 0) ml_s[warp] = make_float2(m, l);
+        __syncthreads();
+        if (turn) return;
+        for (int k = 1; k < wpr; ++k) {
+            const float2 o = ml_s[warp + k];
+            const float mx = fmaxf(m, o.x), mu = mx == -INFINITY ? 0.0f : mx;
+            const float al = ex2(m - mu), f = ex2(o.x - mu);
+            m = mx;
+            l = l * al + o.y * f;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) acc[e] = fmaf(part_s[warp + k][lane * kE + e], f, acc[e] * al);
+        }
+    }
+    if (!live) return;
     // l is 0 only where the row sees nothing (the largest p is 1); NaN stays NaN
     const bool none = padding || l == 0.0f;
     const float inv = none ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int e = 0; e < kE; ++e) acc[e] = none ? 0.0f : acc[e] * inv;
     if (out_bf16) {
-        uint32_t *o = (uint32_t *)((__nv_bfloat16 *)out + row * D) + lane * (kE / 2);
+        uint32_t *o = (uint32_t *)((__nv_bfloat16 *)out + row_of(r) * D) + lane * (kE / 2);
 #pragma unroll
         for (int e = 0; e < kE / 2; ++e) o[e] = as_u32(__floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]));
     } else {
-        float *o = (float *)out + row * D + lane * kE;
+        float *o = (float *)out + row_of(r) * D + lane * kE;
 #pragma unroll
         for (int e = 0; e < kE; ++e) o[e] = acc[e];
     }
 }
 
-// How the finished blocks of a (sequence, KV head) are cut: `chunk` blocks for a CTA.  Fixed
-// sizes, so that long sequences take more CTAs than short ones.  Does not depend on the
-// device, so that the workspace's size and the order of the sums do not either.
-// `parts`: partials of a row.
-struct Plan { int tiles, nt, chunk, splits, parts; bool tree; };
+// Which kernel takes the finished blocks, and how they are cut.  Does not depend on the device,
+// so that the workspace's size and the order of the sums do not either.
+struct Plan {
+    bool tree;
+    int tiles, nt, each, runs;               // row tiles of a CTA's size; partials of a run; most runs
+    DenseCut cut;
+};
 
-Plan plan_of(const DenseGeom &g, int H, int nq, int max_blocks)
+Plan plan_of(const DenseGeom &g, int H, int nq)
 {
     Plan p;
     const int R = nq * (H / g.N);
     p.tree = R > 32 && g.D <= 128;
+    int ctas;
     if (p.tree) {
-        constexpr int kTarget = 304;                       // CTAs, one to an SM
-        const long long heads = (long long)g.S * g.N * ((R + 255) / 256);
-        long long chunk = (heads * max_blocks + kTarget - 1) / kTarget;
-        chunk = (chunk + 15) / 16 * 16;
-        p.nt = p.tiles = 0;
-        p.chunk = (int)(chunk < 32 ? 32 : chunk);
-        p.splits = max(1, (max_blocks + p.chunk - 1) / p.chunk);
-        p.parts = 2 * p.splits;
-        return p;
+        p.nt = 0;
+        p.each = 2;
+        p.tiles = (R + 255) / 256;
+        ctas = 152;                                        // one to an SM
+        p.cut.unit = 8;
+        p.cut.least = 16;
+    } else {
+        p.nt = R <= 8 ? 1 : (R <= 16 || g.D == 256 ? 2 : 4);
+        p.each = 1;
+        p.tiles = (R + 8 * p.nt - 1) / (8 * p.nt);
+        ctas = 608;
+        p.cut.unit = kWarps;
+        p.cut.least = kWarps;
     }
-    p.nt = R <= 8 ? 1 : (R <= 16 || g.D == 256 ? 2 : 4);
-    p.tiles = (R + 8 * p.nt - 1) / (8 * p.nt);
-    constexpr int kTarget = 1024;                          // CTAs
-    const long long work = (long long)g.S * g.N * p.tiles * max_blocks;
-    long long chunk = (work + kTarget - 1) / kTarget;
-    chunk = (chunk + kWarps - 1) / kWarps * kWarps;
-    p.chunk = (int)(chunk < kWarps ? kWarps : chunk);
-    p.parts = p.splits = max(1, (max_blocks + p.chunk - 1) / p.chunk);
+    p.cut.target = max(1, ctas / (g.N * p.tiles));
+    p.runs = max(p.cut.target, g.S);
     return p;
 }
 
@@ -555,20 +614,22 @@ cudaError_t run_split(const DenseGeom &g, const Plan &p, int H, const void *q, i
     });
     if (e != cudaSuccess) return e;
     ProfScope prof("dense_attention_split", s);
-    k_dense_split<D, BITS, NT><<<(unsigned)((size_t)g.S * g.N * p.tiles * p.splits), 32 * kWarps, C::kSmem, s>>>(
+    k_dense_split<D, BITS, NT><<<(unsigned)((size_t)p.runs * g.N * p.tiles), 32 * kWarps, C::kSmem, s>>>(
         (const __nv_bfloat16 *)q, (const uint8_t *)c->codes, (const uint8_t *)c->khdr, len, blocks, lists, n_blocks,
-        g.T, g.N, H / g.N, nq, g.nb, p.splits, p.chunk, p.tiles, scale_log2, part, ml, status);
+        g.S, g.T, g.N, H / g.N, nq, g.nb, p.cut, p.tiles, scale_log2, part, ml, status);
     return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t run_finish(const DenseGeom &g, const Plan &p, int H, const void *q, int nq, const int32_t *parent,
+cudaError_t run_finish(const DenseGeom &g, const Plan &p, int H, const void *q, int nq, int listed, const int32_t *parent,
                        const void *draft, const rkv_dense_cache *c, const int32_t *len, float scale_log2,
                        const float *part, const float2 *ml, void *out, int out_dtype, int32_t *status, cudaStream_t s)
 {
-    const int R = nq * (H / g.N), row_ctas = (R + kFinWarps - 1) / kFinWarps;
+    const int R = nq * (H / g.N);
+    const int wpr = R <= 1 ? 8 : (R <= 2 ? 4 : (R <= 4 ? 2 : 1)), rpc = kFinWarps / wpr;
+    const int row_ctas = (R + rpc - 1) / rpc;
     constexpr int kSmem = 2 * kBlk * (D / 8 + 1) * 16;
-    static_assert(kSmem + kFinWarps * D * 4 + kMaxDraft * 4 <= 48 * 1024, "shared memory of the last pass");
+    static_assert(kSmem + kFinWarps * (D + 4) * 4 + 2048 <= 48 * 1024, "shared memory of the last pass");
     ProfScope prof("dense_attention_finish", s);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
@@ -581,8 +642,8 @@ cudaError_t run_finish(const DenseGeom &g, const Plan &p, int H, const void *q, 
     cfg.attrs = at;
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, k_dense_finish<D>, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)c->tail,
-                                       len, parent, (const __nv_bfloat16 *)draft, g.T, g.N, H / g.N, nq, p.parts,
-                                       row_ctas, scale_log2, part, ml, out, (int)(out_dtype == RKV_BF16), status);
+                                       len, parent, (const __nv_bfloat16 *)draft, g.S, g.T, g.N, H / g.N, nq, p.cut, listed,
+                                       p.each, wpr, row_ctas, scale_log2, part, ml, out, (int)(out_dtype == RKV_BF16), status);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -590,10 +651,10 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
-size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq, int max_blocks)
+size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq)
 {
-    const Plan p = plan_of(g, H, nq, max_blocks);
-    const size_t rows = (size_t)g.S * g.N * p.parts * nq * (H / g.N);
+    const Plan p = plan_of(g, H, nq);
+    const size_t rows = (size_t)p.runs * p.each * nq * H;
     return align256(rows * g.D * sizeof(float)) + align256(rows * sizeof(float2));
 }
 
@@ -602,8 +663,8 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
                                    const int32_t *blocks, int lists, int n_blocks, void *out, int out_dtype,
                                    void *ws, int32_t *status, cudaStream_t s)
 {
-    const Plan p = plan_of(g, H, nq, blocks ? n_blocks : g.nb);
-    const size_t rows = (size_t)g.S * g.N * p.parts * nq * (H / g.N);
+    const Plan p = plan_of(g, H, nq);
+    const size_t rows = (size_t)p.runs * p.each * nq * H;
     float *part = (float *)ws;
     float2 *ml = (float2 *)((uint8_t *)ws + align256(rows * g.D * sizeof(float)));
     const float scale_log2 = (float)(1.4426950408889634 / sqrt((double)g.D));
@@ -611,8 +672,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
         constexpr int B = decltype(bits)::value, D = decltype(d)::value;
         cudaError_t e;
         if (p.tree)
-            e = launch_dense_tree(g, H, q, nq, cache, len, p.splits, p.chunk, scale_log2, out_dtype == RKV_F32, part, ml,
-                                  status, s);
+            e = launch_dense_tree(g, H, q, nq, cache, len, p.cut, scale_log2, out_dtype == RKV_F32, part, ml, status, s);
         else if (p.nt == 1)
             e = run_split<D, B, 1>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
         else if (p.nt == 2)
@@ -622,7 +682,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
         else
             e = cudaErrorInvalidValue;
         if (e != cudaSuccess) return e;
-        return run_finish<D>(g, p, H, q, nq, parent, draft, cache, len, scale_log2, part, ml, out, out_dtype, status, s);
+        return run_finish<D>(g, p, H, q, nq, blocks ? n_blocks : 0, parent, draft, cache, len, scale_log2, part, ml, out, out_dtype, status, s);
     };
     return dense_dispatch(g, go);
 }

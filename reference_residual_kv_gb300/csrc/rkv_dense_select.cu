@@ -12,7 +12,7 @@
 //                   its bits (counts only: nothing depends on an order of atomics); with E
 //                   the largest error bound, blocks above t + 2 E are in and those below
 //                   t - 2 E are out.  If the ones between are more than there is room for,
-//                   they are scored again in fp64 and ranked by (score, lower index).
+//                   they are scored again in 70 bits and ranked by (score, lower index).
 // The fp32 sums of the tensor cores are taken to be within kErr A of the exact score: 512
 // terms at 2^-24 each would give 2^-15 A, even if every addition cut instead of rounding.
 #include "rkv_dense.cuh"
@@ -194,38 +194,97 @@ __device__ __forceinline__ int cta_scan(int v, int &total, int (&red)[kPickWarps
     return x - v + (warp ? red[warp - 1] : 0);
 }
 
-// The exact score of block b for the heads of `heads` KV heads from n0 on, by one warp.
+// A sum held in three floats that do not overlap (Knuth's two-sum from each into the next):
+// about 70 bits, on the fp32 units (fp64 has a sixty-fourth of their rate here).
+struct Sum72 {
+    float a = 0.0f, b = 0.0f, c = 0.0f;
+    static __device__ __forceinline__ float two_sum(float &s, float x)
+    {
+        const float t = __fadd_rn(s, x), v = __fsub_rn(t, s);
+        const float e = __fadd_rn(__fsub_rn(s, __fsub_rn(t, v)), __fsub_rn(x, v));
+        s = t;
+        return e;
+    }
+    __device__ __forceinline__ void add(float x) { c += two_sum(b, two_sum(a, x)); }
+    __device__ __forceinline__ void add(const Sum72 &o)
+    {
+        add(o.a);
+        c += two_sum(b, o.b);
+        c += o.c;
+    }
+};
+
+// The exact score of block b for the query heads of KV head n, as an ordered key, by one warp.
+// max(q lo, q hi) is q times hi or lo by the sign of q, a product that fp32 holds exactly
+// unless it is tiny; those, and sums that are not finite, go through fp64.
 template <int D>
-__device__ double exact_score(const __nv_bfloat16 *q, const uint8_t *khdr, int s, int n0, int heads, int N, int G,
-                              int nb, int b, float qmax, int lane)
+__device__ unsigned long long exact_score(const __nv_bfloat16 *q, const uint8_t *khdr, size_t sn, int G, int nb, int b,
+                                          float qmax, int lane)
 {
-    double best = 0.0;
-    bool first = true;
-    for (int n = n0; n < n0 + heads; ++n) {
-        const uint4 *h = (const uint4 *)(khdr + (((size_t)s * N + n) * nb + b) * (4 * D));
-        for (int j = 0; j < G; ++j) {
-            const uint32_t *qr = (const uint32_t *)(q + (((size_t)s * N + n) * G + j) * D);
-            double sum = 0.0;
-            for (int i = lane; i < D / 4; i += 32) {       // unit i / 4, c = i % 4
-                const uint4 x = __ldg(h + i);
-                const int at = (i >> 2) * 8 + (i & 3);
+    constexpr int kI = (D / 4 + 31) / 32;                  // unit i / 4, c = i % 4 of i = lane + 32 k
+    float lo[kI][4], hi[kI][4];
+    const uint4 *h = (const uint4 *)(khdr + (sn * nb + b) * (4 * D));
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t mn = k ? x.z : x.x, top = top_pair(mn, k ? x.w : x.y, qmax);
-                    const uint32_t qv = __ldg(qr + at + 4 * k);
-                    const float qe[2] = {__uint_as_float(qv << 16), __uint_as_float(qv & 0xffff0000u)};
-                    const float lo[2] = {__uint_as_float(mn << 16), __uint_as_float(mn & 0xffff0000u)};
-                    const float hi[2] = {__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u)};
+    for (int k = 0; k < kI; ++k) {
+        const int i = lane + 32 * k;
+        const uint4 x = i < D / 4 ? __ldg(h + i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        sum += (double)max_nan(qe[e], 0.0f) * hi[e] + (double)-max_nan(-qe[e], 0.0f) * lo[e];
-                }
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t mn = e ? x.z : x.x, top = top_pair(mn, e ? x.w : x.y, qmax);
+            lo[k][2 * e] = __uint_as_float(mn << 16);
+            lo[k][2 * e + 1] = __uint_as_float(mn & 0xffff0000u);
+            hi[k][2 * e] = __uint_as_float(top << 16);
+            hi[k][2 * e + 1] = __uint_as_float(top & 0xffff0000u);
+        }
+    }
+    unsigned long long best = 0ull;
+#pragma unroll 1
+    for (int j = 0; j < G; ++j) {
+        const uint32_t *qr = (const uint32_t *)(q + (sn * G + j) * D);
+        float qe[kI][4];
+#pragma unroll
+        for (int k = 0; k < kI; ++k) {
+            const int i = lane + 32 * k;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t qv = i < D / 4 ? __ldg(qr + (i >> 2) * 8 + (i & 3) + 4 * e) : 0u;
+                qe[k][2 * e] = __uint_as_float(qv << 16);
+                qe[k][2 * e + 1] = __uint_as_float(qv & 0xffff0000u);
+            }
+        }
+        Sum72 sum;
+        bool tiny = false;
+#pragma unroll
+        for (int k = 0; k < kI; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = qe[k][e] >= 0.0f ? hi[k][e] : lo[k][e], p = __fmul_rn(qe[k][e], x);
+                tiny |= qe[k][e] != 0.0f && x != 0.0f && fabsf(p) < 0x1p-100f;
+                sum.add(p);
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (first || sum != sum || sum > best) best = best != best ? best : sum;
-            first = false;
+        for (int o = 16; o > 0; o >>= 1) {
+            Sum72 other;
+            other.a = __shfl_xor_sync(0xffffffffu, sum.a, o);
+            other.b = __shfl_xor_sync(0xffffffffu, sum.b, o);
+            other.c = __shfl_xor_sync(0xffffffffu, sum.c, o);
+            sum.add(other);
         }
+        // lane 0's order of additions for all
+        double v = ((double)sum.c + (double)sum.b) + (double)sum.a;
+        v = __shfl_sync(0xffffffffu, v, 0);
+        if (__any_sync(0xffffffffu, tiny) || !(fabs(v) < 1e300)) {
+            v = 0.0;
+#pragma unroll
+            for (int k = 0; k < kI; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v += (double)max_nan(qe[k][e], 0.0f) * hi[k][e] + (double)-max_nan(-qe[k][e], 0.0f) * lo[k][e];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        }
+        const unsigned long long key = order64(v);
+        best = key > best ? key : best;
     }
     return best;
 }
@@ -243,6 +302,7 @@ k_block_pick(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kh
     __shared__ Sum3 red3[2][kPickWarps];
     __shared__ int red1[kPickWarps + 1];
     __shared__ float emax[kPickWarps];
+    __shared__ int cand_n;
     __shared__ int32_t cand_s[kSmallCand];
     __shared__ unsigned long long exact_s[kSmallCand];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -253,6 +313,7 @@ k_block_pick(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kh
     uint32_t *keys = nb <= kKeysSmem ? smem_u + words : keys_ws + (size_t)list * nb;
     int32_t *out = blocks + (size_t)list * want_all;
     int turn = 0;
+    if (tid == 0) cand_n = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int have = dense_len(len, s, T, status) / kBlk;
     if (have <= want_all) {
@@ -266,10 +327,15 @@ k_block_pick(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kh
     for (int b = tid; b < have; b += kPickThreads) {
         const float2 *p = scores + ((size_t)s * N + n0) * nb + b;
         float2 v = p[0];
-        for (int n = 1; n < heads; ++n) {
-            const float2 x = p[(size_t)n * nb];
-            v.x = max_nan(v.x, x.x);
-            v.y = fmaxf(v.y, x.y);
+        for (int n1 = 1; n1 < heads; n1 += 8) {            // eight loads in flight
+            float2 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = p[(size_t)min(n1 + k, heads - 1) * nb];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v.x = max_nan(v.x, x[k].x);
+                v.y = fmaxf(v.y, x[k].y);
+            }
         }
         e = fmaxf(e, v.y);
         keys[b] = b < keep_first || b >= have - keep_last ? 0u : order32(v.x);
@@ -315,29 +381,36 @@ k_block_pick(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kh
             for (int b = tid; b < have; b += kPickThreads)
                 if (kind(keys[b]) == 1) atomicOr(in + (b >> 5), 1u << (b & 31));
         } else {
-            // the candidates in the order of their index
+            // the candidates: few in any order (their indexes rank them), many in that of the index
             int32_t *cand = cands <= kSmallCand ? cand_s : cand_ws + (size_t)list * nb;
             unsigned long long *ex = cands <= kSmallCand ? exact_s : exact_ws + (size_t)list * nb;
-            int done = 0;
-            for (int b0 = 0; b0 < have; b0 += kPickThreads) {
-                const int b = b0 + tid;
-                const int mine = b < have && kind(keys[b]) == 1;
-                int total;
-                const int at = cta_scan(mine, total, red1);
-                if (mine) cand[done + at] = b;
-                done += total;
+            if (cands <= kSmallCand) {
+                for (int b = tid; b < have; b += kPickThreads)
+                    if (kind(keys[b]) == 1) cand[atomicAdd(&cand_n, 1)] = b;
+            } else {
+                int done = 0;
+                for (int b0 = 0; b0 < have; b0 += kPickThreads) {
+                    const int b = b0 + tid;
+                    const int mine = b < have && kind(keys[b]) == 1;
+                    int total;
+                    const int at = cta_scan(mine, total, red1);
+                    if (mine) cand[done + at] = b;
+                    done += total;
+                }
             }
+            for (int i = tid; i < cands; i += kPickThreads) ex[i] = 0ull;
             __syncthreads();
-            for (int i = warp; i < cands; i += kPickWarps) {
-                const double v = exact_score<D>(q, khdr, s, n0, heads, N, G, nb, cand[i], qmax, lane);
-                if (lane == 0) ex[i] = order64(v);
+            for (int i = warp; i < cands * heads; i += kPickWarps) {
+                const unsigned long long k = exact_score<D>(q, khdr, (size_t)s * N + n0 + i % heads, G, nb,
+                                                            cand[i / heads], qmax, lane);
+                if (lane == 0) atomicMax(ex + i / heads, k);   // a maximum: in any order
             }
             __syncthreads();
             if (cands <= kSmallCand) {
                 if (tid < cands) {
                     const unsigned long long k = ex[tid];
                     int better = 0;
-                    for (int i = 0; i < cands; ++i) better += ex[i] > k || (ex[i] == k && i < tid);
+                    for (int i = 0; i < cands; ++i) better += ex[i] > k || (ex[i] == k && cand[i] < cand[tid]);
                     if (better < need) atomicOr(in + (cand[tid] >> 5), 1u << (cand[tid] & 31));
                 }
             } else {

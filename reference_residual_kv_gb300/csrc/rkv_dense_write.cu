@@ -6,8 +6,12 @@
 //                  stores (transposed for the values), and a group's extremes are three
 //                  warp shuffles away.  Codes and headers leave in the order of
 //                  rkv_dense.cuh.  Rows of a block that stays unfinished go to the tail.
-//   k_dense_read   one warp per (selected token, KV head): codes and headers of the token
-//                  to 2 D values, through a row buffer in shared memory to 16-byte stores.
+//   k_dense_read   one warp per 32 entries of the selection and KV head.  Entries of one block
+//                  are taken together: the block's keys, then its values, become bf16 for all
+//                  32 tokens (one stmatrix for 256 of them) in the warp's row buffer, from
+//                  which the asked rows leave as 16-byte stores; records come by bulk copies,
+//                  two blocks ahead.  A block that fewer than kTogether of the 32 entries ask
+//                  for is read for each of its tokens alone.
 #include "rkv_dense.cuh"
 #include "umma.cuh"
 
@@ -15,7 +19,8 @@ namespace rkv {
 namespace {
 
 constexpr int kWriteWarps = 4;
-constexpr int kReadWarps = 8;
+constexpr int kReadWarps = 4;
+constexpr int kTogether = 4;
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src)
 {
@@ -36,6 +41,22 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     um::smem_u32(dst)), "l"(src), "r"(bytes), "r"(um::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]) : "memory");
+}
+__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, const uint32_t (&r)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+
 __device__ __forceinline__ float lo_f(uint32_t pair) { return __uint_as_float(pair << 16); }
 __device__ __forceinline__ float hi_f(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
 
@@ -46,16 +67,20 @@ __device__ __forceinline__ float diff_error(float a, float b, float s)
     return __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(-b, bb));
 }
 
-// bf16((hi - lo) / qmax) rounded once: the fp32 quotient decides unless it lies on a border
-// of bf16 (its low 16 bits are 0x8000).  There the border times qmax is exact in fp32 (9 + 4
-// bits), and the sign of (hi - lo) minus it, with the difference's own error, decides.
+// bf16((hi - lo) / qmax) rounded once: a product with 1 / qmax (within 3 2^-24 of the quotient)
+// decides, unless it lies within 8 units of a border of bf16 (low 16 bits 0x8000).  There the
+// border times qmax is exact in fp32 (9 + 4 bits), and the sign of (hi - lo) minus it, with
+// the difference's own error, decides.  Subnormal products go through the division: their
+// units are too coarse for the bound.
 __device__ __forceinline__ uint32_t group_step(float lo, float hi, float qmax)
 {
     const float d = __fsub_rn(hi, lo);
-    const float q = __fdiv_rn(d, qmax);
+    float q = __fmul_rn(d, __frcp_rn(qmax));
+    if (q < 0x1p-120f) q = __fdiv_rn(d, qmax);
     uint32_t u = __float_as_uint(q);
-    if ((u & 0xffffu) == 0x8000u) {
-        const float p = __fmul_rn(q, qmax);
+    if (((u + 8u) & 0xffffu) - 0x8000u <= 16u) {
+        u = (u & 0xffff0000u) | 0x8000u;
+        const float p = __fmul_rn(__uint_as_float(u), qmax);
         const float e = d != p ? d - p : diff_error(hi, lo, d);
         u += e > 0.0f ? 0x8000u : (e < 0.0f ? 0u : ((u >> 16) & 1u) << 15);
     } else {
@@ -87,63 +112,76 @@ __device__ __noinline__ uint32_t exact_code(float x, float lo, float st, int qma
     return min(j, (uint32_t)qmax);
 }
 
-// One unit of 32 rows x 16 columns: r[m][i] = register i of operand m (rkv_dense.cuh).
-// Returns the unit's words and its header for this lane's c.  x_at(m, i, e) reads the value
-// of register i's element e again (dynamic indexes stay out of the registers).
-template <int BITS, class F>
-__device__ __forceinline__ void quant_unit(const uint32_t (&r)[2][4], int lane, uint32_t (&w)[2], uint4 &hdr,
-                                           F x_at)
+__device__ __forceinline__ float rcp_fast(float x)
 {
-    constexpr int qmax = (1 << BITS) - 1;
-    // extremes of the four columns (2c, 2c+1 | 2c+8, 2c+9): over the two row halves of both
-    // operands, then over the 8 lanes of equal c; NaN comes through
-    uint32_t mn[2], mx[2];
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Extremes, steps and headers of two units at once: r[x][m][i] = register i of operand m of
+// unit x (rkv_dense.cuh).  A butterfly over the 8 lanes of equal c: the first step keeps one
+// of the units, the second one of the column halves, the third one of a pair's columns, so
+// that each lane ends with one of the 8 columns, works out its {min, step} (a bf16 pair), and
+// hands it to the others.  pk[x][v]: column v (2c, 2c + 1, 2c + 8, 2c + 9) of unit x.
+__device__ __forceinline__ void unit_headers(const uint32_t (&r)[2][2][4], int lane, float qmax, uint32_t (&pk)[2][4])
+{
+    uint32_t mn[2][2], mx[2][2];                           // [unit][half]
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const __nv_bfloat162 a0 = as_bf162(r[x][0][2 * h]), a1 = as_bf162(r[x][0][2 * h + 1]);
+            const __nv_bfloat162 b0 = as_bf162(r[x][1][2 * h]), b1 = as_bf162(r[x][1][2 * h + 1]);
+            mn[x][h] = as_u32(__hmin2_nan(__hmin2_nan(a0, a1), __hmin2_nan(b0, b1)));
+            mx[x][h] = as_u32(__hmax2_nan(__hmax2_nan(a0, a1), __hmax2_nan(b0, b1)));
+        }
+    const int g = lane >> 2, c = lane & 3;
+    auto low = [](uint32_t a, uint32_t b) { return as_u32(__hmin2_nan(as_bf162(a), as_bf162(b))); };
+    auto high = [](uint32_t a, uint32_t b) { return as_u32(__hmax2_nan(as_bf162(a), as_bf162(b))); };
+    uint32_t n1[2], x1[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        __nv_bfloat162 a = as_bf162(r[0][2 * h]), b = a;
-        const uint32_t rest[3] = {r[0][2 * h + 1], r[1][2 * h], r[1][2 * h + 1]};
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            a = __hmin2_nan(a, as_bf162(rest[k]));
-            b = __hmax2_nan(b, as_bf162(rest[k]));
-        }
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            a = __hmin2_nan(a, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(a), o)));
-            b = __hmax2_nan(b, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(b), o)));
-        }
-        mn[h] = as_u32(a);
-        mx[h] = as_u32(b);
+        const uint32_t sn = __shfl_xor_sync(0xffffffffu, (g & 1) ? mn[0][h] : mn[1][h], 4);
+        const uint32_t sx = __shfl_xor_sync(0xffffffffu, (g & 1) ? mx[0][h] : mx[1][h], 4);
+        n1[h] = low((g & 1) ? mn[1][h] : mn[0][h], sn);
+        x1[h] = high((g & 1) ? mx[1][h] : mx[0][h], sx);
     }
-    // lane g works out column g & 3 of its c (the 8 lanes of a c would all find the same)
-    const int g = lane >> 2, c = lane & 3;
-    const uint32_t pm = (g & 2) ? mn[1] : mn[0], px = (g & 2) ? mx[1] : mx[0];
-    const float lo = (g & 1) ? hi_f(pm) : lo_f(pm), hi = (g & 1) ? hi_f(px) : lo_f(px);
-    uint32_t packed = 0x7fff7fffu;                     // NaN, NaN
-    float inv = 0.0f;
-    if (fmaxf(fabsf(lo), fabsf(hi)) < 0x1p126f && lo == lo && hi == hi) {
-        const uint32_t st = group_step(lo, hi, (float)qmax);
-        const float sf = __uint_as_float(st << 16);
-        packed = (__float_as_uint(lo) >> 16) | (st << 16);
-        // NaN where the step has no finite reciprocal: those codes all take the exact path
-        inv = st == 0u ? 0.0f : (sf < 0x1p-100f ? __uint_as_float(0x7fffffffu) : __frcp_rn(sf));
-    }
-    uint32_t pk[4];
-    float iv[4];
+    uint32_t n2 = low((g & 2) ? n1[1] : n1[0], __shfl_xor_sync(0xffffffffu, (g & 2) ? n1[0] : n1[1], 8));
+    uint32_t x2 = high((g & 2) ? x1[1] : x1[0], __shfl_xor_sync(0xffffffffu, (g & 2) ? x1[0] : x1[1], 8));
+    n2 = low(n2, __shfl_xor_sync(0xffffffffu, n2, 16));
+    x2 = high(x2, __shfl_xor_sync(0xffffffffu, x2, 16));
+    const float lo = (g & 4) ? hi_f(n2) : lo_f(n2), hi = (g & 4) ? hi_f(x2) : lo_f(x2);
+    uint32_t packed = 0x7fff7fffu;                         // NaN, NaN
+    if (fmaxf(fabsf(lo), fabsf(hi)) < 0x1p126f && lo == lo && hi == hi)
+        packed = (__float_as_uint(lo) >> 16) | (group_step(lo, hi, qmax) << 16);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        pk[v] = __shfl_sync(0xffffffffu, packed, 4 * v + c);
-        iv[v] = __shfl_sync(0xffffffffu, inv, 4 * v + c);
-    }
-    hdr.x = (pk[0] & 0xffffu) | (pk[1] << 16);
-    hdr.y = (pk[0] >> 16) | (pk[1] & 0xffff0000u);
-    hdr.z = (pk[2] & 0xffffu) | (pk[3] << 16);
-    hdr.w = (pk[2] >> 16) | (pk[3] & 0xffff0000u);
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)                        // the lane of unit x, half v >> 1, element v & 1
+            pk[x][v] = __shfl_sync(0xffffffffu, packed, 4 * (x + (v & 2) + 4 * (v & 1)) + c);
+}
 
-    // codes: y = (x - lo) RN(1/step), rounded to an integer inside an FMA with 1.5 2^23, whose
-    // low mantissa bits are then the code; rest = y - round(y).  y is within 2^-18 of the
-    // quotient, so that |rest| <= 1/2 - 2^-16 proves the code; else exact_code decides.
-    const float2 mg = make_float2(12582912.0f, 12582912.0f);
+// Codes of one unit of 32 rows x 16 columns: r[m][i] = register i of operand m, pk as above.
+// x_at(m, i, e) reads the value of register i's element e again (dynamic indexes stay out of
+// the registers).
+template <int BITS, class F>
+__device__ __forceinline__ void unit_codes(const uint32_t (&r)[2][4], const uint32_t (&pk)[4], uint32_t (&w)[2], F x_at)
+{
+    constexpr int qmax = (1 << BITS) - 1;
+    // y = (x - lo) / step, rounded to an integer inside an FMA with 1.5 2^23, whose low mantissa
+    // bits are then the code; rest = y - round(y).  With the reciprocal good to 2^-23 y is within
+    // 2^-17.9 of the quotient (at most 15.1), so that |rest| <= 1/2 - 2^-16 proves the code; else
+    // exact_code decides.  A step of 0 (a constant group) takes 0 for its reciprocal: code 0.
+    // One without a finite reciprocal gives NaN, and NaN goes to exact_code.
+    float2 nlo[2], inv[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        nlo[h] = make_float2(-lo_f(pk[2 * h]), -lo_f(pk[2 * h + 1]));
+        const float s0 = hi_f(pk[2 * h]), s1 = hi_f(pk[2 * h + 1]);
+        inv[h] = make_float2(s0 == 0.0f ? 0.0f : rcp_fast(s0), s1 == 0.0f ? 0.0f : rcp_fast(s1));
+    }
+    const float2 mg = make_float2(12582912.0f, 12582912.0f), neg = make_float2(-1.0f, -1.0f);
     float worst = 0.0f;
     w[0] = w[1] = 0u;
 #pragma unroll
@@ -151,11 +189,9 @@ __device__ __forceinline__ void quant_unit(const uint32_t (&r)[2][4], int lane, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int h = i >> 1;
-            const float2 nlo = make_float2(-lo_f(hdr_min(hdr, h)), -hi_f(hdr_min(hdr, h)));
-            const float2 i2 = make_float2(iv[2 * h], iv[2 * h + 1]);
-            const float2 d = __fadd2_rn(make_float2(lo_f(r[m][i]), hi_f(r[m][i])), nlo);
-            const float2 t = __ffma2_rn(d, i2, mg);
-            const float2 rest = __ffma2_rn(d, i2, __fadd2_rn(mg, make_float2(-t.x, -t.y)));
+            const float2 d = __fadd2_rn(make_float2(lo_f(r[m][i]), hi_f(r[m][i])), nlo[h]);
+            const float2 t = __ffma2_rn(d, inv[h], mg);
+            const float2 rest = __ffma2_rn(d, inv[h], __ffma2_rn(t, neg, mg));
             worst = max3f_nan(worst, fabsf(rest.x), fabsf(rest.y));
             const int wi = BITS == 4 ? m : 0, j = BITS == 4 ? i : 4 * m + i;
             w[wi] = bfi32(__float_as_uint(t.x), w[wi], BITS * j, BITS);
@@ -170,11 +206,9 @@ __device__ __forceinline__ void quant_unit(const uint32_t (&r)[2][4], int lane, 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int h = i >> 1;
-                const float2 nlo = make_float2(-lo_f(hdr_min(hdr, h)), -hi_f(hdr_min(hdr, h)));
-                const float2 i2 = make_float2(iv[2 * h], iv[2 * h + 1]);
-                const float2 d = __fadd2_rn(make_float2(lo_f(r[m][i]), hi_f(r[m][i])), nlo);
-                const float2 t = __ffma2_rn(d, i2, mg);
-                const float2 rest = __ffma2_rn(d, i2, __fadd2_rn(mg, make_float2(-t.x, -t.y)));
+                const float2 d = __fadd2_rn(make_float2(lo_f(r[m][i]), hi_f(r[m][i])), nlo[h]);
+                const float2 t = __ffma2_rn(d, inv[h], mg);
+                const float2 rest = __ffma2_rn(d, inv[h], __ffma2_rn(t, neg, mg));
                 todo |= (fabsf(rest.x) <= kSure ? 0u : 1u) << (2 * (4 * m + i));
                 todo |= (fabsf(rest.y) <= kSure ? 0u : 1u) << (2 * (4 * m + i) + 1);
             }
@@ -266,30 +300,41 @@ k_dense_write(const TIN *__restrict__ kv, int n, int S, int N, int T, int nb, in
         for (int u0 = 0; u0 < kUnits; u0 += kPer) {
             uint32_t words[4];
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const int u = u0 + k;
-                uint32_t r[2][4];
+            for (int k = 0; k < kPer; k += 2) {
+                uint32_t r[2][2][4], pk[2][4];
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const int i = lane >> 3;
-                    if (is_v)
-                        ldmatrix4_trans(r[m], base + 16 * row_chunk<D>(16 * (u & 1) + 8 * (i >> 1) + (lane & 7),
-                                                                      4 * (u >> 1) + 2 * m + (i & 1)));
-                    else
-                        ldmatrix4(r[m], base + 16 * row_chunk<D>(16 * m + 8 * (i & 1) + (lane & 7), 2 * u + (i >> 1)));
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const int u = u0 + k + x, i = lane >> 3;
+                        if (is_v)
+                            ldmatrix4_trans(r[x][m], base + 16 * row_chunk<D>(16 * (u & 1) + 8 * (i >> 1) + (lane & 7),
+                                                                             4 * (u >> 1) + 2 * m + (i & 1)));
+                        else
+                            ldmatrix4(r[x][m], base + 16 * row_chunk<D>(16 * m + 8 * (i & 1) + (lane & 7), 2 * u + (i >> 1)));
+                    }
+                unit_headers(r, lane, (float)((1 << BITS) - 1), pk);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int u = u0 + k + x;
+                    uint32_t w[2];
+                    unit_codes<BITS>(r[x], pk[x], w, [&](int m, int i, int e) -> float {
+                        const int mr = 16 * m + 8 * (i & 1) + g, kc = 8 * (i >> 1) + 2 * c + e;
+                        const int token = is_v ? 16 * (u & 1) + kc : mr;
+                        const int ch = is_v ? 32 * (u >> 1) + mr : 16 * u + kc;
+                        const uint16_t v = *((const uint16_t *)(buf + row_chunk<D>(token, ch >> 3)) + (ch & 7));
+                        return __uint_as_float((uint32_t)v << 16);
+                    });
+                    if (BITS == 4) { words[2 * (k + x)] = w[0]; words[2 * (k + x) + 1] = w[1]; }
+                    else words[k + x] = w[0];
+                    // lane 4 x + c of the unit's header
+                    if (g == x) {
+                        const uint32_t p0 = pk[x][0], p1 = pk[x][1], p2 = pk[x][2], p3 = pk[x][3];
+                        *(uint4 *)(hout + (size_t)(u * 4 + c) * 16) =
+                            make_uint4((p0 & 0xffffu) | (p1 << 16), (p0 >> 16) | (p1 & 0xffff0000u),
+                                       (p2 & 0xffffu) | (p3 << 16), (p2 >> 16) | (p3 & 0xffff0000u));
+                    }
                 }
-                uint32_t w[2];
-                uint4 hdr;
-                quant_unit<BITS>(r, lane, w, hdr, [&](int m, int i, int e) -> float {
-                    const int mr = 16 * m + 8 * (i & 1) + g, kc = 8 * (i >> 1) + 2 * c + e;
-                    const int token = is_v ? 16 * (u & 1) + kc : mr;
-                    const int ch = is_v ? 32 * (u >> 1) + mr : 16 * u + kc;
-                    const uint16_t v = *((const uint16_t *)(buf + row_chunk<D>(token, ch >> 3)) + (ch & 7));
-                    return __uint_as_float((uint32_t)v << 16);
-                });
-                if (BITS == 4) { words[2 * k] = w[0]; words[2 * k + 1] = w[1]; }
-                else words[k] = w[0];
-                if (g == 0) *(uint4 *)(hout + (size_t)(u * 4 + c) * 16) = hdr;
             }
             *(uint4 *)(out + (size_t)(u0 / kPer) * 512 + slot * 16) = make_uint4(words[0], words[1], words[2], words[3]);
         }
@@ -306,42 +351,15 @@ k_dense_write(const TIN *__restrict__ kv, int n, int S, int N, int T, int nb, in
     }
 }
 
+// K and V of one token of a finished block, to `row` (2 D values): 4 lanes hold a chunk's key
+// codes of the token, 8 lanes its value codes.
 template <int D, int BITS>
-__global__ void __launch_bounds__(32 * kReadWarps)
-k_dense_read(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr,
-             const __nv_bfloat16 *__restrict__ tail, const int32_t *__restrict__ len,
-             const int32_t *__restrict__ sel, int n_sel, int S, int N, int T, int nb,
-             __nv_bfloat16 *__restrict__ out_k, __nv_bfloat16 *__restrict__ out_v, int32_t *status)
+__device__ __forceinline__ void read_token(const uint8_t *rec, const uint8_t *kh, int o, int lane, __nv_bfloat16 *row)
 {
-    __shared__ __align__(16) __nv_bfloat16 rows[kReadWarps][2 * D];
-    constexpr size_t kUnit = (size_t)4 * D * BITS, kRec = 2 * kUnit + 4 * D;
+    constexpr size_t kUnit = (size_t)4 * D * BITS;
     constexpr int kPer = 8 / BITS, kCh = (D / 16) / kPer;  // units of a chunk, chunks
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long id = (long long)blockIdx.x * kReadWarps + warp;
-    const int h = (int)(id % N);
-    const long long at = id / N;                           // (sequence, entry)
-    if (at >= (long long)S * n_sel) return;
-    const int s = (int)(at / n_sel);
-    const int t = __ldg(sel + at);
-    const int length = dense_len(len, s, T, status);
-    uint4 *ok = (uint4 *)(out_k + ((size_t)at * N + h) * D), *ov = (uint4 *)(out_v + ((size_t)at * N + h) * D);
-    if (t < 0 || t >= length) {
-        if (t != -1 && lane == 0) set_status(status, RKV_ERR_INDEX);
-        for (int i = lane; i < D / 8; i += 32) ok[i] = ov[i] = make_uint4(0u, 0u, 0u, 0u);
-        return;
-    }
-    const int b = t / kBlk, o = t % kBlk;
-    const size_t sh = (size_t)s * N + h;
-    if (b >= length / kBlk) {
-        const uint4 *kr = (const uint4 *)(tail + (sh * 2 * kBlk + o) * D);
-        const uint4 *vr = (const uint4 *)(tail + ((sh * 2 + 1) * kBlk + o) * D);
-        for (int i = lane; i < D / 8; i += 32) { ok[i] = kr[i]; ov[i] = vr[i]; }
-        return;
-    }
-    const uint8_t *rec = codes + (sh * nb + b) * kRec, *kh = khdr + (sh * nb + b) * (4 * D);
-    uint32_t *krow = (uint32_t *)rows[warp];
-    __nv_bfloat16 *vrow = rows[warp] + D;
-    // keys: the token is row o of the units; 4 lanes (c) hold a chunk's codes of that row
+    uint32_t *krow = (uint32_t *)row;
+    __nv_bfloat16 *vrow = row + D;
     {
         const int g = o & 7, hi_row = (o >> 3) & 1, m = o >> 4;
         for (int x = lane; x < 4 * kCh; x += 32) {
@@ -359,8 +377,7 @@ k_dense_read(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
             }
         }
     }
-    // values: the token is column o % 16 of the units of its half; 8 lanes (g) hold a chunk's
-    // codes of that column
+    // values: the token is column o % 16 of the units of its half
     {
         const uint8_t *vc = rec + kUnit, *vh = rec + 2 * kUnit;
         const int half = o >> 4, hi_col = (o >> 3) & 1, c = (o & 7) >> 1, e = o & 1;
@@ -386,10 +403,164 @@ k_dense_read(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
             }
         }
     }
+}
+
+// Keys (or values) of a whole finished block, its record in shared memory, as rows [32][D] in
+// the warp's buffer (row_chunk).
+template <int D, int BITS, bool VALUES>
+__device__ __forceinline__ void read_block(const uint8_t *cd, const uint8_t *hd, int lane, uint4 *buf)
+{
+    constexpr int kPer = 8 / BITS, kCh = (D / 16) / kPer;
+    const int g = lane >> 2, c = lane & 3, i = lane >> 3;
+    const uint32_t base = um::smem_u32(buf);
+    const uint8_t *slot = cd + (VALUES ? value_slot(g, c) : key_slot(g, c)) * 16;
+#pragma unroll
+    for (int j = 0; j < kCh; ++j) {
+        const uint4 q = *(const uint4 *)(slot + j * 512);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            const int u = j * kPer + x;
+            const uint4 h = *(const uint4 *)(hd + (u * 4 + c) * 16);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                uint32_t a[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    a[e] = value_pair<BITS>(BITS == 4 ? w[(2 * x + m) & 3] : w[x & 3], BITS == 4 ? e : 4 * m + e,
+                                            e < 2 ? h.x : h.z, e < 2 ? h.y : h.w);
+                // keys: rows of the operand are tokens; values: its columns are
+                if (VALUES)
+                    stmatrix4_trans(base + 16 * row_chunk<D>(16 * (u & 1) + 8 * (i >> 1) + (lane & 7),
+                                                             4 * (u >> 1) + 2 * m + (i & 1)), a);
+                else
+                    stmatrix4(base + 16 * row_chunk<D>(16 * m + 8 * (i & 1) + (lane & 7), 2 * u + (i >> 1)), a);
+            }
+        }
+    }
+}
+
+template <int D, int BITS>
+struct ReadCfg {
+    static constexpr int kUnit = 4 * D * BITS, kRec = 2 * kUnit + 4 * D, kHdr = 4 * D, kStage = kRec + kHdr;
+    static constexpr int kStages = 2, kRows = kBlk * D * 2;
+    static constexpr int kWarp = kStages * kStage + kRows;       // a warp's shared memory
+    static constexpr int kSmem = kReadWarps * (kWarp + kStages * 8);
+};
+
+template <int D, int BITS>
+__global__ void __launch_bounds__(32 * kReadWarps)
+k_dense_read(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr,
+             const __nv_bfloat16 *__restrict__ tail, const int32_t *__restrict__ len,
+             const int32_t *__restrict__ sel, int n_sel, int S, int N, int T, int nb, int groups,
+             __nv_bfloat16 *__restrict__ out_k, __nv_bfloat16 *__restrict__ out_v, int32_t *status)
+{
+    using C = ReadCfg<D, BITS>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kCh = D / 8;                             // 16-byte chunks of a row
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *stage = smem + (size_t)warp * C::kWarp;
+    uint4 *buf = (uint4 *)(stage + C::kStages * C::kStage);
+    uint64_t *bars = (uint64_t *)(smem + (size_t)kReadWarps * C::kWarp) + warp * C::kStages;
+    const long long id = (long long)blockIdx.x * kReadWarps + warp;
+    const int h = (int)(id % N), grp = (int)(id / N % groups), s = (int)(id / N / groups);
+    if (s >= S) return;
+    const int length = dense_len(len, s, T, status), full = length / kBlk;
+    const int i0 = grp * 32, cnt = min(32, n_sel - i0);
+    const size_t at0 = (size_t)s * n_sel + i0, sh = (size_t)s * N + h;
+    const int t = lane < cnt ? __ldg(sel + at0 + lane) : -1;
+    const bool ok = t >= 0 && t < length;
+    if (!ok && t != -1) set_status(status, RKV_ERR_INDEX);
+    const int b = ok ? t / kBlk : -1;
+    // chunk c of entry i's row of K (V)
+    auto row_k = [&](int i) { return (uint4 *)(out_k + ((at0 + i) * N + h) * D); };
+    auto row_v = [&](int i) { return (uint4 *)(out_v + ((at0 + i) * N + h) * D); };
+
+    if (lane == 0) {
+        for (int k = 0; k < C::kStages; ++k) um::mbar_init(bars + k, 1);
+        um::fence_mbar_init();
+    }
     __syncwarp();
-    for (int i = lane; i < D / 8; i += 32) {
-        ok[i] = ((const uint4 *)rows[warp])[i];
-        ov[i] = ((const uint4 *)(rows[warp] + D))[i];
+    const bool held = ok && b < full;
+    const uint32_t mates = __match_any_sync(0xffffffffu, held ? b : -1);
+    const bool together = held && __popc(mates) >= kTogether;
+    // groups of entries of one block, by their first entry; their records come by bulk copies,
+    // two of them ahead
+    uint32_t ahead = __ballot_sync(0xffffffffu, together && (mates & ((1u << lane) - 1u)) == 0u);
+    uint32_t groups_left = ahead;
+    int issued = 0;
+    auto issue = [&]() {
+        if (!ahead) return;
+        const int bb = __shfl_sync(0xffffffffu, b, __ffs(ahead) - 1);
+        ahead &= ahead - 1u;
+        if (lane == 0) {
+            const int st = issued % C::kStages;
+            const size_t rec = sh * nb + bb;
+            um::mbar_arrive_expect_tx(bars + st, C::kStage);
+            bulk_load(stage + st * C::kStage, codes + rec * C::kRec, C::kRec, bars + st);
+            bulk_load(stage + st * C::kStage + C::kRec, khdr + rec * C::kHdr, C::kHdr, bars + st);
+        }
+        ++issued;
+    };
+    for (int k = 0; k < C::kStages; ++k) issue();
+
+    // padding and wrong entries: zero rows; tokens of the unfinished block: as they are
+    uint32_t plain = __ballot_sync(0xffffffffu, lane < cnt && !held);
+    while (plain) {
+        const int i = __ffs(plain) - 1;
+        plain &= plain - 1u;
+        const int ti = __shfl_sync(0xffffffffu, ok ? t : -1, i);
+        const uint4 *kr = (const uint4 *)(tail + (sh * 2 * kBlk + (ti & 31)) * D);
+        for (int x = lane; x < kCh; x += 32) {
+            row_k(i)[x] = ti < 0 ? make_uint4(0u, 0u, 0u, 0u) : kr[x];
+            row_v(i)[x] = ti < 0 ? make_uint4(0u, 0u, 0u, 0u) : kr[kBlk * kCh + x];
+        }
+    }
+    // tokens alone in their block, or nearly so
+    uint32_t alone = __ballot_sync(0xffffffffu, held && !together);
+    while (alone) {
+        const int i = __ffs(alone) - 1;
+        alone &= alone - 1u;
+        const int ti = __shfl_sync(0xffffffffu, t, i);
+        const size_t rec = sh * nb + ti / kBlk;
+        __syncwarp();
+        read_token<D, BITS>(codes + rec * C::kRec, khdr + rec * C::kHdr, ti & 31, lane, (__nv_bfloat16 *)buf);
+        __syncwarp();
+        for (int x = lane; x < kCh; x += 32) {
+            row_k(i)[x] = buf[x];
+            row_v(i)[x] = buf[kCh + x];
+        }
+    }
+    for (int n = 0; groups_left; ++n) {
+        const uint32_t same = __shfl_sync(0xffffffffu, mates, __ffs(groups_left) - 1);
+        groups_left &= groups_left - 1u;
+        const uint8_t *rec = stage + (n % C::kStages) * C::kStage;
+        if (!__all_sync(0xffffffffu, um::mbar_wait(bars + n % C::kStages, (uint32_t)(n / C::kStages) & 1u, kWaitCycles))) {
+            set_status(status, RKV_ERR_DEVICE_TIMEOUT);
+            return;
+        }
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            __syncwarp();
+            if (v == 0) read_block<D, BITS, false>(rec, rec + C::kRec, lane, buf);
+            else read_block<D, BITS, true>(rec + C::kUnit, rec + 2 * C::kUnit, lane, buf);
+            __syncwarp();
+            if (v == 1) issue();
+            // 32 / kCh rows at a time (a row takes kCh lanes)
+            constexpr int kRows = kCh < 32 ? 32 / kCh : 1;
+            uint32_t left = same;
+            while (left) {
+                uint32_t mine = left;                      // the bit of this lane's row
+#pragma unroll
+                for (int k = 1; k < kRows; ++k)
+                    if (lane / kCh >= k) mine &= mine - 1u;
+                const int i = mine ? __ffs(mine) - 1 : 0;
+                const int o = __shfl_sync(0xffffffffu, t, i) & 31;
+                if (mine) (v ? row_v(i) : row_k(i))[lane % kCh] = buf[row_chunk<D>(o, lane % kCh)];
+#pragma unroll
+                for (int k = 0; k < kRows; ++k) left &= left - 1u;
+            }
+        }
     }
 }
 
@@ -418,11 +589,19 @@ template <int D, int BITS>
 cudaError_t run_read(const DenseGeom &g, const rkv_dense_cache *c, const int32_t *len, const int32_t *sel,
                      int n_sel, void *ok, void *ov, int32_t *status, cudaStream_t s)
 {
-    const long long warps = (long long)g.S * n_sel * g.N;
+    const int groups = (n_sel + 31) / 32;
+    const long long warps = (long long)g.S * groups * g.N;
+    constexpr int kSmem = ReadCfg<D, BITS>::kSmem;
+    static PerDevice<int> setup;
+    int unused = 0;
+    cudaError_t e = per_device(setup, unused, [](int &) {
+        return cudaFuncSetAttribute(k_dense_read<D, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    });
+    if (e != cudaSuccess) return e;
     ProfScope prof("dense_read", s);
-    k_dense_read<D, BITS><<<(unsigned)((warps + kReadWarps - 1) / kReadWarps), 32 * kReadWarps, 0, s>>>(
+    k_dense_read<D, BITS><<<(unsigned)((warps + kReadWarps - 1) / kReadWarps), 32 * kReadWarps, kSmem, s>>>(
         (const uint8_t *)c->codes, (const uint8_t *)c->khdr, (const __nv_bfloat16 *)c->tail, len, sel, n_sel, g.S,
-        g.N, g.T, g.nb, (__nv_bfloat16 *)ok, (__nv_bfloat16 *)ov, status);
+        g.N, g.T, g.nb, groups, (__nv_bfloat16 *)ok, (__nv_bfloat16 *)ov, status);
     return cudaGetLastError();
 }
 

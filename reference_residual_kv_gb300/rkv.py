@@ -103,7 +103,7 @@ def lib():
                 ("rkv_dense_read", [DP, DC, V, V, I32, V, V, V, V]),
                 ("rkv_block_select_workspace", [DP, I32, sz]),
                 ("rkv_block_select", [DP, I32, V, DC, V, I32, I32, I32, I32, V, V, Z, V, V]),
-                ("rkv_dense_attention_workspace", [DP, I32, I32, I32, I32, sz]),
+                ("rkv_dense_attention_workspace", [DP, I32, I32, sz]),
                 ("rkv_dense_attention", [DP, I32, V, DC, V, V, I32, I32, V, I32, V, Z, V, V]),
                 ("rkv_tree_attention", [DP, I32, V, I32, V, V, DC, V, V, I32, V, Z, V, V])):
             f = getattr(L, name)
@@ -286,10 +286,9 @@ def rkv_block_select(p: rkv_dense_params, H: int, q, cache: rkv_dense_cache, len
         raise RkvError(st, "rkv_block_select")
 
 
-def rkv_dense_attention_workspace(p: rkv_dense_params, H: int, n_query: int = 1, n_blocks: int = 0,
-                                  listed: bool = False) -> int:
+def rkv_dense_attention_workspace(p: rkv_dense_params, H: int, n_query: int = 1) -> int:
     b = ctypes.c_size_t()
-    st = lib().rkv_dense_attention_workspace(ctypes.byref(p), H, n_query, n_blocks, int(listed), ctypes.byref(b))
+    st = lib().rkv_dense_attention_workspace(ctypes.byref(p), H, n_query, ctypes.byref(b))
     if st:
         raise RkvError(st, "rkv_dense_attention_workspace")
     return b.value
@@ -455,6 +454,12 @@ class Buffers:
         return bad
 
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+# the raw handle of a device's current stream, without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 class DenseCache:
     """The dense cache of one rkv_dense_params on one device: its three buffers, the device
     status, and its operators with their tensors checked (type, shape, contiguity, device).
@@ -466,6 +471,7 @@ class DenseCache:
     def __init__(self, p: rkv_dense_params, device="cuda", guard: int = 0):
         codes, khdr, tail = rkv_dense_sizes(p)
         self.p = p
+        self.S, self.T, self.N, self.D = p.S, p.T, p.N, p.D
         self.guard = guard
         self._raw = {}
         for name, n, fill in (("codes", codes, None), ("khdr", khdr, None), ("tail", tail, None), ("status", 16, 0)):
@@ -477,7 +483,8 @@ class DenseCache:
         self.cache = rkv_dense_cache(_ptr(self.codes), _ptr(self.khdr), _ptr(self.tail))
         self._sizes = {}
 
-    def _check(self, name, t, dtypes, shape):
+    def _refuse(self, name, t, dtypes, shape):
+        """Says what is wrong with an argument, if anything is."""
         if t.dtype not in dtypes:
             raise ValueError("%s: %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
         if tuple(t.shape) != shape:
@@ -487,98 +494,101 @@ class DenseCache:
         if t.device != self.device:
             raise ValueError("%s is on %s, the cache on %s" % (name, t.device, self.device))
 
-    def _run(self, stream, key, query, call):
-        """Runs call(workspace, bytes) with the cache's device current and scratch of
-        query() bytes from the pool of the stream that the call runs on."""
-        need = self._sizes.get(key)
-        if need is None:
-            need = self._sizes[key] = query()
-        if stream is None and torch.cuda.current_device() == self.device.index:
-            return call(*self._scratch(need))
-        with torch.cuda.device(self.device):
+    def _check(self, name, t, dtypes, shape):
+        if not (t.dtype in dtypes and t.shape == shape and t.device == self.device and t.is_contiguous()):
+            self._refuse(name, t, dtypes, shape)
+
+    def _run(self, stream, need, call):
+        """call(workspace, bytes, stream) with the cache's device current, and scratch of `need`
+        bytes from the pool of the stream that the call runs on."""
+        dev = self.device.index
+        if stream is None and torch.cuda.current_device() == dev:
+            return call(self._scratch(need), need, _raw_stream(dev))
+        with torch.cuda.device(dev):
             if stream is None:
-                return call(*self._scratch(need))
+                return call(self._scratch(need), need, _raw_stream(dev))
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device=self.device)
             with torch.cuda.stream(stream):
-                return call(*self._scratch(need))
+                return call(self._scratch(need), need, stream.cuda_stream)
 
     def _scratch(self, need):
         if need == 0:
-            return None, 0
+            return None
         if not self.guard:
-            return torch.empty(need, dtype=torch.uint8, device=self.device), need
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
         t, raw = guarded_empty((need,), torch.uint8, self.device, self.guard)
         self._raw["scratch %d" % len(self._raw)] = (t, raw)
-        return t, need
+        return t
+
+    def _size(self, *key):
+        """Bytes of scratch: ("select", lists) or ("attend", H, n_query)."""
+        need = self._sizes.get(key)
+        if need is None:
+            f = rkv_block_select_workspace if key[0] == "select" else rkv_dense_attention_workspace
+            need = self._sizes[key] = f(self.p, *key[1:])
+        return need
 
     def write(self, kv, pos, n_new=None, stream=None):
         """kv [S][n][2ND] (bf16 or fp32) as tokens pos[s] .. of each sequence; n_new[s] of its n
         rows (all of them where n_new is None)."""
-        p = self.p
         n = kv.shape[1] if kv.dim() == 3 else -1
-        self._check("kv", kv, (torch.bfloat16, torch.float32), (p.S, n, 2 * p.N * p.D))
-        self._check("pos", pos, (torch.int32,), (p.S,))
+        self._check("kv", kv, (_BF16, _F32), (self.S, n, 2 * self.N * self.D))
+        self._check("pos", pos, (_I32,), (self.S,))
         if n_new is not None:
-            self._check("n_new", n_new, (torch.int32,), (p.S,))
-        dt = RKV_F32 if kv.dtype == torch.float32 else RKV_BF16
-        self._run(stream, None, lambda: 0, lambda ws, nb: rkv_dense_write(
-            p, kv, dt, n, pos, n_new, self.cache, self.status))
+            self._check("n_new", n_new, (_I32,), (self.S,))
+        dt = RKV_F32 if kv.dtype is _F32 else RKV_BF16
+        self._run(stream, 0, lambda ws, nb, st: rkv_dense_write(
+            self.p, kv, dt, n, pos, n_new, self.cache, self.status, st))
 
     def read(self, length, sel, out_k, out_v, stream=None):
         """K and V of tokens sel [S][n_sel] (-1: zero rows) to out_k, out_v bf16 [S][n_sel][ND]."""
-        p = self.p
         n = sel.shape[1] if sel.dim() == 2 else -1
-        self._check("length", length, (torch.int32,), (p.S,))
-        self._check("sel", sel, (torch.int32,), (p.S, n))
-        self._check("out_k", out_k, (torch.bfloat16,), (p.S, n, p.N * p.D))
-        self._check("out_v", out_v, (torch.bfloat16,), (p.S, n, p.N * p.D))
-        self._run(stream, None, lambda: 0, lambda ws, nb: rkv_dense_read(
-            p, self.cache, length, sel, n, out_k, out_v, self.status))
+        rows = (self.S, n, self.N * self.D)
+        self._check("length", length, (_I32,), (self.S,))
+        self._check("sel", sel, (_I32,), (self.S, n))
+        self._check("out_k", out_k, (_BF16,), rows)
+        self._check("out_v", out_v, (_BF16,), rows)
+        self._run(stream, 0, lambda ws, nb, st: rkv_dense_read(
+            self.p, self.cache, length, sel, n, out_k, out_v, self.status, st))
 
     def select(self, H: int, q, length, blocks, keep_first: int = 0, keep_last: int = 0, stream=None):
         """The blocks [S][N or 1][n_blocks] (output) with the largest score bounds for q [S][H][D]."""
-        p = self.p
-        lists, n = (blocks.shape[1], blocks.shape[2]) if blocks.dim() == 3 else (-1, -1)
-        self._check("q", q, (torch.bfloat16,), (p.S, H, p.D))
-        self._check("length", length, (torch.int32,), (p.S,))
-        self._check("blocks", blocks, (torch.int32,), (p.S, lists, n))
-        self._run(stream, ("select", lists), lambda: rkv_block_select_workspace(p, lists),
-                  lambda ws, nb: rkv_block_select(p, H, q, self.cache, length, lists, n, keep_first, keep_last,
-                                                  blocks, ws, nb, self.status))
+        lists, n = blocks.shape[1:] if blocks.dim() == 3 else (-1, -1)
+        self._check("q", q, (_BF16,), (self.S, H, self.D))
+        self._check("length", length, (_I32,), (self.S,))
+        self._check("blocks", blocks, (_I32,), (self.S, lists, n))
+        self._run(stream, self._size("select", lists), lambda ws, nb, st: rkv_block_select(
+            self.p, H, q, self.cache, length, lists, n, keep_first, keep_last, blocks, ws, nb, self.status, st))
 
     def attend(self, H: int, q, length, out, blocks=None, stream=None):
         """out [S][H][D] (fp32 or bf16): attention of q [S][H][D] over the cache, or over the
         listed blocks [S][N or 1][n_blocks] and the unfinished one."""
-        p = self.p
-        self._check("q", q, (torch.bfloat16,), (p.S, H, p.D))
-        self._check("length", length, (torch.int32,), (p.S,))
-        self._check("out", out, (torch.float32, torch.bfloat16), (p.S, H, p.D))
+        self._check("q", q, (_BF16,), (self.S, H, self.D))
+        self._check("length", length, (_I32,), (self.S,))
+        self._check("out", out, (_F32, _BF16), (self.S, H, self.D))
         lists, n = 1, 0
         if blocks is not None:
-            lists, n = (blocks.shape[1], blocks.shape[2]) if blocks.dim() == 3 else (-1, -1)
-            self._check("blocks", blocks, (torch.int32,), (p.S, lists, n))
+            lists, n = blocks.shape[1:] if blocks.dim() == 3 else (-1, -1)
+            self._check("blocks", blocks, (_I32,), (self.S, lists, n))
             if n < 1:
                 raise ValueError("blocks: an empty list")
-        dt = RKV_F32 if out.dtype == torch.float32 else RKV_BF16
-        self._run(stream, ("attend", H, 1, n), lambda: rkv_dense_attention_workspace(p, H, 1, n, blocks is not None),
-                  lambda ws, nb: rkv_dense_attention(p, H, q, self.cache, length, blocks, lists, n, out, dt, ws, nb,
-                                                     self.status))
+        dt = RKV_F32 if out.dtype is _F32 else RKV_BF16
+        self._run(stream, self._size("attend", H, 1), lambda ws, nb, st: rkv_dense_attention(
+            self.p, H, q, self.cache, length, blocks, lists, n, out, dt, ws, nb, self.status, st))
 
     def tree_attend(self, H: int, q, parent, draft_kv, length, out, stream=None):
         """out [S][n][H][D] (fp32 or bf16): attention of the drafted tokens' q [S][n][H][D] over
         the cache and their own line of parents; draft_kv bf16 [S][n][2ND], parent [S][n]."""
-        p = self.p
         n = q.shape[1] if q.dim() == 4 else -1
-        self._check("q", q, (torch.bfloat16,), (p.S, n, H, p.D))
-        self._check("parent", parent, (torch.int32,), (p.S, n))
-        self._check("draft_kv", draft_kv, (torch.bfloat16,), (p.S, n, 2 * p.N * p.D))
-        self._check("length", length, (torch.int32,), (p.S,))
-        self._check("out", out, (torch.float32, torch.bfloat16), (p.S, n, H, p.D))
-        dt = RKV_F32 if out.dtype == torch.float32 else RKV_BF16
-        self._run(stream, ("attend", H, n, 0), lambda: rkv_dense_attention_workspace(p, H, n),
-                  lambda ws, nb: rkv_tree_attention(p, H, q, n, parent, draft_kv, self.cache, length, out, dt, ws,
-                                                    nb, self.status))
+        self._check("q", q, (_BF16,), (self.S, n, H, self.D))
+        self._check("parent", parent, (_I32,), (self.S, n))
+        self._check("draft_kv", draft_kv, (_BF16,), (self.S, n, 2 * self.N * self.D))
+        self._check("length", length, (_I32,), (self.S,))
+        self._check("out", out, (_F32, _BF16), (self.S, n, H, self.D))
+        dt = RKV_F32 if out.dtype is _F32 else RKV_BF16
+        self._run(stream, self._size("attend", H, n), lambda ws, nb, st: rkv_tree_attention(
+            self.p, H, q, n, parent, draft_kv, self.cache, length, out, dt, ws, nb, self.status, st))
 
     def device_status(self) -> int:
         return int(self.status[0].item())

@@ -105,8 +105,6 @@ def test_selection_and_attention_refuse(lib):
     for nq in (0, 65):
         with pytest.raises(rkv.RkvError):
             rkv.rkv_dense_attention_workspace(p, 8, nq)
-    with pytest.raises(rkv.RkvError):
-        rkv.rkv_dense_attention_workspace(p, 8, 1, 0, True)
 
 
 def test_the_cache_object_checks_its_tensors(lib):
