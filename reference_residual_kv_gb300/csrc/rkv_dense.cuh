@@ -71,10 +71,10 @@ __device__ __forceinline__ int value_slot(int g, int c) { return 8 * c + ((g + 2
 // ---- how finished blocks are dealt out ---------------------------------------------------
 // The blocks to attend (of all sequences, for one KV head) are cut into runs of at most `chunk`
 // blocks of one sequence, numbered through; chunk follows from the lengths that the device
-// holds, so that a batch of uneven or short sequences fills the GPU as full ones do: it is
-// near the smallest that makes no more than `target` runs (or one for every sequence, where
-// there are more sequences than that).  So there are at most max(target, S) runs (the host's
-// grid and workspace).  Every lane of a warp takes part.
+// holds, so that a batch of uneven or short sequences fills the GPU as full ones do: one of a
+// few sizes from the ideal on that makes no more than `target` runs (or one run for every
+// sequence, where there are at least `target` sequences).  So there are at most
+// max(target, S) runs (the host's grid and workspace).  One warp works it out for its CTA.
 struct DenseCut {
     int target, unit, least;                 // wanted runs; chunk is a multiple of unit, at least `least`
 };
@@ -86,28 +86,43 @@ __device__ __forceinline__ int blocks_of(const int32_t *len, int s, int S, int T
     if (s >= S) return 0;
     return listed ? listed : dense_len(len, s, T, status) / kBlk;
 }
-__device__ __forceinline__ int dense_chunk(const int32_t *len, int S, int T, int listed, const DenseCut &c,
+// ceil(n / chunk) for 0 <= n < 2^27: the fp32 quotient is off by less than 2^4, relative to at
+// most 2^27, and its multiple is put right.
+__device__ __forceinline__ int runs_of(int n, int chunk, float inv)
+{
+    int r = (int)((float)n * inv);
+    int left = n - r * chunk;
+    while (left > 0) { ++r; left -= chunk; }
+    while (left <= -chunk) { --r; left += chunk; }
+    return r;
+}
+__device__ __forceinline__ int dense_chunk(const int32_t *len, int S, int T, int listed, const DenseCut &c, int n0,
                                            int32_t *status)
 {
     const int lane = threadIdx.x & 31;
-    long long all = 0;
-    int most = 0;
-    for (int s0 = 0; s0 < S; s0 += 32) {
+    long long all = __reduce_add_sync(0xffffffffu, n0);    // n0: blocks of sequence `lane`
+    int most = __reduce_max_sync(0xffffffffu, n0);
+    for (int s0 = 32; s0 < S; s0 += 32) {
         const int n = blocks_of(len, s0 + lane, S, T, listed, status);
         all += __reduce_add_sync(0xffffffffu, n);
         most = max(most, __reduce_max_sync(0xffffffffu, n));
     }
-    if (S >= c.target) return max(most, 1);
-    int chunk = max(c.least, (int)((all + c.target - 1) / c.target));
-    while (true) {
-        chunk = (chunk + c.unit - 1) / c.unit * c.unit;
+    most = max(most, 1);
+    if (S >= c.target) return most;
+    const float ideal = (float)all / (float)c.target;
+    for (int k = 0; k < 6; ++k) {                          // 1, 1.125, ... times the ideal
+        const int want = max(c.least, (int)(ideal * (1.0f + 0.125f * (float)k)) + 1);
+        const int chunk = (want + c.unit - 1) / c.unit * c.unit;
         if (chunk >= most) return chunk;                   // a run for every sequence: S < target
-        int runs = 0;
-        for (int s0 = 0; s0 < S; s0 += 32)
-            runs += __reduce_add_sync(0xffffffffu, (blocks_of(len, s0 + lane, S, T, listed, status) + chunk - 1) / chunk);
+        const float inv = 1.0f / (float)chunk;
+        int runs = __reduce_add_sync(0xffffffffu, runs_of(n0, chunk, inv));
+        for (int s0 = 32; s0 < S; s0 += 32)
+            runs += __reduce_add_sync(0xffffffffu, runs_of(blocks_of(len, s0 + lane, S, T, listed, status), chunk, inv));
         if (runs <= c.target) return chunk;
-        chunk += max(1, chunk >> 4);
     }
+    // sum of ceil(n / chunk) <= all / chunk + S
+    const int want = max(c.least, (int)((all + c.target - S - 1) / (c.target - S)));
+    return (want + c.unit - 1) / c.unit * c.unit;
 }
 // Inclusive sum over the lanes.
 __device__ __forceinline__ int lane_scan(int v)
@@ -120,33 +135,38 @@ __device__ __forceinline__ int lane_scan(int v)
     }
     return v;
 }
-// Run number p.
+// Run number p, by one warp.
 __device__ __forceinline__ DenseRun dense_run(const int32_t *len, int S, int T, int listed, const DenseCut &c, int p,
                                               int32_t *status)
 {
-    const int chunk = dense_chunk(len, S, T, listed, c, status), lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, n0 = blocks_of(len, lane, S, T, listed, status);
+    const int chunk = dense_chunk(len, S, T, listed, c, n0, status);
+    const float inv = 1.0f / (float)chunk;
     int base = 0;
     for (int s0 = 0; s0 < S; s0 += 32) {
-        const int n = blocks_of(len, s0 + lane, S, T, listed, status), runs = (n + chunk - 1) / chunk;
+        const int n = s0 ? blocks_of(len, s0 + lane, S, T, listed, status) : n0, runs = runs_of(n, chunk, inv);
         const int upto = base + lane_scan(runs);
         const uint32_t hit = __ballot_sync(0xffffffffu, p < upto);
         if (hit) {
             const int l = __ffs(hit) - 1;
             const int k = p - __shfl_sync(0xffffffffu, upto - runs, l);
-            return DenseRun{s0 + l, k * chunk, min(__shfl_sync(0xffffffffu, n, l), (k + 1) * chunk), p};
+            const int left = __shfl_sync(0xffffffffu, n, l) - k * chunk;
+            return DenseRun{s0 + l, k * chunk, k * chunk + min(left, chunk), p};
         }
         base = __shfl_sync(0xffffffffu, upto, 31);
     }
     return DenseRun{-1, 0, 0, 0};
 }
-// The runs of sequence s: first number in .first, one past the last in .end.
+// The runs of sequence s, by one warp: first number in .first, one past the last in .end.
 __device__ __forceinline__ DenseRun dense_runs_of(const int32_t *len, int S, int T, int listed, const DenseCut &c, int s,
                                                   int32_t *status)
 {
-    const int chunk = dense_chunk(len, S, T, listed, c, status), lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, n0 = blocks_of(len, lane, S, T, listed, status);
+    const int chunk = dense_chunk(len, S, T, listed, c, n0, status);
+    const float inv = 1.0f / (float)chunk;
     int base = 0;
     for (int s0 = 0; s0 <= s; s0 += 32) {
-        const int runs = (blocks_of(len, s0 + lane, S, T, listed, status) + chunk - 1) / chunk;
+        const int n = s0 ? blocks_of(len, s0 + lane, S, T, listed, status) : n0, runs = runs_of(n, chunk, inv);
         const int upto = base + lane_scan(runs);
         if (s < s0 + 32)
             return DenseRun{s, __shfl_sync(0xffffffffu, upto - runs, s - s0), __shfl_sync(0xffffffffu, upto, s - s0), 0};

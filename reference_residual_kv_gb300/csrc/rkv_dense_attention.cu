@@ -97,7 +97,13 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     // the row tiles of a run are neighbours, then its KV heads: they read the same blocks
     const int tile = blockIdx.x % tiles, n = blockIdx.x / tiles % N;
-    const DenseRun run = dense_run(len, S, T, blocks ? n_blocks : 0, cut, blockIdx.x / tiles / N, status);
+    __shared__ DenseRun run_s;
+    if (warp == 0) {
+        const DenseRun r = dense_run(len, S, T, blocks ? n_blocks : 0, cut, blockIdx.x / tiles / N, status);
+        if (lane == 0) run_s = r;
+    }
+    __syncthreads();
+    const DenseRun run = run_s;
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (run.s < 0) return;
     const int s = run.s, sn = s * N + n, i0 = run.first, i1 = run.end;
@@ -391,6 +397,11 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
             if (lane == 0) set_status(status, RKV_ERR_INDEX);
         }
     }
+    __shared__ DenseRun runs_s;
+    if (warp == kFinWarps - 1) {
+        const DenseRun x = dense_runs_of(len, S, T, listed, cut, s, status);
+        if (lane == 0) runs_s = x;
+    }
     // warps 0 and 1: the rows as the second operand (columns behind the last row are zero)
     uint32_t qr[D / 16][2];
     if (warp < 2 && (rest || parent)) {
@@ -478,11 +489,12 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
             }
         }
     }
-    const DenseRun runs = dense_runs_of(len, S, T, listed, cut, s, status);
 
     // the finished blocks' partials: launched as a programmatic dependent, this waits for them
     asm volatile("griddepcontrol.wait;" ::: "memory");
     bool bad = false;
+    __syncthreads();
+    const DenseRun runs = runs_s;
     if (!padding) {
         // `each` partials for every run and KV head, this warp's every wpr-th; 32 at a time:
         // their weights, a lane each, then their sums, those with nothing in them left out

@@ -239,51 +239,79 @@ __device__ unsigned long long exact_score(const __nv_bfloat16 *q, const uint8_t 
     }
     unsigned long long best = 0ull;
 #pragma unroll 1
-    for (int j = 0; j < G; ++j) {
-        const uint32_t *qr = (const uint32_t *)(q + (sn * G + j) * D);
-        float qe[kI][4];
+    for (int j0 = 0; j0 < G; j0 += 4) {                    // four heads at once (the last one repeats)
+        float qe[4][kI][4];
 #pragma unroll
-        for (int k = 0; k < kI; ++k) {
-            const int i = lane + 32 * k;
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t qv = i < D / 4 ? __ldg(qr + (i >> 2) * 8 + (i & 3) + 4 * e) : 0u;
-                qe[k][2 * e] = __uint_as_float(qv << 16);
-                qe[k][2 * e + 1] = __uint_as_float(qv & 0xffff0000u);
+            for (int k = 0; k < kI; ++k) {
+                const int i = lane + 32 * k;
+                const uint32_t *qr = (const uint32_t *)(q + (sn * G + min(j0 + j, G - 1)) * D);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t qv = i < D / 4 ? __ldg(qr + (i >> 2) * 8 + (i & 3) + 4 * e) : 0u;
+                    qe[j][k][2 * e] = __uint_as_float(qv << 16);
+                    qe[j][k][2 * e + 1] = __uint_as_float(qv & 0xffff0000u);
+                }
             }
-        }
-        Sum72 sum;
+        Sum72 sum[4];
         bool tiny = false;
 #pragma unroll
         for (int k = 0; k < kI; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = qe[k][e] >= 0.0f ? hi[k][e] : lo[k][e], p = __fmul_rn(qe[k][e], x);
-                tiny |= qe[k][e] != 0.0f && x != 0.0f && fabsf(p) < 0x1p-100f;
-                sum.add(p);
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x = qe[j][k][e] >= 0.0f ? hi[k][e] : lo[k][e], p = __fmul_rn(qe[j][k][e], x);
+                    tiny |= qe[j][k][e] != 0.0f && x != 0.0f && fabsf(p) < 0x1p-100f;
+                    sum[j].add(p);
+                }
+        // a butterfly: two steps that halve the heads, then whole sums; lanes of head j end with
+        // lane & 3 == (j >> 1) + 2 (j & 1)
+        auto swapped = [&](const Sum72 &keep, const Sum72 &send, int o) {
+            Sum72 r = keep, x;
+            x.a = __shfl_xor_sync(0xffffffffu, send.a, o);
+            x.b = __shfl_xor_sync(0xffffffffu, send.b, o);
+            x.c = __shfl_xor_sync(0xffffffffu, send.c, o);
+            r.add(x);
+            return r;
+        };
+        const bool b0 = lane & 1, b1 = lane & 2;
+        const Sum72 p0 = swapped(b0 ? sum[2] : sum[0], b0 ? sum[0] : sum[2], 1);
+        const Sum72 p1 = swapped(b0 ? sum[3] : sum[1], b0 ? sum[1] : sum[3], 1);
+        Sum72 t = swapped(b1 ? p1 : p0, b1 ? p0 : p1, 2);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) t = swapped(t, t, o);
+        double v = ((double)t.c + (double)t.b) + (double)t.a;
+        unsigned long long key = order64(v);
+        if (__any_sync(0xffffffffu, tiny || !(fabs(v) < 1e300))) {
+            key = 0ull;
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                v = 0.0;
+                const uint32_t *qr = (const uint32_t *)(q + (sn * G + min(j0 + j, G - 1)) * D);
+#pragma unroll
+                for (int k = 0; k < kI; ++k) {
+                    const int i = lane + 32 * k;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t qv = i < D / 4 ? __ldg(qr + (i >> 2) * 8 + (i & 3) + 4 * (e >> 1)) : 0u;
+                        const float x = __uint_as_float((e & 1) ? qv & 0xffff0000u : qv << 16);
+                        v += (double)max_nan(x, 0.0f) * hi[k][e] + (double)-max_nan(-x, 0.0f) * lo[k][e];
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                const unsigned long long kj = order64(v);
+                key = kj > key ? kj : key;
             }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            Sum72 other;
-            other.a = __shfl_xor_sync(0xffffffffu, sum.a, o);
-            other.b = __shfl_xor_sync(0xffffffffu, sum.b, o);
-            other.c = __shfl_xor_sync(0xffffffffu, sum.c, o);
-            sum.add(other);
         }
-        // lane 0's order of additions for all
-        double v = ((double)sum.c + (double)sum.b) + (double)sum.a;
-        v = __shfl_sync(0xffffffffu, v, 0);
-        if (__any_sync(0xffffffffu, tiny) || !(fabs(v) < 1e300)) {
-            v = 0.0;
 #pragma unroll
-            for (int k = 0; k < kI; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v += (double)max_nan(qe[k][e], 0.0f) * hi[k][e] + (double)-max_nan(-qe[k][e], 0.0f) * lo[k][e];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        for (int o = 1; o < 4; o <<= 1) {
+            const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, o);
+            key = other > key ? other : key;
         }
-        const unsigned long long key = order64(v);
+        key = __shfl_sync(0xffffffffu, key, 0);            // one order of additions for all
         best = key > best ? key : best;
     }
     return best;

@@ -196,7 +196,13 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile = blockIdx.x % tiles, n = blockIdx.x / tiles % N;
-    const DenseRun run = dense_run(len, S, T, 0, cut, blockIdx.x / tiles / N, status);
+    __shared__ DenseRun run_s;
+    if (warp == 0) {
+        const DenseRun r = dense_run(len, S, T, 0, cut, blockIdx.x / tiles / N, status);
+        if (lane == 0) run_s = r;
+    }
+    __syncthreads();
+    const DenseRun run = run_s;
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (run.s < 0) return;
     const int s = run.s, sn = s * N + n, b0 = run.first, blocks = run.end - run.first;

@@ -1,8 +1,8 @@
 // rkv_dense_write.cu -- the dense cache is written and read back token by token.
 //
 //   k_dense_write  one warp per (sequence, block, KV head, keys | values): the 32 rows of
-//                  the block come to shared memory (new rows from the input, the ones
-//                  before from the tail), ldmatrix hands each lane the columns that it
+//                  the block come to shared memory (whole new blocks of bf16 rows by TMA; rows
+//                  of an earlier call from the tail), ldmatrix hands each lane the columns that it
 //                  stores (transposed for the values), and a group's extremes are three
 //                  warp shuffles away.  Codes and headers leave in the order of
 //                  rkv_dense.cuh.  Rows of a block that stays unfinished go to the tail.
@@ -122,9 +122,12 @@ __device__ __forceinline__ float rcp_fast(float x)
 // Extremes, steps and headers of two units at once: r[x][m][i] = register i of operand m of
 // unit x (rkv_dense.cuh).  A butterfly over the 8 lanes of equal c: the first step keeps one
 // of the units, the second one of the column halves, the third one of a pair's columns, so
-// that each lane ends with one of the 8 columns, works out its {min, step} (a bf16 pair), and
-// hands it to the others.  pk[x][v]: column v (2c, 2c + 1, 2c + 8, 2c + 9) of unit x.
-__device__ __forceinline__ void unit_headers(const uint32_t (&r)[2][2][4], int lane, float qmax, uint32_t (&pk)[2][4])
+// that each lane ends with one of the 8 columns, works out its {min, step} (a bf16 pair, both
+// with their signs flipped: the codes need them so) and the step's reciprocal, and hands them
+// to the others.  pk[x][v], iv[x][v]: column v (2c, 2c + 1, 2c + 8, 2c + 9) of unit x.  The
+// reciprocal is 0 for a step of 0, and NaN where the codes' fast path does not hold.
+__device__ __forceinline__ void unit_headers(const uint32_t (&r)[2][2][4], int lane, float qmax, uint32_t (&pk)[2][4],
+                                             float (&iv)[2][4])
 {
     uint32_t mn[2][2], mx[2][2];                           // [unit][half]
 #pragma unroll
@@ -152,71 +155,96 @@ __device__ __forceinline__ void unit_headers(const uint32_t (&r)[2][2][4], int l
     n2 = low(n2, __shfl_xor_sync(0xffffffffu, n2, 16));
     x2 = high(x2, __shfl_xor_sync(0xffffffffu, x2, 16));
     const float lo = (g & 4) ? hi_f(n2) : lo_f(n2), hi = (g & 4) ? hi_f(x2) : lo_f(x2);
-    uint32_t packed = 0x7fff7fffu;                         // NaN, NaN
-    if (fmaxf(fabsf(lo), fabsf(hi)) < 0x1p126f && lo == lo && hi == hi)
-        packed = (__float_as_uint(lo) >> 16) | (group_step(lo, hi, qmax) << 16);
+    uint32_t packed = 0xffffffffu;                         // NaN, NaN
+    float inv = NAN;
+    if (fmaxf(fabsf(lo), fabsf(hi)) < 0x1p126f && lo == lo && hi == hi) {
+        const uint32_t st = group_step(lo, hi, qmax);
+        const float sf = __uint_as_float(st << 16);
+        packed = ((__float_as_uint(lo) >> 16) | (st << 16)) ^ 0x80008000u;
+        inv = st == 0u ? 0.0f : rcp_fast(sf);
+        if ((st != 0u && sf < 0x1p-100f) || (lo != 0.0f && fabsf(lo) < sf * 0x1p-11f)) inv = NAN;
+    }
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int v = 0; v < 4; ++v)                        // the lane of unit x, half v >> 1, element v & 1
+        for (int v = 0; v < 4; ++v) {                      // the lane of unit x, half v >> 1, element v & 1
             pk[x][v] = __shfl_sync(0xffffffffu, packed, 4 * (x + (v & 2) + 4 * (v & 1)) + c);
+            iv[x][v] = __shfl_sync(0xffffffffu, inv, 4 * (x + (v & 2) + 4 * (v & 1)) + c);
+        }
 }
 
-// Codes of one unit of 32 rows x 16 columns: r[m][i] = register i of operand m, pk as above.
+// Codes of one unit of 32 rows x 16 columns: r[m][i] = register i of operand m, pk, iv as above.
 // x_at(m, i, e) reads the value of register i's element e again (dynamic indexes stay out of
 // the registers).
+//
+// bf16 data meets half steps exactly in every few hundred values, so that a code has to come
+// right there without a detour: y = d RN(1/step) with d = x - lo, corrected by its residual,
+// y' = y + (d - y step) RN(1/step), is the quotient rounded once (2^-45 beside that), and
+// adding 1.5 2^23 rounds it to the nearest integer, ties to even.  y' is on the right side of
+// a half step, and on it only where the quotient is, if d is exact and the quotient never
+// nearer to a half step than 2^-20 without being on it.  That holds where x and lo are 0 or
+// at least 2^-11 step: both are then multiples of a power of two P > 2^-19 step, |d| < 2^23 P
+// is exact, and 2 d - (2 j + 1) step is 0 or at least 2^-19 step.  (Zeros take the detour
+// too, except for lo, which is often 0.)  What does not meet that, about one value in ten
+// thousand, goes to exact_code, as do groups of steps below 2^-100 and NaN.
 template <int BITS, class F>
-__device__ __forceinline__ void unit_codes(const uint32_t (&r)[2][4], const uint32_t (&pk)[4], uint32_t (&w)[2], F x_at)
+__device__ __forceinline__ void unit_codes(const uint32_t (&r)[2][4], const uint32_t (&pk)[4], const float (&iv)[4], uint32_t (&w)[2],
+                                           F x_at)
 {
     constexpr int qmax = (1 << BITS) - 1;
-    // y = (x - lo) / step, rounded to an integer inside an FMA with 1.5 2^23, whose low mantissa
-    // bits are then the code; rest = y - round(y).  With the reciprocal good to 2^-23 y is within
-    // 2^-17.9 of the quotient (at most 15.1), so that |rest| <= 1/2 - 2^-16 proves the code; else
-    // exact_code decides.  A step of 0 (a constant group) takes 0 for its reciprocal: code 0.
-    // One without a finite reciprocal gives NaN, and NaN goes to exact_code.
-    float2 nlo[2], inv[2];
+    // Codes are packed by multiply-adds of t's bits, kMagic + code: the multiples of kMagic that
+    // come with them are known, and taken off at the start (mod 2^32).
+    constexpr uint32_t kMagic = 0x4b400000u;
+    constexpr uint32_t kStart4 = 0u - kMagic * 0x11111111u, kStart2 = 0u - kMagic * 0x55555555u;
+    const float2 mg = make_float2(12582912.0f, 12582912.0f);
+    w[0] = w[1] = BITS == 4 ? kStart4 : kStart2;
+    float limit[4];                                        // least magnitude; NaN: none is enough
+    bool sure = true;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        nlo[h] = make_float2(-lo_f(pk[2 * h]), -lo_f(pk[2 * h + 1]));
-        const float s0 = hi_f(pk[2 * h]), s1 = hi_f(pk[2 * h + 1]);
-        inv[h] = make_float2(s0 == 0.0f ? 0.0f : rcp_fast(s0), s1 == 0.0f ? 0.0f : rcp_fast(s1));
-    }
-    const float2 mg = make_float2(12582912.0f, 12582912.0f), neg = make_float2(-1.0f, -1.0f);
-    float worst = 0.0f;
-    w[0] = w[1] = 0u;
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int h = i >> 1;
-            const float2 d = __fadd2_rn(make_float2(lo_f(r[m][i]), hi_f(r[m][i])), nlo[h]);
-            const float2 t = __ffma2_rn(d, inv[h], mg);
-            const float2 rest = __ffma2_rn(d, inv[h], __ffma2_rn(t, neg, mg));
-            worst = max3f_nan(worst, fabsf(rest.x), fabsf(rest.y));
-            const int wi = BITS == 4 ? m : 0, j = BITS == 4 ? i : 4 * m + i;
-            w[wi] = bfi32(__float_as_uint(t.x), w[wi], BITS * j, BITS);
-            w[wi] = bfi32(__float_as_uint(t.y), w[wi], 16 + BITS * j, BITS);
-        }
-    constexpr float kSure = 0.5f - 0x1p-16f;
-    if (!(worst <= kSure)) {
-        // which of the 16 are near a border (or not a number), then those alone
-        uint32_t todo = 0u;
+        const float2 nlo = make_float2(lo_f(pk[2 * h]), lo_f(pk[2 * h + 1]));
+        const float2 nst = make_float2(hi_f(pk[2 * h]), hi_f(pk[2 * h + 1]));
+        const float2 inv = make_float2(iv[2 * h], iv[2 * h + 1]);
+        limit[2 * h] = fmaf(nst.x, -0x1p-11f, inv.x * 0.0f);       // NaN where inv is
+        limit[2 * h + 1] = fmaf(nst.y, -0x1p-11f, inv.y * 0.0f);
+        const __nv_bfloat162 least = __hmin2_nan(__hmin2_nan(__habs2(as_bf162(r[0][2 * h])), __habs2(as_bf162(r[0][2 * h + 1]))),
+                                                 __hmin2_nan(__habs2(as_bf162(r[1][2 * h])), __habs2(as_bf162(r[1][2 * h + 1]))));
+        sure = sure && __low2float(least) >= limit[2 * h] && __high2float(least) >= limit[2 * h + 1];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int h = i >> 1;
-                const float2 d = __fadd2_rn(make_float2(lo_f(r[m][i]), hi_f(r[m][i])), nlo[h]);
-                const float2 t = __ffma2_rn(d, inv[h], mg);
-                const float2 rest = __ffma2_rn(d, inv[h], __ffma2_rn(t, neg, mg));
-                todo |= (fabsf(rest.x) <= kSure ? 0u : 1u) << (2 * (4 * m + i));
-                todo |= (fabsf(rest.y) <= kSure ? 0u : 1u) << (2 * (4 * m + i) + 1);
+            for (int k = 0; k < 2; ++k) {
+                const int i = 2 * h + k;
+                const float2 d = __fadd2_rn(make_float2(lo_f(r[m][i]), hi_f(r[m][i])), nlo);
+                const float2 y = __fmul2_rn(d, inv);
+                const float2 t = __fadd2_rn(__ffma2_rn(__ffma2_rn(y, nst, d), inv, y), mg);
+                const int wi = BITS == 4 ? m : 0, j = BITS == 4 ? i : 4 * m + i;
+                w[wi] += __float_as_uint(t.x) * (1u << (BITS * j));
+                w[wi] += __float_as_uint(t.y) * (1u << (16 + BITS * j));
             }
+    }
+    if (!sure) {
+        uint32_t todo = 0u;
+        bool odd = false;                                  // NaN or infinite values: their bits went over others'
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float x = fabsf(e ? hi_f(r[m][i]) : lo_f(r[m][i])), lim = limit[2 * (i >> 1) + e];
+                    todo |= (x >= lim ? 0u : 1u) << (2 * (4 * m + i) + e);
+                    odd = odd || lim != lim || !(x < 0x1p126f);
+                }
+        if (odd) {
+            todo = 0xffffu;
+            w[0] = w[1] = 0u;
+        }
         while (todo) {
             const int k = __ffs(todo) - 1, e = k & 1, i = (k >> 1) & 3, m = k >> 3, h = i >> 1;
             todo &= todo - 1u;
             const uint32_t p = h ? (e ? pk[3] : pk[2]) : (e ? pk[1] : pk[0]);
-            const uint32_t code = exact_code(x_at(m, i, e), lo_f(p), hi_f(p), qmax);
+            const uint32_t code = exact_code(x_at(m, i, e), -lo_f(p), -hi_f(p), qmax);
             const int at = BITS * (BITS == 4 ? i : 4 * m + i) + 16 * e;
             const uint32_t keep = ~((uint32_t)qmax << at);
             if (BITS == 4 && m) w[1] = (w[1] & keep) | (code << at);
@@ -225,17 +253,22 @@ __device__ __forceinline__ void unit_codes(const uint32_t (&r)[2][4], const uint
     }
 }
 
-// 16-byte chunk ch of row r in a warp's row buffer (swizzled: ldmatrix reads 8 rows of one
-// chunk at a time)
+// 16-byte chunk ch of row r in a warp's row buffer (swizzled: ldmatrix and stmatrix touch 8
+// rows of one chunk at a time)
 template <int D> __device__ __forceinline__ int row_chunk(int r, int ch) { return r * (D / 8) + (ch ^ (r & 7)); }
+// The same in the buffer of the write: tiles of 32 rows x 64 channels, as TMA swizzles rows of
+// 128 bytes.
+__device__ __forceinline__ int tile_chunk(int r, int ch) { return (ch >> 3) * 256 + r * 8 + ((ch & 7) ^ (r & 7)); }
 
 template <int D, int BITS, typename TIN>
 __global__ void __launch_bounds__(32 * kWriteWarps)
-k_dense_write(const TIN *__restrict__ kv, int n, int S, int N, int T, int nb, int n_items,
+k_dense_write(const __grid_constant__ CUtensorMap map, int mapped, const TIN *__restrict__ kv, int n, int S, int N, int T, int nb, int n_items,
               const int32_t *__restrict__ pos, const int32_t *__restrict__ n_new, uint8_t *__restrict__ codes,
               uint8_t *__restrict__ khdr, __nv_bfloat16 *tail, int32_t *status)
 {
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (um::smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ uint64_t bars[kWriteWarps];
     constexpr int kUnits = D / 16, kChunks = D / 8;        // 16-byte chunks of a row
     constexpr size_t kUnit = (size_t)4 * D * BITS, kRec = 2 * kUnit + 4 * D;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -274,62 +307,84 @@ k_dense_write(const TIN *__restrict__ kv, int n, int S, int N, int T, int nb, in
 
     if (b < b_end) {
         const int t0 = b * kBlk;
-#pragma unroll 4
-        for (int i = lane; i < kBlk * kChunks; i += 32) {
-            const int r = i / kChunks, ch = i % kChunks;
-            uint4 *dst = buf + row_chunk<D>(r, ch);
-            if (t0 + r < p0) {                             // an earlier row of this block
-                cp_async16(dst, (const uint4 *)(trow + (size_t)r * D) + ch);
-            } else if constexpr (sizeof(TIN) == 2) {
-                cp_async16(dst, (const uint4 *)(src + (size_t)(t0 + r - p0) * row) + ch);
-            } else {
-                *dst = chunk_of(t0 + r - p0, ch);
+        if (mapped && t0 >= p0) {
+            // all rows are new: a tile copy for each 64 channels
+            if (lane == 0) {
+                um::mbar_init(bars + warp, 1);
+                um::fence_mbar_init();
+                um::mbar_arrive_expect_tx(bars + warp, kBlk * D * 2);
+#pragma unroll
+                for (int k = 0; k < D / 64; ++k)
+                    um::tma_load_3d((uint8_t *)buf + k * 4096, &map, bars + warp, (is_v * N + h) * D + 64 * k, t0 - p0, s);
             }
+            __syncwarp();
+            if (!__all_sync(0xffffffffu, um::mbar_wait(bars + warp, 0, kWaitCycles))) {
+                set_status(status, RKV_ERR_DEVICE_TIMEOUT);
+                return;
+            }
+        } else {
+#pragma unroll 4
+            for (int i = lane; i < kBlk * kChunks; i += 32) {
+                const int r = i / kChunks, ch = i % kChunks;
+                uint4 *dst = buf + tile_chunk(r, ch);
+                if (t0 + r < p0) {                         // an earlier row of this block
+                    cp_async16(dst, (const uint4 *)(trow + (size_t)r * D) + ch);
+                } else if constexpr (sizeof(TIN) == 2) {
+                    cp_async16(dst, (const uint4 *)(src + (size_t)(t0 + r - p0) * row) + ch);
+                } else {
+                    *dst = chunk_of(t0 + r - p0, ch);
+                }
+            }
+            cp_async_wait();
+            __syncwarp();
         }
-        cp_async_wait();
-        __syncwarp();
 
         const size_t rec = ((size_t)s * N + h) * nb + b;
         uint8_t *out = codes + rec * kRec + (is_v ? kUnit : 0);
         uint8_t *hout = is_v ? codes + rec * kRec + 2 * kUnit : khdr + rec * (4 * D);
         const int g = lane >> 2, c = lane & 3;
         const int slot = is_v ? value_slot(g, c) : key_slot(g, c);
-        const uint32_t base = um::smem_u32(buf);
         constexpr int kPer = 8 / BITS;                     // units of a chunk
+        // ldmatrix: lane's place for unit 0, operand 0; units and operands flip chunk bits or go
+        // on by whole rows or tiles
+        const int i8 = lane >> 3;
+        const uint32_t base = um::smem_u32(buf) + 16 * (is_v ? tile_chunk(8 * (i8 >> 1) + (lane & 7), i8 & 1)
+                                                             : tile_chunk(8 * (i8 & 1) + (lane & 7), i8 >> 1));
 #pragma unroll 1
         for (int u0 = 0; u0 < kUnits; u0 += kPer) {
             uint32_t words[4];
 #pragma unroll
             for (int k = 0; k < kPer; k += 2) {
                 uint32_t r[2][2][4], pk[2][4];
+                float iv[2][4];
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        const int u = u0 + k + x, i = lane >> 3;
+                        const int u = u0 + k + x;
                         if (is_v)
-                            ldmatrix4_trans(r[x][m], base + 16 * row_chunk<D>(16 * (u & 1) + 8 * (i >> 1) + (lane & 7),
-                                                                             4 * (u >> 1) + 2 * m + (i & 1)));
+                            ldmatrix4_trans(r[x][m], (base ^ ((((u >> 1) & 1) << 6) | (m << 5))) + (u >> 2) * 4096 + (u & 1) * 2048);
                         else
-                            ldmatrix4(r[x][m], base + 16 * row_chunk<D>(16 * m + 8 * (i & 1) + (lane & 7), 2 * u + (i >> 1)));
+                            ldmatrix4(r[x][m], (base ^ ((u & 3) << 5)) + (u >> 2) * 4096 + m * 2048);
                     }
-                unit_headers(r, lane, (float)((1 << BITS) - 1), pk);
+                unit_headers(r, lane, (float)((1 << BITS) - 1), pk, iv);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int u = u0 + k + x;
                     uint32_t w[2];
-                    unit_codes<BITS>(r[x], pk[x], w, [&](int m, int i, int e) -> float {
+                    unit_codes<BITS>(r[x], pk[x], iv[x], w, [&](int m, int i, int e) -> float {
                         const int mr = 16 * m + 8 * (i & 1) + g, kc = 8 * (i >> 1) + 2 * c + e;
                         const int token = is_v ? 16 * (u & 1) + kc : mr;
                         const int ch = is_v ? 32 * (u >> 1) + mr : 16 * u + kc;
-                        const uint16_t v = *((const uint16_t *)(buf + row_chunk<D>(token, ch >> 3)) + (ch & 7));
+                        const uint16_t v = *((const uint16_t *)(buf + tile_chunk(token, ch >> 3)) + (ch & 7));
                         return __uint_as_float((uint32_t)v << 16);
                     });
                     if (BITS == 4) { words[2 * (k + x)] = w[0]; words[2 * (k + x) + 1] = w[1]; }
                     else words[k + x] = w[0];
                     // lane 4 x + c of the unit's header
                     if (g == x) {
-                        const uint32_t p0 = pk[x][0], p1 = pk[x][1], p2 = pk[x][2], p3 = pk[x][3];
+                        const uint32_t flip = 0x80008000u;
+                        const uint32_t p0 = pk[x][0] ^ flip, p1 = pk[x][1] ^ flip, p2 = pk[x][2] ^ flip, p3 = pk[x][3] ^ flip;
                         *(uint4 *)(hout + (size_t)(u * 4 + c) * 16) =
                             make_uint4((p0 & 0xffffu) | (p1 << 16), (p0 >> 16) | (p1 & 0xffff0000u),
                                        (p2 & 0xffffu) | (p3 << 16), (p2 >> 16) | (p3 & 0xffff0000u));
@@ -571,7 +626,10 @@ cudaError_t run_write(const DenseGeom &g, const void *kv, int n, const int32_t *
     // blocks that n rows can finish from any start in a block; at least the tail's own item
     const int items = max(1, (n + kBlk - 1) / kBlk);
     const long long warps = (long long)g.S * items * 2 * g.N;
-    constexpr int kSmem = kWriteWarps * kBlk * D * 2;
+    constexpr int kSmem = kWriteWarps * kBlk * D * 2 + 1024;
+    // whole new blocks of bf16 rows come by TMA
+    CUtensorMap map = {};
+    const int mapped = sizeof(TIN) == 2 && n >= kBlk && make_map(&map, kv, (uint64_t)2 * g.N * D, n, g.S, kBlk);
     static PerDevice<int> setup;
     int unused = 0;
     cudaError_t e = per_device(setup, unused, [](int &) {
@@ -580,7 +638,7 @@ cudaError_t run_write(const DenseGeom &g, const void *kv, int n, const int32_t *
     if (e != cudaSuccess) return e;
     ProfScope prof("dense_write", s);
     k_dense_write<D, BITS, TIN><<<(unsigned)((warps + kWriteWarps - 1) / kWriteWarps), 32 * kWriteWarps, kSmem, s>>>(
-        (const TIN *)kv, n, g.S, g.N, g.T, g.nb, items, pos, n_new, (uint8_t *)c->codes, (uint8_t *)c->khdr,
+        map, mapped, (const TIN *)kv, n, g.S, g.N, g.T, g.nb, items, pos, n_new, (uint8_t *)c->codes, (uint8_t *)c->khdr,
         (__nv_bfloat16 *)c->tail, status);
     return cudaGetLastError();
 }

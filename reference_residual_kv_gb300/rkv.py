@@ -482,6 +482,8 @@ class DenseCache:
         self.device = self.status.device
         self.cache = rkv_dense_cache(_ptr(self.codes), _ptr(self.khdr), _ptr(self.tail))
         self._sizes = {}
+        self._p_ref, self._cache_ref = ctypes.byref(self.p), ctypes.byref(self.cache)
+        self._status_ptr = self.status.data_ptr()
 
     def _refuse(self, name, t, dtypes, shape):
         """Says what is wrong with an argument, if anything is."""
@@ -498,26 +500,36 @@ class DenseCache:
         if not (t.dtype in dtypes and t.shape == shape and t.device == self.device and t.is_contiguous()):
             self._refuse(name, t, dtypes, shape)
 
-    def _run(self, stream, need, call):
-        """call(workspace, bytes, stream) with the cache's device current, and scratch of `need`
-        bytes from the pool of the stream that the call runs on."""
+    def _call(self, name, stream, need, *args):
+        """The entry point `name` with (params, *args, [workspace, bytes,] status, stream): the
+        cache's device current, scratch of `need` bytes (None: it takes none) from the pool of the
+        stream that the call runs on."""
         dev = self.device.index
         if stream is None and torch.cuda.current_device() == dev:
-            return call(self._scratch(need), need, _raw_stream(dev))
-        with torch.cuda.device(dev):
-            if stream is None:
-                return call(self._scratch(need), need, _raw_stream(dev))
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=self.device)
-            with torch.cuda.stream(stream):
-                return call(self._scratch(need), need, stream.cuda_stream)
+            st = self._enter(name, need, args, _raw_stream(dev))
+        else:
+            with torch.cuda.device(dev):
+                if stream is None:
+                    st = self._enter(name, need, args, _raw_stream(dev))
+                else:
+                    if isinstance(stream, int):
+                        stream = torch.cuda.ExternalStream(stream, device=self.device)
+                    with torch.cuda.stream(stream):
+                        st = self._enter(name, need, args, stream.cuda_stream)
+        if st:
+            raise RkvError(st, name)
+
+    def _enter(self, name, need, args, stream):
+        f = getattr(lib(), name)
+        if need is None:
+            return f(self._p_ref, *args, self._status_ptr, stream)
+        ws = self._scratch(need)
+        return f(self._p_ref, *args, ws.data_ptr(), need, self._status_ptr, stream)
 
     def _scratch(self, need):
-        if need == 0:
-            return None
         if not self.guard:
-            return torch.empty(need, dtype=torch.uint8, device=self.device)
-        t, raw = guarded_empty((need,), torch.uint8, self.device, self.guard)
+            return torch.empty(max(need, 1), dtype=torch.uint8, device=self.device)
+        t, raw = guarded_empty((max(need, 1),), torch.uint8, self.device, self.guard)
         self._raw["scratch %d" % len(self._raw)] = (t, raw)
         return t
 
@@ -538,8 +550,8 @@ class DenseCache:
         if n_new is not None:
             self._check("n_new", n_new, (_I32,), (self.S,))
         dt = RKV_F32 if kv.dtype is _F32 else RKV_BF16
-        self._run(stream, 0, lambda ws, nb, st: rkv_dense_write(
-            self.p, kv, dt, n, pos, n_new, self.cache, self.status, st))
+        self._call("rkv_dense_write", stream, None, kv.data_ptr(), dt, n, pos.data_ptr(),
+                   None if n_new is None else n_new.data_ptr(), self._cache_ref)
 
     def read(self, length, sel, out_k, out_v, stream=None):
         """K and V of tokens sel [S][n_sel] (-1: zero rows) to out_k, out_v bf16 [S][n_sel][ND]."""
@@ -549,8 +561,8 @@ class DenseCache:
         self._check("sel", sel, (_I32,), (self.S, n))
         self._check("out_k", out_k, (_BF16,), rows)
         self._check("out_v", out_v, (_BF16,), rows)
-        self._run(stream, 0, lambda ws, nb, st: rkv_dense_read(
-            self.p, self.cache, length, sel, n, out_k, out_v, self.status, st))
+        self._call("rkv_dense_read", stream, None, self._cache_ref, length.data_ptr(), sel.data_ptr(), n,
+                   out_k.data_ptr(), out_v.data_ptr())
 
     def select(self, H: int, q, length, blocks, keep_first: int = 0, keep_last: int = 0, stream=None):
         """The blocks [S][N or 1][n_blocks] (output) with the largest score bounds for q [S][H][D]."""
@@ -558,8 +570,8 @@ class DenseCache:
         self._check("q", q, (_BF16,), (self.S, H, self.D))
         self._check("length", length, (_I32,), (self.S,))
         self._check("blocks", blocks, (_I32,), (self.S, lists, n))
-        self._run(stream, self._size("select", lists), lambda ws, nb, st: rkv_block_select(
-            self.p, H, q, self.cache, length, lists, n, keep_first, keep_last, blocks, ws, nb, self.status, st))
+        self._call("rkv_block_select", stream, self._size("select", lists), H, q.data_ptr(), self._cache_ref,
+                   length.data_ptr(), lists, n, keep_first, keep_last, blocks.data_ptr())
 
     def attend(self, H: int, q, length, out, blocks=None, stream=None):
         """out [S][H][D] (fp32 or bf16): attention of q [S][H][D] over the cache, or over the
@@ -567,15 +579,16 @@ class DenseCache:
         self._check("q", q, (_BF16,), (self.S, H, self.D))
         self._check("length", length, (_I32,), (self.S,))
         self._check("out", out, (_F32, _BF16), (self.S, H, self.D))
-        lists, n = 1, 0
+        lists, n, listed = 1, 0, None
         if blocks is not None:
             lists, n = blocks.shape[1:] if blocks.dim() == 3 else (-1, -1)
             self._check("blocks", blocks, (_I32,), (self.S, lists, n))
             if n < 1:
                 raise ValueError("blocks: an empty list")
+            listed = blocks.data_ptr()
         dt = RKV_F32 if out.dtype is _F32 else RKV_BF16
-        self._run(stream, self._size("attend", H, 1), lambda ws, nb, st: rkv_dense_attention(
-            self.p, H, q, self.cache, length, blocks, lists, n, out, dt, ws, nb, self.status, st))
+        self._call("rkv_dense_attention", stream, self._size("attend", H, 1), H, q.data_ptr(), self._cache_ref,
+                   length.data_ptr(), listed, lists, n, out.data_ptr(), dt)
 
     def tree_attend(self, H: int, q, parent, draft_kv, length, out, stream=None):
         """out [S][n][H][D] (fp32 or bf16): attention of the drafted tokens' q [S][n][H][D] over
@@ -587,8 +600,8 @@ class DenseCache:
         self._check("length", length, (_I32,), (self.S,))
         self._check("out", out, (_F32, _BF16), (self.S, n, H, self.D))
         dt = RKV_F32 if out.dtype is _F32 else RKV_BF16
-        self._run(stream, self._size("attend", H, n), lambda ws, nb, st: rkv_tree_attention(
-            self.p, H, q, n, parent, draft_kv, self.cache, length, out, dt, ws, nb, self.status, st))
+        self._call("rkv_tree_attention", stream, self._size("attend", H, n), H, q.data_ptr(), n, parent.data_ptr(),
+                   draft_kv.data_ptr(), self._cache_ref, length.data_ptr(), out.data_ptr(), dt)
 
     def device_status(self) -> int:
         return int(self.status[0].item())

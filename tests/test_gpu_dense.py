@@ -23,6 +23,9 @@ def make_rows(rng, S, T, N, D, kind="normal"):
         x[:, :, 0] += rng.normal(size=(1, 1, N, D)) * np.where(rng.random((1, 1, N, D)) < 0.05, 6.0, 0.7)
     elif kind == "ties":            # small whole numbers: many exact half steps
         x = rng.integers(-15, 16, size=x.shape).astype(np.float64)
+    elif kind == "grid":            # offsets, tiny values among large ones, zeros, coarse grids
+        x = np.choose(rng.integers(0, 4, size=x.shape), [rng.integers(-200, 200, size=x.shape) / 8.0, x, x * 2.0 ** -10, 0.0])
+        x = x + np.where(rng.random((S, 1, 2, N, D)) < 0.3, 100.0, 0.0)
     elif kind == "wide":            # exponents far apart: differences that fp32 rounds
         x = x * 2.0 ** rng.integers(-40, 41, size=x.shape)
     return do.bf16(x)
@@ -87,7 +90,7 @@ class Case:
 
 
 # ------------------------------------------------------------------ write and read
-@pytest.mark.parametrize("kind", ["normal", "ties", "wide"])
+@pytest.mark.parametrize("kind", ["normal", "ties", "wide", "grid"])
 @pytest.mark.parametrize("bits", [2, 4])
 @pytest.mark.parametrize("N,D", [(1, 64), (3, 128), (2, 256)])
 def test_written_rows_read_back_as_defined(N, D, bits, kind):
