@@ -57,8 +57,11 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                      um::smem_u32(dst)), "l"(src), "r"(bytes), "r"(um::smem_u32(bar)) : "memory");
 }
 
-template <int D, int BITS, int NT>
+// NT = 0: up to 4 query rows, in columns 0..3 and again in 4..7, so that one product takes the
+// probabilities' first parts (columns 0..3) and second parts (4..7).
+template <int D, int BITS, int NT0>
 struct SplitCfg {
+    static constexpr int NT = NT0 ? NT0 : 1;
     static constexpr int kUnit = 4 * D * BITS, kRec = 2 * kUnit + 4 * D, kHdr = 4 * D;
     static constexpr int kStage = kRec + kHdr;
     // ring depth: about 80 KB in flight per CTA, two CTAs to an SM where registers allow
@@ -83,14 +86,16 @@ __device__ __forceinline__ int block_at(const int32_t *list, int i, int have, in
 }
 
 // Partials: sums [run][N][R][D] and {max, sum} [run][N][R] (max in base 2).
-template <int D, int BITS, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 && D <= 128 ? 2 : 1)
+template <int D, int BITS, int NT0>
+__global__ void __launch_bounds__(32 * kWarps, NT0 <= 1 && D <= 128 ? 2 : 1)
 k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ codes,
               const uint8_t *__restrict__ khdr, const int32_t *__restrict__ len, const int32_t *__restrict__ blocks,
               int lists, int n_blocks, int S, int T, int N, int G, int nq, int nb, DenseCut cut, int tiles,
               float scale_log2, float *__restrict__ part, float2 *__restrict__ ml, int32_t *status)
 {
-    using C = SplitCfg<D, BITS, NT>;
+    using C = SplitCfg<D, BITS, NT0>;
+    constexpr int NT = C::NT;
+    constexpr bool kTwice = NT0 == 0;
     constexpr int kUnits = D / 16, kPer = 8 / BITS;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 sml[kWarps][8 * NT];
@@ -147,7 +152,7 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
         return (const uint32_t *)(q + (((size_t)s * nq + r / G) * N * G + n * G + r % G) * D);
     };
     if constexpr (NT == 1) {
-        const int r = row0 + g;
+        const int r = row0 + (kTwice ? g & 3 : g);
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             qr[u][0] = r < R ? __ldg(q_row(r) + u * 8 + c) : 0u;
@@ -260,8 +265,12 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
                     l_run[nt][1] += p1;
                     const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
                     const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - __low2float(hi), p1 - __high2float(hi));
-                    ph[nt][m][h] = trans8x8(as_u32(hi));
-                    pl[nt][m][h] = trans8x8(as_u32(lo));
+                    if (kTwice) {
+                        ph[nt][m][h] = trans8x8(as_u32(c < 2 ? hi : lo));
+                    } else {
+                        ph[nt][m][h] = trans8x8(as_u32(hi));
+                        pl[nt][m][h] = trans8x8(as_u32(lo));
+                    }
                 }
         }
         // out^T: D channels x 8 NT rows
@@ -283,7 +292,7 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         mma16816(acc[nt][(u & ~1) + m], a, ph[nt][ks][0], ph[nt][ks][1]);
-                        mma16816(acc[nt][(u & ~1) + m], a, pl[nt][ks][0], pl[nt][ks][1]);
+                        if (!kTwice) mma16816(acc[nt][(u & ~1) + m], a, pl[nt][ks][0], pl[nt][ks][1]);
                     }
                 }
             }
@@ -303,6 +312,12 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
             if (g == 0)
                 sml[warp][8 * nt + 2 * c + e] = make_float2(ok ? m_run[nt][e] : __uint_as_float(0x7fffffffu), l_run[nt][e]);
         }
+    if (kTwice) {                                          // both parts of a row's outputs
+#pragma unroll
+        for (int i = 0; i < 2 * (D / 32); ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[0][i][e] += __shfl_xor_sync(0xffffffffu, acc[0][i][e], 2);
+    }
     __syncthreads();                                       // every warp is done with its ring
     float *rows = (float *)smem + (size_t)warp * 8 * NT * C::kRow;
 #pragma unroll
@@ -344,22 +359,21 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
 }
 
 // The last pass: 8 / wpr query rows of a KV head per CTA, wpr warps for each.  Tokens that are
-// not in finished blocks come in groups of 32 through shared memory: the unfinished block's
-// rows, then drafted tokens 0..31, 32..63.  A group's scores for all rows are one product
-// (two warps, 16 tokens each); every row then takes its own, and adds p v for the tokens that
-// it sees alone.  The warps of a row deal tokens and partials among them.
+// not in finished blocks lie in shared memory in groups of 32: the unfinished block's rows,
+// then drafted tokens 0..31, 32..63.  A group's scores for all rows are one product (two
+// warps, 16 tokens each); every row then takes its own, and adds p v for the tokens that it
+// sees alone.  The warps of a row deal tokens and partials among them.
 template <int D>
 __global__ void __launch_bounds__(32 * kFinWarps)
 k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ tail,
                const int32_t *__restrict__ len, const int32_t *__restrict__ parent,
                const __nv_bfloat16 *__restrict__ draft, int S, int T, int N, int G, int nq, DenseCut cut, int listed,
-               int each, int wpr, int row_ctas, float scale_log2, const float *__restrict__ part,
+               int each_log, int wpr, int row_ctas, float scale_log2, const float *__restrict__ part,
                const float2 *__restrict__ ml, void *__restrict__ out, int out_bf16, int32_t *status)
 {
     constexpr int kCh = D / 8, kPad = kCh + 1, kE = D / 32;   // 16-byte chunks of a row; channels of a lane
     extern __shared__ __align__(128) uint8_t smem[];
-    uint4 *ks = (uint4 *)smem, *vs = ks + kBlk * kPad;
-    __shared__ float sc[8][kBlk + 1];
+    __shared__ float sc[8][3 * kBlk + 1];
     __shared__ __align__(16) float part_s[kFinWarps][D + 4];
     __shared__ float2 ml_s[kFinWarps];
     __shared__ int par[kMaxDraft];
@@ -373,10 +387,25 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
     const int j = live ? r / G : 0;
     auto row_of = [&](int x) { return (((size_t)s * nq + x / G) * N + n) * G + x % G; };
     const int groups = parent ? 1 + (nq + kBlk - 1) / kBlk : 1;
-    if (parent) {
-        for (int i = threadIdx.x; i < nq; i += blockDim.x) par[i] = __ldg(parent + (size_t)s * nq + i);
-        __syncthreads();
+    uint4 *ks = (uint4 *)smem, *vs = ks + groups * kBlk * kPad;
+    if (parent && threadIdx.x < nq) par[threadIdx.x] = __ldg(parent + (size_t)s * nq + threadIdx.x);
+    // all tokens of all groups, a row to kCh threads
+    for (int i = threadIdx.x; i < groups * kBlk * kCh; i += 32 * kFinWarps) {
+        const int t = i / kCh, ch = i % kCh;
+        const uint4 *kr, *vr;
+        if (t < kBlk) {
+            if (t >= rest) continue;
+            kr = (const uint4 *)(tail + ((size_t)sn * 2 * kBlk + t) * D);
+            vr = kr + kBlk * kCh;
+        } else {
+            if (t - kBlk >= nq) continue;
+            kr = (const uint4 *)(draft + (((size_t)s * nq + t - kBlk) * 2 * N + n) * D);
+            vr = kr + N * kCh;
+        }
+        ks[t * kPad + ch] = __ldg(kr + ch);
+        vs[t * kPad + ch] = __ldg(vr + ch);
     }
+    __syncthreads();
     // the drafted tokens that the row sees; parents come before their children, so that the
     // way up ends
     uint64_t sees = 0;
@@ -402,59 +431,38 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
         const DenseRun x = dense_runs_of(len, S, T, listed, cut, s, status);
         if (lane == 0) runs_s = x;
     }
-    // warps 0 and 1: the rows as the second operand (columns behind the last row are zero)
-    uint32_t qr[D / 16][2];
-    if (warp < 2 && (rest || parent)) {
+    if (warp < 2 * groups && (warp >= 2 || rest)) {
+        // tokens 16 warp ..: rows of the first operand (those that are not there give scores
+        // that no row takes); the query rows are the second one's columns (zero behind the last)
         const int g = lane >> 2, c = lane & 3;
         const bool there = g < rpc && r0 + g < R;
         const uint32_t *src = (const uint32_t *)(q + row_of(there ? r0 + g : 0) * D);
+        uint32_t qr[D / 16][2];
 #pragma unroll
         for (int u = 0; u < D / 16; ++u) {
             qr[u][0] = there ? __ldg(src + u * 8 + c) : 0u;
             qr[u][1] = there ? __ldg(src + u * 8 + 4 + c) : 0u;
         }
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint32_t at = um::smem_u32(ks + (16 * warp + 8 * ((lane >> 3) & 1) + (lane & 7)) * kPad + (lane >> 4));
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u) {
+            uint32_t a[4];
+            ldmatrix4(a, at + u * 32);
+            mma16816(d, a, qr[u][0], qr[u][1]);
+        }
+        sc[2 * c][16 * warp + g] = d[0];
+        sc[2 * c + 1][16 * warp + g] = d[1];
+        sc[2 * c][16 * warp + g + 8] = d[2];
+        sc[2 * c + 1][16 * warp + g + 8] = d[3];
     }
+    __syncthreads();
 
     float m = -INFINITY, l = 0.0f, acc[kE];
 #pragma unroll
     for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
 #pragma unroll 1
     for (int grp = 0; grp < groups; ++grp) {
-        const int cnt = grp == 0 ? rest : min(kBlk, nq - (grp - 1) * kBlk);
-        if (cnt == 0) continue;
-        if (grp) __syncthreads();
-        for (int i = threadIdx.x; i < cnt * kCh; i += blockDim.x) {
-            const int t = i / kCh, ch = i % kCh;
-            const uint4 *kr, *vr;
-            if (grp == 0) {
-                kr = (const uint4 *)(tail + ((size_t)sn * 2 * kBlk + t) * D);
-                vr = kr + kBlk * kCh;
-            } else {
-                kr = (const uint4 *)(draft + (((size_t)s * nq + (grp - 1) * kBlk + t) * 2 * N + n) * D);
-                vr = kr + N * kCh;
-            }
-            ks[t * kPad + ch] = kr[ch];
-            vs[t * kPad + ch] = vr[ch];
-        }
-        __syncthreads();
-        if (warp < 2) {
-            // tokens 16 warp ..: rows of the first operand (those behind cnt give scores that
-            // no row takes)
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            const uint32_t at = um::smem_u32(ks + (16 * warp + 8 * ((lane >> 3) & 1) + (lane & 7)) * kPad + (lane >> 4));
-#pragma unroll
-            for (int u = 0; u < D / 16; ++u) {
-                uint32_t a[4];
-                ldmatrix4(a, at + u * 32);
-                mma16816(d, a, qr[u][0], qr[u][1]);
-            }
-            const int g = lane >> 2, c = lane & 3;
-            sc[2 * c][16 * warp + g] = d[0];
-            sc[2 * c + 1][16 * warp + g] = d[1];
-            sc[2 * c][16 * warp + g + 8] = d[2];
-            sc[2 * c + 1][16 * warp + g + 8] = d[3];
-        }
-        __syncthreads();
         uint32_t mask = 0u;
         if (!padding)
             mask = grp == 0 ? (1u << rest) - 1u : (uint32_t)(sees >> ((grp - 1) * kBlk));
@@ -463,7 +471,7 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
         else if (wpr == 4) mask &= 0x11111111u << turn;
         else if (wpr == 8) mask &= 0x01010101u << turn;
         if (mask == 0u) continue;                          // the same for the whole warp
-        const float x = ((mask >> lane) & 1u) ? sc[slot][lane] * scale_log2 : -INFINITY;
+        const float x = ((mask >> lane) & 1u) ? sc[slot][grp * kBlk + lane] * scale_log2 : -INFINITY;
         float mx = x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -481,7 +489,7 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
             const int t = __ffs(mask) - 1;
             mask &= mask - 1u;
             const float pt = __shfl_sync(0xffffffffu, p, t);
-            const uint32_t *v = (const uint32_t *)(vs + t * kPad) + lane * (kE / 2);
+            const uint32_t *v = (const uint32_t *)(vs + (grp * kBlk + t) * kPad) + lane * (kE / 2);
 #pragma unroll
             for (int e = 0; e < kE / 2; ++e) {
                 acc[2 * e] = fmaf(pt, __uint_as_float(v[e] << 16), acc[2 * e]);
@@ -493,14 +501,15 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
     // the finished blocks' partials: launched as a programmatic dependent, this waits for them
     asm volatile("griddepcontrol.wait;" ::: "memory");
     bool bad = false;
-    __syncthreads();
     const DenseRun runs = runs_s;
     if (!padding) {
-        // `each` partials for every run and KV head, this warp's every wpr-th; 32 at a time:
+        // 1 << each_log partials for every run and KV head, this warp's every wpr-th; 32 at a time:
         // their weights, a lane each, then their sums, those with nothing in them left out
-        const int parts = (runs.end - runs.first) * each;
+        const int parts = (runs.end - runs.first) << each_log;
+        const size_t first = (((size_t)runs.first * N + n) << each_log) * R + r;
+        const size_t next_run = ((size_t)N << each_log) * R;
         auto part_at = [&](int i) {
-            return ((size_t)(runs.first + i / each) * N * each + (size_t)n * each + i % each) * R + r;
+            return first + (size_t)(i >> each_log) * next_run + (each_log ? (size_t)(i & 1) * R : 0);
         };
         for (int i0 = turn; i0 < parts; i0 += 32 * wpr) {
             const int mine = i0 + lane * wpr;
@@ -601,10 +610,10 @@ Plan plan_of(const DenseGeom &g, int H, int nq)
         p.cut.unit = 8;
         p.cut.least = 16;
     } else {
-        p.nt = R <= 8 ? 1 : (R <= 16 || g.D == 256 ? 2 : 4);
+        p.nt = R <= 4 ? 0 : (R <= 8 ? 1 : (R <= 16 || g.D == 256 ? 2 : 4));
         p.each = 1;
-        p.tiles = (R + 8 * p.nt - 1) / (8 * p.nt);
-        ctas = 608;
+        p.tiles = p.nt ? (R + 8 * p.nt - 1) / (8 * p.nt) : 1;
+        ctas = 304;
         p.cut.unit = kWarps;
         p.cut.least = kWarps;
     }
@@ -613,20 +622,20 @@ Plan plan_of(const DenseGeom &g, int H, int nq)
     return p;
 }
 
-template <int D, int BITS, int NT>
+template <int D, int BITS, int NT0>
 cudaError_t run_split(const DenseGeom &g, const Plan &p, int H, const void *q, int nq, const rkv_dense_cache *c,
                       const int32_t *len, const int32_t *blocks, int lists, int n_blocks, float scale_log2,
                       float *part, float2 *ml, int32_t *status, cudaStream_t s)
 {
-    using C = SplitCfg<D, BITS, NT>;
+    using C = SplitCfg<D, BITS, NT0>;
     static PerDevice<int> setup;
     int unused = 0;
     cudaError_t e = per_device(setup, unused, [](int &) {
-        return cudaFuncSetAttribute(k_dense_split<D, BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        return cudaFuncSetAttribute(k_dense_split<D, BITS, NT0>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (e != cudaSuccess) return e;
     ProfScope prof("dense_attention_split", s);
-    k_dense_split<D, BITS, NT><<<(unsigned)((size_t)p.runs * g.N * p.tiles), 32 * kWarps, C::kSmem, s>>>(
+    k_dense_split<D, BITS, NT0><<<(unsigned)((size_t)p.runs * g.N * p.tiles), 32 * kWarps, C::kSmem, s>>>(
         (const __nv_bfloat16 *)q, (const uint8_t *)c->codes, (const uint8_t *)c->khdr, len, blocks, lists, n_blocks,
         g.S, g.T, g.N, H / g.N, nq, g.nb, p.cut, p.tiles, scale_log2, part, ml, status);
     return cudaGetLastError();
@@ -640,8 +649,14 @@ cudaError_t run_finish(const DenseGeom &g, const Plan &p, int H, const void *q, 
     const int R = nq * (H / g.N);
     const int wpr = R <= 1 ? 8 : (R <= 2 ? 4 : (R <= 4 ? 2 : 1)), rpc = kFinWarps / wpr;
     const int row_ctas = (R + rpc - 1) / rpc;
-    constexpr int kSmem = 2 * kBlk * (D / 8 + 1) * 16;
-    static_assert(kSmem + kFinWarps * (D + 4) * 4 + 2048 <= 48 * 1024, "shared memory of the last pass");
+    constexpr int kGroup = 2 * kBlk * (D / 8 + 1) * 16;    // K and V rows of 32 tokens
+    static_assert(3 * kGroup + kFinWarps * (D + 4) * 4 + 8192 <= 227 * 1024, "shared memory of the last pass");
+    static PerDevice<int> setup;
+    int unused = 0;
+    cudaError_t e = per_device(setup, unused, [](int &) {
+        return cudaFuncSetAttribute(k_dense_finish<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * kGroup);
+    });
+    if (e != cudaSuccess) return e;
     ProfScope prof("dense_attention_finish", s);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
@@ -649,13 +664,13 @@ cudaError_t run_finish(const DenseGeom &g, const Plan &p, int H, const void *q, 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)((size_t)g.S * g.N * row_ctas), 1, 1);
     cfg.blockDim = dim3(32 * kFinWarps, 1, 1);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = (parent ? 1 + (nq + kBlk - 1) / kBlk : 1) * kGroup;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k_dense_finish<D>, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)c->tail,
+    e = cudaLaunchKernelEx(&cfg, k_dense_finish<D>, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)c->tail,
                                        len, parent, (const __nv_bfloat16 *)draft, g.S, g.T, g.N, H / g.N, nq, p.cut, listed,
-                                       p.each, wpr, row_ctas, scale_log2, part, ml, out, (int)(out_dtype == RKV_BF16), status);
+                                       p.each - 1, wpr, row_ctas, scale_log2, part, ml, out, (int)(out_dtype == RKV_BF16), status);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -685,6 +700,8 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
         cudaError_t e;
         if (p.tree)
             e = launch_dense_tree(g, H, q, nq, cache, len, p.cut, scale_log2, out_dtype == RKV_F32, part, ml, status, s);
+        else if (p.nt == 0)
+            e = run_split<D, B, 0>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
         else if (p.nt == 1)
             e = run_split<D, B, 1>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
         else if (p.nt == 2)
