@@ -8,8 +8,8 @@
 //                   order, with q: two 16 x 8 x 16 steps per unit of channels, and a third
 //                   for A = sum |q| max(|lo|, |hi|), which bounds the rounding of the other
 //                   two.  Bound by the headers' bytes (4 D per block and head).
-//   k_block_pick    one CTA per list.  The K-th largest fp32 score t is found by bisection of
-//                   its bits (counts only: nothing depends on an order of atomics); with E
+//   k_block_pick    one CTA per list.  The K-th largest fp32 score t is found byte by byte
+//                   (counts only: nothing depends on an order of atomics); with E
 //                   the largest error bound, blocks above t + 2 E are in and those below
 //                   t - 2 E are out.  If the ones between are more than there is room for,
 //                   they are scored again in 70 bits and ranked by (score, lower index).
@@ -151,18 +151,43 @@ __device__ __forceinline__ Sum3 cta_sum3(Sum3 v, Sum3 (&red)[2][kPickWarps], int
     return r;
 }
 
-// The `want`-th largest of count(lo, hi)'s keys: the largest t with at least `want` keys >= t,
-// two bits at a time.  counts(t1, t2, t3) returns how many keys are >= each.
-template <typename K, class F>
-__device__ __forceinline__ K kth_largest(int want, F counts)
+// The `want`-th largest of n keys, a byte at a time from the top: how many of the keys that
+// agree so far have each value of the next byte (increments in shared memory, which do not
+// depend on their order), then the value that the want-th falls into.  (By bisection with
+// votes or warp reductions the counts alone took 400 cycles a key and thread.)
+template <typename K>
+__device__ __forceinline__ K kth_largest(int want, const K *keys, int n, int (&hist)[256], int (&found)[2])
 {
+    const int tid = threadIdx.x, lane = tid & 31;
     K t = 0;
 #pragma unroll 1
-    for (int bit = (int)sizeof(K) * 8 - 2; bit >= 0; bit -= 2) {
-        const Sum3 n = counts(t | ((K)1 << bit), t | ((K)2 << bit), t | ((K)3 << bit));
-        if (n.c >= want) t |= (K)3 << bit;
-        else if (n.b >= want) t |= (K)2 << bit;
-        else if (n.a >= want) t |= (K)1 << bit;
+    for (int shift = (int)sizeof(K) * 8 - 8; shift >= 0; shift -= 8) {
+        if (tid < 256) hist[tid] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int i = tid; i < n; i += kPickThreads) {
+            const K k = keys[i];
+            // the bits above this byte (two shifts: all of them at the first step)
+            if ((((k ^ t) >> shift) >> 8) == 0) atomicAdd(hist + (int)((k >> shift) & 255), 1);
+        }
+        __syncthreads();
+        if (tid < 32) {                                    // lane l: values 255 - 8 l and the 7 below
+            int c[8], sum = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += c[k] = hist[255 - 8 * lane - k];
+            const int upto = lane_scan(sum);
+            if (upto >= want && upto - sum < want) {       // one lane
+                int left = want - (upto - sum), d = 255 - 8 * lane;
+#pragma unroll
+                for (int k = 0; k < 7; ++k)
+                    if (d == 255 - 8 * lane - k && left > c[k]) { left -= c[k]; --d; }
+                found[0] = d;
+                found[1] = left;
+            }
+        }
+        __syncthreads();
+        t |= (K)found[0] << shift;
+        want = found[1];
     }
     return t;
 }
@@ -331,6 +356,7 @@ k_block_pick(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kh
     __shared__ int red1[kPickWarps + 1];
     __shared__ float emax[kPickWarps];
     __shared__ int cand_n;
+    __shared__ int hist[256], found[2];
     __shared__ int32_t cand_s[kSmallCand];
     __shared__ unsigned long long exact_s[kSmallCand];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -377,16 +403,7 @@ k_block_pick(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kh
     for (int b = have - keep_last + tid; b < have; b += kPickThreads) atomicOr(in + (b >> 5), 1u << (b & 31));
     __syncthreads();
     if (want > 0) {
-        const uint32_t kt = kth_largest<uint32_t>(want, [&](uint32_t t1, uint32_t t2, uint32_t t3) {
-            Sum3 n{0, 0, 0};
-            for (int b = tid; b < have; b += kPickThreads) {
-                const uint32_t k = keys[b];
-                n.a += k >= t1;
-                n.b += k >= t2;
-                n.c += k >= t3;
-            }
-            return cta_sum3(n, red3, turn);
-        });
+        const uint32_t kt = kth_largest<uint32_t>(want, keys, have, hist, found);
         // NaN bounds cannot arise (e starts from 0 and fmaxf leaves NaN out); infinite ones make
         // every block a candidate
         const float t = value32(kt), band = 2.01f * e;
@@ -442,17 +459,7 @@ k_block_pick(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kh
                     if (better < need) atomicOr(in + (cand[tid] >> 5), 1u << (cand[tid] & 31));
                 }
             } else {
-                const unsigned long long kx = kth_largest<unsigned long long>(
-                    need, [&](unsigned long long t1, unsigned long long t2, unsigned long long t3) {
-                        Sum3 m{0, 0, 0};
-                        for (int i = tid; i < cands; i += kPickThreads) {
-                            const unsigned long long k = ex[i];
-                            m.a += k >= t1;
-                            m.b += k >= t2;
-                            m.c += k >= t3;
-                        }
-                        return cta_sum3(m, red3, turn);
-                    });
+                const unsigned long long kx = kth_largest<unsigned long long>(need, ex, cands, hist, found);
                 Sum3 m{0, 0, 0};
                 for (int i = tid; i < cands; i += kPickThreads) m.a += ex[i] > kx;
                 m = cta_sum3(m, red3, turn);
