@@ -363,8 +363,9 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
 // then drafted tokens 0..31, 32..63.  A group's scores for all rows are one product (two
 // warps, 16 tokens each); every row then takes its own, and adds p v for the tokens that it
 // sees alone.  The warps of a row deal tokens and partials among them.
-template <int D>
-__global__ void __launch_bounds__(32 * kFinWarps)
+// With RPW = 2 a warp has two rows, 8 apart (wpr is 1 then), and a CTA's tokens serve 16 rows.
+template <int D, int RPW>
+__global__ void __launch_bounds__(32 * kFinWarps, D <= 128 ? 4 : 2)
 k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ tail,
                const int32_t *__restrict__ len, const int32_t *__restrict__ parent,
                const __nv_bfloat16 *__restrict__ draft, int S, int T, int N, int G, int nq, DenseCut cut, int listed,
@@ -373,23 +374,23 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
 {
     constexpr int kCh = D / 8, kPad = kCh + 1, kE = D / 32;   // 16-byte chunks of a row; channels of a lane
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float sc[8][3 * kBlk + 1];
+    __shared__ float sc[8 * RPW][3 * kBlk + 1];
     __shared__ __align__(16) float part_s[kFinWarps][D + 4];
     __shared__ float2 ml_s[kFinWarps];
     __shared__ int par[kMaxDraft];
+    __shared__ DenseRun runs_s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sn = blockIdx.x / row_ctas, s = sn / N, n = sn % N;
-    const int R = nq * G, rpc = kFinWarps / wpr, r0 = (blockIdx.x % row_ctas) * rpc;
-    const int slot = warp / wpr, turn = warp % wpr, r = r0 + slot;
+    const int R = nq * G, rpc = kFinWarps / wpr * RPW, r0 = (blockIdx.x % row_ctas) * rpc;
+    const int slot = warp / wpr, turn = warp % wpr;        // row r0 + slot + 8 k
     const int length = dense_len(len, s, T, status);
     const int rest = length % kBlk;
-    const bool live = r < R;
-    const int j = live ? r / G : 0;
     auto row_of = [&](int x) { return (((size_t)s * nq + x / G) * N + n) * G + x % G; };
     const int groups = parent ? 1 + (nq + kBlk - 1) / kBlk : 1;
     uint4 *ks = (uint4 *)smem, *vs = ks + groups * kBlk * kPad;
     if (parent && threadIdx.x < nq) par[threadIdx.x] = __ldg(parent + (size_t)s * nq + threadIdx.x);
     // all tokens of all groups, a row to kCh threads
+#pragma unroll 2
     for (int i = threadIdx.x; i < groups * kBlk * kCh; i += 32 * kFinWarps) {
         const int t = i / kCh, ch = i % kCh;
         const uint4 *kr, *vr;
@@ -406,27 +407,6 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
         vs[t * kPad + ch] = __ldg(vr + ch);
     }
     __syncthreads();
-    // the drafted tokens that the row sees; parents come before their children, so that the
-    // way up ends
-    uint64_t sees = 0;
-    bool padding = !live;
-    if (parent && live) {
-        bool bad = false;
-        int p = j;
-        if (par[j] == -2) padding = true;
-        else
-            while (p >= 0) {
-                sees |= 1ull << p;
-                const int up = par[p];
-                if (up >= p || up < -1) { bad = true; break; }
-                p = up;
-            }
-        if (bad) {
-            padding = true;
-            if (lane == 0) set_status(status, RKV_ERR_INDEX);
-        }
-    }
-    __shared__ DenseRun runs_s;
     if (warp == kFinWarps - 1) {
         const DenseRun x = dense_runs_of(len, S, T, listed, cut, s, status);
         if (lane == 0) runs_s = x;
@@ -435,82 +415,121 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
         // tokens 16 warp ..: rows of the first operand (those that are not there give scores
         // that no row takes); the query rows are the second one's columns (zero behind the last)
         const int g = lane >> 2, c = lane & 3;
-        const bool there = g < rpc && r0 + g < R;
-        const uint32_t *src = (const uint32_t *)(q + row_of(there ? r0 + g : 0) * D);
-        uint32_t qr[D / 16][2];
-#pragma unroll
-        for (int u = 0; u < D / 16; ++u) {
-            qr[u][0] = there ? __ldg(src + u * 8 + c) : 0u;
-            qr[u][1] = there ? __ldg(src + u * 8 + 4 + c) : 0u;
-        }
-        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         const uint32_t at = um::smem_u32(ks + (16 * warp + 8 * ((lane >> 3) & 1) + (lane & 7)) * kPad + (lane >> 4));
+        float d[RPW][4];
 #pragma unroll
-        for (int u = 0; u < D / 16; ++u) {
-            uint32_t a[4];
-            ldmatrix4(a, at + u * 32);
-            mma16816(d, a, qr[u][0], qr[u][1]);
+        for (int k = 0; k < RPW; ++k) {
+            const bool there = g + 8 * k < rpc && r0 + g + 8 * k < R;
+            const uint32_t *src = (const uint32_t *)(q + row_of(there ? r0 + g + 8 * k : 0) * D);
+            uint32_t qr[D / 16][2];
+#pragma unroll
+            for (int u = 0; u < D / 16; ++u) {
+                qr[u][0] = there ? __ldg(src + u * 8 + c) : 0u;
+                qr[u][1] = there ? __ldg(src + u * 8 + 4 + c) : 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[k][e] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < D / 16; ++u) {
+                uint32_t a[4];
+                ldmatrix4(a, at + u * 32);
+                mma16816(d[k], a, qr[u][0], qr[u][1]);
+            }
         }
-        sc[2 * c][16 * warp + g] = d[0];
-        sc[2 * c + 1][16 * warp + g] = d[1];
-        sc[2 * c][16 * warp + g + 8] = d[2];
-        sc[2 * c + 1][16 * warp + g + 8] = d[3];
+#pragma unroll
+        for (int k = 0; k < RPW; ++k) {
+            sc[8 * k + 2 * c][16 * warp + g] = d[k][0];
+            sc[8 * k + 2 * c + 1][16 * warp + g] = d[k][1];
+            sc[8 * k + 2 * c][16 * warp + g + 8] = d[k][2];
+            sc[8 * k + 2 * c + 1][16 * warp + g + 8] = d[k][3];
+        }
     }
     __syncthreads();
 
-    float m = -INFINITY, l = 0.0f, acc[kE];
+    float m[RPW], l[RPW], acc[RPW][kE];
+    bool padding[RPW];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) acc[e] = 0.0f;
+    for (int k = 0; k < RPW; ++k) {
+        const int r = r0 + slot + 8 * k;
+        // the drafted tokens that the row sees; parents come before their children, so that the
+        // way up ends
+        uint64_t sees = 0;
+        padding[k] = r >= R;
+        if (parent && r < R) {
+            bool bad = false;
+            int p = r / G;
+            if (par[p] == -2) padding[k] = true;
+            else
+                while (p >= 0) {
+                    sees |= 1ull << p;
+                    const int up = par[p];
+                    if (up >= p || up < -1) { bad = true; break; }
+                    p = up;
+                }
+            if (bad) {
+                padding[k] = true;
+                if (lane == 0) set_status(status, RKV_ERR_INDEX);
+            }
+        }
+        m[k] = -INFINITY;
+        l[k] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[k][e] = 0.0f;
 #pragma unroll 1
-    for (int grp = 0; grp < groups; ++grp) {
-        uint32_t mask = 0u;
-        if (!padding)
-            mask = grp == 0 ? (1u << rest) - 1u : (uint32_t)(sees >> ((grp - 1) * kBlk));
-        // this warp's tokens of the row: bits turn, turn + wpr, ...
-        if (wpr == 2) mask &= 0x55555555u << turn;
-        else if (wpr == 4) mask &= 0x11111111u << turn;
-        else if (wpr == 8) mask &= 0x01010101u << turn;
-        if (mask == 0u) continue;                          // the same for the whole warp
-        const float x = ((mask >> lane) & 1u) ? sc[slot][grp * kBlk + lane] * scale_log2 : -INFINITY;
-        float mx = x;
+        for (int grp = 0; grp < groups; ++grp) {
+            uint32_t mask = 0u;
+            if (!padding[k])
+                mask = grp == 0 ? (1u << rest) - 1u : (uint32_t)(sees >> ((grp - 1) * kBlk));
+            // this warp's tokens of the row: bits turn, turn + wpr, ...
+            if (wpr == 2) mask &= 0x55555555u << turn;
+            else if (wpr == 4) mask &= 0x11111111u << turn;
+            else if (wpr == 8) mask &= 0x01010101u << turn;
+            if (mask == 0u) continue;                      // the same for the whole warp
+            const float x = ((mask >> lane) & 1u) ? sc[slot + 8 * k][grp * kBlk + lane] * scale_log2 : -INFINITY;
+            float mx = x;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        mx = fmaxf(mx, m);
-        const float mu = mx == -INFINITY ? 0.0f : mx;
-        const float al = ex2(m - mu), p = ex2(x - mu);
-        m = mx;
-        float ps = p;
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            mx = fmaxf(mx, m[k]);
+            const float mu = mx == -INFINITY ? 0.0f : mx;
+            const float al = ex2(m[k] - mu), p = ex2(x - mu);
+            m[k] = mx;
+            float ps = p;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
-        l = fmaf(l, al, ps);
+            for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
+            l[k] = fmaf(l[k], al, ps);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) acc[e] *= al;
-        while (mask) {
-            const int t = __ffs(mask) - 1;
-            mask &= mask - 1u;
-            const float pt = __shfl_sync(0xffffffffu, p, t);
-            const uint32_t *v = (const uint32_t *)(vs + (grp * kBlk + t) * kPad) + lane * (kE / 2);
+            for (int e = 0; e < kE; ++e) acc[k][e] *= al;
+            const uint4 *vg = vs + grp * kBlk * kPad;
+            while (mask) {
+                const int t = __ffs(mask) - 1;
+                mask &= mask - 1u;
+                const float pt = __shfl_sync(0xffffffffu, p, t);
+                const uint32_t *v = (const uint32_t *)(vg + t * kPad) + lane * (kE / 2);
 #pragma unroll
-            for (int e = 0; e < kE / 2; ++e) {
-                acc[2 * e] = fmaf(pt, __uint_as_float(v[e] << 16), acc[2 * e]);
-                acc[2 * e + 1] = fmaf(pt, __uint_as_float(v[e] & 0xffff0000u), acc[2 * e + 1]);
+                for (int e = 0; e < kE / 2; ++e) {
+                    acc[k][2 * e] = fmaf(pt, __uint_as_float(v[e] << 16), acc[k][2 * e]);
+                    acc[k][2 * e + 1] = fmaf(pt, __uint_as_float(v[e] & 0xffff0000u), acc[k][2 * e + 1]);
+                }
             }
         }
     }
 
     // the finished blocks' partials: launched as a programmatic dependent, this waits for them
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    bool bad = false;
+    // 1 << each_log partials for every run and KV head, this warp's every wpr-th; 32 at a time:
+    // their weights, a lane each, then their sums, those with nothing in them left out
     const DenseRun runs = runs_s;
-    if (!padding) {
-        // 1 << each_log partials for every run and KV head, this warp's every wpr-th; 32 at a time:
-        // their weights, a lane each, then their sums, those with nothing in them left out
-        const int parts = (runs.end - runs.first) << each_log;
-        const size_t first = (((size_t)runs.first * N + n) << each_log) * R + r;
-        const size_t next_run = ((size_t)N << each_log) * R;
+    const int parts = (runs.end - runs.first) << each_log;
+    const size_t next_run = ((size_t)N << each_log) * R;
+#pragma unroll
+    for (int k = 0; k < RPW; ++k) {
+        if (padding[k]) continue;
+        const size_t first = (((size_t)runs.first * N + n) << each_log) * R + r0 + slot + 8 * k;
         auto part_at = [&](int i) {
             return first + (size_t)(i >> each_log) * next_run + (each_log ? (size_t)(i & 1) * R : 0);
         };
+        bool bad = false;
+#pragma unroll 1
         for (int i0 = turn; i0 < parts; i0 += 32 * wpr) {
             const int mine = i0 + lane * wpr;
             const float2 v = mine < parts ? ml[part_at(mine)] : make_float2(-INFINITY, 0.0f);
@@ -518,73 +537,78 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
             float mx = v.x;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            mx = fmaxf(mx, m);
+            mx = fmaxf(mx, m[k]);
             const float mu = mx == -INFINITY ? 0.0f : mx;
-            const float al = ex2(m - mu), f = ex2(v.x - mu);
-            m = mx;
+            const float al = ex2(m[k] - mu), f = ex2(v.x - mu);
+            m[k] = mx;
             float ls = v.y * f;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-            l = fmaf(l, al, ls);
+            l[k] = fmaf(l[k], al, ls);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) acc[e] *= al;
+            for (int e = 0; e < kE; ++e) acc[k][e] *= al;
             uint32_t todo = __ballot_sync(0xffffffffu, v.x > -INFINITY);
-            constexpr int kU = kE <= 4 ? 8 : 4;            // sums in flight
+            constexpr int kU = RPW > 1 || kE > 4 ? 4 : 8;  // sums in flight
             while (todo) {
                 float x[kU][kE], w[kU];
 #pragma unroll
-                for (int k = 0; k < kU; ++k) {
+                for (int j = 0; j < kU; ++j) {
                     const int i = todo ? __ffs(todo) - 1 : 0;
-                    w[k] = __shfl_sync(0xffffffffu, f, i);
-                    if (!todo) w[k] = 0.0f;
+                    w[j] = __shfl_sync(0xffffffffu, f, i);
+                    if (!todo) w[j] = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < kE; ++e) x[k][e] = 0.0f;
+                    for (int e = 0; e < kE; ++e) x[j][e] = 0.0f;
                     if (todo) {
                         const float *pr = part + part_at(i0 + i * wpr) * D + lane * kE;
 #pragma unroll
-                        for (int e = 0; e < kE; ++e) x[k][e] = pr[e];
+                        for (int e = 0; e < kE; ++e) x[j][e] = pr[e];
                     }
                     todo &= todo - 1u;
                 }
 #pragma unroll
-                for (int k = 0; k < kU; ++k)
+                for (int j = 0; j < kU; ++j)
 #pragma unroll
-                    for (int e = 0; e < kE; ++e) acc[e] = fmaf(x[k][e], w[k], acc[e]);
+                    for (int e = 0; e < kE; ++e) acc[k][e] = fmaf(x[j][e], w[j], acc[k][e]);
             }
         }
-        if (__any_sync(0xffffffffu, bad)) l = __uint_as_float(0x7fffffffu);
+        if (__any_sync(0xffffffffu, bad)) l[k] = __uint_as_float(0x7fffffffu);
     }
-    if (wpr > 1) {
+    if (RPW == 1 && wpr > 1) {
         // the warps of a row, in order
 #pragma unroll
-        for (int e = 0; e < kE; ++e) part_s[warp][lane * kE + e] = acc[e];
-        if (lane == 0) ml_s[warp] = make_float2(m, l);
+        for (int e = 0; e < kE; ++e) part_s[warp][lane * kE + e] = acc[0][e];
+        if (lane == 0) ml_s[warp] = make_float2(m[0], l[0]);
         __syncthreads();
         if (turn) return;
-        for (int k = 1; k < wpr; ++k) {
-            const float2 o = ml_s[warp + k];
-            const float mx = fmaxf(m, o.x), mu = mx == -INFINITY ? 0.0f : mx;
-            const float al = ex2(m - mu), f = ex2(o.x - mu);
-            m = mx;
-            l = l * al + o.y * f;
+        for (int w = 1; w < wpr; ++w) {
+            const float2 o = ml_s[warp + w];
+            const float mx = fmaxf(m[0], o.x), mu = mx == -INFINITY ? 0.0f : mx;
+            const float al = ex2(m[0] - mu), f = ex2(o.x - mu);
+            m[0] = mx;
+            l[0] = l[0] * al + o.y * f;
 #pragma unroll
-            for (int e = 0; e < kE; ++e) acc[e] = fmaf(part_s[warp + k][lane * kE + e], f, acc[e] * al);
+            for (int e = 0; e < kE; ++e) acc[0][e] = fmaf(part_s[warp + w][lane * kE + e], f, acc[0][e] * al);
         }
     }
-    if (!live) return;
-    // l is 0 only where the row sees nothing (the largest p is 1); NaN stays NaN
-    const bool none = padding || l == 0.0f;
-    const float inv = none ? 0.0f : 1.0f / l;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) acc[e] = none ? 0.0f : acc[e] * inv;
-    if (out_bf16) {
-        uint32_t *o = (uint32_t *)((__nv_bfloat16 *)out + row_of(r) * D) + lane * (kE / 2);
+    for (int k = 0; k < RPW; ++k) {
+        const int r = r0 + slot + 8 * k;
+        if (r >= R) continue;
+        // l is 0 only where the row sees nothing (the largest p is 1); NaN stays NaN
+        const bool none = padding[k] || l[k] == 0.0f;
+        const float inv = none ? 0.0f : 1.0f / l[k];
+        float o[kE];
 #pragma unroll
-        for (int e = 0; e < kE / 2; ++e) o[e] = as_u32(__floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]));
-    } else {
-        float *o = (float *)out + row_of(r) * D + lane * kE;
+        for (int e = 0; e < kE; ++e) o[e] = none ? 0.0f : acc[k][e] * inv;
+        if (out_bf16) {
+            uint32_t *dst = (uint32_t *)((__nv_bfloat16 *)out + row_of(r) * D) + lane * (kE / 2);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] = acc[e];
+            for (int e = 0; e < kE / 2; ++e) dst[e] = as_u32(__floats2bfloat162_rn(o[2 * e], o[2 * e + 1]));
+        } else {
+            float *dst = (float *)out + row_of(r) * D + lane * kE;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) dst[e] = o[e];
+        }
     }
 }
 
@@ -647,14 +671,21 @@ cudaError_t run_finish(const DenseGeom &g, const Plan &p, int H, const void *q, 
                        const float *part, const float2 *ml, void *out, int out_dtype, int32_t *status, cudaStream_t s)
 {
     const int R = nq * (H / g.N);
-    const int wpr = R <= 1 ? 8 : (R <= 2 ? 4 : (R <= 4 ? 2 : 1)), rpc = kFinWarps / wpr;
+    const int wpr = R <= 1 ? 8 : (R <= 2 ? 4 : (R <= 4 ? 2 : 1));
+    // two rows to a warp where one to a warp makes more CTAs than the GPU holds at a time
+    // (24 x 7 rows, 16 sequences, 4 KV heads: 31 against 26 us; 256 rows of 8 heads: 17 against 23)
+    const bool twice = R > kFinWarps && (long long)g.S * g.N * ((R + kFinWarps - 1) / kFinWarps) > 4 * 152;
+    const int rpc = kFinWarps / wpr * (twice ? 2 : 1);
     const int row_ctas = (R + rpc - 1) / rpc;
     constexpr int kGroup = 2 * kBlk * (D / 8 + 1) * 16;    // K and V rows of 32 tokens
     static_assert(3 * kGroup + kFinWarps * (D + 4) * 4 + 8192 <= 227 * 1024, "shared memory of the last pass");
     static PerDevice<int> setup;
     int unused = 0;
     cudaError_t e = per_device(setup, unused, [](int &) {
-        return cudaFuncSetAttribute(k_dense_finish<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * kGroup);
+        cudaError_t err = cudaFuncSetAttribute(k_dense_finish<D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * kGroup);
+        if (err == cudaSuccess)
+            err = cudaFuncSetAttribute(k_dense_finish<D, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * kGroup);
+        return err;
     });
     if (e != cudaSuccess) return e;
     ProfScope prof("dense_attention_finish", s);
@@ -668,7 +699,7 @@ cudaError_t run_finish(const DenseGeom &g, const Plan &p, int H, const void *q, 
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_dense_finish<D>, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)c->tail,
+    e = cudaLaunchKernelEx(&cfg, twice ? k_dense_finish<D, 2> : k_dense_finish<D, 1>, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)c->tail,
                                        len, parent, (const __nv_bfloat16 *)draft, g.S, g.T, g.N, H / g.N, nq, p.cut, listed,
                                        p.each - 1, wpr, row_ctas, scale_log2, part, ml, out, (int)(out_dtype == RKV_BF16), status);
     return e == cudaSuccess ? cudaGetLastError() : e;

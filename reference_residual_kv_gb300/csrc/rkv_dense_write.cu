@@ -6,12 +6,12 @@
 //                  stores (transposed for the values), and a group's extremes are three
 //                  warp shuffles away.  Codes and headers leave in the order of
 //                  rkv_dense.cuh.  Rows of a block that stays unfinished go to the tail.
-//   k_dense_read   one warp per 32 entries of the selection and KV head.  Entries of one block
-//                  are taken together: the block's keys, then its values, become bf16 for all
-//                  32 tokens (one stmatrix for 256 of them) in the warp's row buffer, from
-//                  which the asked rows leave as 16-byte stores; records come by bulk copies,
-//                  two blocks ahead.  A block that fewer than kTogether of the 32 entries ask
-//                  for is read for each of its tokens alone.
+//   k_dense_read   one warp per 64 entries of the selection, KV head and keys | values.  Entries
+//                  of one block are taken together, wherever they are among the 64: the block's
+//                  keys (or values) become bf16 for all 32 tokens (one stmatrix for 256 of
+//                  them) in the warp's row buffer, from which the asked rows leave as 16-byte stores;
+//                  records come by bulk copies, one block ahead.  A block that fewer than
+//                  kTogether of the entries ask for is read for each of its tokens alone.
 #include "rkv_dense.cuh"
 #include "umma.cuh"
 
@@ -19,8 +19,9 @@ namespace rkv {
 namespace {
 
 constexpr int kWriteWarps = 4;
-constexpr int kReadWarps = 4;
+constexpr int kReadWarps = 2;
 constexpr int kTogether = 4;
+constexpr int kSets = 2;                     // sets of 32 entries of a warp
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src)
 {
@@ -406,25 +407,24 @@ k_dense_write(const __grid_constant__ CUtensorMap map, int mapped, const TIN *__
     }
 }
 
-// K and V of one token of a finished block, to `row` (2 D values): 4 lanes hold a chunk's key
+// K (or V) of token o of a finished block, to `row` (D values): 4 lanes hold a chunk's key
 // codes of the token, 8 lanes its value codes.
 template <int D, int BITS>
-__device__ __forceinline__ void read_token(const uint8_t *rec, const uint8_t *kh, int o, int lane, __nv_bfloat16 *row)
+__device__ __forceinline__ void read_token(const uint8_t *cd, const uint8_t *hp, bool is_v, int o, int lane,
+                                           __nv_bfloat16 *row)
 {
-    constexpr size_t kUnit = (size_t)4 * D * BITS;
     constexpr int kPer = 8 / BITS, kCh = (D / 16) / kPer;  // units of a chunk, chunks
-    uint32_t *krow = (uint32_t *)row;
-    __nv_bfloat16 *vrow = row + D;
-    {
+    if (!is_v) {
+        uint32_t *krow = (uint32_t *)row;
         const int g = o & 7, hi_row = (o >> 3) & 1, m = o >> 4;
         for (int x = lane; x < 4 * kCh; x += 32) {
             const int j = x >> 2, c = x & 3;
-            const uint4 q = __ldg((const uint4 *)(rec + j * 512 + key_slot(g, c) * 16));
+            const uint4 q = __ldg((const uint4 *)(cd + j * 512 + key_slot(g, c) * 16));
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 const int u = j * kPer + k;
-                const uint4 hd = __ldg((const uint4 *)(kh + (u * 4 + c) * 16));
+                const uint4 hd = __ldg((const uint4 *)(hp + (u * 4 + c) * 16));
                 const uint32_t word = BITS == 4 ? (m ? w[(2 * k + 1) & 3] : w[(2 * k) & 3]) : w[k & 3];
                 const int p = (BITS == 4 ? 0 : 4 * m) + hi_row;
                 krow[(u * 16 + 2 * c) >> 1] = value_pair<BITS>(word, p, hd.x, hd.y);
@@ -433,17 +433,16 @@ __device__ __forceinline__ void read_token(const uint8_t *rec, const uint8_t *kh
         }
     }
     // values: the token is column o % 16 of the units of its half
-    {
-        const uint8_t *vc = rec + kUnit, *vh = rec + 2 * kUnit;
+    else {
         const int half = o >> 4, hi_col = (o >> 3) & 1, c = (o & 7) >> 1, e = o & 1;
         for (int x = lane; x < 8 * kCh; x += 32) {
             const int j = x >> 3, g = x & 7;
-            const uint4 q = __ldg((const uint4 *)(vc + j * 512 + value_slot(g, c) * 16));
+            const uint4 q = __ldg((const uint4 *)(cd + j * 512 + value_slot(g, c) * 16));
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int k0 = 0; k0 < kPer; k0 += 2) {         // units come in pairs of token halves
                 const int u = j * kPer + k0 + half;
-                const uint2 hd = __ldg((const uint2 *)(vh + (u * 4 + c) * 16 + hi_col * 8));
+                const uint2 hd = __ldg((const uint2 *)(hp + (u * 4 + c) * 16 + hi_col * 8));
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     const uint32_t word = BITS == 4 ? (half ? w[2 + m] : w[m]) : (half ? w[(k0 + 1) & 3] : w[k0 & 3]);
@@ -451,7 +450,7 @@ __device__ __forceinline__ void read_token(const uint8_t *rec, const uint8_t *kh
                     for (int rr = 0; rr < 2; ++rr) {
                         const int p = (BITS == 4 ? 0 : 4 * m) + 2 * hi_col + rr;
                         const uint32_t v = value_pair<BITS>(word, p, hd.x, hd.y);
-                        vrow[(u >> 1) * 32 + m * 16 + rr * 8 + g] =
+                        row[(u >> 1) * 32 + m * 16 + rr * 8 + g] =
                             __ushort_as_bfloat16((unsigned short)(e ? v >> 16 : v & 0xffffu));
                     }
                 }
@@ -497,8 +496,9 @@ __device__ __forceinline__ void read_block(const uint8_t *cd, const uint8_t *hd,
 
 template <int D, int BITS>
 struct ReadCfg {
-    static constexpr int kUnit = 4 * D * BITS, kRec = 2 * kUnit + 4 * D, kHdr = 4 * D, kStage = kRec + kHdr;
+    static constexpr int kUnit = 4 * D * BITS, kRec = 2 * kUnit + 4 * D, kHdr = 4 * D, kStage = kUnit + kHdr;
     static constexpr int kStages = 2, kRows = kBlk * D * 2;
+    static_assert(kStages >= 2, "one block is read while the next one is on its way");
     static constexpr int kWarp = kStages * kStage + kRows;       // a warp's shared memory
     static constexpr int kSmem = kReadWarps * (kWarp + kStages * 8);
 };
@@ -518,104 +518,141 @@ k_dense_read(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
     uint4 *buf = (uint4 *)(stage + C::kStages * C::kStage);
     uint64_t *bars = (uint64_t *)(smem + (size_t)kReadWarps * C::kWarp) + warp * C::kStages;
     const long long id = (long long)blockIdx.x * kReadWarps + warp;
-    const int h = (int)(id % N), grp = (int)(id / N % groups), s = (int)(id / N / groups);
+    const bool is_v = id & 1;
+    const int h = (int)((id >> 1) % N), grp = (int)((id >> 1) / N % groups), s = (int)((id >> 1) / N / groups);
     if (s >= S) return;
     const int length = dense_len(len, s, T, status), full = length / kBlk;
-    const int i0 = grp * 32, cnt = min(32, n_sel - i0);
+    const int i0 = grp * 32 * kSets, left_n = n_sel - i0;
     const size_t at0 = (size_t)s * n_sel + i0, sh = (size_t)s * N + h;
-    const int t = lane < cnt ? __ldg(sel + at0 + lane) : -1;
-    const bool ok = t >= 0 && t < length;
-    if (!ok && t != -1) set_status(status, RKV_ERR_INDEX);
-    const int b = ok ? t / kBlk : -1;
-    // chunk c of entry i's row of K (V)
-    auto row_k = [&](int i) { return (uint4 *)(out_k + ((at0 + i) * N + h) * D); };
-    auto row_v = [&](int i) { return (uint4 *)(out_v + ((at0 + i) * N + h) * D); };
-
+    // entry 32 k + lane: token t[k] in block b[k]; -1: not in a finished block, or not there
+    int t[kSets], b[kSets];
+    uint32_t todo[kSets], plain[kSets];
+#pragma unroll
+    for (int k = 0; k < kSets; ++k) {
+        const bool there = 32 * k + lane < left_n;
+        t[k] = there ? __ldg(sel + at0 + 32 * k + lane) : -1;
+        const bool ok = t[k] >= 0 && t[k] < length;
+        if (!ok && t[k] != -1) set_status(status, RKV_ERR_INDEX);
+        b[k] = ok && t[k] / kBlk < full ? t[k] / kBlk : -1;
+        if (!ok) t[k] = -1;
+        todo[k] = __ballot_sync(0xffffffffu, b[k] >= 0);
+        plain[k] = __ballot_sync(0xffffffffu, there && b[k] < 0);
+    }
+    __nv_bfloat16 *out = is_v ? out_v : out_k;
+    auto row_of = [&](int i) { return (uint4 *)(out + ((at0 + i) * N + h) * D); };
+    // codes and headers of block bb
+    auto codes_of = [&](int bb) { return codes + (sh * nb + bb) * C::kRec + (is_v ? C::kUnit : 0); };
+    auto heads_of = [&](int bb) {
+        return is_v ? codes + (sh * nb + bb) * C::kRec + 2 * C::kUnit : khdr + (sh * nb + bb) * C::kHdr;
+    };
     if (lane == 0) {
         for (int k = 0; k < C::kStages; ++k) um::mbar_init(bars + k, 1);
         um::fence_mbar_init();
     }
     __syncwarp();
-    const bool held = ok && b < full;
-    const uint32_t mates = __match_any_sync(0xffffffffu, held ? b : -1);
-    const bool together = held && __popc(mates) >= kTogether;
-    // groups of entries of one block, by their first entry; their records come by bulk copies,
-    // two of them ahead
-    uint32_t ahead = __ballot_sync(0xffffffffu, together && (mates & ((1u << lane) - 1u)) == 0u);
-    uint32_t groups_left = ahead;
+
+    // The next block among the entries left, taken off them: its entries, and its record on the
+    // way (stage `issued`) if they are at least kTogether.
     int issued = 0;
-    auto issue = [&]() {
-        if (!ahead) return;
-        const int bb = __shfl_sync(0xffffffffu, b, __ffs(ahead) - 1);
-        ahead &= ahead - 1u;
+    auto take = [&](int &bb, uint32_t (&same)[kSets]) -> bool {
+        bb = -1;
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < kSets; ++k)
+            if (bb < 0 && todo[k]) bb = __shfl_sync(0xffffffffu, b[k], __ffs(todo[k]) - 1);
+#pragma unroll
+        for (int k = 0; k < kSets; ++k) {
+            same[k] = __ballot_sync(0xffffffffu, b[k] == bb) & todo[k];
+            todo[k] &= ~same[k];
+            n += __popc(same[k]);
+        }
+        if (bb < 0 || n < kTogether) return false;
         if (lane == 0) {
-            const int st = issued % C::kStages;
-            const size_t rec = sh * nb + bb;
-            um::mbar_arrive_expect_tx(bars + st, C::kStage);
-            bulk_load(stage + st * C::kStage, codes + rec * C::kRec, C::kRec, bars + st);
-            bulk_load(stage + st * C::kStage + C::kRec, khdr + rec * C::kHdr, C::kHdr, bars + st);
+            uint8_t *dst = stage + issued % C::kStages * C::kStage;
+            um::mbar_arrive_expect_tx(bars + issued % C::kStages, C::kStage);
+            bulk_load(dst, codes_of(bb), C::kUnit, bars + issued % C::kStages);
+            bulk_load(dst + C::kUnit, heads_of(bb), C::kHdr, bars + issued % C::kStages);
         }
         ++issued;
+        return true;
     };
-    for (int k = 0; k < C::kStages; ++k) issue();
+    int now, next;
+    uint32_t of_now[kSets], of_next[kSets];
+    bool staged = take(now, of_now);
 
-    // padding and wrong entries: zero rows; tokens of the unfinished block: as they are
-    uint32_t plain = __ballot_sync(0xffffffffu, lane < cnt && !held);
-    while (plain) {
-        const int i = __ffs(plain) - 1;
-        plain &= plain - 1u;
-        const int ti = __shfl_sync(0xffffffffu, ok ? t : -1, i);
-        const uint4 *kr = (const uint4 *)(tail + (sh * 2 * kBlk + (ti & 31)) * D);
-        for (int x = lane; x < kCh; x += 32) {
-            row_k(i)[x] = ti < 0 ? make_uint4(0u, 0u, 0u, 0u) : kr[x];
-            row_v(i)[x] = ti < 0 ? make_uint4(0u, 0u, 0u, 0u) : kr[kBlk * kCh + x];
-        }
-    }
-    // tokens alone in their block, or nearly so
-    uint32_t alone = __ballot_sync(0xffffffffu, held && !together);
-    while (alone) {
-        const int i = __ffs(alone) - 1;
-        alone &= alone - 1u;
-        const int ti = __shfl_sync(0xffffffffu, t, i);
-        const size_t rec = sh * nb + ti / kBlk;
-        __syncwarp();
-        read_token<D, BITS>(codes + rec * C::kRec, khdr + rec * C::kHdr, ti & 31, lane, (__nv_bfloat16 *)buf);
-        __syncwarp();
-        for (int x = lane; x < kCh; x += 32) {
-            row_k(i)[x] = buf[x];
-            row_v(i)[x] = buf[kCh + x];
-        }
-    }
-    for (int n = 0; groups_left; ++n) {
-        const uint32_t same = __shfl_sync(0xffffffffu, mates, __ffs(groups_left) - 1);
-        groups_left &= groups_left - 1u;
-        const uint8_t *rec = stage + (n % C::kStages) * C::kStage;
-        if (!__all_sync(0xffffffffu, um::mbar_wait(bars + n % C::kStages, (uint32_t)(n / C::kStages) & 1u, kWaitCycles))) {
-            set_status(status, RKV_ERR_DEVICE_TIMEOUT);
-            return;
-        }
+    // a row takes kCh lanes: kRows rows at a time.  The entry of this lane's row among `left`
+    // (-1: none), and `left` without those kRows
+    constexpr int kRows = kCh < 32 ? 32 / kCh : 1;
+    auto next_rows = [&](uint32_t &left) -> int {
+        uint32_t mine = left;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            __syncwarp();
-            if (v == 0) read_block<D, BITS, false>(rec, rec + C::kRec, lane, buf);
-            else read_block<D, BITS, true>(rec + C::kUnit, rec + 2 * C::kUnit, lane, buf);
-            __syncwarp();
-            if (v == 1) issue();
-            // 32 / kCh rows at a time (a row takes kCh lanes)
-            constexpr int kRows = kCh < 32 ? 32 / kCh : 1;
-            uint32_t left = same;
-            while (left) {
-                uint32_t mine = left;                      // the bit of this lane's row
+        for (int x = 1; x < kRows; ++x)
+            if (lane / kCh >= x) mine &= mine - 1u;
 #pragma unroll
-                for (int k = 1; k < kRows; ++k)
-                    if (lane / kCh >= k) mine &= mine - 1u;
-                const int i = mine ? __ffs(mine) - 1 : 0;
-                const int o = __shfl_sync(0xffffffffu, t, i) & 31;
-                if (mine) (v ? row_v(i) : row_k(i))[lane % kCh] = buf[row_chunk<D>(o, lane % kCh)];
+        for (int x = 0; x < kRows; ++x) left &= left - 1u;
+        return mine ? __ffs(mine) - 1 : -1;
+    };
+    // padding and wrong entries: zero rows; tokens of the unfinished block: as they are (four
+    // loads in flight)
+    const uint4 *tail_rows = (const uint4 *)(tail + (sh * 2 + is_v) * kBlk * D) + lane % kCh;
 #pragma unroll
-                for (int k = 0; k < kRows; ++k) left &= left - 1u;
+    for (int k = 0; k < kSets; ++k)
+        while (plain[k]) {
+            uint4 val[4];
+            int at[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                at[j] = next_rows(plain[k]);
+                const int ti = __shfl_sync(0xffffffffu, t[k], max(at[j], 0));
+                val[j] = at[j] >= 0 && ti >= 0 ? tail_rows[(ti & 31) * kCh] : make_uint4(0u, 0u, 0u, 0u);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (at[j] >= 0) row_of(32 * k + at[j])[lane % kCh] = val[j];
         }
+    int used = 0;
+    while (now >= 0) {
+        const bool staged_next = take(next, of_next);
+        if (staged) {
+            const int st = used % C::kStages;
+            const uint8_t *rec = stage + st * C::kStage;
+            const bool here = um::mbar_wait(bars + st, (uint32_t)(used / C::kStages) & 1u, kWaitCycles);
+            if (!__all_sync(0xffffffffu, here)) {
+                set_status(status, RKV_ERR_DEVICE_TIMEOUT);
+                return;
+            }
+            ++used;
+            if (is_v) read_block<D, BITS, true>(rec, rec + C::kUnit, lane, buf);
+            else read_block<D, BITS, false>(rec, rec + C::kUnit, lane, buf);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < kSets; ++k) {
+                uint32_t left = of_now[k];
+                while (left) {
+                    const int i = next_rows(left), o = __shfl_sync(0xffffffffu, t[k], max(i, 0)) & 31;
+                    if (i >= 0) row_of(32 * k + i)[lane % kCh] = buf[row_chunk<D>(o, lane % kCh)];
+                }
+            }
+            __syncwarp();
+        } else {
+            // tokens alone in their block, or nearly so
+#pragma unroll
+            for (int k = 0; k < kSets; ++k)
+                while (of_now[k]) {
+                    const int i = __ffs(of_now[k]) - 1;
+                    of_now[k] &= of_now[k] - 1u;
+                    const int ti = __shfl_sync(0xffffffffu, t[k], i);
+                    __syncwarp();
+                    read_token<D, BITS>(codes_of(now), heads_of(now), is_v, ti & 31, lane, (__nv_bfloat16 *)buf);
+                    __syncwarp();
+                    for (int x = lane; x < kCh; x += 32) row_of(32 * k + i)[x] = buf[x];
+                }
+            __syncwarp();
+        }
+        now = next;
+        staged = staged_next;
+#pragma unroll
+        for (int k = 0; k < kSets; ++k) of_now[k] = of_next[k];
     }
 }
 
@@ -647,8 +684,8 @@ template <int D, int BITS>
 cudaError_t run_read(const DenseGeom &g, const rkv_dense_cache *c, const int32_t *len, const int32_t *sel,
                      int n_sel, void *ok, void *ov, int32_t *status, cudaStream_t s)
 {
-    const int groups = (n_sel + 31) / 32;
-    const long long warps = (long long)g.S * groups * g.N;
+    const int groups = (n_sel + 32 * kSets - 1) / (32 * kSets);
+    const long long warps = (long long)g.S * groups * g.N * 2;
     constexpr int kSmem = ReadCfg<D, BITS>::kSmem;
     static PerDevice<int> setup;
     int unused = 0;
