@@ -86,7 +86,8 @@ __device__ __forceinline__ int block_at(const int32_t *list, int i, int have, in
 }
 
 // Partials: sums [run][N][R][D] and {max, sum} [run][N][R] (max in base 2).
-template <int D, int BITS, int NT0>
+// P3: the probabilities' third parts too (fp32 outputs).
+template <int D, int BITS, int NT0, bool P3>
 __global__ void __launch_bounds__(32 * kWarps, NT0 <= 1 && D <= 128 ? 2 : 1)
 k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ codes,
               const uint8_t *__restrict__ khdr, const int32_t *__restrict__ len, const int32_t *__restrict__ blocks,
@@ -229,31 +230,23 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
             }
         }
         // softmax: rows 2c, 2c + 1 of each column tile; this lane's tokens are 16 m + g, + 8
-        uint32_t ph[NT][2][2], pl[NT][2][2];
+        uint32_t ph[NT][2][2], pl[NT][2][2], pt[P3 ? NT : 1][2][2];
+        float al[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float mx[2], al[2];
+            float mx[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float v = fmaxf(fmaxf(sc[nt][0][e], sc[nt][0][e + 2]), fmaxf(sc[nt][1][e], sc[nt][1][e + 2]));
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
                 mx[e] = fmaxf(m_run[nt][e], v * scale_log2);
-                al[e] = ex2(m_run[nt][e] - (mx[e] == -INFINITY ? 0.0f : mx[e]));
+                al[nt][e] = ex2(m_run[nt][e] - (mx[e] == -INFINITY ? 0.0f : mx[e]));
             }
-            if (__any_sync(0xffffffffu, mx[0] != m_run[nt][0] || mx[1] != m_run[nt][1])) {
-#pragma unroll
-                for (int i = 0; i < 2 * (D / 32); ++i) {
-                    acc[nt][i][0] *= al[0];
-                    acc[nt][i][1] *= al[1];
-                    acc[nt][i][2] *= al[0];
-                    acc[nt][i][3] *= al[1];
-                }
-                l_run[nt][0] *= al[0];
-                l_run[nt][1] *= al[1];
-                m_run[nt][0] = mx[0];
-                m_run[nt][1] = mx[1];
-            }
+            l_run[nt][0] *= al[nt][0];
+            l_run[nt][1] *= al[nt][1];
+            m_run[nt][0] = mx[0];
+            m_run[nt][1] = mx[1];
             const float o0 = mx[0] == -INFINITY ? 0.0f : mx[0], o1 = mx[1] == -INFINITY ? 0.0f : mx[1];
 #pragma unroll
             for (int m = 0; m < 2; ++m)
@@ -265,6 +258,11 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
                     l_run[nt][1] += p1;
                     const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
                     const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - __low2float(hi), p1 - __high2float(hi));
+                    if (P3) {
+                        const float r0 = (p0 - __low2float(hi)) - __low2float(lo), r1 = (p1 - __high2float(hi)) - __high2float(lo);
+                        const uint32_t third = as_u32(__floats2bfloat162_rn(r0, r1));
+                        pt[P3 ? nt : 0][m][h] = trans8x8(kTwice && c >= 2 ? 0u : third);
+                    }
                     if (kTwice) {
                         ph[nt][m][h] = trans8x8(as_u32(c < 2 ? hi : lo));
                     } else {
@@ -273,28 +271,50 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
                     }
                 }
         }
-        // out^T: D channels x 8 NT rows
+        // out^T: D channels x 8 NT rows, 32 channels at a time; a block's sums are its own and
+        // join the running ones rounded (the products' accumulators cut: over a whole run that
+        // was 1.2e-6 of the outputs, against 4e-7)
 #pragma unroll
         for (int u0 = 0; u0 < kUnits; u0 += kPer) {
             const uint4 w4 = *(const uint4 *)(vc + (u0 / kPer) * 512 + vslot);
             const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-            for (int x = 0; x < kPer; ++x) {
-                const int u = u0 + x, ks = u & 1;
-                const uint4 hd = *(const uint4 *)(vh + (u * 4 + c) * 16);
+            for (int x0 = 0; x0 < kPer; x0 += 2) {
+                float sum[NT][2][4];
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    uint32_t a[4];
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        a[i] = value_pair<BITS>(BITS == 4 ? w[(2 * x + m) & 3] : w[x & 3], BITS == 4 ? i : 4 * m + i,
-                                                i < 2 ? hd.x : hd.z, i < 2 ? hd.y : hd.w);
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma16816(acc[nt][(u & ~1) + m], a, ph[nt][ks][0], ph[nt][ks][1]);
-                        if (!kTwice) mma16816(acc[nt][(u & ~1) + m], a, pl[nt][ks][0], pl[nt][ks][1]);
+                        for (int e = 0; e < 4; ++e) sum[nt][m][e] = 0.0f;
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    const int x = x0 + ks, u = u0 + x;
+                    const uint4 hd = *(const uint4 *)(vh + (u * 4 + c) * 16);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        uint32_t a[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            a[i] = value_pair<BITS>(BITS == 4 ? w[(2 * x + m) & 3] : w[x & 3], BITS == 4 ? i : 4 * m + i,
+                                                    i < 2 ? hd.x : hd.z, i < 2 ? hd.y : hd.w);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816(sum[nt][m], a, ph[nt][ks][0], ph[nt][ks][1]);
+                            if (!kTwice) mma16816(sum[nt][m], a, pl[nt][ks][0], pl[nt][ks][1]);
+                            if (P3) mma16816(sum[nt][m], a, pt[P3 ? nt : 0][ks][0], pt[P3 ? nt : 0][ks][1]);
+                        }
                     }
                 }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float &o = acc[nt][u0 + x0 + m][e];
+                            o = fmaf(o, al[nt][e & 1], sum[nt][m][e]);
+                        }
             }
         }
         __syncwarp();
@@ -646,7 +666,7 @@ Plan plan_of(const DenseGeom &g, int H, int nq)
     return p;
 }
 
-template <int D, int BITS, int NT0>
+template <int D, int BITS, int NT0, bool P3 = false>
 cudaError_t run_split(const DenseGeom &g, const Plan &p, int H, const void *q, int nq, const rkv_dense_cache *c,
                       const int32_t *len, const int32_t *blocks, int lists, int n_blocks, float scale_log2,
                       float *part, float2 *ml, int32_t *status, cudaStream_t s)
@@ -655,11 +675,11 @@ cudaError_t run_split(const DenseGeom &g, const Plan &p, int H, const void *q, i
     static PerDevice<int> setup;
     int unused = 0;
     cudaError_t e = per_device(setup, unused, [](int &) {
-        return cudaFuncSetAttribute(k_dense_split<D, BITS, NT0>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        return cudaFuncSetAttribute(k_dense_split<D, BITS, NT0, P3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (e != cudaSuccess) return e;
     ProfScope prof("dense_attention_split", s);
-    k_dense_split<D, BITS, NT0><<<(unsigned)((size_t)p.runs * g.N * p.tiles), 32 * kWarps, C::kSmem, s>>>(
+    k_dense_split<D, BITS, NT0, P3><<<(unsigned)((size_t)p.runs * g.N * p.tiles), 32 * kWarps, C::kSmem, s>>>(
         (const __nv_bfloat16 *)q, (const uint8_t *)c->codes, (const uint8_t *)c->khdr, len, blocks, lists, n_blocks,
         g.S, g.T, g.N, H / g.N, nq, g.nb, p.cut, p.tiles, scale_log2, part, ml, status);
     return cudaGetLastError();
@@ -731,8 +751,12 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
         cudaError_t e;
         if (p.tree)
             e = launch_dense_tree(g, H, q, nq, cache, len, p.cut, scale_log2, out_dtype == RKV_F32, part, ml, status, s);
+        else if (p.nt == 0 && out_dtype == RKV_F32)
+            e = run_split<D, B, 0, true>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
         else if (p.nt == 0)
             e = run_split<D, B, 0>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
+        else if (p.nt == 1 && out_dtype == RKV_F32)
+            e = run_split<D, B, 1, true>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
         else if (p.nt == 1)
             e = run_split<D, B, 1>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
         else if (p.nt == 2)
