@@ -285,8 +285,10 @@ rkv_status rkv_dense_sizes(const rkv_dense_params *p, size_t *codes_bytes, size_
  * kv: [S][n][2 N D] in kv_dtype (RKV_F32 rows are rounded to bf16 first), K of all heads
  * then V of all heads, as in rkv_compress; keys as the queries will meet them (rotated, if
  * the model rotates).  Blocks that these rows finish are quantised; rows of the last,
- * unfinished block go to the tail.  The tokens before pos[s] must have been written, and
- * pos[s] must not lie before the start of the unfinished block.
+ * unfinished block go to the tail.  The tokens before pos[s] must have been written.  pos[s]
+ * is the sequence's length, any other place in its unfinished block, or the start of any
+ * block (a sequence cut back to that length, or begun anew at 0): a finished block's bf16
+ * rows are gone, so that it cannot be gone on with from inside.
  * pos, n_new: int32 [S], device; n_new may be NULL: n rows for every sequence.  Where
  * pos < 0, n_new is outside [0, n] or pos + n_new > T, RKV_ERR_INDEX is set and nothing of
  * that sequence is written.  n may be 1 (a decode step) or any prompt length.            */
@@ -328,7 +330,8 @@ rkv_status rkv_block_select(const rkv_dense_params *p, int32_t H, const void *q,
  * is skipped; an entry < -1 or >= floor(len/32) sets RKV_ERR_INDEX and is skipped; a block
  * listed twice enters twice.  A sequence with nothing to attend gives zeros.
  * q: bf16 [S][H][D]; out: [S][H][D] in out_dtype (RKV_F32 or RKV_BF16).  Scores, softmax and
- * sums in fp32; probabilities meet the values as bf16 hi + lo (relative error about 2^-16).
+ * sums in fp32; probabilities meet the values of finished blocks as bf16 in two parts (relative
+ * error 2^-16), for fp32 outputs in three.
  * workspace: >= the bytes of rkv_dense_attention_workspace(p, H, 1), 256-byte
  * aligned.  Requires H a multiple of N, H/N <= 8.                               */
 rkv_status rkv_dense_attention_workspace(const rkv_dense_params *p, int32_t H, int32_t n_query, size_t *bytes);
@@ -345,9 +348,9 @@ rkv_status rkv_dense_attention(const rkv_dense_params *p, int32_t H, const void 
  * that is padding, set RKV_ERR_INDEX and give zero rows for the tokens whose line holds it.
  * draft_kv: bf16 [S][n_draft][2 N D], K then V, as for rkv_dense_write; the cache is not
  * changed (accepted tokens are written with rkv_dense_write).  What lies in rows that a
- * token does not see has no effect on it, NaN included.  Probabilities meet the values as
- * in rkv_dense_attention, except for more than 32 query rows to a KV head (n_draft H/N) of
- * D <= 128 with bf16 outputs: there as bf16 (2^-8 for each, half a step of the outputs).
+ * token does not see has no effect on it, NaN included.  Probabilities meet the values of
+ * finished blocks as bf16 in two parts; where a KV head has more than 32 query rows (n_draft
+ * H/N) of D <= 128 and outputs are bf16, in one (2^-8 for each, half a step of the outputs).
  * q: bf16 [S][n_draft][H][D]; out: [S][n_draft][H][D] in out_dtype.  1 <= n_draft <= 64.
  * workspace: >= the bytes of rkv_dense_attention_workspace(p, H, n_draft), 256-byte
  * aligned.  Requires H a multiple of N, H/N <= 8.                                        */

@@ -71,10 +71,10 @@ __device__ __forceinline__ int value_slot(int g, int c) { return 8 * c + ((g + 2
 // ---- how finished blocks are dealt out ---------------------------------------------------
 // The blocks to attend (of all sequences, for one KV head) are cut into runs of at most `chunk`
 // blocks of one sequence, numbered through; chunk follows from the lengths that the device
-// holds, so that a batch of uneven or short sequences fills the GPU as full ones do: one of a
-// few sizes from the ideal on that makes no more than `target` runs (or one run for every
-// sequence, where there are at least `target` sequences).  So there are at most
-// max(target, S) runs (the host's grid and workspace).  One warp works it out for its CTA.
+// holds, so that a batch of uneven or short sequences fills the GPU as full ones do: about
+// all / target blocks, or up to 5/8 more where that brings the runs down to `target` (a CTA
+// for each at a time).  There are at most target + S of them (the host's grid and workspace).
+// One warp works it out for its CTA.
 struct DenseCut {
     int target, unit, least;                 // wanted runs; chunk is a multiple of unit, at least `least`
 };
@@ -101,28 +101,19 @@ __device__ __forceinline__ int dense_chunk(const int32_t *len, int S, int T, int
 {
     const int lane = threadIdx.x & 31;
     long long all = __reduce_add_sync(0xffffffffu, n0);    // n0: blocks of sequence `lane`
-    int most = __reduce_max_sync(0xffffffffu, n0);
-    for (int s0 = 32; s0 < S; s0 += 32) {
-        const int n = blocks_of(len, s0 + lane, S, T, listed, status);
-        all += __reduce_add_sync(0xffffffffu, n);
-        most = max(most, __reduce_max_sync(0xffffffffu, n));
-    }
-    most = max(most, 1);
-    if (S >= c.target) return most;
-    const float ideal = (float)all / (float)c.target;
-    for (int k = 0; k < 6; ++k) {                          // 1, 1.125, ... times the ideal
-        const int want = max(c.least, (int)(ideal * (1.0f + 0.125f * (float)k)) + 1);
-        const int chunk = (want + c.unit - 1) / c.unit * c.unit;
-        if (chunk >= most) return chunk;                   // a run for every sequence: S < target
+    for (int s0 = 32; s0 < S; s0 += 32)
+        all += __reduce_add_sync(0xffffffffu, blocks_of(len, s0 + lane, S, T, listed, status));
+    const int ideal = max(c.least, (int)((all + c.target - 1) / c.target));
+    const int tries = S < c.target ? 6 : 0;
+    for (int k = 0; k < tries; ++k) {                      // 1, 1.125, ... times the ideal
+        const int chunk = (ideal + (int)((long long)ideal * k >> 3) + c.unit - 1) / c.unit * c.unit;
         const float inv = 1.0f / (float)chunk;
         int runs = __reduce_add_sync(0xffffffffu, runs_of(n0, chunk, inv));
         for (int s0 = 32; s0 < S; s0 += 32)
             runs += __reduce_add_sync(0xffffffffu, runs_of(blocks_of(len, s0 + lane, S, T, listed, status), chunk, inv));
         if (runs <= c.target) return chunk;
     }
-    // sum of ceil(n / chunk) <= all / chunk + S
-    const int want = max(c.least, (int)((all + c.target - S - 1) / (c.target - S)));
-    return (want + c.unit - 1) / c.unit * c.unit;
+    return (ideal + c.unit - 1) / c.unit * c.unit;
 }
 // Inclusive sum over the lanes.
 __device__ __forceinline__ int lane_scan(int v)

@@ -186,6 +186,9 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
         const int st = k % C::kStages;
         const bool landed = um::mbar_wait(bars + st, (uint32_t)(k / C::kStages) & 1u, kWaitCycles);
         if (!__all_sync(0xffffffffu, landed)) {
+            // what is on its way gets as long again; the partial is given up either way
+            for (int i = k; i < issued; ++i)
+                um::mbar_wait(bars + i % C::kStages, (uint32_t)(i / C::kStages) & 1u, kWaitCycles);
             ok = false;
             break;
         }
@@ -662,7 +665,7 @@ Plan plan_of(const DenseGeom &g, int H, int nq)
         p.cut.least = kWarps;
     }
     p.cut.target = max(1, ctas / (g.N * p.tiles));
-    p.runs = max(p.cut.target, g.S);
+    p.runs = p.cut.target + g.S;
     return p;
 }
 

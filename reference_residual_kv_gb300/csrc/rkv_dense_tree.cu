@@ -544,7 +544,7 @@ cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dens
     if (e != cudaSuccess) return e;
     const int tiles = (nq * (H / g.N) + 255) / 256;
     ProfScope prof("dense_attention_tree", s);
-    k_dense_tree<D, BITS, LO><<<(unsigned)((size_t)max(cut.target, g.S) * g.N * tiles), kThreads, C::kSmem, s>>>(
+    k_dense_tree<D, BITS, LO><<<(unsigned)((size_t)(cut.target + g.S) * g.N * tiles), kThreads, C::kSmem, s>>>(
         (const __nv_bfloat16 *)q, (const uint8_t *)c->codes, (const uint8_t *)c->khdr, len, g.S, g.T, g.N, H / g.N,
         nq, g.nb, cut, tiles, scale_log2, part, ml, status);
     return cudaGetLastError();

@@ -618,6 +618,9 @@ k_dense_read(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
             const uint8_t *rec = stage + st * C::kStage;
             const bool here = um::mbar_wait(bars + st, (uint32_t)(used / C::kStages) & 1u, kWaitCycles);
             if (!__all_sync(0xffffffffu, here)) {
+                // what is on its way gets as long again
+                for (int i = used; i < issued; ++i)
+                    um::mbar_wait(bars + i % C::kStages, (uint32_t)(i / C::kStages) & 1u, kWaitCycles);
                 set_status(status, RKV_ERR_DEVICE_TIMEOUT);
                 return;
             }

@@ -6,6 +6,8 @@ Two views are kept apart:
   Sec. V-A): with beta = H_full / H the share of full-attention layers,
       q_b = b/16 + 2/32                      (b-bit payload + two FP16 extremes per 32)
       KR  = beta q_4 + (1 - beta)(rho_ref / 2 + q_b d_c / (2 d_k));
+  (the dense cache of the full-attention layers stores exactly q_b: two bf16 numbers per 32
+  codes, dense_layer_bytes_per_token);
 * the bytes this library actually stores per token (fp32 group extremes, so that a
   constant group is kept exactly, and the per-token reference relation, which the
   paper's KR leaves out).
@@ -38,3 +40,9 @@ def layer_bytes_per_token(W: int, d_c: int, bits: int, stride: int, ref_elem_byt
     (a reference's record is all zero but present, which keeps random access uniform),
     and one token in `stride` also keeps its reference vector."""
     return record_bytes(d_c, bits, group, k) + W * ref_elem_bytes / stride
+
+
+def dense_layer_bytes_per_token(N: int, D: int, bits: int) -> float:
+    """Stored bytes per token of one layer-sequence of the dense cache (finished blocks of 32
+    tokens: K and V codes, a bf16 minimum and step for each 32 of them)."""
+    return 2 * N * D * (bits / 8 + 4 / 32)

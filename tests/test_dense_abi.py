@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import _dense_oracle as do
-from reference_residual_kv_gb300 import build, rkv
+from reference_residual_kv_gb300 import build, rkv, storage
 
 INVALID, UNSUPPORTED = rkv.RKV_ERR_INVALID_ARG, rkv.RKV_ERR_UNSUPPORTED
 ALIGN, WORKSPACE = rkv.RKV_ERR_ALIGNMENT, rkv.RKV_ERR_WORKSPACE
@@ -28,6 +28,14 @@ def test_sizes(lib):
     assert codes == 2 * 4 * 31 * 128 * 36 and khdr == 2 * 4 * 31 * 512 and tail == 2 * 4 * 2 * 32 * 128 * 2
     assert rkv.rkv_dense_sizes(params(T=31, bits=2))[:2] == (0, 0)
     assert codes + khdr == 2 * 4 * 31 * 32 * 2 * 128 * 5 // 8
+
+
+def test_stored_bytes_are_the_paper_s_share(lib):
+    # a layer-sequence of whole blocks: the accounting's bytes, and q_b of the fp16 cache's
+    for D, bits in ((64, 2), (128, 4), (256, 2), (256, 4)):
+        codes, khdr, _ = rkv.rkv_dense_sizes(params(S=1, T=640, N=3, D=D, bits=bits))
+        per_token = storage.dense_layer_bytes_per_token(3, D, bits)
+        assert (codes + khdr) / 640 == per_token == storage.q_b(bits) * 2 * 3 * D * 2
 
 
 @pytest.mark.parametrize("field,value,code", [

@@ -533,6 +533,88 @@ def test_captured_steps_replay_on_new_lengths_and_other_streams():
     case.check_all()
 
 
+def test_many_sequences_of_all_lengths():
+    # more sequences than a warp has lanes, empty ones among them, one far longer than the rest:
+    # single tokens, lists and trees, for both ways of cutting the blocks into runs (fewer
+    # sequences than runs, and more)
+    rng = np.random.default_rng(71)
+    for S, N, G, n in ((35, 8, 1, 6), (70, 1, 2, 20)):
+        lens = [int(x) for x in rng.integers(0, 130, S)]
+        lens[0], lens[7], lens[33], lens[S - 1] = 0, 1600, 64, 1
+        case = Case(make_rows(rng, S, 1600, N, 64), lens, 4)
+        q = do.bf16(rng.normal(size=(S, N * G, 64)))
+        check_attend(case, q, attend_gpu(case, q))
+        blocks = select_gpu(case, q, N, 3, 1, 0)
+        for s in range(S):
+            assert np.array_equal(blocks[s], do.select(q[s], case.held(s)[2], 3, 1, 0, False))
+        check_attend(case, q, attend_gpu(case, q, blocks), blocks)
+        qt, draft, parent = do.bf16(rng.normal(size=(S, n, N * G, 64))), make_rows(rng, S, n, N, 64), random_tree(rng, S, n)
+        check_tree(case, qt, parent, draft, tree_gpu(case, qt, parent, draft))
+        case.done()
+
+
+def test_selection_over_more_blocks_than_shared_memory_holds():
+    # 42000 blocks of one head; all keys equal but for nine blocks that stand out: those, the
+    # kept ends, and the lowest of the others
+    ensure_lib()
+    T = 42000 * 32 + 5
+    c = rkv.DenseCache(rkv.make_dense_params(1, T, 1, 64, 2), guard=GUARD)
+    kv = torch.full((1, T, 128), 0.5, dtype=torch.bfloat16, device="cuda")
+    high = [3, 40959, 40960, 40961, 41000, 20000, 20001, 77, 39999]
+    for b in high:
+        kv[0, 32 * b + b % 32, 9] = 2.0
+    c.write(kv, i32([0]))
+    q = torch.ones(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    for n, first, last in ((9, 0, 0), (40, 1, 2), (5000, 3, 0), (5, 0, 0)):
+        blocks = out_buffer((1, 1, n), torch.int32)
+        c.select(1, q, i32([T]), blocks, keep_first=first, keep_last=last)
+        want = set(range(first)) | set(range(42000 - last, 42000))
+        for b in sorted(high) + list(range(42000)):
+            if len(want) < n:
+                want.add(b)
+        assert blocks[0, 0].tolist() == sorted(want), n
+    torch.cuda.synchronize()
+    assert c.device_status() == 0 and not c.guard_violations()
+    assert_guards()
+
+
+def test_a_sequence_is_cut_back_or_begun_anew_at_a_block():
+    rng = np.random.default_rng(81)
+    rows = make_rows(rng, 2, 200, 2, 64)
+    case = Case(rows, [200, 150], 4)
+    new = make_rows(rng, 2, 75, 2, 64)
+    case.c.write(to_bf16(new.reshape(2, 75, -1)), i32([96, 0]), i32([75, 50]))
+    rows[0, 96:171], rows[1, :50] = new[0], new[1, :50]
+    case.lens = [171, 50]
+    case.len = i32(case.lens)
+    case.check_all()
+
+
+def test_readers_of_one_cache_at_once():
+    # single tokens and a tree on two streams, over and over: each with scratch of its own
+    rng = np.random.default_rng(91)
+    case = Case(make_rows(rng, 2, 3000, 2, 128), [3000, 1700], 4)
+    q, qt = to_bf16(rng.normal(size=(2, 8, 128))), to_bf16(rng.normal(size=(2, 16, 8, 128)))
+    dr, pa = to_bf16(rng.normal(size=(2, 16, 512))), i32(random_tree(rng, 2, 16))
+    outs = [torch.empty(2, 8, 128, device="cuda"), torch.empty(2, 16, 8, 128, device="cuda")]
+    c = rkv.DenseCache(case.c.p)
+    c.write(to_bf16(case.rows.reshape(2, 3000, -1)), i32([0, 0]), case.len)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    want = None
+    for i in range(30):
+        outs[0].zero_(), outs[1].zero_()
+        torch.cuda.synchronize()
+        c.attend(8, q, case.len, outs[0], stream=streams[0])
+        c.tree_attend(8, qt, pa, dr, case.len, outs[1], stream=streams[1].cuda_stream)
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        if want is None:
+            want = got
+            assert all(o.isfinite().all() for o in outs)
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), i
+
+
 def test_offsets_past_32_bits():
     # 2000 sequences: codes, input rows and outputs pass 2^32 bytes; the last one is checked
     S, N, D, T = 2000, 8, 128, 1920
