@@ -73,10 +73,11 @@ __device__ __forceinline__ int value_slot(int g, int c) { return 8 * c + ((g + 2
 // blocks of one sequence, numbered through; chunk follows from the lengths that the device
 // holds, so that a batch of uneven or short sequences fills the GPU as full ones do: about
 // all / target blocks, or up to 5/8 more where that brings the runs down to `target` (a CTA
-// for each at a time).  There are at most target + S of them (the host's grid and workspace).
+// for each at a time).  There are at most max(target, capacity / most) + S of them (the host's
+// grid and workspace).
 // One warp works it out for its CTA.
 struct DenseCut {
-    int target, unit, least;                 // wanted runs; chunk is a multiple of unit, at least `least`
+    int target, unit, least, most;           // wanted runs; chunk: a multiple of unit, from least to most
 };
 struct DenseRun { int s, first, end, slot; };   // s < 0: none
 
@@ -103,10 +104,11 @@ __device__ __forceinline__ int dense_chunk(const int32_t *len, int S, int T, int
     long long all = __reduce_add_sync(0xffffffffu, n0);    // n0: blocks of sequence `lane`
     for (int s0 = 32; s0 < S; s0 += 32)
         all += __reduce_add_sync(0xffffffffu, blocks_of(len, s0 + lane, S, T, listed, status));
-    const int ideal = max(c.least, (int)((all + c.target - 1) / c.target));
+    const int ideal = min(c.most, max(c.least, (int)((all + c.target - 1) / c.target)));
     const int tries = S < c.target ? 6 : 0;
     for (int k = 0; k < tries; ++k) {                      // 1, 1.125, ... times the ideal
         const int chunk = (ideal + (int)((long long)ideal * k >> 3) + c.unit - 1) / c.unit * c.unit;
+        if (chunk > c.most) break;
         const float inv = 1.0f / (float)chunk;
         int runs = __reduce_add_sync(0xffffffffu, runs_of(n0, chunk, inv));
         for (int s0 = 32; s0 < S; s0 += 32)
@@ -215,7 +217,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
 // The finished blocks against many query rows (rkv_dense_tree.cu), D <= 128: two partials for
 // each run and KV head.
 cudaError_t launch_dense_tree(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *cache,
-                              const int32_t *len, const DenseCut &cut, float scale_log2, bool p_lo, float *part,
+                              const int32_t *len, const DenseCut &cut, int runs, float scale_log2, bool p_lo, float *part,
                               float2 *ml, int32_t *status, cudaStream_t s);
 
 }  // namespace rkv

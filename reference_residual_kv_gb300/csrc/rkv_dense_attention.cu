@@ -19,6 +19,7 @@
 #include "rkv_dense.cuh"
 #include "umma.cuh"
 
+#include <limits.h>
 #include <math.h>
 
 namespace rkv {
@@ -643,7 +644,7 @@ struct Plan {
     DenseCut cut;
 };
 
-Plan plan_of(const DenseGeom &g, int H, int nq)
+Plan plan_of(const DenseGeom &g, int H, int nq, bool f32)
 {
     Plan p;
     const int R = nq * (H / g.N);
@@ -653,7 +654,11 @@ Plan plan_of(const DenseGeom &g, int H, int nq)
         p.nt = 0;
         p.each = 2;
         p.tiles = (R + 255) / 256;
-        ctas = 152;                                        // one to an SM
+        // one to an SM; for fp32 outputs no run above 96 blocks, since the products' accumulators
+        // cut what they add (64 drafts over 131072 tokens, error against 64 bits: 6.7e-6 at 216
+        // blocks and 289 us, 3.1e-6 at 96 blocks and 395 us; smaller work is not cut finer)
+        ctas = 152;
+        p.cut.most = f32 ? 96 : INT_MAX / 2;
         p.cut.unit = 8;
         p.cut.least = 16;
     } else {
@@ -661,15 +666,16 @@ Plan plan_of(const DenseGeom &g, int H, int nq)
         p.each = 1;
         p.tiles = p.nt ? (R + 8 * p.nt - 1) / (8 * p.nt) : 1;
         ctas = 304;
+        p.cut.most = INT_MAX / 2;
         p.cut.unit = kWarps;
         p.cut.least = kWarps;
     }
     p.cut.target = max(1, ctas / (g.N * p.tiles));
-    p.runs = p.cut.target + g.S;
+    p.runs = (int)max((long long)p.cut.target, (long long)g.S * g.nb / p.cut.most + 1) + g.S;
     return p;
 }
 
-template <int D, int BITS, int NT0, bool P3 = false>
+template <int D, int BITS, int NT0, bool P3>
 cudaError_t run_split(const DenseGeom &g, const Plan &p, int H, const void *q, int nq, const rkv_dense_cache *c,
                       const int32_t *len, const int32_t *blocks, int lists, int n_blocks, float scale_log2,
                       float *part, float2 *ml, int32_t *status, cudaStream_t s)
@@ -734,7 +740,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq)
 {
-    const Plan p = plan_of(g, H, nq);
+    const Plan p = plan_of(g, H, nq, true);                // the larger one
     const size_t rows = (size_t)p.runs * p.each * nq * H;
     return align256(rows * g.D * sizeof(float)) + align256(rows * sizeof(float2));
 }
@@ -744,7 +750,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
                                    const int32_t *blocks, int lists, int n_blocks, void *out, int out_dtype,
                                    void *ws, int32_t *status, cudaStream_t s)
 {
-    const Plan p = plan_of(g, H, nq);
+    const Plan p = plan_of(g, H, nq, out_dtype == RKV_F32);
     const size_t rows = (size_t)p.runs * p.each * nq * H;
     float *part = (float *)ws;
     float2 *ml = (float2 *)((uint8_t *)ws + align256(rows * g.D * sizeof(float)));
@@ -752,22 +758,28 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
     auto go = [&](auto bits, auto d) -> cudaError_t {
         constexpr int B = decltype(bits)::value, D = decltype(d)::value;
         cudaError_t e;
+        auto split = [&](auto third) -> cudaError_t {
+            constexpr bool P3 = decltype(third)::value;
+            auto by = [&](auto nt) -> cudaError_t {
+                return run_split<D, B, decltype(nt)::value, P3>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks,
+                                                                scale_log2, part, ml, status, s);
+            };
+            using std::integral_constant;
+            switch (p.nt) {
+            case 0: return by(integral_constant<int, 0>{});
+            case 1: return by(integral_constant<int, 1>{});
+            case 2: return by(integral_constant<int, 2>{});
+            default:
+                if constexpr (D < 256) return by(integral_constant<int, 4>{});
+                return cudaErrorInvalidValue;
+            }
+        };
         if (p.tree)
-            e = launch_dense_tree(g, H, q, nq, cache, len, p.cut, scale_log2, out_dtype == RKV_F32, part, ml, status, s);
-        else if (p.nt == 0 && out_dtype == RKV_F32)
-            e = run_split<D, B, 0, true>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
-        else if (p.nt == 0)
-            e = run_split<D, B, 0>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
-        else if (p.nt == 1 && out_dtype == RKV_F32)
-            e = run_split<D, B, 1, true>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
-        else if (p.nt == 1)
-            e = run_split<D, B, 1>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
-        else if (p.nt == 2)
-            e = run_split<D, B, 2>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
-        else if constexpr (D < 256)
-            e = run_split<D, B, 4>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks, scale_log2, part, ml, status, s);
+            e = launch_dense_tree(g, H, q, nq, cache, len, p.cut, p.runs, scale_log2, out_dtype == RKV_F32, part, ml, status, s);
+        else if (out_dtype == RKV_F32)
+            e = split(std::true_type{});
         else
-            e = cudaErrorInvalidValue;
+            e = split(std::false_type{});
         if (e != cudaSuccess) return e;
         return run_finish<D>(g, p, H, q, nq, blocks ? n_blocks : 0, parent, draft, cache, len, scale_log2, part, ml, out, out_dtype, status, s);
     };

@@ -21,8 +21,9 @@
 //                in fp32 sums and has the same relative error in bf16), so that the output
 //                accumulator is rescaled only where the maximum grows by more than that; P
 //                goes back to tensor memory, over the scores, as the first operand of P V.
-// P is bf16 for bf16 outputs (2^-9 for each p, as the output's own rounding) and bf16
-// hi + lo for fp32 outputs (2^-17).
+// P is bf16 for bf16 outputs (2^-8 for each p, half a step, as the output's own rounding), and
+// three parts of bf16 for fp32 outputs; those take the columns of both buffers, so that there
+// is one.
 // All waits are bounded; a CTA whose wait runs out sets RKV_ERR_DEVICE_TIMEOUT and writes NaN
 // as its partials' maxima, so that its rows read NaN.
 #include "rkv_dense.cuh"
@@ -185,6 +186,7 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
              int32_t *status)
 {
     using C = TreeCfg<D, BITS>;
+    constexpr int kBufs = LO ? 1 : 2;                      // buffers for a half's scores and P
     extern __shared__ uint8_t smem_raw[];
     uint8_t *qs = smem_raw + ((1024u - (um::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *kt = qs + C::kQ, *vt = kt + 2 * C::kTile, *ring = vt + 2 * C::kTile;
@@ -283,29 +285,28 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
         // scores of step j: K is there, and the output product that read P from the same buffer
         // is complete.  A tile's operands are free after each half's last step in it.
         auto scores = [&](int j) {
-            const int g = step_of(t, j), b = (g >> 1) & 1, buf = j & 1;
+            const int g = step_of(t, j), b = (g >> 1) & 1;
             wait(k_full + b, g >> 2);
-            if (j >= 2) wait(o_done + 2 * t + buf, (j >> 1) - 1);
+            if (j >= kBufs) wait(o_done + 2 * t + j % kBufs, j / kBufs - 1);
             if (!ok) return;
             um::tc_fence_after();
             if (elect_one()) {
                 const uint64_t k0 = kd + b * kTileD + (g & 1) * (kStep * 128 / 16);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    um::mma_bf16(tm + kColS + buf * kStep, qd + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
+                    um::mma_bf16(tm + kColS + j % kBufs * kStep, qd + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
                                  k0 + (k >> 2) * (kTok * 128 / 16) + 2 * (k & 3), id_s, k != 0);
-                um::mma_commit(s_full + 2 * t + buf);
+                um::mma_commit(s_full + 2 * t + j % kBufs);
                 if (!two || (g & 1)) um::mma_commit(k_empty + b);
             }
             __syncwarp();
         };
         wait(q_full, 0);
-        if (end > 0 && ok) scores(0);
-        if (end > 1 && ok) scores(1);
+        for (int j = 0; j < min(kBufs, end) && ok; ++j) scores(j);
         for (int j = 0; j < end && ok; ++j) {
-            const int g = step_of(t, j), b = (g >> 1) & 1, buf = j & 1;
+            const int g = step_of(t, j), b = (g >> 1) & 1, buf = j % kBufs;
             wait(v_full + b, g >> 2);
-            wait(p_full + 2 * t + buf, j >> 1);
+            wait(p_full + 2 * t + buf, j / kBufs);
             if (!ok) break;
             um::tc_fence_after();
             if (elect_one()) {
@@ -315,13 +316,16 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
                 for (int k = 0; k < kStep / 16; ++k) {
                     const uint32_t ak = a + 32 * (k >> 1) + 8 * (k & 1);
                     mma_bf16_ta(tm, ak, v + 2 * k, id_o, (j | k) != 0);
-                    if (LO) mma_bf16_ta(tm, ak + 16, v + 2 * k, id_o, 1);
+                    if (LO) {
+                        mma_bf16_ta(tm, ak + 16, v + 2 * k, id_o, 1);
+                        mma_bf16_ta(tm, a + kStep + 8 * k, v + 2 * k, id_o, 1);
+                    }
                 }
                 um::mma_commit(o_done + 2 * t + buf);
                 if (!two || (g & 1)) um::mma_commit(v_empty + b);
             }
             __syncwarp();
-            if (j + 2 < end) scores(j + 2);
+            if (j + kBufs < end) scores(j + kBufs);
         }
         if (lane == 0 && !ok) *abort_flag = 1;
         // every issued product completes before tensor memory is released
@@ -413,8 +417,8 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
         bool ok = true;
         const int end = count_of(t);
         for (int j = 0; j < end; ++j) {
-            const int buf = j & 1;
-            bool here = !*abort_flag && um::mbar_wait(s_full + 2 * t + buf, (uint32_t)(j >> 1) & 1u, kWaitCycles);
+            const int buf = j % kBufs;
+            bool here = !*abort_flag && um::mbar_wait(s_full + 2 * t + buf, (uint32_t)(j / kBufs) & 1u, kWaitCycles);
             if (!__all_sync(0xffffffffu, here)) { ok = false; break; }
             um::tc_fence_after();
             if (busy) {
@@ -441,7 +445,7 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
                     const float f = move ? (m_ref == -INFINITY ? 0.0f : ex2(m_ref - top)) : 1.0f;
                     if (j > 0) {
                         // the last step's output product may still be under way
-                        here = um::mbar_wait(o_done + 2 * t + (buf ^ 1), (uint32_t)((j - 1) >> 1) & 1u, kWaitCycles);
+                        here = um::mbar_wait(o_done + 2 * t + (j - 1) % kBufs, (uint32_t)((j - 1) / kBufs) & 1u, kWaitCycles);
                         if (!__all_sync(0xffffffffu, here)) { ok = false; break; }
                         um::tc_fence_after();
 #pragma unroll 1
@@ -461,10 +465,11 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
                 const float mu = m_ref == -INFINITY ? 0.0f : m_ref;
                 const float2 sc2 = make_float2(scale_log2, scale_log2), mu2 = make_float2(-mu, -mu);
                 float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                // 32 tokens of P in columns 32 k .. + 15, of its second part behind them
+                // 32 tokens of P in columns 32 k .. + 15, of its second part behind them, of its
+                // third part in the other buffer's columns 16 k ..
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    uint32_t hi[16], lo[16];
+                    uint32_t hi[16], lo[16], th[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float2 x = __ffma2_rn(make_float2(v[k][2 * e], v[k][2 * e + 1]), sc2, mu2);
@@ -472,10 +477,18 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
                         sums[e & 1] = __fadd2_rn(sums[e & 1], pp);
                         const __nv_bfloat162 h2 = __floats2bfloat162_rn(pp.x, pp.y);
                         hi[e] = as_u32(h2);
-                        if (LO) lo[e] = as_u32(__floats2bfloat162_rn(pp.x - __low2float(h2), pp.y - __high2float(h2)));
+                        if (LO) {
+                            const float rx = pp.x - __low2float(h2), ry = pp.y - __high2float(h2);
+                            const __nv_bfloat162 l2 = __floats2bfloat162_rn(rx, ry);
+                            lo[e] = as_u32(l2);
+                            th[e] = as_u32(__floats2bfloat162_rn(rx - __low2float(l2), ry - __high2float(l2)));
+                        }
                     }
                     tmem_st16(ts + 32 * k, hi);
-                    if (LO) tmem_st16(ts + 32 * k + 16, lo);
+                    if (LO) {
+                        tmem_st16(ts + 32 * k + 16, lo);
+                        tmem_st16(ts + kStep + 16 * k, th);
+                    }
                 }
                 l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
                 tmem_wait_st();
@@ -485,7 +498,7 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
             if (lane == 0) um::mbar_arrive(p_full + 2 * t + buf);
         }
         if (ok && end > 0) {
-            const bool here = um::mbar_wait(o_done + 2 * t + ((end - 1) & 1), (uint32_t)((end - 1) >> 1) & 1u, kWaitCycles);
+            const bool here = um::mbar_wait(o_done + 2 * t + (end - 1) % kBufs, (uint32_t)((end - 1) / kBufs) & 1u, kWaitCycles);
             ok = __all_sync(0xffffffffu, here);
             um::tc_fence_after();
         }
@@ -533,7 +546,7 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
 
 template <int D, int BITS, bool LO>
 cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *c, const int32_t *len,
-                const DenseCut &cut, float scale_log2, float *part, float2 *ml, int32_t *status, cudaStream_t s)
+                const DenseCut &cut, int runs, float scale_log2, float *part, float2 *ml, int32_t *status, cudaStream_t s)
 {
     using C = TreeCfg<D, BITS>;
     static PerDevice<int> setup;
@@ -544,7 +557,7 @@ cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dens
     if (e != cudaSuccess) return e;
     const int tiles = (nq * (H / g.N) + 255) / 256;
     ProfScope prof("dense_attention_tree", s);
-    k_dense_tree<D, BITS, LO><<<(unsigned)((size_t)(cut.target + g.S) * g.N * tiles), kThreads, C::kSmem, s>>>(
+    k_dense_tree<D, BITS, LO><<<(unsigned)((size_t)runs * g.N * tiles), kThreads, C::kSmem, s>>>(
         (const __nv_bfloat16 *)q, (const uint8_t *)c->codes, (const uint8_t *)c->khdr, len, g.S, g.T, g.N, H / g.N,
         nq, g.nb, cut, tiles, scale_log2, part, ml, status);
     return cudaGetLastError();
@@ -553,14 +566,14 @@ cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dens
 }  // namespace
 
 cudaError_t launch_dense_tree(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *c,
-                              const int32_t *len, const DenseCut &cut, float scale_log2, bool p_lo, float *part,
+                              const int32_t *len, const DenseCut &cut, int runs, float scale_log2, bool p_lo, float *part,
                               float2 *ml, int32_t *status, cudaStream_t s)
 {
     auto go = [&](auto bits, auto d) -> cudaError_t {
         constexpr int B = decltype(bits)::value, D = decltype(d)::value;
         if constexpr (D <= 128)
-            return p_lo ? run<D, B, true>(g, H, q, nq, c, len, cut, scale_log2, part, ml, status, s)
-                        : run<D, B, false>(g, H, q, nq, c, len, cut, scale_log2, part, ml, status, s);
+            return p_lo ? run<D, B, true>(g, H, q, nq, c, len, cut, runs, scale_log2, part, ml, status, s)
+                        : run<D, B, false>(g, H, q, nq, c, len, cut, runs, scale_log2, part, ml, status, s);
         else
             return cudaErrorInvalidValue;
     };
