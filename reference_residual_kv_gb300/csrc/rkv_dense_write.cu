@@ -11,7 +11,9 @@
 //                  keys (or values) become bf16 for all 32 tokens (one stmatrix for 256 of
 //                  them) in the warp's row buffer, from which the asked rows leave as 16-byte stores;
 //                  records come by bulk copies, one block ahead.  A block that fewer than
-//                  kTogether of the entries ask for is read for each of its tokens alone.
+//                  kTogether of the entries ask for is read for that token alone (4 x 131072
+//                  tokens, 1 / 6 / 12 % of them: 65 / 120 / 150 us; all by blocks 74 / 131 / 153,
+//                  blocks from 4 entries on 66 / 138 / 163).
 #include "rkv_dense.cuh"
 #include "umma.cuh"
 
@@ -20,7 +22,7 @@ namespace {
 
 constexpr int kWriteWarps = 4;
 constexpr int kReadWarps = 2;
-constexpr int kTogether = 4;
+constexpr int kTogether = 2;
 constexpr int kSets = 2;                     // sets of 32 entries of a warp
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src)
@@ -254,11 +256,8 @@ __device__ __forceinline__ void unit_codes(const uint32_t (&r)[2][4], const uint
     }
 }
 
-// 16-byte chunk ch of row r in a warp's row buffer (swizzled: ldmatrix and stmatrix touch 8
-// rows of one chunk at a time)
-template <int D> __device__ __forceinline__ int row_chunk(int r, int ch) { return r * (D / 8) + (ch ^ (r & 7)); }
-// The same in the buffer of the write: tiles of 32 rows x 64 channels, as TMA swizzles rows of
-// 128 bytes.
+// 16-byte chunk ch of row r in a warp's row buffer: tiles of 32 rows x 64 channels, swizzled as
+// TMA swizzles rows of 128 bytes (ldmatrix and stmatrix touch 8 rows of one chunk at a time).
 __device__ __forceinline__ int tile_chunk(int r, int ch) { return (ch >> 3) * 256 + r * 8 + ((ch & 7) ^ (r & 7)); }
 
 template <int D, int BITS, typename TIN>
@@ -460,13 +459,15 @@ __device__ __forceinline__ void read_token(const uint8_t *cd, const uint8_t *hp,
 }
 
 // Keys (or values) of a whole finished block, its record in shared memory, as rows [32][D] in
-// the warp's buffer (row_chunk).
+// the warp's buffer (tile_chunk).
 template <int D, int BITS, bool VALUES>
 __device__ __forceinline__ void read_block(const uint8_t *cd, const uint8_t *hd, int lane, uint4 *buf)
 {
     constexpr int kPer = 8 / BITS, kCh = (D / 16) / kPer;
     const int g = lane >> 2, c = lane & 3, i = lane >> 3;
-    const uint32_t base = um::smem_u32(buf);
+    // stmatrix: lane's place for unit 0, operand 0, as in k_dense_write
+    const uint32_t base = um::smem_u32(buf) + 16 * (VALUES ? tile_chunk(8 * (i >> 1) + (lane & 7), i & 1)
+                                                           : tile_chunk(8 * (i & 1) + (lane & 7), i >> 1));
     const uint8_t *slot = cd + (VALUES ? value_slot(g, c) : key_slot(g, c)) * 16;
 #pragma unroll
     for (int j = 0; j < kCh; ++j) {
@@ -485,10 +486,9 @@ __device__ __forceinline__ void read_block(const uint8_t *cd, const uint8_t *hd,
                                             e < 2 ? h.x : h.z, e < 2 ? h.y : h.w);
                 // keys: rows of the operand are tokens; values: its columns are
                 if (VALUES)
-                    stmatrix4_trans(base + 16 * row_chunk<D>(16 * (u & 1) + 8 * (i >> 1) + (lane & 7),
-                                                             4 * (u >> 1) + 2 * m + (i & 1)), a);
+                    stmatrix4_trans((base ^ ((((u >> 1) & 1) << 6) | (m << 5))) + (u >> 2) * 4096 + (u & 1) * 2048, a);
                 else
-                    stmatrix4(base + 16 * row_chunk<D>(16 * m + 8 * (i & 1) + (lane & 7), 2 * u + (i >> 1)), a);
+                    stmatrix4((base ^ ((u & 3) << 5)) + (u >> 2) * 4096 + m * 2048, a);
             }
         }
     }
@@ -633,7 +633,7 @@ k_dense_read(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
                 uint32_t left = of_now[k];
                 while (left) {
                     const int i = next_rows(left), o = __shfl_sync(0xffffffffu, t[k], max(i, 0)) & 31;
-                    if (i >= 0) row_of(32 * k + i)[lane % kCh] = buf[row_chunk<D>(o, lane % kCh)];
+                    if (i >= 0) row_of(32 * k + i)[lane % kCh] = buf[tile_chunk(o, lane % kCh)];
                 }
             }
             __syncwarp();
