@@ -458,25 +458,26 @@ __device__ __forceinline__ void read_token(const uint8_t *cd, const uint8_t *hp,
     }
 }
 
-// Keys (or values) of a whole finished block, its record in shared memory, as rows [32][D] in
-// the warp's buffer (tile_chunk).
-template <int D, int BITS, bool VALUES>
-__device__ __forceinline__ void read_block(const uint8_t *cd, const uint8_t *hd, int lane, uint4 *buf)
+// 64 channels, from 64 part on, of the keys (or values) of a whole finished block, its record in
+// shared memory, as rows [32][64] in the warp's buffer (tile_chunk).
+template <int BITS, bool VALUES>
+__device__ __forceinline__ void read_block(const uint8_t *cd, const uint8_t *hd, int part, int lane, uint4 *buf)
 {
-    constexpr int kPer = 8 / BITS, kCh = (D / 16) / kPer;
+    constexpr int kPer = 8 / BITS;
     const int g = lane >> 2, c = lane & 3, i = lane >> 3;
     // stmatrix: lane's place for unit 0, operand 0, as in k_dense_write
     const uint32_t base = um::smem_u32(buf) + 16 * (VALUES ? tile_chunk(8 * (i >> 1) + (lane & 7), i & 1)
                                                            : tile_chunk(8 * (i & 1) + (lane & 7), i >> 1));
-    const uint8_t *slot = cd + (VALUES ? value_slot(g, c) : key_slot(g, c)) * 16;
+    const uint8_t *slot = cd + (VALUES ? value_slot(g, c) : key_slot(g, c)) * 16 + part * (4 / kPer) * 512;
+    const uint8_t *heads = hd + (part * 16 + c) * 16;
 #pragma unroll
-    for (int j = 0; j < kCh; ++j) {
+    for (int j = 0; j < 4 / kPer; ++j) {
         const uint4 q = *(const uint4 *)(slot + j * 512);
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int x = 0; x < kPer; ++x) {
-            const int u = j * kPer + x;
-            const uint4 h = *(const uint4 *)(hd + (u * 4 + c) * 16);
+            const int u = j * kPer + x;                    // of the part's four units
+            const uint4 h = *(const uint4 *)(heads + u * 64);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 uint32_t a[4];
@@ -485,10 +486,8 @@ __device__ __forceinline__ void read_block(const uint8_t *cd, const uint8_t *hd,
                     a[e] = value_pair<BITS>(BITS == 4 ? w[(2 * x + m) & 3] : w[x & 3], BITS == 4 ? e : 4 * m + e,
                                             e < 2 ? h.x : h.z, e < 2 ? h.y : h.w);
                 // keys: rows of the operand are tokens; values: its columns are
-                if (VALUES)
-                    stmatrix4_trans((base ^ ((((u >> 1) & 1) << 6) | (m << 5))) + (u >> 2) * 4096 + (u & 1) * 2048, a);
-                else
-                    stmatrix4((base ^ ((u & 3) << 5)) + (u >> 2) * 4096 + m * 2048, a);
+                if (VALUES) stmatrix4_trans((base ^ (((u >> 1) << 6) | (m << 5))) + (u & 1) * 2048, a);
+                else stmatrix4((base ^ (u << 5)) + m * 2048, a);
             }
         }
     }
@@ -497,9 +496,11 @@ __device__ __forceinline__ void read_block(const uint8_t *cd, const uint8_t *hd,
 template <int D, int BITS>
 struct ReadCfg {
     static constexpr int kUnit = 4 * D * BITS, kRec = 2 * kUnit + 4 * D, kHdr = 4 * D, kStage = kUnit + kHdr;
-    static constexpr int kStages = 2, kRows = kBlk * D * 2;
+    static constexpr int kStages = 2, kRows = kBlk * 64 * 2;
     static_assert(kStages >= 2, "one block is read while the next one is on its way");
-    static constexpr int kWarp = kStages * kStage + kRows;       // a warp's shared memory
+    static constexpr int kWarp = kRows + kStages * kStage + 128; // a warp's shared memory: 32 rows of 64
+                                                                 // channels, records, a list of entries
+    static_assert(kWarp % 128 == 0, "the rows' places are flipped bits of their addresses");
     static constexpr int kSmem = kReadWarps * (kWarp + kStages * 8);
 };
 
@@ -514,8 +515,9 @@ k_dense_read(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kCh = D / 8;                             // 16-byte chunks of a row
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint8_t *stage = smem + (size_t)warp * C::kWarp;
-    uint4 *buf = (uint4 *)(stage + C::kStages * C::kStage);
+    uint4 *buf = (uint4 *)(smem + (size_t)warp * C::kWarp);
+    uint8_t *stage = (uint8_t *)buf + C::kRows;
+    uint16_t *rows = (uint16_t *)(stage + C::kStages * C::kStage);   // entry * 32 + token of the block
     uint64_t *bars = (uint64_t *)(smem + (size_t)kReadWarps * C::kWarp) + warp * C::kStages;
     const long long id = (long long)blockIdx.x * kReadWarps + warp;
     const bool is_v = id & 1;
@@ -625,15 +627,24 @@ k_dense_read(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
                 return;
             }
             ++used;
-            if (is_v) read_block<D, BITS, true>(rec, rec + C::kUnit, lane, buf);
-            else read_block<D, BITS, false>(rec, rec + C::kUnit, lane, buf);
-            __syncwarp();
+            int n = 0;
 #pragma unroll
             for (int k = 0; k < kSets; ++k) {
-                uint32_t left = of_now[k];
-                while (left) {
-                    const int i = next_rows(left), o = __shfl_sync(0xffffffffu, t[k], max(i, 0)) & 31;
-                    if (i >= 0) row_of(32 * k + i)[lane % kCh] = buf[tile_chunk(o, lane % kCh)];
+                if ((of_now[k] >> lane) & 1u)
+                    rows[n + __popc(of_now[k] & ((1u << lane) - 1u))] = (uint16_t)((32 * k + lane) * 32 + (t[k] & 31));
+                n += __popc(of_now[k]);
+            }
+#pragma unroll 1
+            for (int part = 0; part < D / 64; ++part) {
+                __syncwarp();
+                if (is_v) read_block<BITS, true>(rec, rec + C::kUnit, part, lane, buf);
+                else read_block<BITS, false>(rec, rec + C::kUnit, part, lane, buf);
+                __syncwarp();
+                // a row takes 8 lanes
+#pragma unroll 2
+                for (int r = lane >> 3; r < n; r += 4) {
+                    const int x = rows[r];
+                    row_of(x >> 5)[8 * part + (lane & 7)] = buf[tile_chunk(x & 31, lane & 7)];
                 }
             }
             __syncwarp();
