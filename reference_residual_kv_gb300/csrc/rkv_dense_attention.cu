@@ -11,8 +11,9 @@
 //                   multiplies: scores^T = K q^T and out^T = V^T p^T, 16 x 8 x 16, so that
 //                   the 32 tokens (or 32 channels) fill the operand's rows and the few
 //                   query rows its columns.  Probabilities go from one product to the
-//                   other by movmatrix, as bf16 hi + lo.  Softmax: running maximum and sum
-//                   for each warp, in base 2.  No masks: a finished block is whole.
+//                   other by movmatrix, as bf16 in two or three parts.  Softmax: running
+//                   reference and sum for each warp, in base 2.  No masks: a finished block
+//                   is whole.
 //   k_dense_finish  the bf16 rows of the unfinished block and the drafted tokens that a row
 //                   sees (the values of a token that it does not see are not touched), while
 //                   the first kernel still runs, then the merge of the runs' partials.
@@ -235,23 +236,35 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
         }
         // softmax: rows 2c, 2c + 1 of each column tile; this lane's tokens are 16 m + g, + 8
         uint32_t ph[NT][2][2], pl[NT][2][2], pt[P3 ? NT : 1][2][2];
-        float al[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+            // against a running reference that lags the maximum by at most 8: it moves, and the
+            // sums are rescaled, where a score is more than that above it
             float mx[2];
+            bool move = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float v = fmaxf(fmaxf(sc[nt][0][e], sc[nt][0][e + 2]), fmaxf(sc[nt][1][e], sc[nt][1][e + 2]));
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-                mx[e] = fmaxf(m_run[nt][e], v * scale_log2);
-                al[nt][e] = ex2(m_run[nt][e] - (mx[e] == -INFINITY ? 0.0f : mx[e]));
+                mx[e] = fmaxf(fmaxf(sc[nt][0][e], sc[nt][0][e + 2]), fmaxf(sc[nt][1][e], sc[nt][1][e + 2])) * scale_log2;
+                move = move || mx[e] > m_run[nt][e] + 8.0f;
             }
-            l_run[nt][0] *= al[nt][0];
-            l_run[nt][1] *= al[nt][1];
-            m_run[nt][0] = mx[0];
-            m_run[nt][1] = mx[1];
-            const float o0 = mx[0] == -INFINITY ? 0.0f : mx[0], o1 = mx[1] == -INFINITY ? 0.0f : mx[1];
+            if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
+                    mx[e] = fmaxf(m_run[nt][e], mx[e]);
+                    const float al = ex2(m_run[nt][e] - (mx[e] == -INFINITY ? 0.0f : mx[e]));
+                    m_run[nt][e] = mx[e];
+                    l_run[nt][e] *= al;
+#pragma unroll
+                    for (int i = 0; i < 2 * (D / 32); ++i) {
+                        acc[nt][i][e] *= al;
+                        acc[nt][i][e + 2] *= al;
+                    }
+                }
+            }
+            const float o0 = m_run[nt][0] == -INFINITY ? 0.0f : m_run[nt][0];
+            const float o1 = m_run[nt][1] == -INFINITY ? 0.0f : m_run[nt][1];
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -315,10 +328,7 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float &o = acc[nt][u0 + x0 + m][e];
-                            o = fmaf(o, al[nt][e & 1], sum[nt][m][e]);
-                        }
+                        for (int e = 0; e < 4; ++e) acc[nt][u0 + x0 + m][e] += sum[nt][m][e];
             }
         }
         __syncwarp();
