@@ -356,6 +356,11 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
             const uint8_t *cd = rec + (is_v ? C::kUnit : 0) + slot;
             const uint8_t *hp = rec + (is_v ? 2 * C::kUnit : C::kRec) + c * 16;
             bool here = !*abort_flag && um::mbar_wait(empty + b, ((uint32_t)(i >> 1) & 1u) ^ 1u, kWaitCycles);
+            // A parity names a phase only to a thread that knows the phase before to be complete, that
+            // is, block blk - kSlots to have landed.  With two tiles of slots it is in a tile that has
+            // been multiplied; with fewer it may be in the last one, another warp's.
+            if (C::kSlots < 8 && i > 0)
+                here = here && um::mbar_wait(full + ((i - 1) & 1), (uint32_t)((i - 1) >> 1) & 1u, kWaitCycles);
             if (there) here = here && um::mbar_wait(raw_full + st, (uint32_t)(blk / C::kSlots) & 1u, kWaitCycles);
             if (!__all_sync(0xffffffffu, here)) { ok = false; break; }
 #pragma unroll
