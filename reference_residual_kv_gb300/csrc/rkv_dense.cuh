@@ -69,53 +69,23 @@ __device__ __forceinline__ int key_slot(int g, int c) { return 4 * g + c; }
 __device__ __forceinline__ int value_slot(int g, int c) { return 8 * c + ((g + 2 * c) & 7); }
 
 // ---- how finished blocks are dealt out ---------------------------------------------------
-// The blocks to attend (of all sequences, for one KV head) are cut into runs of at most `chunk`
-// blocks of one sequence, numbered through; chunk follows from the lengths that the device
-// holds, so that a batch of uneven or short sequences fills the GPU as full ones do: about
-// all / target blocks, or up to 5/8 more where that brings the runs down to `target` (a CTA
-// for each at a time).  There are at most max(target, capacity / most) + S of them (the host's
-// grid and workspace).
-// One warp works it out for its CTA.
+// The blocks to attend (of all sequences behind one another, for one KV head) are dealt to
+// CTAs in equal shares of `per` blocks, which follows from the lengths that the device holds:
+// a batch of uneven or short sequences fills the GPU as full ones do.  A share may reach over
+// several sequences; its part of one sequence is a run, with a partial of its own.  CTA i's
+// run of sequence s has number i + s: the numbers of a sequence's runs follow one another, and
+// no two runs have the same (the next CTA's first sequence is this one's last, or a later one).
 struct DenseCut {
-    int target, unit, least, most;           // wanted runs; chunk: a multiple of unit, from least to most
+    int ctas, unit, least, most;             // wanted CTAs; per: a multiple of unit, from least to most
 };
-struct DenseRun { int s, first, end, slot; };   // s < 0: none
+struct DenseRun { int s, first, end, slot; };   // blocks first .. end - 1 of sequence s; s < 0: none
+struct DenseCursor { int at, end, s0, base; };  // block reached; the share's end; sequences s0 .. begin at block base
 
 // blocks of sequence s: finished ones, or the entries of its list
 __device__ __forceinline__ int blocks_of(const int32_t *len, int s, int S, int T, int listed, int32_t *status)
 {
     if (s >= S) return 0;
     return listed ? listed : dense_len(len, s, T, status) / kBlk;
-}
-// ceil(n / chunk) for 0 <= n < 2^27: the fp32 quotient is off by less than 2^4, relative to at
-// most 2^27, and its multiple is put right.
-__device__ __forceinline__ int runs_of(int n, int chunk, float inv)
-{
-    int r = (int)((float)n * inv);
-    int left = n - r * chunk;
-    while (left > 0) { ++r; left -= chunk; }
-    while (left <= -chunk) { --r; left += chunk; }
-    return r;
-}
-__device__ __forceinline__ int dense_chunk(const int32_t *len, int S, int T, int listed, const DenseCut &c, int n0,
-                                           int32_t *status)
-{
-    const int lane = threadIdx.x & 31;
-    long long all = __reduce_add_sync(0xffffffffu, n0);    // n0: blocks of sequence `lane`
-    for (int s0 = 32; s0 < S; s0 += 32)
-        all += __reduce_add_sync(0xffffffffu, blocks_of(len, s0 + lane, S, T, listed, status));
-    const int ideal = min(c.most, max(c.least, (int)((all + c.target - 1) / c.target)));
-    const int tries = S < c.target ? 6 : 0;
-    for (int k = 0; k < tries; ++k) {                      // 1, 1.125, ... times the ideal
-        const int chunk = (ideal + (int)((long long)ideal * k >> 3) + c.unit - 1) / c.unit * c.unit;
-        if (chunk > c.most) break;
-        const float inv = 1.0f / (float)chunk;
-        int runs = __reduce_add_sync(0xffffffffu, runs_of(n0, chunk, inv));
-        for (int s0 = 32; s0 < S; s0 += 32)
-            runs += __reduce_add_sync(0xffffffffu, runs_of(blocks_of(len, s0 + lane, S, T, listed, status), chunk, inv));
-        if (runs <= c.target) return chunk;
-    }
-    return (ideal + c.unit - 1) / c.unit * c.unit;
 }
 // Inclusive sum over the lanes.
 __device__ __forceinline__ int lane_scan(int v)
@@ -128,41 +98,58 @@ __device__ __forceinline__ int lane_scan(int v)
     }
     return v;
 }
-// Run number p, by one warp.
-__device__ __forceinline__ DenseRun dense_run(const int32_t *len, int S, int T, int listed, const DenseCut &c, int p,
+// {blocks in all, per}, by one warp.
+__device__ __forceinline__ int2 dense_shares(const int32_t *len, int S, int T, int listed, const DenseCut &c,
+                                             int32_t *status)
+{
+    const int lane = threadIdx.x & 31;
+    int all = 0;
+    for (int s0 = 0; s0 < S; s0 += 32)
+        all += __reduce_add_sync(0xffffffffu, blocks_of(len, s0 + lane, S, T, listed, status));
+    const int per = min(c.most, max(c.least, (int)(((long long)all + c.ctas - 1) / c.ctas)));
+    return make_int2(all, (per + c.unit - 1) / c.unit * c.unit);
+}
+// CTA i's share.
+__device__ __forceinline__ DenseCursor dense_share(int2 all, int i)
+{
+    return DenseCursor{(int)min((long long)i * all.y, (long long)all.x),
+                       (int)min(((long long)i + 1) * all.y, (long long)all.x), 0, 0};
+}
+// The next run of CTA i, by one warp.
+__device__ __forceinline__ DenseRun dense_run(const int32_t *len, int S, int T, int listed, int i, DenseCursor &c,
                                               int32_t *status)
 {
-    const int lane = threadIdx.x & 31, n0 = blocks_of(len, lane, S, T, listed, status);
-    const int chunk = dense_chunk(len, S, T, listed, c, n0, status);
-    const float inv = 1.0f / (float)chunk;
-    int base = 0;
-    for (int s0 = 0; s0 < S; s0 += 32) {
-        const int n = s0 ? blocks_of(len, s0 + lane, S, T, listed, status) : n0, runs = runs_of(n, chunk, inv);
-        const int upto = base + lane_scan(runs);
-        const uint32_t hit = __ballot_sync(0xffffffffu, p < upto);
+    const int lane = threadIdx.x & 31;
+    if (c.at >= c.end) return DenseRun{-1, 0, 0, 0};
+    for (; c.s0 < S; c.s0 += 32) {
+        const int n = blocks_of(len, c.s0 + lane, S, T, listed, status), upto = c.base + lane_scan(n);
+        const uint32_t hit = __ballot_sync(0xffffffffu, c.at < upto);
         if (hit) {
-            const int l = __ffs(hit) - 1;
-            const int k = p - __shfl_sync(0xffffffffu, upto - runs, l);
-            const int left = __shfl_sync(0xffffffffu, n, l) - k * chunk;
-            return DenseRun{s0 + l, k * chunk, k * chunk + min(left, chunk), p};
+            const int l = __ffs(hit) - 1, s = c.s0 + l;
+            const int begin = __shfl_sync(0xffffffffu, upto - n, l), stop = min(c.end, __shfl_sync(0xffffffffu, upto, l));
+            const DenseRun r{s, c.at - begin, stop - begin, i + s};
+            c.at = stop;
+            return r;
         }
-        base = __shfl_sync(0xffffffffu, upto, 31);
+        c.base = __shfl_sync(0xffffffffu, upto, 31);
     }
+    c.at = c.end;                            // lengths that changed under the call
     return DenseRun{-1, 0, 0, 0};
 }
 // The runs of sequence s, by one warp: first number in .first, one past the last in .end.
 __device__ __forceinline__ DenseRun dense_runs_of(const int32_t *len, int S, int T, int listed, const DenseCut &c, int s,
                                                   int32_t *status)
 {
-    const int lane = threadIdx.x & 31, n0 = blocks_of(len, lane, S, T, listed, status);
-    const int chunk = dense_chunk(len, S, T, listed, c, n0, status);
-    const float inv = 1.0f / (float)chunk;
+    const int lane = threadIdx.x & 31;
+    const int per = dense_shares(len, S, T, listed, c, status).y;
     int base = 0;
     for (int s0 = 0; s0 <= s; s0 += 32) {
-        const int n = s0 ? blocks_of(len, s0 + lane, S, T, listed, status) : n0, runs = runs_of(n, chunk, inv);
-        const int upto = base + lane_scan(runs);
-        if (s < s0 + 32)
-            return DenseRun{s, __shfl_sync(0xffffffffu, upto - runs, s - s0), __shfl_sync(0xffffffffu, upto, s - s0), 0};
+        const int n = blocks_of(len, s0 + lane, S, T, listed, status), upto = base + lane_scan(n);
+        if (s < s0 + 32) {
+            const int begin = __shfl_sync(0xffffffffu, upto - n, s - s0), stop = __shfl_sync(0xffffffffu, upto, s - s0);
+            if (begin == stop) break;
+            return DenseRun{s, begin / per + s, (stop - 1) / per + s + 1, 0};
+        }
         base = __shfl_sync(0xffffffffu, upto, 31);
     }
     return DenseRun{s, 0, 0, 0};
@@ -217,7 +204,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
 // The finished blocks against many query rows (rkv_dense_tree.cu), D <= 128: two partials for
 // each run and KV head.
 cudaError_t launch_dense_tree(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *cache,
-                              const int32_t *len, const DenseCut &cut, int runs, float scale_log2, bool p_lo, float *part,
+                              const int32_t *len, const DenseCut &cut, int ctas, float scale_log2, bool p_lo, float *part,
                               float2 *ml, int32_t *status, cudaStream_t s);
 
 }  // namespace rkv

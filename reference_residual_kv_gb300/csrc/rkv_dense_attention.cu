@@ -103,37 +103,53 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 sml[kWarps][8 * NT];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    // the row tiles of a run are neighbours, then its KV heads: they read the same blocks
-    const int tile = blockIdx.x % tiles, n = blockIdx.x / tiles % N;
+    // the row tiles of a share are neighbours, then its KV heads: they read the same blocks
+    const int tile = blockIdx.x % tiles, n = blockIdx.x / tiles % N, share = blockIdx.x / tiles / N;
+    const int listed = blocks ? n_blocks : 0;
     __shared__ DenseRun run_s;
+    __shared__ DenseCursor cursor_s;
     if (warp == 0) {
-        const DenseRun r = dense_run(len, S, T, blocks ? n_blocks : 0, cut, blockIdx.x / tiles / N, status);
-        if (lane == 0) run_s = r;
+        const DenseCursor at = dense_share(dense_shares(len, S, T, listed, cut, status), share);
+        if (lane == 0) cursor_s = at;
+        __syncwarp();
     }
-    __syncthreads();
-    const DenseRun run = run_s;
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (run.s < 0) return;
-    const int s = run.s, sn = s * N + n, i0 = run.first, i1 = run.end;
     const int R = nq * G, row0 = tile * 8 * NT;
     uint8_t *ring = smem + warp * C::kStages * C::kStage;
     uint64_t *bars = (uint64_t *)(smem + C::kBody + C::kQ) + warp * C::kStages;
-    const int have = blocks ? dense_len(len, s, T, status) / kBlk : 0;
-    const int32_t *list = blocks ? blocks + ((size_t)s * lists + (lists > 1 ? n : 0)) * n_blocks : nullptr;
     if (lane == 0) {
         for (int i = 0; i < C::kStages; ++i) um::mbar_init(bars + i, 1);
         um::fence_mbar_init();
     }
-    __syncwarp();
+    int issued = 0, used = 0;
+    bool ok = true;
+  // one run after another; a share rarely has more than two
+#pragma unroll 1
+  while (true) {
+    if (warp == 0) {
+        DenseCursor at = cursor_s;
+        const DenseRun r = dense_run(len, S, T, listed, share, at, status);
+        __syncwarp();
+        if (lane == 0) {
+            run_s = r;
+            cursor_s = at;
+        }
+    }
+    __syncthreads();
+    const DenseRun run = run_s;
+    if (run.s < 0) return;
+    const int s = run.s, sn = s * N + n, i0 = run.first, i1 = run.end;
+    const int have = blocks ? dense_len(len, s, T, status) / kBlk : 0;
+    const int32_t *list = blocks ? blocks + ((size_t)s * lists + (lists > 1 ? n : 0)) * n_blocks : nullptr;
     // the warp's blocks: i0 + warp, + 8, ..., those that are to be skipped left out
-    int next = i0 + warp, issued = 0;
+    int next = i0 + warp;
     auto issue = [&]() {
         int b = -1;
         while (next < i1 && b < 0) {
             b = block_at(list, next, have, status);
             next += kWarps;
         }
-        if (b < 0) return;
+        if (b < 0 || !ok) return;
         if (lane == 0) {
             const int st = issued % C::kStages;
             uint8_t *dst = ring + st * C::kStage;
@@ -181,15 +197,14 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
         m_run[nt][0] = m_run[nt][1] = -INFINITY;
         l_run[nt][0] = l_run[nt][1] = 0.0f;
     }
-    bool ok = true;
     const int kslot = key_slot(g, c) * 16, vslot = value_slot(g, c) * 16;
 #pragma unroll 1
-    for (int k = 0; k < issued; ++k) {
-        const int st = k % C::kStages;
-        const bool landed = um::mbar_wait(bars + st, (uint32_t)(k / C::kStages) & 1u, kWaitCycles);
+    for (; used < issued && ok; ++used) {
+        const int st = used % C::kStages;
+        const bool landed = um::mbar_wait(bars + st, (uint32_t)(used / C::kStages) & 1u, kWaitCycles);
         if (!__all_sync(0xffffffffu, landed)) {
-            // what is on its way gets as long again; the partial is given up either way
-            for (int i = k; i < issued; ++i)
+            // what is on its way gets as long again; the partials are given up either way
+            for (int i = used; i < issued; ++i)
                 um::mbar_wait(bars + i % C::kStages, (uint32_t)(i / C::kStages) & 1u, kWaitCycles);
             ok = false;
             break;
@@ -386,10 +401,14 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
             o.w = fmaf(v.w, f, o.w);
             l = fmaf(sml[w][r].y, f, l);
         }
-        const size_t at = ((size_t)run.slot * N + n) * R + row0 + r;
-        *(float4 *)(part + at * D + d) = o;
-        if (d == 0) ml[at] = make_float2(bad ? __uint_as_float(0x7fffffffu) : m, l);
+        const size_t to = ((size_t)run.slot * N + n) * R + row0 + r;
+        *(float4 *)(part + to * D + d) = o;
+        if (d == 0) ml[to] = make_float2(bad ? __uint_as_float(0x7fffffffu) : m, l);
     }
+    // the next run's copies go over what was merged
+    um::fence_proxy_async_smem();
+    __syncthreads();
+  }
 }
 
 // The last pass: 8 / wpr query rows of a KV head per CTA, wpr warps for each.  Tokens that are
@@ -650,7 +669,7 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
 // so that the workspace's size and the order of the sums do not either.
 struct Plan {
     bool tree;
-    int tiles, nt, each, runs;               // row tiles of a CTA's size; partials of a run; most runs
+    int tiles, nt, each, ctas, slots;        // row tiles of a CTA's size; partials of a run; most shares and runs
     DenseCut cut;
 };
 
@@ -660,28 +679,28 @@ Plan plan_of(const DenseGeom &g, int H, int nq, bool f32)
     const int R = nq * (H / g.N);
     p.tree = R > 32 && g.D <= 128;
     int ctas;
+    p.cut.unit = 8;
+    p.cut.most = INT_MAX / 2;
     if (p.tree) {
         p.nt = 0;
         p.each = 2;
         p.tiles = (R + 255) / 256;
-        // one to an SM; for fp32 outputs no run above 96 blocks, since the products' accumulators
+        // one to an SM; for fp32 outputs no share above 96 blocks, since the products' accumulators
         // cut what they add (64 drafts over 131072 tokens, error against 64 bits: 6.7e-6 at 216
         // blocks and 289 us, 3.1e-6 at 96 blocks and 395 us; smaller work is not cut finer)
         ctas = 152;
-        p.cut.most = f32 ? 96 : INT_MAX / 2;
-        p.cut.unit = 8;
+        if (f32) p.cut.most = 96;
         p.cut.least = 16;
     } else {
         p.nt = R <= 4 ? 0 : (R <= 8 ? 1 : (R <= 16 || g.D == 256 ? 2 : 4));
         p.each = 1;
         p.tiles = p.nt ? (R + 8 * p.nt - 1) / (8 * p.nt) : 1;
         ctas = 304;
-        p.cut.most = INT_MAX / 2;
-        p.cut.unit = kWarps;
         p.cut.least = kWarps;
     }
-    p.cut.target = max(1, ctas / (g.N * p.tiles));
-    p.runs = (int)max((long long)p.cut.target, (long long)g.S * g.nb / p.cut.most + 1) + g.S;
+    p.cut.ctas = max(1, ctas / (g.N * p.tiles));
+    p.ctas = (int)max((long long)p.cut.ctas, (long long)g.S * g.nb / p.cut.most + 1);
+    p.slots = p.ctas + g.S;
     return p;
 }
 
@@ -698,7 +717,7 @@ cudaError_t run_split(const DenseGeom &g, const Plan &p, int H, const void *q, i
     });
     if (e != cudaSuccess) return e;
     ProfScope prof("dense_attention_split", s);
-    k_dense_split<D, BITS, NT0, P3><<<(unsigned)((size_t)p.runs * g.N * p.tiles), 32 * kWarps, C::kSmem, s>>>(
+    k_dense_split<D, BITS, NT0, P3><<<(unsigned)((size_t)p.ctas * g.N * p.tiles), 32 * kWarps, C::kSmem, s>>>(
         (const __nv_bfloat16 *)q, (const uint8_t *)c->codes, (const uint8_t *)c->khdr, len, blocks, lists, n_blocks,
         g.S, g.T, g.N, H / g.N, nq, g.nb, p.cut, p.tiles, scale_log2, part, ml, status);
     return cudaGetLastError();
@@ -751,7 +770,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq)
 {
     const Plan p = plan_of(g, H, nq, true);                // the larger one
-    const size_t rows = (size_t)p.runs * p.each * nq * H;
+    const size_t rows = (size_t)p.slots * p.each * nq * H;
     return align256(rows * g.D * sizeof(float)) + align256(rows * sizeof(float2));
 }
 
@@ -761,7 +780,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
                                    void *ws, int32_t *status, cudaStream_t s)
 {
     const Plan p = plan_of(g, H, nq, out_dtype == RKV_F32);
-    const size_t rows = (size_t)p.runs * p.each * nq * H;
+    const size_t rows = (size_t)p.slots * p.each * nq * H;
     float *part = (float *)ws;
     float2 *ml = (float2 *)((uint8_t *)ws + align256(rows * g.D * sizeof(float)));
     const float scale_log2 = (float)(1.4426950408889634 / sqrt((double)g.D));
@@ -785,7 +804,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
             }
         };
         if (p.tree)
-            e = launch_dense_tree(g, H, q, nq, cache, len, p.cut, p.runs, scale_log2, out_dtype == RKV_F32, part, ml, status, s);
+            e = launch_dense_tree(g, H, q, nq, cache, len, p.cut, p.ctas, scale_log2, out_dtype == RKV_F32, part, ml, status, s);
         else if (out_dtype == RKV_F32)
             e = split(std::true_type{});
         else

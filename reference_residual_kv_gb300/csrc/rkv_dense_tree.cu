@@ -4,8 +4,9 @@
 // With R query rows a block's codes are turned into bf16 once for all of them, and both
 // products are large: scores = Q K^T (M = 128 rows, N = 128 tokens, K = D) and
 // out = P V (M = 128 rows, N = D, K = 128 tokens), accumulators in tensor memory.  A CTA has
-// a run of blocks of one (sequence, KV head), in tiles of 128 tokens, and up to 256 rows as
-// two row tiles.  A half of the CTA has a row tile and walks through steps of 64 tokens, with
+// a share of a KV head's blocks: runs of blocks of one sequence each, in tiles of 128 tokens, with
+// the copies and products of one run after those of the other without a pause; and up to 256 rows
+// as two row tiles.  A half of the CTA has a row tile and walks through steps of 64 tokens, with
 // two buffers for the scores, so that the next scores are computed while it is at its softmax;
 // with 128 rows or fewer both halves have the same rows and take the steps in turn.
 //   warp 0       producer: block records (codes, extremes) by bulk copies into a ring
@@ -64,7 +65,7 @@ struct TreeCfg {
     static constexpr int kSlots = D == 128 && BITS == 4 ? 5 : 8;
     static constexpr int kSmem = kQ + 4 * kTile + kSlots * kBlkBytes + 512 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory of the tree pass");
-    static_assert(8 * 32 * 33 * 4 <= 4 * kTile, "the outputs' staging takes the operand tiles");
+    static_assert(8 * 32 * 32 * 4 <= kQ, "the outputs' staging takes the query rows' place");
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -172,6 +173,18 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
 }
 
+// barrier 1 of the rows' 256 threads: whether p holds for all of them
+__device__ __forceinline__ bool bar_all(bool p)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((uint32_t)p) : "memory");
+    return r != 0;
+}
+
 // byte of 16-byte chunk ch of row r in a K-major tile of `rows` rows, 64 bf16 to a row of 128 bytes
 __device__ __forceinline__ uint32_t tile_at(int rows, int r, int ch)
 {
@@ -192,25 +205,31 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
     uint8_t *kt = qs + C::kQ, *vt = kt + 2 * C::kTile, *ring = vt + 2 * C::kTile;
     uint64_t *raw_full = (uint64_t *)(ring + C::kSlots * C::kBlkBytes), *raw_empty = raw_full + C::kSlots;
     uint64_t *k_full = raw_empty + C::kSlots, *k_empty = k_full + 2, *v_full = k_empty + 2, *v_empty = v_full + 2;
-    uint64_t *s_full = v_empty + 2, *p_full = s_full + 4, *o_done = p_full + 4, *q_full = o_done + 4, *drain = q_full + 1;
+    uint64_t *s_full = v_empty + 2, *p_full = s_full + 4, *o_done = p_full + 4, *q_full = o_done + 4, *drain = q_full + 4;
     uint32_t *tmem_slot = (uint32_t *)(drain + 2);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tile = blockIdx.x % tiles, n = blockIdx.x / tiles % N;
+    const int tile = blockIdx.x % tiles, n = blockIdx.x / tiles % N, share = blockIdx.x / tiles / N;
+    __shared__ int2 share_s;
     __shared__ DenseRun run_s;
     if (warp == 0) {
-        const DenseRun r = dense_run(len, S, T, 0, cut, blockIdx.x / tiles / N, status);
-        if (lane == 0) run_s = r;
+        const int2 all = dense_shares(len, S, T, 0, cut, status);
+        if (lane == 0) share_s = all;
     }
     __syncthreads();
-    const DenseRun run = run_s;
+    DenseCursor cursor = dense_share(share_s, share);
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (run.s < 0) return;
-    const int s = run.s, sn = s * N + n, b0 = run.first, blocks = run.end - run.first;
+    if (cursor.at >= cursor.end) return;
     const int R = nq * G, row0 = tile * 256, rows = min(256, R - row0);
     const bool two = rows > 128;                           // two row tiles, or two halves of the tokens
-    const int nt = (blocks + 3) / 4, ns = (blocks + 1) / 2;   // token tiles, steps
+    // Every warp walks through the share's runs by itself: blocks, token tiles and steps count on
+    // over them, and so do the barriers' phases.
+    auto next_run = [&]() { return dense_run(len, S, T, 0, share, cursor, status); };
+    auto tiles_of = [](int blocks) { return (blocks + 3) / 4; };
+    // the j-th step of half t in a run of ns: all steps with two row tiles, else every other one
+    auto step_of = [&](int t, int j) { return two ? j : 2 * j + t; };
+    auto count_of = [&](int t, int ns) { return two ? ns : (ns + 1 - t) / 2; };
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             um::mbar_init(raw_full + i, 1);
@@ -227,7 +246,7 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
             um::mbar_init(p_full + i, 4);
             um::mbar_init(o_done + i, 1);
         }
-        um::mbar_init(q_full, 8);
+        for (int i = 0; i < 4; ++i) um::mbar_init(q_full + i, 8);
         um::mbar_init(drain, 1);
         um::mbar_init(drain + 1, 1);
         *abort_flag = 0;
@@ -241,38 +260,44 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
     __syncthreads();
     um::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // the j-th step of half t: all steps with two row tiles, else every other one
-    auto step_of = [&](int t, int j) { return two ? j : 2 * j + t; };
-    auto count_of = [&](int t) { return two ? ns : (ns + 1 - t) / 2; };
-
     if (warp < 4) regs_down<kRegsFew>();
     if (warp == 0) {
-        if (lane == 0) {
-            int i = 0;
-            bool ok = true;
-            for (; i < blocks && ok; ++i) {
-                const int st = i % C::kSlots;
-                // slot i % kSlots is free once block i - kSlots has been turned into bf16
-                long long t0 = clock64();
-                while (!um::mbar_try_wait(raw_empty + st, ((uint32_t)(i / C::kSlots) & 1u) ^ 1u))
-                    if (*abort_flag || clock64() - t0 > kWaitCycles) { ok = false; break; }
-                if (!ok) break;
-                const size_t rec = (size_t)sn * nb + b0 + i;
-                uint8_t *dst = ring + st * C::kBlkBytes;
-                um::mbar_arrive_expect_tx(raw_full + st, C::kBlkBytes);
-                bulk_load(dst, codes + rec * C::kRec, C::kRec, raw_full + st);
-                bulk_load(dst + C::kRec, khdr + rec * C::kHdr, C::kHdr, raw_full + st);
+        int q0 = 0;                                        // blocks of the runs before
+        bool ok = true;
+        for (DenseRun run = next_run(); run.s >= 0 && ok; run = next_run()) {
+            const int blocks = run.end - run.first;
+            if (lane == 0) {
+                for (int i = q0; i < q0 + blocks && ok; ++i) {
+                    const int st = i % C::kSlots;
+                    // slot i % kSlots is free once block i - kSlots has been turned into bf16
+                    const long long t0 = clock64();
+                    while (!um::mbar_try_wait(raw_empty + st, ((uint32_t)(i / C::kSlots) & 1u) ^ 1u))
+                        if (*abort_flag || clock64() - t0 > kWaitCycles) { ok = false; break; }
+                    if (!ok) {
+                        // no copy is in flight when the CTA leaves
+                        for (int k = max(0, i - C::kSlots); k < i; ++k)
+                            um::mbar_wait(raw_full + k % C::kSlots, (uint32_t)(k / C::kSlots) & 1u, kWaitCycles);
+                        *abort_flag = 1;
+                        break;
+                    }
+                    const size_t rec = ((size_t)run.s * N + n) * nb + run.first + i - q0;
+                    uint8_t *dst = ring + st * C::kBlkBytes;
+                    um::mbar_arrive_expect_tx(raw_full + st, C::kBlkBytes);
+                    bulk_load(dst, codes + rec * C::kRec, C::kRec, raw_full + st);
+                    bulk_load(dst + C::kRec, khdr + rec * C::kHdr, C::kHdr, raw_full + st);
+                }
             }
-            if (!ok) *abort_flag = 1;
-            // no copy is in flight when the CTA leaves
-            for (int k = max(0, i - C::kSlots); k < i; ++k)
-                um::mbar_wait(raw_full + k % C::kSlots, (uint32_t)(k / C::kSlots) & 1u, kWaitCycles);
+            q0 += blocks;
+            ok = __all_sync(0xffffffffu, ok);
         }
+        if (lane == 0 && ok)
+            for (int k = max(0, q0 - C::kSlots); k < q0; ++k)
+                um::mbar_wait(raw_full + k % C::kSlots, (uint32_t)(k / C::kSlots) & 1u, kWaitCycles);
     } else if (warp < 3) {
         // The whole warp walks through the loop, with votes for conditions and the addresses in
         // values that are the same for all lanes, so that the products' operands stay in uniform
         // registers; one elected lane issues.
-        const int t = warp - 1, end = count_of(t);
+        const int t = warp - 1;
         const uint32_t id_s = um::idesc_bf16_f32(128, kStep), id_o = um::idesc_bf16_f32(128, D);
         const uint32_t tm = __reduce_or_sync(0xffffffffu, tmem) + t * 128;
         const uint64_t qd = um::sdesc_sw128(um::smem_u32(qs)) + (two ? t : 0) * (128 * D * 2 / 16);
@@ -282,50 +307,74 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
         auto wait = [&](uint64_t *bar, int phase) {
             ok = ok && __all_sync(0xffffffffu, !*abort_flag && um::mbar_wait(bar, (uint32_t)phase & 1u, kWaitCycles));
         };
-        // scores of step j: K is there, and the output product that read P from the same buffer
-        // is complete.  A tile's operands are free after each half's last step in it.
-        auto scores = [&](int j) {
-            const int g = step_of(t, j), b = (g >> 1) & 1;
-            wait(k_full + b, g >> 2);
-            if (j >= kBufs) wait(o_done + 2 * t + j % kBufs, j / kBufs - 1);
-            if (!ok) return;
-            um::tc_fence_after();
-            if (elect_one()) {
-                const uint64_t k0 = kd + b * kTileD + (g & 1) * (kStep * 128 / 16);
+        int tiles0 = 0, steps0 = 0, runs0 = 0;             // token tiles and this half's steps of the runs before
+        for (DenseRun run = next_run(); run.s >= 0 && ok; run = next_run(), ++runs0) {
+            const int blocks = run.end - run.first, ns = (blocks + 1) / 2, end = count_of(t, ns);
+            // whether step g is this half's last one in its token tile: the tile's operands are
+            // free after that of both halves
+            auto leaves = [&](int g) { return !two || (g & 1) || g + 1 == ns; };
+            // scores of step j: K is there, and the output product that read P from the same
+            // buffer is complete
+            auto scores = [&](int j) {
+                const int g = step_of(t, j), i = tiles0 + (g >> 1), b = i & 1, jj = steps0 + j, buf = jj % kBufs;
+                wait(k_full + b, i >> 1);
+                if (jj >= kBufs) wait(o_done + 2 * t + buf, jj / kBufs - 1);
+                if (!ok) return;
+                um::tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t k0 = kd + b * kTileD + (g & 1) * (kStep * 128 / 16);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    um::mma_bf16(tm + kColS + j % kBufs * kStep, qd + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
-                                 k0 + (k >> 2) * (kTok * 128 / 16) + 2 * (k & 3), id_s, k != 0);
-                um::mma_commit(s_full + 2 * t + j % kBufs);
-                if (!two || (g & 1)) um::mma_commit(k_empty + b);
-            }
-            __syncwarp();
-        };
-        wait(q_full, 0);
-        for (int j = 0; j < min(kBufs, end) && ok; ++j) scores(j);
-        for (int j = 0; j < end && ok; ++j) {
-            const int g = step_of(t, j), b = (g >> 1) & 1, buf = j % kBufs;
-            wait(v_full + b, g >> 2);
-            wait(p_full + 2 * t + buf, j / kBufs);
-            if (!ok) break;
-            um::tc_fence_after();
-            if (elect_one()) {
-                const uint32_t a = tm + kColS + buf * kStep;
-                const uint64_t v = vd + b * kTileD + (g & 1) * (D * 128 / 16);
-#pragma unroll
-                for (int k = 0; k < kStep / 16; ++k) {
-                    const uint32_t ak = a + 32 * (k >> 1) + 8 * (k & 1);
-                    mma_bf16_ta(tm, ak, v + 2 * k, id_o, (j | k) != 0);
-                    if (LO) {
-                        mma_bf16_ta(tm, ak + 16, v + 2 * k, id_o, 1);
-                        mma_bf16_ta(tm, a + kStep + 8 * k, v + 2 * k, id_o, 1);
-                    }
+                    for (int k = 0; k < D / 16; ++k)
+                        um::mma_bf16(tm + kColS + buf * kStep, qd + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
+                                     k0 + (k >> 2) * (kTok * 128 / 16) + 2 * (k & 3), id_s, k != 0);
+                    um::mma_commit(s_full + 2 * t + buf);
+                    if (leaves(g)) um::mma_commit(k_empty + b);
                 }
-                um::mma_commit(o_done + 2 * t + buf);
-                if (!two || (g & 1)) um::mma_commit(v_empty + b);
+                __syncwarp();
+            };
+            // A half without steps in short runs can be two runs behind the rows' warps (its
+            // arrival for a tile holds back the tile after the next), not four
+            wait(q_full + (runs0 & 3), runs0 >> 2);
+            for (int j = 0; j < min(kBufs, end) && ok; ++j) scores(j);
+            for (int j = 0; j < end && ok; ++j) {
+                const int g = step_of(t, j), i = tiles0 + (g >> 1), b = i & 1, jj = steps0 + j, buf = jj % kBufs;
+                wait(v_full + b, i >> 1);
+                wait(p_full + 2 * t + buf, jj / kBufs);
+                if (!ok) break;
+                um::tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t a = tm + kColS + buf * kStep;
+                    const uint64_t v = vd + b * kTileD + (g & 1) * (D * 128 / 16);
+#pragma unroll
+                    for (int k = 0; k < kStep / 16; ++k) {
+                        const uint32_t ak = a + 32 * (k >> 1) + 8 * (k & 1);
+                        mma_bf16_ta(tm, ak, v + 2 * k, id_o, (j | k) != 0);
+                        if (LO) {
+                            mma_bf16_ta(tm, ak + 16, v + 2 * k, id_o, 1);
+                            mma_bf16_ta(tm, a + kStep + 8 * k, v + 2 * k, id_o, 1);
+                        }
+                    }
+                    um::mma_commit(o_done + 2 * t + buf);
+                    if (leaves(g)) um::mma_commit(v_empty + b);
+                }
+                __syncwarp();
+                if (j + kBufs < end) scores(j + kBufs);
             }
-            __syncwarp();
-            if (j + kBufs < end) scores(j + kBufs);
+            // a run of an odd number of steps: the second half has none in its last tile
+            if (!two && t == 1 && (ns & 1) && ok) {
+                // the tile has to be there first: an arrival before that would count for the tile
+                // that was in its place
+                const int i = tiles0 + (ns >> 1), b = i & 1;
+                wait(k_full + b, i >> 1);
+                wait(v_full + b, i >> 1);
+                if (ok && elect_one()) {
+                    um::mbar_arrive(k_empty + b);
+                    um::mbar_arrive(v_empty + b);
+                }
+                __syncwarp();
+            }
+            tiles0 += tiles_of(blocks);
+            steps0 += end;
         }
         if (lane == 0 && !ok) *abort_flag = 1;
         // every issued product completes before tensor memory is released
@@ -348,9 +397,12 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
         constexpr int kUnits = D / 16, kPer = 8 / BITS;
         uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
         bool ok = true;
-        for (int i = 0; i < nt && ok; ++i) {
-            const int b = i & 1, blk = 4 * i + w, st = blk % C::kSlots;
-            const bool there = blk < blocks;
+        int tiles0 = 0, q0 = 0;                            // token tiles and blocks of the runs before
+        for (DenseRun run = next_run(); run.s >= 0 && ok; run = next_run()) {
+          const int blocks = run.end - run.first;
+          for (int i = tiles0; i < tiles0 + tiles_of(blocks); ++i) {
+            const int b = i & 1, in_run = 4 * (i - tiles0) + w, blk = q0 + in_run, st = blk % C::kSlots;
+            const bool there = in_run < blocks;
             const uint32_t dst = um::smem_u32((is_v ? vt : kt) + b * C::kTile) + place;
             const uint8_t *rec = ring + st * C::kBlkBytes;
             const uint8_t *cd = rec + (is_v ? C::kUnit : 0) + slot;
@@ -392,14 +444,35 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
                 um::mbar_arrive(full + b);
                 if (there) um::mbar_arrive(raw_empty + st);
             }
+          }
+          tiles0 += tiles_of(blocks);
+          q0 += blocks;
         }
         if (!ok && lane == 0) *abort_flag = 1;
     } else if (warp >= 12) {
         regs_up<kRegsRows>();
         const int t = (warp - 12) >> 2, w = warp & 3;
+        const int r = (two ? 128 * t : 0) + 32 * w + lane;  // row of the CTA
+        const bool busy = (two ? 128 * t : 0) + 32 * w < rows;   // any row of this warp
+        const uint32_t lanes = (uint32_t)(32 * w) << 16;
+        const uint32_t to = tmem + lanes + t * 128;
+        bool ok = true;
+        int steps0 = 0, runs0 = 0;                         // this half's steps and the runs before
+        // The eight warps take the run from one of them, and whether all is well from a vote: they
+        // meet at the same barriers whatever happens.  After a wait that ran out, the runs that
+        // are left get their NaN.
+        while (true) {
+        if (warp == 12) {
+            const DenseRun r12 = next_run();
+            if (lane == 0) run_s = r12;
+        }
+        um::bar_sync(1, 256);
+        const DenseRun run = run_s;
+        if (run.s < 0) break;
+        const int s = run.s, blocks = run.end - run.first, end = ok ? count_of(t, (blocks + 1) / 2) : 0;
         // query rows, K-major (rows from `rows` on are zero)
         // a thread takes a row; rows of the second tile are not read where there is one tile
-        {
+        if (ok) {
             const int qr = threadIdx.x - 384, rr = row0 + qr;
             const uint4 *src = (const uint4 *)(q + (((size_t)s * nq + rr / G) * N * G + n * G + rr % G) * D);
             uint8_t *dst = qs + (qr >> 7) * (128 * D * 2);
@@ -413,17 +486,11 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
         cp_async_wait();
         um::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) um::mbar_arrive(q_full);
-        const int r = (two ? 128 * t : 0) + 32 * w + lane;  // row of the CTA
-        const bool busy = (two ? 128 * t : 0) + 32 * w < rows;   // any row of this warp
-        const uint32_t lanes = (uint32_t)(32 * w) << 16;
-        const uint32_t to = tmem + lanes + t * 128;
+        if (lane == 0 && ok) um::mbar_arrive(q_full + (runs0 & 3));
         float m_ref = -INFINITY, l = 0.0f;
-        bool ok = true;
-        const int end = count_of(t);
         for (int j = 0; j < end; ++j) {
-            const int buf = j % kBufs;
-            bool here = !*abort_flag && um::mbar_wait(s_full + 2 * t + buf, (uint32_t)(j / kBufs) & 1u, kWaitCycles);
+            const int jj = steps0 + j, buf = jj % kBufs;
+            bool here = !*abort_flag && um::mbar_wait(s_full + 2 * t + buf, (uint32_t)(jj / kBufs) & 1u, kWaitCycles);
             if (!__all_sync(0xffffffffu, here)) { ok = false; break; }
             um::tc_fence_after();
             if (busy) {
@@ -450,7 +517,7 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
                     const float f = move ? (m_ref == -INFINITY ? 0.0f : ex2(m_ref - top)) : 1.0f;
                     if (j > 0) {
                         // the last step's output product may still be under way
-                        here = um::mbar_wait(o_done + 2 * t + (j - 1) % kBufs, (uint32_t)((j - 1) / kBufs) & 1u, kWaitCycles);
+                        here = um::mbar_wait(o_done + 2 * t + (jj - 1) % kBufs, (uint32_t)((jj - 1) / kBufs) & 1u, kWaitCycles);
                         if (!__all_sync(0xffffffffu, here)) { ok = false; break; }
                         um::tc_fence_after();
 #pragma unroll 1
@@ -503,7 +570,8 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
             if (lane == 0) um::mbar_arrive(p_full + 2 * t + buf);
         }
         if (ok && end > 0) {
-            const bool here = um::mbar_wait(o_done + 2 * t + (end - 1) % kBufs, (uint32_t)((end - 1) / kBufs) & 1u, kWaitCycles);
+            const bool here = um::mbar_wait(o_done + 2 * t + (steps0 + end - 1) % kBufs,
+                                            (uint32_t)((steps0 + end - 1) / kBufs) & 1u, kWaitCycles);
             ok = __all_sync(0xffffffffu, here);
             um::tc_fence_after();
         }
@@ -511,14 +579,14 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
             *abort_flag = 1;
             set_status(status, RKV_ERR_DEVICE_TIMEOUT);
         }
-        // outputs: through shared memory, so that a warp stores whole lines.  K's tiles are free
-        // once both halves' products are complete
+        // outputs: through shared memory, so that a warp stores whole lines.  The query rows' place
+        // is free once both halves' products are complete
         um::bar_sync(1, 256);
         if (busy) {
-            const size_t at = ((size_t)(run.slot * N + n) * 2 + (two ? 0 : t)) * R + row0;
+            const size_t base = (((size_t)run.slot * N + n) * 2 + (two ? 0 : t)) * R + row0;
             const int r_warp = (two ? 128 * t : 0) + 32 * w;
             if (end > 0 && ok) {
-                float *stage = (float *)kt + (size_t)(warp - 12) * 32 * 33;
+                float *stage = (float *)qs + (size_t)(warp - 12) * 32 * 32;
 #pragma unroll 1
                 for (int k = 0; k < D / 32; ++k) {
                     float v[32];
@@ -526,18 +594,22 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
                     tmem_wait_ld(v);
                     __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) stage[lane * 33 + e] = v[e];
+                    for (int e = 0; e < 32; ++e) stage[lane * 32 + (e ^ lane)] = v[e];
                     __syncwarp();
 #pragma unroll 4
                     for (int x = 0; x < 32; ++x)
-                        if (r_warp + x < rows) part[(at + r_warp + x) * D + 32 * k + lane] = stage[x * 33 + lane];
+                        if (r_warp + x < rows) part[(base + r_warp + x) * D + 32 * k + lane] = stage[x * 32 + (lane ^ x)];
                 }
             }
             if (r < rows) {
-                ml[at + r] = make_float2(ok ? m_ref : __uint_as_float(0x7fffffffu), l);
+                ml[base + r] = make_float2(ok ? m_ref : __uint_as_float(0x7fffffffu), l);
                 if (two)                                   // the second partial of the run is empty
-                    ml[at + R + r] = make_float2(-INFINITY, 0.0f);
+                    ml[base + R + r] = make_float2(-INFINITY, 0.0f);
             }
+        }
+        ok = bar_all(ok);                                  // then the next run's query rows go there
+        steps0 += end;
+        ++runs0;
         }
     }
     um::tc_fence_before();
@@ -551,7 +623,7 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
 
 template <int D, int BITS, bool LO>
 cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *c, const int32_t *len,
-                const DenseCut &cut, int runs, float scale_log2, float *part, float2 *ml, int32_t *status, cudaStream_t s)
+                const DenseCut &cut, int ctas, float scale_log2, float *part, float2 *ml, int32_t *status, cudaStream_t s)
 {
     using C = TreeCfg<D, BITS>;
     static PerDevice<int> setup;
@@ -562,7 +634,7 @@ cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dens
     if (e != cudaSuccess) return e;
     const int tiles = (nq * (H / g.N) + 255) / 256;
     ProfScope prof("dense_attention_tree", s);
-    k_dense_tree<D, BITS, LO><<<(unsigned)((size_t)runs * g.N * tiles), kThreads, C::kSmem, s>>>(
+    k_dense_tree<D, BITS, LO><<<(unsigned)((size_t)ctas * g.N * tiles), kThreads, C::kSmem, s>>>(
         (const __nv_bfloat16 *)q, (const uint8_t *)c->codes, (const uint8_t *)c->khdr, len, g.S, g.T, g.N, H / g.N,
         nq, g.nb, cut, tiles, scale_log2, part, ml, status);
     return cudaGetLastError();
@@ -571,14 +643,14 @@ cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dens
 }  // namespace
 
 cudaError_t launch_dense_tree(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *c,
-                              const int32_t *len, const DenseCut &cut, int runs, float scale_log2, bool p_lo, float *part,
+                              const int32_t *len, const DenseCut &cut, int ctas, float scale_log2, bool p_lo, float *part,
                               float2 *ml, int32_t *status, cudaStream_t s)
 {
     auto go = [&](auto bits, auto d) -> cudaError_t {
         constexpr int B = decltype(bits)::value, D = decltype(d)::value;
         if constexpr (D <= 128)
-            return p_lo ? run<D, B, true>(g, H, q, nq, c, len, cut, runs, scale_log2, part, ml, status, s)
-                        : run<D, B, false>(g, H, q, nq, c, len, cut, runs, scale_log2, part, ml, status, s);
+            return p_lo ? run<D, B, true>(g, H, q, nq, c, len, cut, ctas, scale_log2, part, ml, status, s)
+                        : run<D, B, false>(g, H, q, nq, c, len, cut, ctas, scale_log2, part, ml, status, s);
         else
             return cudaErrorInvalidValue;
     };

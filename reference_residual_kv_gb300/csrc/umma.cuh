@@ -47,20 +47,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity)
         : "memory");
     return ok != 0;
 }
-// Whether the phase with the given parity is complete, without the wait that try_wait may
-// make: for threads that look at several barriers in turn.
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 // Wait for the phase with the given parity to complete; false after `budget` cycles.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, long long budget)
 {

@@ -553,6 +553,25 @@ def test_many_sequences_of_all_lengths():
         case.done()
 
 
+@pytest.mark.parametrize("D,bits,G,n", [(64, 4, 2, 17), (128, 4, 4, 10), (128, 2, 4, 33), (64, 2, 4, 40)])
+def test_trees_over_many_short_sequences_among_long_ones(D, bits, G, n):
+    # 16 blocks at least go to one CTA: a dozen sequences of one block, in which half of the CTA
+    # has nothing to do, then sequences of more, and a long one that several share
+    rng = np.random.default_rng(n)
+    lens = [32 + i % 32 for i in range(23)] + [31, 0, 70, 96, 129, 700] + [33] * 7 + [224, 64, 5] + [40] * 6 + [600, 32]
+    S = len(lens)
+    case = Case(make_rows(rng, S, 705, 1, D), lens, bits)
+    q = do.bf16(rng.normal(size=(S, n, G, D)) * 1.5)
+    draft = make_rows(rng, S, n, 1, D)
+    parent = random_tree(rng, S, n)
+    for dtype in (torch.float32, torch.bfloat16):
+        got = tree_gpu(case, q, parent, draft, dtype)
+        again = tree_gpu(case, q, parent, draft, dtype)
+        assert np.array_equal(got, again)
+        check_tree(case, q, parent, draft, got, dtype == torch.bfloat16)
+    case.done()
+
+
 def test_selection_over_more_blocks_than_shared_memory_holds():
     # 42000 blocks of one head; all keys equal but for nine blocks that stand out: those, the
     # kept ends, and the lowest of the others

@@ -198,11 +198,16 @@ def one_run(rng):
     return [rng.choice([3, 16, 25])]
 
 
+def short_runs(rng):
+    return [rng.choice([1, 1, 2, 3, 4, 5, 6, 9, 17]) for _ in range(rng.randint(2, 14))]
+
+
 # ring slots of the kernel's variants; with fewer than two tiles of them its warps wait for the last tile
 @pytest.mark.parametrize("slots", [5, 8])
-def test_no_schedule_goes_wrong(slots):
+@pytest.mark.parametrize("lengths", [one_run, short_runs])
+def test_no_schedule_goes_wrong(slots, lengths):
     for seed in range(150):
-        play(seed, slots, slots < 8, one_run)
+        play(seed, slots, slots < 8, lengths)
 
 
 def test_a_short_ring_needs_the_wait_for_the_last_tile():
