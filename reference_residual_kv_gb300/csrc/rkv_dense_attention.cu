@@ -2,8 +2,8 @@
 // sequence (all finished blocks, or listed ones) and for trees of drafted tokens.
 //
 // The R = n_query H/N query rows of a KV head share its blocks.  Two kernels:
-//   k_dense_split   the finished blocks.  A CTA has a run of blocks of one (sequence, KV
-//                   head) and 8 NT query rows; its warps take blocks in turn, each through
+//   k_dense_split   the finished blocks.  A CTA has a share of a KV head's blocks, runs of
+//                   one sequence each, and 8 NT query rows; its warps take blocks in turn, each through
 //                   a ring of its own (cp.async.bulk, one record and one header a block),
 //                   so that no warp waits for another.  A record is already in operand
 //                   order: a lane reads 16 bytes of codes, turns pairs of them into bf16
@@ -13,10 +13,13 @@
 //                   query rows its columns.  Probabilities go from one product to the
 //                   other by movmatrix, as bf16 in two or three parts.  Softmax: running
 //                   reference and sum for each warp, in base 2.  No masks: a finished block
-//                   is whole.
+//                   is whole.  Bound by instruction issue, most of it codes to bf16 (issue 64 %,
+//                   integer pipe 60 %, products 24 %, DRAM 42 %): 8 uneven caches of up to
+//                   32768 tokens, 8 KV heads of 4 queries, 214 MB in 66-69 us, 3.2 TB/s.
 //   k_dense_finish  the bf16 rows of the unfinished block and the drafted tokens that a row
 //                   sees (the values of a token that it does not see are not touched), while
-//                   the first kernel still runs, then the merge of the runs' partials.
+//                   the first kernel still runs, then the merge of the runs' partials (24 drafts
+//                   x 7 heads, 16 sequences of 4 KV heads: 26 us, issue 52 %).
 #include "rkv_dense.cuh"
 #include "umma.cuh"
 
@@ -66,7 +69,8 @@ struct SplitCfg {
     static constexpr int NT = NT0 ? NT0 : 1;
     static constexpr int kUnit = 4 * D * BITS, kRec = 2 * kUnit + 4 * D, kHdr = 4 * D;
     static constexpr int kStage = kRec + kHdr;
-    // ring depth: about 80 KB in flight per CTA, two CTAs to an SM where registers allow
+    // ring depth: about 80 KB in flight per CTA (8 warps x 2 blocks of 5 KB at D = 128, 4 bits),
+    // two CTAs to an SM where registers allow
     static constexpr int kStages = D == 256 ? 2 : (D == 128 ? (BITS == 4 ? 2 : 3) : 4);
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kRow = D + 4;                     // merge row, padded
@@ -123,292 +127,292 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
     }
     int issued = 0, used = 0;
     bool ok = true;
-  // one run after another; a share rarely has more than two
+    // one run after another; a share rarely has more than two
 #pragma unroll 1
-  while (true) {
-    if (warp == 0) {
-        DenseCursor at = cursor_s;
-        const DenseRun r = dense_run(len, S, T, listed, share, at, status);
-        __syncwarp();
-        if (lane == 0) {
-            run_s = r;
-            cursor_s = at;
-        }
-    }
-    __syncthreads();
-    const DenseRun run = run_s;
-    if (run.s < 0) return;
-    const int s = run.s, sn = s * N + n, i0 = run.first, i1 = run.end;
-    const int have = blocks ? dense_len(len, s, T, status) / kBlk : 0;
-    const int32_t *list = blocks ? blocks + ((size_t)s * lists + (lists > 1 ? n : 0)) * n_blocks : nullptr;
-    // the warp's blocks: i0 + warp, + 8, ..., those that are to be skipped left out
-    int next = i0 + warp;
-    auto issue = [&]() {
-        int b = -1;
-        while (next < i1 && b < 0) {
-            b = block_at(list, next, have, status);
-            next += kWarps;
-        }
-        if (b < 0 || !ok) return;
-        if (lane == 0) {
-            const int st = issued % C::kStages;
-            uint8_t *dst = ring + st * C::kStage;
-            const size_t rec = (size_t)sn * nb + b;
-            um::mbar_arrive_expect_tx(bars + st, C::kStage);
-            bulk_load(dst, codes + rec * C::kRec, C::kRec, bars + st);
-            bulk_load(dst + C::kRec, khdr + rec * C::kHdr, C::kHdr, bars + st);
-        }
-        ++issued;
-    };
-#pragma unroll 1
-    for (int i = 0; i < C::kStages; ++i) issue();
-
-    // query rows as the second operand: column g is row 8 nt + g, lane (g, c) holds channels
-    // 2c, 2c + 1 and 2c + 8, 2c + 9 of each unit
-    uint32_t qr[NT == 1 ? kUnits : 1][2];
-    const uint2 *qs = (const uint2 *)(smem + C::kBody);
-    auto q_row = [&](int r) -> const uint32_t * {
-        return (const uint32_t *)(q + (((size_t)s * nq + r / G) * N * G + n * G + r % G) * D);
-    };
-    if constexpr (NT == 1) {
-        const int r = row0 + (kTwice ? g & 3 : g);
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            qr[u][0] = r < R ? __ldg(q_row(r) + u * 8 + c) : 0u;
-            qr[u][1] = r < R ? __ldg(q_row(r) + u * 8 + 4 + c) : 0u;
-        }
-    } else {
-        for (int i = threadIdx.x; i < kUnits * NT * 32; i += blockDim.x) {
-            const int l = i & 31, nt = (i >> 5) % NT, u = (i >> 5) / NT, r = row0 + 8 * nt + (l >> 2);
-            uint2 v = make_uint2(0u, 0u);
-            if (r < R) v = make_uint2(__ldg(q_row(r) + u * 8 + (l & 3)), __ldg(q_row(r) + u * 8 + 4 + (l & 3)));
-            ((uint2 *)(smem + C::kBody))[i] = v;
+    while (true) {
+        if (warp == 0) {
+            DenseCursor at = cursor_s;
+            const DenseRun r = dense_run(len, S, T, listed, share, at, status);
+            __syncwarp();
+            if (lane == 0) {
+                run_s = r;
+                cursor_s = at;
+            }
         }
         __syncthreads();
-    }
-
-    float acc[NT][2 * (D / 32)][4], m_run[NT][2], l_run[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int i = 0; i < 2 * (D / 32); ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.0f;
-        m_run[nt][0] = m_run[nt][1] = -INFINITY;
-        l_run[nt][0] = l_run[nt][1] = 0.0f;
-    }
-    const int kslot = key_slot(g, c) * 16, vslot = value_slot(g, c) * 16;
+        const DenseRun run = run_s;
+        if (run.s < 0) return;
+        const int s = run.s, sn = s * N + n, i0 = run.first, i1 = run.end;
+        const int have = blocks ? dense_len(len, s, T, status) / kBlk : 0;
+        const int32_t *list = blocks ? blocks + ((size_t)s * lists + (lists > 1 ? n : 0)) * n_blocks : nullptr;
+        // the warp's blocks: i0 + warp, + 8, ..., those that are to be skipped left out
+        int next = i0 + warp;
+        auto issue = [&]() {
+            int b = -1;
+            while (next < i1 && b < 0) {
+                b = block_at(list, next, have, status);
+                next += kWarps;
+            }
+            if (b < 0 || !ok) return;
+            if (lane == 0) {
+                const int st = issued % C::kStages;
+                uint8_t *dst = ring + st * C::kStage;
+                const size_t rec = (size_t)sn * nb + b;
+                um::mbar_arrive_expect_tx(bars + st, C::kStage);
+                bulk_load(dst, codes + rec * C::kRec, C::kRec, bars + st);
+                bulk_load(dst + C::kRec, khdr + rec * C::kHdr, C::kHdr, bars + st);
+            }
+            ++issued;
+        };
 #pragma unroll 1
-    for (; used < issued && ok; ++used) {
-        const int st = used % C::kStages;
-        const bool landed = um::mbar_wait(bars + st, (uint32_t)(used / C::kStages) & 1u, kWaitCycles);
-        if (!__all_sync(0xffffffffu, landed)) {
-            // what is on its way gets as long again; the partials are given up either way
-            for (int i = used; i < issued; ++i)
-                um::mbar_wait(bars + i % C::kStages, (uint32_t)(i / C::kStages) & 1u, kWaitCycles);
-            ok = false;
-            break;
+        for (int i = 0; i < C::kStages; ++i) issue();
+
+        // query rows as the second operand: column g is row 8 nt + g, lane (g, c) holds channels
+        // 2c, 2c + 1 and 2c + 8, 2c + 9 of each unit
+        uint32_t qr[NT == 1 ? kUnits : 1][2];
+        const uint2 *qs = (const uint2 *)(smem + C::kBody);
+        auto q_row = [&](int r) -> const uint32_t * {
+            return (const uint32_t *)(q + (((size_t)s * nq + r / G) * N * G + n * G + r % G) * D);
+        };
+        if constexpr (NT == 1) {
+            const int r = row0 + (kTwice ? g & 3 : g);
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                qr[u][0] = r < R ? __ldg(q_row(r) + u * 8 + c) : 0u;
+                qr[u][1] = r < R ? __ldg(q_row(r) + u * 8 + 4 + c) : 0u;
+            }
+        } else {
+            for (int i = threadIdx.x; i < kUnits * NT * 32; i += blockDim.x) {
+                const int l = i & 31, nt = (i >> 5) % NT, u = (i >> 5) / NT, r = row0 + 8 * nt + (l >> 2);
+                uint2 v = make_uint2(0u, 0u);
+                if (r < R) v = make_uint2(__ldg(q_row(r) + u * 8 + (l & 3)), __ldg(q_row(r) + u * 8 + 4 + (l & 3)));
+                ((uint2 *)(smem + C::kBody))[i] = v;
+            }
+            __syncthreads();
         }
-        const uint8_t *kc = ring + st * C::kStage, *vc = kc + C::kUnit, *vh = vc + C::kUnit, *kh = kc + C::kRec;
-        // scores^T: 32 tokens x 8 NT rows
-        float sc[NT][2][4];
+
+        float acc[NT][2 * (D / 32)][4], m_run[NT][2], l_run[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int i = 0; i < 2 * (D / 32); ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[nt][m][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) acc[nt][i][e] = 0.0f;
+            m_run[nt][0] = m_run[nt][1] = -INFINITY;
+            l_run[nt][0] = l_run[nt][1] = 0.0f;
+        }
+        const int kslot = key_slot(g, c) * 16, vslot = value_slot(g, c) * 16;
+#pragma unroll 1
+        for (; used < issued && ok; ++used) {
+            const int st = used % C::kStages;
+            const bool landed = um::mbar_wait(bars + st, (uint32_t)(used / C::kStages) & 1u, kWaitCycles);
+            if (!__all_sync(0xffffffffu, landed)) {
+                // what is on its way gets as long again; the partials are given up either way
+                for (int i = used; i < issued; ++i)
+                    um::mbar_wait(bars + i % C::kStages, (uint32_t)(i / C::kStages) & 1u, kWaitCycles);
+                ok = false;
+                break;
+            }
+            const uint8_t *kc = ring + st * C::kStage, *vc = kc + C::kUnit, *vh = vc + C::kUnit, *kh = kc + C::kRec;
+            // scores^T: 32 tokens x 8 NT rows
+            float sc[NT][2][4];
 #pragma unroll
-        for (int u0 = 0; u0 < kUnits; u0 += kPer) {
-            const uint4 w4 = *(const uint4 *)(kc + (u0 / kPer) * 512 + kslot);
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-            for (int x = 0; x < kPer; ++x) {
-                const int u = u0 + x;
-                const uint4 hd = *(const uint4 *)(kh + (u * 4 + c) * 16);
-                uint32_t a[2][4];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        a[m][i] = value_pair<BITS>(BITS == 4 ? w[(2 * x + m) & 3] : w[x & 3], BITS == 4 ? i : 4 * m + i,
-                                                   i < 2 ? hd.x : hd.z, i < 2 ? hd.y : hd.w);
+                    for (int e = 0; e < 4; ++e) sc[nt][m][e] = 0.0f;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    uint32_t b0, b1;
-                    if constexpr (NT == 1) {
-                        b0 = qr[u][0];
-                        b1 = qr[u][1];
-                    } else {
-                        const uint2 t = qs[(u * NT + nt) * 32 + lane];
-                        b0 = t.x;
-                        b1 = t.y;
-                    }
-                    mma16816(sc[nt][0], a[0], b0, b1);
-                    mma16816(sc[nt][1], a[1], b0, b1);
-                }
-            }
-        }
-        // softmax: rows 2c, 2c + 1 of each column tile; this lane's tokens are 16 m + g, + 8
-        uint32_t ph[NT][2][2], pl[NT][2][2], pt[P3 ? NT : 1][2][2];
+            for (int u0 = 0; u0 < kUnits; u0 += kPer) {
+                const uint4 w4 = *(const uint4 *)(kc + (u0 / kPer) * 512 + kslot);
+                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            // against a running reference that lags the maximum by at most 8: it moves, and the
-            // sums are rescaled, where a score is more than that above it
-            float mx[2];
-            bool move = false;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                mx[e] = fmaxf(fmaxf(sc[nt][0][e], sc[nt][0][e + 2]), fmaxf(sc[nt][1][e], sc[nt][1][e + 2])) * scale_log2;
-                move = move || mx[e] > m_run[nt][e] + 8.0f;
-            }
-            if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
-                    mx[e] = fmaxf(m_run[nt][e], mx[e]);
-                    const float al = ex2(m_run[nt][e] - (mx[e] == -INFINITY ? 0.0f : mx[e]));
-                    m_run[nt][e] = mx[e];
-                    l_run[nt][e] *= al;
-#pragma unroll
-                    for (int i = 0; i < 2 * (D / 32); ++i) {
-                        acc[nt][i][e] *= al;
-                        acc[nt][i][e + 2] *= al;
-                    }
-                }
-            }
-            const float o0 = m_run[nt][0] == -INFINITY ? 0.0f : m_run[nt][0];
-            const float o1 = m_run[nt][1] == -INFINITY ? 0.0f : m_run[nt][1];
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float p0 = ex2(fmaf(sc[nt][m][2 * h], scale_log2, -o0));
-                    const float p1 = ex2(fmaf(sc[nt][m][2 * h + 1], scale_log2, -o1));
-                    l_run[nt][0] += p0;
-                    l_run[nt][1] += p1;
-                    const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
-                    const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - __low2float(hi), p1 - __high2float(hi));
-                    if (P3) {
-                        const float r0 = (p0 - __low2float(hi)) - __low2float(lo), r1 = (p1 - __high2float(hi)) - __high2float(lo);
-                        const uint32_t third = as_u32(__floats2bfloat162_rn(r0, r1));
-                        pt[P3 ? nt : 0][m][h] = trans8x8(kTwice && c >= 2 ? 0u : third);
-                    }
-                    if (kTwice) {
-                        ph[nt][m][h] = trans8x8(as_u32(c < 2 ? hi : lo));
-                    } else {
-                        ph[nt][m][h] = trans8x8(as_u32(hi));
-                        pl[nt][m][h] = trans8x8(as_u32(lo));
-                    }
-                }
-        }
-        // out^T: D channels x 8 NT rows, 32 channels at a time; a block's sums are its own and
-        // join the running ones rounded (the products' accumulators cut: over a whole run that
-        // was 1.2e-6 of the outputs, against 4e-7)
-#pragma unroll
-        for (int u0 = 0; u0 < kUnits; u0 += kPer) {
-            const uint4 w4 = *(const uint4 *)(vc + (u0 / kPer) * 512 + vslot);
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-            for (int x0 = 0; x0 < kPer; x0 += 2) {
-                float sum[NT][2][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int x = 0; x < kPer; ++x) {
+                    const int u = u0 + x;
+                    const uint4 hd = *(const uint4 *)(kh + (u * 4 + c) * 16);
+                    uint32_t a[2][4];
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sum[nt][m][e] = 0.0f;
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    const int x = x0 + ks, u = u0 + x;
-                    const uint4 hd = *(const uint4 *)(vh + (u * 4 + c) * 16);
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        uint32_t a[4];
-#pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            a[i] = value_pair<BITS>(BITS == 4 ? w[(2 * x + m) & 3] : w[x & 3], BITS == 4 ? i : 4 * m + i,
-                                                    i < 2 ? hd.x : hd.z, i < 2 ? hd.y : hd.w);
+                            a[m][i] = value_pair<BITS>(BITS == 4 ? w[(2 * x + m) & 3] : w[x & 3], BITS == 4 ? i : 4 * m + i,
+                                                       i < 2 ? hd.x : hd.z, i < 2 ? hd.y : hd.w);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma16816(sum[nt][m], a, ph[nt][ks][0], ph[nt][ks][1]);
-                            if (!kTwice) mma16816(sum[nt][m], a, pl[nt][ks][0], pl[nt][ks][1]);
-                            if (P3) mma16816(sum[nt][m], a, pt[P3 ? nt : 0][ks][0], pt[P3 ? nt : 0][ks][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint32_t b0, b1;
+                        if constexpr (NT == 1) {
+                            b0 = qr[u][0];
+                            b1 = qr[u][1];
+                        } else {
+                            const uint2 t = qs[(u * NT + nt) * 32 + lane];
+                            b0 = t.x;
+                            b1 = t.y;
+                        }
+                        mma16816(sc[nt][0], a[0], b0, b1);
+                        mma16816(sc[nt][1], a[1], b0, b1);
+                    }
+                }
+            }
+            // softmax: rows 2c, 2c + 1 of each column tile; this lane's tokens are 16 m + g, + 8
+            uint32_t ph[NT][2][2], pl[NT][2][2], pt[P3 ? NT : 1][2][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                // against a running reference that lags the maximum by at most 8: it moves, and the
+                // sums are rescaled, where a score is more than that above it
+                float mx[2];
+                bool move = false;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[e] = fmaxf(fmaxf(sc[nt][0][e], sc[nt][0][e + 2]), fmaxf(sc[nt][1][e], sc[nt][1][e + 2])) * scale_log2;
+                    move = move || mx[e] > m_run[nt][e] + 8.0f;
+                }
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
+                        mx[e] = fmaxf(m_run[nt][e], mx[e]);
+                        const float al = ex2(m_run[nt][e] - (mx[e] == -INFINITY ? 0.0f : mx[e]));
+                        m_run[nt][e] = mx[e];
+                        l_run[nt][e] *= al;
+#pragma unroll
+                        for (int i = 0; i < 2 * (D / 32); ++i) {
+                            acc[nt][i][e] *= al;
+                            acc[nt][i][e + 2] *= al;
                         }
                     }
                 }
+                const float o0 = m_run[nt][0] == -INFINITY ? 0.0f : m_run[nt][0];
+                const float o1 = m_run[nt][1] == -INFINITY ? 0.0f : m_run[nt][1];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[nt][u0 + x0 + m][e] += sum[nt][m][e];
+                    for (int h = 0; h < 2; ++h) {
+                        const float p0 = ex2(fmaf(sc[nt][m][2 * h], scale_log2, -o0));
+                        const float p1 = ex2(fmaf(sc[nt][m][2 * h + 1], scale_log2, -o1));
+                        l_run[nt][0] += p0;
+                        l_run[nt][1] += p1;
+                        const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
+                        const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - __low2float(hi), p1 - __high2float(hi));
+                        if (P3) {
+                            const float r0 = (p0 - __low2float(hi)) - __low2float(lo), r1 = (p1 - __high2float(hi)) - __high2float(lo);
+                            const uint32_t third = as_u32(__floats2bfloat162_rn(r0, r1));
+                            pt[P3 ? nt : 0][m][h] = trans8x8(kTwice && c >= 2 ? 0u : third);
+                        }
+                        if (kTwice) {
+                            ph[nt][m][h] = trans8x8(as_u32(c < 2 ? hi : lo));
+                        } else {
+                            ph[nt][m][h] = trans8x8(as_u32(hi));
+                            pl[nt][m][h] = trans8x8(as_u32(lo));
+                        }
+                    }
             }
+            // out^T: D channels x 8 NT rows, 32 channels at a time; a block's sums are its own and
+            // join the running ones rounded (the products' accumulators cut: over a whole run that
+            // was 1.2e-6 of the outputs, against 4e-7)
+#pragma unroll
+            for (int u0 = 0; u0 < kUnits; u0 += kPer) {
+                const uint4 w4 = *(const uint4 *)(vc + (u0 / kPer) * 512 + vslot);
+                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                for (int x0 = 0; x0 < kPer; x0 += 2) {
+                    float sum[NT][2][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sum[nt][m][e] = 0.0f;
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks) {
+                        const int x = x0 + ks, u = u0 + x;
+                        const uint4 hd = *(const uint4 *)(vh + (u * 4 + c) * 16);
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            uint32_t a[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                a[i] = value_pair<BITS>(BITS == 4 ? w[(2 * x + m) & 3] : w[x & 3], BITS == 4 ? i : 4 * m + i,
+                                                        i < 2 ? hd.x : hd.z, i < 2 ? hd.y : hd.w);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma16816(sum[nt][m], a, ph[nt][ks][0], ph[nt][ks][1]);
+                                if (!kTwice) mma16816(sum[nt][m], a, pl[nt][ks][0], pl[nt][ks][1]);
+                                if (P3) mma16816(sum[nt][m], a, pt[P3 ? nt : 0][ks][0], pt[P3 ? nt : 0][ks][1]);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[nt][u0 + x0 + m][e] += sum[nt][m][e];
+                }
+            }
+            __syncwarp();
+            issue();
         }
-        __syncwarp();
-        issue();
-    }
-    if (!ok && lane == 0) set_status(status, RKV_ERR_DEVICE_TIMEOUT);
+        if (!ok && lane == 0) set_status(status, RKV_ERR_DEVICE_TIMEOUT);
 
-    // the lanes' sums, then the warps' partials through shared memory
+        // the lanes' sums, then the warps' partials through shared memory
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], o);
-            if (g == 0)
-                sml[warp][8 * nt + 2 * c + e] = make_float2(ok ? m_run[nt][e] : __uint_as_float(0x7fffffffu), l_run[nt][e]);
+                for (int o = 4; o < 32; o <<= 1) l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], o);
+                if (g == 0)
+                    sml[warp][8 * nt + 2 * c + e] = make_float2(ok ? m_run[nt][e] : __uint_as_float(0x7fffffffu), l_run[nt][e]);
+            }
+        if (kTwice) {                                          // both parts of a row's outputs
+#pragma unroll
+            for (int i = 0; i < 2 * (D / 32); ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[0][i][e] += __shfl_xor_sync(0xffffffffu, acc[0][i][e], 2);
         }
-    if (kTwice) {                                          // both parts of a row's outputs
+        __syncthreads();                                       // every warp is done with its ring
+        float *rows = (float *)smem + (size_t)warp * 8 * NT * C::kRow;
 #pragma unroll
-        for (int i = 0; i < 2 * (D / 32); ++i)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[0][i][e] += __shfl_xor_sync(0xffffffffu, acc[0][i][e], 2);
+            for (int i = 0; i < 2 * (D / 32); ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    rows[(8 * nt + 2 * c + (e & 1)) * C::kRow + 16 * i + g + 8 * (e >> 1)] = acc[nt][i][e];
+        __syncthreads();
+        const float *all = (const float *)smem;
+        for (int x = threadIdx.x; x < 8 * NT * (D / 4); x += blockDim.x) {
+            const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+            if (row0 + r >= R) break;
+            float m = -INFINITY;
+            bool bad = false;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                m = fmaxf(m, sml[w][r].x);
+                bad |= sml[w][r].x != sml[w][r].x;
+            }
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float l = 0.0f;
+            const float mu = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ex2(sml[w][r].x - mu);
+                const float4 v = *(const float4 *)(all + ((size_t)w * 8 * NT + r) * C::kRow + d);
+                o.x = fmaf(v.x, f, o.x);
+                o.y = fmaf(v.y, f, o.y);
+                o.z = fmaf(v.z, f, o.z);
+                o.w = fmaf(v.w, f, o.w);
+                l = fmaf(sml[w][r].y, f, l);
+            }
+            const size_t to = ((size_t)run.slot * N + n) * R + row0 + r;
+            *(float4 *)(part + to * D + d) = o;
+            if (d == 0) ml[to] = make_float2(bad ? __uint_as_float(0x7fffffffu) : m, l);
+        }
+        // the next run's copies go over what was merged
+        um::fence_proxy_async_smem();
+        __syncthreads();
     }
-    __syncthreads();                                       // every warp is done with its ring
-    float *rows = (float *)smem + (size_t)warp * 8 * NT * C::kRow;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2 * (D / 32); ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                rows[(8 * nt + 2 * c + (e & 1)) * C::kRow + 16 * i + g + 8 * (e >> 1)] = acc[nt][i][e];
-    __syncthreads();
-    const float *all = (const float *)smem;
-    for (int x = threadIdx.x; x < 8 * NT * (D / 4); x += blockDim.x) {
-        const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-        if (row0 + r >= R) break;
-        float m = -INFINITY;
-        bool bad = false;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            m = fmaxf(m, sml[w][r].x);
-            bad |= sml[w][r].x != sml[w][r].x;
-        }
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float l = 0.0f;
-        const float mu = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(sml[w][r].x - mu);
-            const float4 v = *(const float4 *)(all + ((size_t)w * 8 * NT + r) * C::kRow + d);
-            o.x = fmaf(v.x, f, o.x);
-            o.y = fmaf(v.y, f, o.y);
-            o.z = fmaf(v.z, f, o.z);
-            o.w = fmaf(v.w, f, o.w);
-            l = fmaf(sml[w][r].y, f, l);
-        }
-        const size_t to = ((size_t)run.slot * N + n) * R + row0 + r;
-        *(float4 *)(part + to * D + d) = o;
-        if (d == 0) ml[to] = make_float2(bad ? __uint_as_float(0x7fffffffu) : m, l);
-    }
-    // the next run's copies go over what was merged
-    um::fence_proxy_async_smem();
-    __syncthreads();
-  }
 }
 
 // The last pass: 8 / wpr query rows of a KV head per CTA, wpr warps for each.  Tokens that are

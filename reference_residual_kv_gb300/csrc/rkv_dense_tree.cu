@@ -25,6 +25,9 @@
 // P is bf16 for bf16 outputs (2^-8 for each p, half a step, as the output's own rounding), and
 // three parts of bf16 for fp32 outputs; those take the columns of both buffers, so that there
 // is one.
+// 64 drafts x 4 heads over 131072 tokens, 8 KV heads: 133-135 us, 1.0 PFLOP/s.  No unit is full
+// (issue 57 %, integer pipe 46 %, tensor pipe 45 %, its memory 52 %): the chain scores, softmax,
+// P, outputs of the two halves is what the time goes to.
 // All waits are bounded; a CTA whose wait runs out sets RKV_ERR_DEVICE_TIMEOUT and writes NaN
 // as its partials' maxima, so that its rows read NaN.
 #include "rkv_dense.cuh"
@@ -399,54 +402,54 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
         bool ok = true;
         int tiles0 = 0, q0 = 0;                            // token tiles and blocks of the runs before
         for (DenseRun run = next_run(); run.s >= 0 && ok; run = next_run()) {
-          const int blocks = run.end - run.first;
-          for (int i = tiles0; i < tiles0 + tiles_of(blocks); ++i) {
-            const int b = i & 1, in_run = 4 * (i - tiles0) + w, blk = q0 + in_run, st = blk % C::kSlots;
-            const bool there = in_run < blocks;
-            const uint32_t dst = um::smem_u32((is_v ? vt : kt) + b * C::kTile) + place;
-            const uint8_t *rec = ring + st * C::kBlkBytes;
-            const uint8_t *cd = rec + (is_v ? C::kUnit : 0) + slot;
-            const uint8_t *hp = rec + (is_v ? 2 * C::kUnit : C::kRec) + c * 16;
-            bool here = !*abort_flag && um::mbar_wait(empty + b, ((uint32_t)(i >> 1) & 1u) ^ 1u, kWaitCycles);
-            // A parity names a phase only to a thread that knows the phase before to be complete, that
-            // is, block blk - kSlots to have landed.  With two tiles of slots it is in a tile that has
-            // been multiplied; with fewer it may be in the last one, another warp's.
-            if (C::kSlots < 8 && i > 0)
-                here = here && um::mbar_wait(full + ((i - 1) & 1), (uint32_t)((i - 1) >> 1) & 1u, kWaitCycles);
-            if (there) here = here && um::mbar_wait(raw_full + st, (uint32_t)(blk / C::kSlots) & 1u, kWaitCycles);
-            if (!__all_sync(0xffffffffu, here)) { ok = false; break; }
+            const int blocks = run.end - run.first;
+            for (int i = tiles0; i < tiles0 + tiles_of(blocks); ++i) {
+                const int b = i & 1, in_run = 4 * (i - tiles0) + w, blk = q0 + in_run, st = blk % C::kSlots;
+                const bool there = in_run < blocks;
+                const uint32_t dst = um::smem_u32((is_v ? vt : kt) + b * C::kTile) + place;
+                const uint8_t *rec = ring + st * C::kBlkBytes;
+                const uint8_t *cd = rec + (is_v ? C::kUnit : 0) + slot;
+                const uint8_t *hp = rec + (is_v ? 2 * C::kUnit : C::kRec) + c * 16;
+                bool here = !*abort_flag && um::mbar_wait(empty + b, ((uint32_t)(i >> 1) & 1u) ^ 1u, kWaitCycles);
+                // A parity names a phase only to a thread that knows the phase before to be complete, that
+                // is, block blk - kSlots to have landed.  With two tiles of slots it is in a tile that has
+                // been multiplied; with fewer it may be in the last one, another warp's.
+                if (C::kSlots < 8 && i > 0)
+                    here = here && um::mbar_wait(full + ((i - 1) & 1), (uint32_t)((i - 1) >> 1) & 1u, kWaitCycles);
+                if (there) here = here && um::mbar_wait(raw_full + st, (uint32_t)(blk / C::kSlots) & 1u, kWaitCycles);
+                if (!__all_sync(0xffffffffu, here)) { ok = false; break; }
 #pragma unroll
-            for (int u0 = 0; u0 < kUnits; u0 += kPer) {
-                uint4 w4 = make_uint4(0u, 0u, 0u, 0u);
-                if (there) w4 = *(const uint4 *)(cd + (u0 / kPer) * 512);
-                const uint32_t wd[4] = {w4.x, w4.y, w4.z, w4.w};
+                for (int u0 = 0; u0 < kUnits; u0 += kPer) {
+                    uint4 w4 = make_uint4(0u, 0u, 0u, 0u);
+                    if (there) w4 = *(const uint4 *)(cd + (u0 / kPer) * 512);
+                    const uint32_t wd[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                for (int x = 0; x < kPer; ++x) {
-                    const int u = u0 + x;
-                    uint4 hd = make_uint4(0u, 0u, 0u, 0u);
-                    if (there) hd = *(const uint4 *)(hp + u * 64);
+                    for (int x = 0; x < kPer; ++x) {
+                        const int u = u0 + x;
+                        uint4 hd = make_uint4(0u, 0u, 0u, 0u);
+                        if (there) hd = *(const uint4 *)(hp + u * 64);
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        uint32_t a[4];
+                        for (int m = 0; m < 2; ++m) {
+                            uint32_t a[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            a[e] = value_pair<BITS>(BITS == 4 ? wd[(2 * x + m) & 3] : wd[x & 3], BITS == 4 ? e : 4 * m + e,
-                                                    e < 2 ? hd.x : hd.z, e < 2 ? hd.y : hd.w);
-                        const uint32_t at = is_v ? (dst ^ ((u & 1) << 5)) + (32 * (u >> 1) + 16 * m) * 128
-                                                 : (dst ^ ((u & 3) << 5)) + (u >> 2) * kTok * 128 + 16 * m * 128;
-                        stmatrix4(at, a);
+                            for (int e = 0; e < 4; ++e)
+                                a[e] = value_pair<BITS>(BITS == 4 ? wd[(2 * x + m) & 3] : wd[x & 3], BITS == 4 ? e : 4 * m + e,
+                                                        e < 2 ? hd.x : hd.z, e < 2 ? hd.y : hd.w);
+                            const uint32_t at = is_v ? (dst ^ ((u & 1) << 5)) + (32 * (u >> 1) + 16 * m) * 128
+                                                     : (dst ^ ((u & 3) << 5)) + (u >> 2) * kTok * 128 + 16 * m * 128;
+                            stmatrix4(at, a);
+                        }
                     }
                 }
+                um::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    um::mbar_arrive(full + b);
+                    if (there) um::mbar_arrive(raw_empty + st);
+                }
             }
-            um::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                um::mbar_arrive(full + b);
-                if (there) um::mbar_arrive(raw_empty + st);
-            }
-          }
-          tiles0 += tiles_of(blocks);
-          q0 += blocks;
+            tiles0 += tiles_of(blocks);
+            q0 += blocks;
         }
         if (!ok && lane == 0) *abort_flag = 1;
     } else if (warp >= 12) {
@@ -462,154 +465,154 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
         // meet at the same barriers whatever happens.  After a wait that ran out, the runs that
         // are left get their NaN.
         while (true) {
-        if (warp == 12) {
-            const DenseRun r12 = next_run();
-            if (lane == 0) run_s = r12;
-        }
-        um::bar_sync(1, 256);
-        const DenseRun run = run_s;
-        if (run.s < 0) break;
-        const int s = run.s, blocks = run.end - run.first, end = ok ? count_of(t, (blocks + 1) / 2) : 0;
-        // query rows, K-major (rows from `rows` on are zero)
-        // a thread takes a row; rows of the second tile are not read where there is one tile
-        if (ok) {
-            const int qr = threadIdx.x - 384, rr = row0 + qr;
-            const uint4 *src = (const uint4 *)(q + (((size_t)s * nq + rr / G) * N * G + n * G + rr % G) * D);
-            uint8_t *dst = qs + (qr >> 7) * (128 * D * 2);
-            if (two || qr < 128)
-#pragma unroll
-                for (int ch = 0; ch < D / 8; ++ch) {
-                    if (qr < rows) cp_async16(dst + tile_at(128, qr & 127, ch), src + ch);
-                    else *(uint4 *)(dst + tile_at(128, qr & 127, ch)) = make_uint4(0u, 0u, 0u, 0u);
-                }
-        }
-        cp_async_wait();
-        um::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && ok) um::mbar_arrive(q_full + (runs0 & 3));
-        float m_ref = -INFINITY, l = 0.0f;
-        for (int j = 0; j < end; ++j) {
-            const int jj = steps0 + j, buf = jj % kBufs;
-            bool here = !*abort_flag && um::mbar_wait(s_full + 2 * t + buf, (uint32_t)(jj / kBufs) & 1u, kWaitCycles);
-            if (!__all_sync(0xffffffffu, here)) { ok = false; break; }
-            um::tc_fence_after();
-            if (busy) {
-                const uint32_t ts = tmem + lanes + kColS + t * 128 + buf * kStep;
-                const bool whole = blocks - 2 * step_of(t, j) >= 2;   // else the step's second block is not there
-                float v[2][32];
-                tmem_ld32(ts, v[0]);
-                tmem_ld32(ts + 32, v[1]);
-                tmem_wait_ld(v[0]);
-                tmem_wait_ld(v[1]);
-                if (!whole)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[1][e] = -INFINITY;
-                float top = -INFINITY, top1 = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    top = max3f(top, v[0][e], v[0][e + 1]);
-                    top1 = max3f(top1, v[1][e], v[1][e + 1]);
-                }
-                top = fmaxf(top, top1) * scale_log2;
-                // the reference moves where the maximum is more than 8 above it, and at the start
-                const bool move = top > m_ref + 8.0f || (m_ref == -INFINITY && top != -INFINITY);
-                if (__any_sync(0xffffffffu, move)) {
-                    const float f = move ? (m_ref == -INFINITY ? 0.0f : ex2(m_ref - top)) : 1.0f;
-                    if (j > 0) {
-                        // the last step's output product may still be under way
-                        here = um::mbar_wait(o_done + 2 * t + (jj - 1) % kBufs, (uint32_t)((jj - 1) / kBufs) & 1u, kWaitCycles);
-                        if (!__all_sync(0xffffffffu, here)) { ok = false; break; }
-                        um::tc_fence_after();
-#pragma unroll 1
-                        for (int k = 0; k < D / 16; ++k) {
-                            float o[16];
-                            tmem_ld16(to + 16 * k, o);
-                            tmem_wait_ld(o);
-                            uint32_t x[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[e] * f);
-                            tmem_st16(to + 16 * k, x);
-                        }
-                    }
-                    l *= f;
-                    if (move) m_ref = top;
-                }
-                const float mu = m_ref == -INFINITY ? 0.0f : m_ref;
-                const float2 sc2 = make_float2(scale_log2, scale_log2), mu2 = make_float2(-mu, -mu);
-                float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                // 32 tokens of P in columns 32 k .. + 15, of its second part behind them, of its
-                // third part in the other buffer's columns 16 k ..
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t hi[16], lo[16], th[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 x = __ffma2_rn(make_float2(v[k][2 * e], v[k][2 * e + 1]), sc2, mu2);
-                        const float2 pp = make_float2(ex2(x.x), ex2(x.y));
-                        sums[e & 1] = __fadd2_rn(sums[e & 1], pp);
-                        const __nv_bfloat162 h2 = __floats2bfloat162_rn(pp.x, pp.y);
-                        hi[e] = as_u32(h2);
-                        if (LO) {
-                            const float rx = pp.x - __low2float(h2), ry = pp.y - __high2float(h2);
-                            const __nv_bfloat162 l2 = __floats2bfloat162_rn(rx, ry);
-                            lo[e] = as_u32(l2);
-                            th[e] = as_u32(__floats2bfloat162_rn(rx - __low2float(l2), ry - __high2float(l2)));
-                        }
-                    }
-                    tmem_st16(ts + 32 * k, hi);
-                    if (LO) {
-                        tmem_st16(ts + 32 * k + 16, lo);
-                        tmem_st16(ts + kStep + 16 * k, th);
-                    }
-                }
-                l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
-                tmem_wait_st();
+            if (warp == 12) {
+                const DenseRun r12 = next_run();
+                if (lane == 0) run_s = r12;
             }
-            um::tc_fence_before();
+            um::bar_sync(1, 256);
+            const DenseRun run = run_s;
+            if (run.s < 0) break;
+            const int s = run.s, blocks = run.end - run.first, end = ok ? count_of(t, (blocks + 1) / 2) : 0;
+            // query rows, K-major (rows from `rows` on are zero)
+            // a thread takes a row; rows of the second tile are not read where there is one tile
+            if (ok) {
+                const int qr = threadIdx.x - 384, rr = row0 + qr;
+                const uint4 *src = (const uint4 *)(q + (((size_t)s * nq + rr / G) * N * G + n * G + rr % G) * D);
+                uint8_t *dst = qs + (qr >> 7) * (128 * D * 2);
+                if (two || qr < 128)
+#pragma unroll
+                    for (int ch = 0; ch < D / 8; ++ch) {
+                        if (qr < rows) cp_async16(dst + tile_at(128, qr & 127, ch), src + ch);
+                        else *(uint4 *)(dst + tile_at(128, qr & 127, ch)) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+            }
+            cp_async_wait();
+            um::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) um::mbar_arrive(p_full + 2 * t + buf);
-        }
-        if (ok && end > 0) {
-            const bool here = um::mbar_wait(o_done + 2 * t + (steps0 + end - 1) % kBufs,
-                                            (uint32_t)((steps0 + end - 1) / kBufs) & 1u, kWaitCycles);
-            ok = __all_sync(0xffffffffu, here);
-            um::tc_fence_after();
-        }
-        if (!ok && lane == 0) {
-            *abort_flag = 1;
-            set_status(status, RKV_ERR_DEVICE_TIMEOUT);
-        }
-        // outputs: through shared memory, so that a warp stores whole lines.  The query rows' place
-        // is free once both halves' products are complete
-        um::bar_sync(1, 256);
-        if (busy) {
-            const size_t base = (((size_t)run.slot * N + n) * 2 + (two ? 0 : t)) * R + row0;
-            const int r_warp = (two ? 128 * t : 0) + 32 * w;
-            if (end > 0 && ok) {
-                float *stage = (float *)qs + (size_t)(warp - 12) * 32 * 32;
-#pragma unroll 1
-                for (int k = 0; k < D / 32; ++k) {
-                    float v[32];
-                    tmem_ld32(to + 32 * k, v);
-                    tmem_wait_ld(v);
-                    __syncwarp();
+            if (lane == 0 && ok) um::mbar_arrive(q_full + (runs0 & 3));
+            float m_ref = -INFINITY, l = 0.0f;
+            for (int j = 0; j < end; ++j) {
+                const int jj = steps0 + j, buf = jj % kBufs;
+                bool here = !*abort_flag && um::mbar_wait(s_full + 2 * t + buf, (uint32_t)(jj / kBufs) & 1u, kWaitCycles);
+                if (!__all_sync(0xffffffffu, here)) { ok = false; break; }
+                um::tc_fence_after();
+                if (busy) {
+                    const uint32_t ts = tmem + lanes + kColS + t * 128 + buf * kStep;
+                    const bool whole = blocks - 2 * step_of(t, j) >= 2;   // else the step's second block is not there
+                    float v[2][32];
+                    tmem_ld32(ts, v[0]);
+                    tmem_ld32(ts + 32, v[1]);
+                    tmem_wait_ld(v[0]);
+                    tmem_wait_ld(v[1]);
+                    if (!whole)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) stage[lane * 32 + (e ^ lane)] = v[e];
-                    __syncwarp();
+                        for (int e = 0; e < 32; ++e) v[1][e] = -INFINITY;
+                    float top = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        top = max3f(top, v[0][e], v[0][e + 1]);
+                        top1 = max3f(top1, v[1][e], v[1][e + 1]);
+                    }
+                    top = fmaxf(top, top1) * scale_log2;
+                    // the reference moves where the maximum is more than 8 above it, and at the start
+                    const bool move = top > m_ref + 8.0f || (m_ref == -INFINITY && top != -INFINITY);
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float f = move ? (m_ref == -INFINITY ? 0.0f : ex2(m_ref - top)) : 1.0f;
+                        if (j > 0) {
+                            // the last step's output product may still be under way
+                            here = um::mbar_wait(o_done + 2 * t + (jj - 1) % kBufs, (uint32_t)((jj - 1) / kBufs) & 1u, kWaitCycles);
+                            if (!__all_sync(0xffffffffu, here)) { ok = false; break; }
+                            um::tc_fence_after();
+#pragma unroll 1
+                            for (int k = 0; k < D / 16; ++k) {
+                                float o[16];
+                                tmem_ld16(to + 16 * k, o);
+                                tmem_wait_ld(o);
+                                uint32_t x[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[e] * f);
+                                tmem_st16(to + 16 * k, x);
+                            }
+                        }
+                        l *= f;
+                        if (move) m_ref = top;
+                    }
+                    const float mu = m_ref == -INFINITY ? 0.0f : m_ref;
+                    const float2 sc2 = make_float2(scale_log2, scale_log2), mu2 = make_float2(-mu, -mu);
+                    float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    // 32 tokens of P in columns 32 k .. + 15, of its second part behind them, of its
+                    // third part in the other buffer's columns 16 k ..
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t hi[16], lo[16], th[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 x = __ffma2_rn(make_float2(v[k][2 * e], v[k][2 * e + 1]), sc2, mu2);
+                            const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+                            sums[e & 1] = __fadd2_rn(sums[e & 1], pp);
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(pp.x, pp.y);
+                            hi[e] = as_u32(h2);
+                            if (LO) {
+                                const float rx = pp.x - __low2float(h2), ry = pp.y - __high2float(h2);
+                                const __nv_bfloat162 l2 = __floats2bfloat162_rn(rx, ry);
+                                lo[e] = as_u32(l2);
+                                th[e] = as_u32(__floats2bfloat162_rn(rx - __low2float(l2), ry - __high2float(l2)));
+                            }
+                        }
+                        tmem_st16(ts + 32 * k, hi);
+                        if (LO) {
+                            tmem_st16(ts + 32 * k + 16, lo);
+                            tmem_st16(ts + kStep + 16 * k, th);
+                        }
+                    }
+                    l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+                    tmem_wait_st();
+                }
+                um::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) um::mbar_arrive(p_full + 2 * t + buf);
+            }
+            if (ok && end > 0) {
+                const bool here = um::mbar_wait(o_done + 2 * t + (steps0 + end - 1) % kBufs,
+                                                (uint32_t)((steps0 + end - 1) / kBufs) & 1u, kWaitCycles);
+                ok = __all_sync(0xffffffffu, here);
+                um::tc_fence_after();
+            }
+            if (!ok && lane == 0) {
+                *abort_flag = 1;
+                set_status(status, RKV_ERR_DEVICE_TIMEOUT);
+            }
+            // outputs: through shared memory, so that a warp stores whole lines.  The query rows' place
+            // is free once both halves' products are complete
+            um::bar_sync(1, 256);
+            if (busy) {
+                const size_t base = (((size_t)run.slot * N + n) * 2 + (two ? 0 : t)) * R + row0;
+                const int r_warp = (two ? 128 * t : 0) + 32 * w;
+                if (end > 0 && ok) {
+                    float *stage = (float *)qs + (size_t)(warp - 12) * 32 * 32;
+#pragma unroll 1
+                    for (int k = 0; k < D / 32; ++k) {
+                        float v[32];
+                        tmem_ld32(to + 32 * k, v);
+                        tmem_wait_ld(v);
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) stage[lane * 32 + (e ^ lane)] = v[e];
+                        __syncwarp();
 #pragma unroll 4
-                    for (int x = 0; x < 32; ++x)
-                        if (r_warp + x < rows) part[(base + r_warp + x) * D + 32 * k + lane] = stage[x * 32 + (lane ^ x)];
+                        for (int x = 0; x < 32; ++x)
+                            if (r_warp + x < rows) part[(base + r_warp + x) * D + 32 * k + lane] = stage[x * 32 + (lane ^ x)];
+                    }
+                }
+                if (r < rows) {
+                    ml[base + r] = make_float2(ok ? m_ref : __uint_as_float(0x7fffffffu), l);
+                    if (two)                                   // the second partial of the run is empty
+                        ml[base + R + r] = make_float2(-INFINITY, 0.0f);
                 }
             }
-            if (r < rows) {
-                ml[base + r] = make_float2(ok ? m_ref : __uint_as_float(0x7fffffffu), l);
-                if (two)                                   // the second partial of the run is empty
-                    ml[base + R + r] = make_float2(-INFINITY, 0.0f);
-            }
-        }
-        ok = bar_all(ok);                                  // then the next run's query rows go there
-        steps0 += end;
-        ++runs0;
+            ok = bar_all(ok);                                  // then the next run's query rows go there
+            steps0 += end;
+            ++runs0;
         }
     }
     um::tc_fence_before();
