@@ -104,8 +104,9 @@ __device__ __forceinline__ int2 dense_shares(const int32_t *len, int S, int T, i
 {
     const int lane = threadIdx.x & 31;
     int all = 0;
-    for (int s0 = 0; s0 < S; s0 += 32)
-        all += __reduce_add_sync(0xffffffffu, blocks_of(len, s0 + lane, S, T, listed, status));
+#pragma unroll 8
+    for (int s = lane; s < S; s += 32) all += blocks_of(len, s, S, T, listed, status);
+    all = __reduce_add_sync(0xffffffffu, all);
     const int per = min(c.most, max(c.least, (int)(((long long)all + c.ctas - 1) / c.ctas)));
     return make_int2(all, (per + c.unit - 1) / c.unit * c.unit);
 }
@@ -122,6 +123,17 @@ __device__ __forceinline__ DenseRun dense_run(const int32_t *len, int S, int T, 
     const int lane = threadIdx.x & 31;
     if (c.at >= c.end) return DenseRun{-1, 0, 0, 0};
     for (; c.s0 < S; c.s0 += 32) {
+        if (c.s0 % 256 == 0 && c.s0 + 256 <= S) {          // past 256 sequences at once, loads in flight
+            int n = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) n += blocks_of(len, c.s0 + 32 * k + lane, S, T, listed, status);
+            n = __reduce_add_sync(0xffffffffu, n);
+            if (c.at >= c.base + n) {
+                c.base += n;
+                c.s0 += 256 - 32;
+                continue;
+            }
+        }
         const int n = blocks_of(len, c.s0 + lane, S, T, listed, status), upto = c.base + lane_scan(n);
         const uint32_t hit = __ballot_sync(0xffffffffu, c.at < upto);
         if (hit) {
@@ -136,23 +148,17 @@ __device__ __forceinline__ DenseRun dense_run(const int32_t *len, int S, int T, 
     c.at = c.end;                            // lengths that changed under the call
     return DenseRun{-1, 0, 0, 0};
 }
-// The runs of sequence s, by one warp: first number in .first, one past the last in .end.
-__device__ __forceinline__ DenseRun dense_runs_of(const int32_t *len, int S, int T, int listed, const DenseCut &c, int s,
-                                                  int32_t *status)
+// The runs of sequence s.  The first kernel leaves what the last pass needs to find them: place[s],
+// the block (of all of them) that sequence s begins at, if it has any, and place[S] = per.  (Worked
+// out from all lengths in each CTA of the last pass, 2048 sequences of 2 heads took it 150 us
+// instead of 43.)  First number in .first, one past the last in .end, both within the workspace's
+// `slots` even where lengths changed under the call.
+__device__ __forceinline__ DenseRun dense_runs_of(const int32_t *place, int S, int s, int blocks, int slots)
 {
-    const int lane = threadIdx.x & 31;
-    const int per = dense_shares(len, S, T, listed, c, status).y;
-    int base = 0;
-    for (int s0 = 0; s0 <= s; s0 += 32) {
-        const int n = blocks_of(len, s0 + lane, S, T, listed, status), upto = base + lane_scan(n);
-        if (s < s0 + 32) {
-            const int begin = __shfl_sync(0xffffffffu, upto - n, s - s0), stop = __shfl_sync(0xffffffffu, upto, s - s0);
-            if (begin == stop) break;
-            return DenseRun{s, begin / per + s, (stop - 1) / per + s + 1, 0};
-        }
-        base = __shfl_sync(0xffffffffu, upto, 31);
-    }
-    return DenseRun{s, 0, 0, 0};
+    if (blocks == 0) return DenseRun{s, 0, 0, 0};
+    const unsigned per = max(__ldcg(place + S), 1), begin = max(__ldcg(place + s), 0);
+    const int first = (int)min(begin / per + s, (unsigned)slots);
+    return DenseRun{s, first, max(first, (int)min((begin + blocks - 1u) / per + s + 1u, (unsigned)slots)), 0};
 }
 
 // The two codes at pair j of a word as bf16: 128 + code is exact in 8 significant bits.
@@ -205,6 +211,6 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
 // each run and KV head.
 cudaError_t launch_dense_tree(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *cache,
                               const int32_t *len, const DenseCut &cut, int ctas, float scale_log2, bool p_lo, float *part,
-                              float2 *ml, int32_t *status, cudaStream_t s);
+                              float2 *ml, int32_t *place, int32_t *status, cudaStream_t s);
 
 }  // namespace rkv

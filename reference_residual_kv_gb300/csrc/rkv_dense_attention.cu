@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT0 <= 1 && D <= 128 ? 2 : 1)
 k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ codes,
               const uint8_t *__restrict__ khdr, const int32_t *__restrict__ len, const int32_t *__restrict__ blocks,
               int lists, int n_blocks, int S, int T, int N, int G, int nq, int nb, DenseCut cut, int tiles,
-              float scale_log2, float *__restrict__ part, float2 *__restrict__ ml, int32_t *status)
+              float scale_log2, float *__restrict__ part, float2 *__restrict__ ml, int32_t *place, int32_t *status)
 {
     using C = SplitCfg<D, BITS, NT0>;
     constexpr int NT = C::NT;
@@ -113,8 +113,12 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
     __shared__ DenseRun run_s;
     __shared__ DenseCursor cursor_s;
     if (warp == 0) {
-        const DenseCursor at = dense_share(dense_shares(len, S, T, listed, cut, status), share);
-        if (lane == 0) cursor_s = at;
+        const int2 all = dense_shares(len, S, T, listed, cut, status);
+        const DenseCursor at = dense_share(all, share);
+        if (lane == 0) {
+            cursor_s = at;
+            if (blockIdx.x == 0) place[S] = all.y;
+        }
         __syncwarp();
     }
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -132,11 +136,14 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
     while (true) {
         if (warp == 0) {
             DenseCursor at = cursor_s;
+            const int before = at.at;
             const DenseRun r = dense_run(len, S, T, listed, share, at, status);
             __syncwarp();
             if (lane == 0) {
                 run_s = r;
                 cursor_s = at;
+                // a sequence that begins here
+                if (r.s >= 0 && r.first == 0 && n == 0 && tile == 0) place[r.s] = before;
             }
         }
         __syncthreads();
@@ -425,9 +432,10 @@ template <int D, int RPW>
 __global__ void __launch_bounds__(32 * kFinWarps, D <= 128 ? 4 : 2)
 k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ tail,
                const int32_t *__restrict__ len, const int32_t *__restrict__ parent,
-               const __nv_bfloat16 *__restrict__ draft, int S, int T, int N, int G, int nq, DenseCut cut, int listed,
+               const __nv_bfloat16 *__restrict__ draft, int S, int T, int N, int G, int nq, int listed, int slots,
                int each_log, int wpr, int row_ctas, float scale_log2, const float *__restrict__ part,
-               const float2 *__restrict__ ml, void *__restrict__ out, int out_bf16, int32_t *status)
+               const float2 *__restrict__ ml, const int32_t *place, void *__restrict__ out, int out_bf16,
+               int32_t *status)
 {
     constexpr int kCh = D / 8, kPad = kCh + 1, kE = D / 32;   // 16-byte chunks of a row; channels of a lane
     extern __shared__ __align__(128) uint8_t smem[];
@@ -435,7 +443,6 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
     __shared__ __align__(16) float part_s[kFinWarps][D + 4];
     __shared__ float2 ml_s[kFinWarps];
     __shared__ int par[kMaxDraft];
-    __shared__ DenseRun runs_s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sn = blockIdx.x / row_ctas, s = sn / N, n = sn % N;
     const int R = nq * G, rpc = kFinWarps / wpr * RPW, r0 = (blockIdx.x % row_ctas) * rpc;
@@ -464,10 +471,6 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
         vs[t * kPad + ch] = __ldg(vr + ch);
     }
     __syncthreads();
-    if (warp == kFinWarps - 1) {
-        const DenseRun x = dense_runs_of(len, S, T, listed, cut, s, status);
-        if (lane == 0) runs_s = x;
-    }
     if (warp < 2 * groups && (warp >= 2 || rest)) {
         // tokens 16 warp ..: rows of the first operand (those that are not there give scores
         // that no row takes); the query rows are the second one's columns (zero behind the last)
@@ -575,7 +578,7 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // 1 << each_log partials for every run and KV head, this warp's every wpr-th; 32 at a time:
     // their weights, a lane each, then their sums, those with nothing in them left out
-    const DenseRun runs = runs_s;
+    const DenseRun runs = dense_runs_of(place, S, s, listed ? listed : length / kBlk, slots);
     const int parts = (runs.end - runs.first) << each_log;
     const size_t next_run = ((size_t)N << each_log) * R;
 #pragma unroll
@@ -691,7 +694,7 @@ Plan plan_of(const DenseGeom &g, int H, int nq, bool f32)
         p.tiles = (R + 255) / 256;
         // one to an SM; for fp32 outputs no share above 96 blocks, since the products' accumulators
         // cut what they add (64 drafts over 131072 tokens, error against 64 bits: 6.7e-6 at 216
-        // blocks and 289 us, 3.1e-6 at 96 blocks and 395 us; smaller work is not cut finer)
+        // blocks and 289 us, 3.1e-6 at 96 blocks and 390 us; smaller work is not cut finer)
         ctas = 152;
         if (f32) p.cut.most = 96;
         p.cut.least = 16;
@@ -711,7 +714,7 @@ Plan plan_of(const DenseGeom &g, int H, int nq, bool f32)
 template <int D, int BITS, int NT0, bool P3>
 cudaError_t run_split(const DenseGeom &g, const Plan &p, int H, const void *q, int nq, const rkv_dense_cache *c,
                       const int32_t *len, const int32_t *blocks, int lists, int n_blocks, float scale_log2,
-                      float *part, float2 *ml, int32_t *status, cudaStream_t s)
+                      float *part, float2 *ml, int32_t *place, int32_t *status, cudaStream_t s)
 {
     using C = SplitCfg<D, BITS, NT0>;
     static PerDevice<int> setup;
@@ -723,14 +726,15 @@ cudaError_t run_split(const DenseGeom &g, const Plan &p, int H, const void *q, i
     ProfScope prof("dense_attention_split", s);
     k_dense_split<D, BITS, NT0, P3><<<(unsigned)((size_t)p.ctas * g.N * p.tiles), 32 * kWarps, C::kSmem, s>>>(
         (const __nv_bfloat16 *)q, (const uint8_t *)c->codes, (const uint8_t *)c->khdr, len, blocks, lists, n_blocks,
-        g.S, g.T, g.N, H / g.N, nq, g.nb, p.cut, p.tiles, scale_log2, part, ml, status);
+        g.S, g.T, g.N, H / g.N, nq, g.nb, p.cut, p.tiles, scale_log2, part, ml, place, status);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t run_finish(const DenseGeom &g, const Plan &p, int H, const void *q, int nq, int listed, const int32_t *parent,
                        const void *draft, const rkv_dense_cache *c, const int32_t *len, float scale_log2,
-                       const float *part, const float2 *ml, void *out, int out_dtype, int32_t *status, cudaStream_t s)
+                       const float *part, const float2 *ml, const int32_t *place, void *out, int out_dtype, int32_t *status,
+                       cudaStream_t s)
 {
     const int R = nq * (H / g.N);
     const int wpr = R <= 1 ? 8 : (R <= 2 ? 4 : (R <= 4 ? 2 : 1));
@@ -761,9 +765,10 @@ cudaError_t run_finish(const DenseGeom &g, const Plan &p, int H, const void *q, 
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, twice ? k_dense_finish<D, 2> : k_dense_finish<D, 1>, (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)c->tail,
-                                       len, parent, (const __nv_bfloat16 *)draft, g.S, g.T, g.N, H / g.N, nq, p.cut, listed,
-                                       p.each - 1, wpr, row_ctas, scale_log2, part, ml, out, (int)(out_dtype == RKV_BF16), status);
+    e = cudaLaunchKernelEx(&cfg, twice ? k_dense_finish<D, 2> : k_dense_finish<D, 1>, (const __nv_bfloat16 *)q,
+                           (const __nv_bfloat16 *)c->tail, len, parent, (const __nv_bfloat16 *)draft, g.S, g.T, g.N,
+                           H / g.N, nq, listed, p.slots, p.each - 1, wpr, row_ctas, scale_log2, part, ml, place, out,
+                           (int)(out_dtype == RKV_BF16), status);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -775,7 +780,7 @@ size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq)
 {
     const Plan p = plan_of(g, H, nq, true);                // the larger one
     const size_t rows = (size_t)p.slots * p.each * nq * H;
-    return align256(rows * g.D * sizeof(float)) + align256(rows * sizeof(float2));
+    return align256(rows * g.D * sizeof(float)) + align256(rows * sizeof(float2)) + ((size_t)g.S + 1) * 4;
 }
 
 cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int nq, const int32_t *parent,
@@ -787,6 +792,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
     const size_t rows = (size_t)p.slots * p.each * nq * H;
     float *part = (float *)ws;
     float2 *ml = (float2 *)((uint8_t *)ws + align256(rows * g.D * sizeof(float)));
+    int32_t *place = (int32_t *)((uint8_t *)ml + align256(rows * sizeof(float2)));
     const float scale_log2 = (float)(1.4426950408889634 / sqrt((double)g.D));
     auto go = [&](auto bits, auto d) -> cudaError_t {
         constexpr int B = decltype(bits)::value, D = decltype(d)::value;
@@ -795,7 +801,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
             constexpr bool P3 = decltype(third)::value;
             auto by = [&](auto nt) -> cudaError_t {
                 return run_split<D, B, decltype(nt)::value, P3>(g, p, H, q, nq, cache, len, blocks, lists, n_blocks,
-                                                                scale_log2, part, ml, status, s);
+                                                                scale_log2, part, ml, place, status, s);
             };
             using std::integral_constant;
             switch (p.nt) {
@@ -808,13 +814,15 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
             }
         };
         if (p.tree)
-            e = launch_dense_tree(g, H, q, nq, cache, len, p.cut, p.ctas, scale_log2, out_dtype == RKV_F32, part, ml, status, s);
+            e = launch_dense_tree(g, H, q, nq, cache, len, p.cut, p.ctas, scale_log2, out_dtype == RKV_F32, part, ml, place,
+                                  status, s);
         else if (out_dtype == RKV_F32)
             e = split(std::true_type{});
         else
             e = split(std::false_type{});
         if (e != cudaSuccess) return e;
-        return run_finish<D>(g, p, H, q, nq, blocks ? n_blocks : 0, parent, draft, cache, len, scale_log2, part, ml, out, out_dtype, status, s);
+        return run_finish<D>(g, p, H, q, nq, blocks ? n_blocks : 0, parent, draft, cache, len, scale_log2, part, ml, place,
+                             out, out_dtype, status, s);
     };
     return dense_dispatch(g, go);
 }

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ codes,
              const uint8_t *__restrict__ khdr, const int32_t *__restrict__ len, int S, int T, int N, int G, int nq, int nb,
              DenseCut cut, int tiles, float scale_log2, float *__restrict__ part, float2 *__restrict__ ml,
-             int32_t *status)
+             int32_t *place, int32_t *status)
 {
     using C = TreeCfg<D, BITS>;
     constexpr int kBufs = LO ? 1 : 2;                      // buffers for a half's scores and P
@@ -222,6 +222,7 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
     }
     __syncthreads();
     DenseCursor cursor = dense_share(share_s, share);
+    if (blockIdx.x == 0 && threadIdx.x == 0) place[S] = share_s.y;
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (cursor.at >= cursor.end) return;
     const int R = nq * G, row0 = tile * 256, rows = min(256, R - row0);
@@ -466,8 +467,13 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
         // are left get their NaN.
         while (true) {
             if (warp == 12) {
+                const int before = cursor.at;
                 const DenseRun r12 = next_run();
-                if (lane == 0) run_s = r12;
+                if (lane == 0) {
+                    run_s = r12;
+                    // a sequence that begins here
+                    if (r12.s >= 0 && r12.first == 0 && n == 0 && tile == 0) place[r12.s] = before;
+                }
             }
             um::bar_sync(1, 256);
             const DenseRun run = run_s;
@@ -626,7 +632,8 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
 
 template <int D, int BITS, bool LO>
 cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *c, const int32_t *len,
-                const DenseCut &cut, int ctas, float scale_log2, float *part, float2 *ml, int32_t *status, cudaStream_t s)
+                const DenseCut &cut, int ctas, float scale_log2, float *part, float2 *ml, int32_t *place, int32_t *status,
+                cudaStream_t s)
 {
     using C = TreeCfg<D, BITS>;
     static PerDevice<int> setup;
@@ -639,7 +646,7 @@ cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dens
     ProfScope prof("dense_attention_tree", s);
     k_dense_tree<D, BITS, LO><<<(unsigned)((size_t)ctas * g.N * tiles), kThreads, C::kSmem, s>>>(
         (const __nv_bfloat16 *)q, (const uint8_t *)c->codes, (const uint8_t *)c->khdr, len, g.S, g.T, g.N, H / g.N,
-        nq, g.nb, cut, tiles, scale_log2, part, ml, status);
+        nq, g.nb, cut, tiles, scale_log2, part, ml, place, status);
     return cudaGetLastError();
 }
 
@@ -647,13 +654,13 @@ cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dens
 
 cudaError_t launch_dense_tree(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *c,
                               const int32_t *len, const DenseCut &cut, int ctas, float scale_log2, bool p_lo, float *part,
-                              float2 *ml, int32_t *status, cudaStream_t s)
+                              float2 *ml, int32_t *place, int32_t *status, cudaStream_t s)
 {
     auto go = [&](auto bits, auto d) -> cudaError_t {
         constexpr int B = decltype(bits)::value, D = decltype(d)::value;
         if constexpr (D <= 128)
-            return p_lo ? run<D, B, true>(g, H, q, nq, c, len, cut, ctas, scale_log2, part, ml, status, s)
-                        : run<D, B, false>(g, H, q, nq, c, len, cut, ctas, scale_log2, part, ml, status, s);
+            return p_lo ? run<D, B, true>(g, H, q, nq, c, len, cut, ctas, scale_log2, part, ml, place, status, s)
+                        : run<D, B, false>(g, H, q, nq, c, len, cut, ctas, scale_log2, part, ml, place, status, s);
         else
             return cudaErrorInvalidValue;
     };
