@@ -505,6 +505,8 @@ class DenseCache:
         cache's device current, scratch of `need` bytes (None: it takes none) from the pool of the
         stream that the call runs on."""
         dev = self.device.index
+        if dev is None:
+            raise ValueError("%s: the cache is on %s, not on a GPU" % (name, self.device))
         if stream is None and torch.cuda.current_device() == dev:
             st = self._enter(name, need, args, _raw_stream(dev))
         else:

@@ -136,6 +136,21 @@ def test_the_cache_object_checks_its_tensors(lib):
             f()
 
 
+def test_a_cache_off_the_gpu_is_refused(lib):
+    c = rkv.DenseCache(rkv.make_dense_params(2, 100, 4, 128), device="cpu")
+    pos = torch.zeros(2, dtype=torch.int32)
+    kv = torch.zeros(2, 3, 1024, dtype=torch.bfloat16)
+    q, out = torch.zeros(2, 8, 128, dtype=torch.bfloat16), torch.zeros(2, 8, 128)
+    rows, blocks = torch.zeros(2, 3, 512, dtype=torch.bfloat16), torch.zeros(2, 4, 2, dtype=torch.int32)
+    qt, parent = torch.zeros(2, 3, 8, 128, dtype=torch.bfloat16), torch.zeros(2, 3, dtype=torch.int32)
+    for f in (lambda s: c.write(kv, pos, stream=s), lambda s: c.read(pos, parent, rows, rows, stream=s),
+              lambda s: c.select(8, q, pos, blocks, stream=s), lambda s: c.attend(8, q, pos, out, stream=s),
+              lambda s: c.tree_attend(8, qt, parent, kv, pos, torch.zeros(2, 3, 8, 128), stream=s)):
+        for stream in (None, 1):
+            with pytest.raises(ValueError, match="not on a GPU"):
+                f(stream)
+
+
 def test_oracle_rounding_and_codes():
     # bf16 rounding with one rounding: ties to even, and a border that fp32 alone would hit
     assert list(do.bf16([1.0 + 2.0 ** -8, 1.0 + 3 * 2.0 ** -8, 1.0 + 2.0 ** -8 + 2.0 ** -40, -(1.0 + 2.0 ** -8 - 2.0 ** -40)]) ) \

@@ -572,6 +572,25 @@ def test_trees_over_many_short_sequences_among_long_ones(D, bits, G, n):
     case.done()
 
 
+def test_hundreds_of_sequences():
+    # more than 256, which are passed over at once where none of them is a CTA's; empty ones, and
+    # one long one beyond the first 256
+    rng = np.random.default_rng(5)
+    S = 601
+    lens = [int(x) for x in rng.integers(0, 100, S)]
+    lens[0], lens[255], lens[256], lens[511], lens[580] = 31, 0, 64, 1, 640
+    case = Case(make_rows(rng, S, 650, 1, 64), lens, 4)
+    q = do.bf16(rng.normal(size=(S, 2, 64)))
+    check_attend(case, q, attend_gpu(case, q))
+    blocks = rng.integers(-1, 3, (S, 1, 4)).astype(np.int32)
+    blocks[(blocks >= np.array(lens)[:, None, None] // 32)] = -1
+    check_attend(case, q, attend_gpu(case, q, blocks), blocks)
+    for n in (3, 17):
+        qt, draft, parent = do.bf16(rng.normal(size=(S, n, 2, 64))), make_rows(rng, S, n, 1, 64), random_tree(rng, S, n)
+        check_tree(case, qt, parent, draft, tree_gpu(case, qt, parent, draft))
+    case.done()
+
+
 def test_selection_over_more_blocks_than_shared_memory_holds():
     # 42000 blocks of one head; all keys equal but for nine blocks that stand out: those, the
     # kept ends, and the lowest of the others
