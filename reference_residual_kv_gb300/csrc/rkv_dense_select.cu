@@ -15,7 +15,7 @@
 //                   the largest error bound, blocks above t + 2 E are in and those below
 //                   t - 2 E are out.  If the ones between are more than there is room for,
 //                   they are scored again in 70 bits and ranked by (score, lower index).
-//                   512 of 4096 blocks in 19 us: a chain of passes over the keys with barriers
+//                   512 of 4096 blocks in 17.5 us: a chain of passes over the keys with barriers
 //                   between them, by one CTA where there is one list (43 % of its SM's issue).
 // The fp32 sums of the tensor cores are taken to be within kErr A of the exact score: 512
 // terms at 2^-24 each would give 2^-15 A, even if every addition cut instead of rounding.
@@ -449,10 +449,24 @@ k_block_pick(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kh
             }
             for (int i = tid; i < cands; i += kPickThreads) ex[i] = 0ull;
             __syncthreads();
-            for (int i = warp; i < cands * heads; i += kPickWarps) {
-                const unsigned long long k = exact_score<D>(q, khdr, (size_t)s * N + n0 + i % heads, G, nb,
-                                                            cand[i / heads], qmax, lane);
-                if (lane == 0) atomicMax(ex + i / heads, k);   // a maximum: in any order
+            // a lane looks at a pair of candidate and head: heads whose score plus its error cannot
+            // reach the candidate's largest one do not decide it (the 512 best of 4096 blocks of 8
+            // heads: 19.5 -> 17.5 us)
+            for (int i0 = warp; i0 < cands * heads; i0 += 32 * kPickWarps) {
+                const int i = i0 + lane * kPickWarps;
+                bool needed = i < cands * heads;
+                if (needed && heads > 1) {
+                    const int b = cand[i / heads];
+                    needed = !(scores[((size_t)s * N + n0 + i % heads) * nb + b].x < value32(keys[b]) - band);
+                }
+                uint32_t todo = __ballot_sync(0xffffffffu, needed);
+                while (todo) {
+                    const int j = i0 + (__ffs(todo) - 1) * kPickWarps;
+                    todo &= todo - 1u;
+                    const unsigned long long k = exact_score<D>(q, khdr, (size_t)s * N + n0 + j % heads, G, nb,
+                                                                cand[j / heads], qmax, lane);
+                    if (lane == 0) atomicMax(ex + j / heads, k);   // a maximum: in any order
+                }
             }
             __syncthreads();
             if (cands <= kSmallCand) {
