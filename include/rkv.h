@@ -349,9 +349,7 @@ rkv_status rkv_dense_attention(const rkv_dense_params *p, int32_t H, const void 
  * draft_kv: bf16 [S][n_draft][2 N D], K then V, as for rkv_dense_write; the cache is not
  * changed (accepted tokens are written with rkv_dense_write).  What lies in rows that a
  * token does not see has no effect on it, NaN included.  Probabilities meet the values of
- * finished blocks as in rkv_dense_attention, except where a KV head has more than 32 query
- * rows (n_draft H/N) of D <= 128 and outputs are bf16: in one part (2^-8 for each, half a step
- * of the outputs).
+ * finished blocks as in rkv_dense_attention.
  * q: bf16 [S][n_draft][H][D]; out: [S][n_draft][H][D] in out_dtype.  1 <= n_draft <= 64.
  * workspace: >= the bytes of rkv_dense_attention_workspace(p, H, n_draft), 256-byte
  * aligned.  Requires H a multiple of N, H/N <= 8.                                        */

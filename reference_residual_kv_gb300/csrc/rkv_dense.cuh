@@ -210,7 +210,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
 // The finished blocks against many query rows (rkv_dense_tree.cu), D <= 128: two partials for
 // each run and KV head.
 cudaError_t launch_dense_tree(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *cache,
-                              const int32_t *len, const DenseCut &cut, int ctas, float scale_log2, bool p_lo, float *part,
+                              const int32_t *len, const DenseCut &cut, int ctas, float scale_log2, bool p3, float *part,
                               float2 *ml, int32_t *place, int32_t *status, cudaStream_t s);
 
 }  // namespace rkv

@@ -22,12 +22,12 @@
 //                in fp32 sums and has the same relative error in bf16), so that the output
 //                accumulator is rescaled only where the maximum grows by more than that; P
 //                goes back to tensor memory, over the scores, as the first operand of P V.
-// P is bf16 for bf16 outputs (2^-8 for each p, half a step, as the output's own rounding), and
-// three parts of bf16 for fp32 outputs; those take the columns of both buffers, so that there
-// is one.
-// 64 drafts x 4 heads over 131072 tokens, 8 KV heads: 133-135 us, 1.0 PFLOP/s.  No unit is full
-// (issue 57 %, integer pipe 46 %, tensor pipe 45 %, its memory 52 %): the chain scores, softmax,
-// P, outputs of the two halves is what the time goes to.
+// P is bf16 in two parts (the scores' 64 columns hold both), as in the split pass, so that the
+// number of query rows does not change the outputs' precision; fp32 outputs have three, which take
+// the columns of both buffers, so that there is one.  In one part P put bf16 outputs 1.85e-3 off
+// instead of 1.6e-3, which is their own rounding.
+// 64 drafts x 4 heads over 131072 tokens, 8 KV heads: a call of 173 us (145 with one part).  The
+// chain scores, softmax, P, outputs of the two halves is what the time goes to.
 // All waits are bounded; a CTA whose wait runs out sets RKV_ERR_DEVICE_TIMEOUT and writes NaN
 // as its partials' maxima, so that its rows read NaN.
 #include "rkv_dense.cuh"
@@ -194,7 +194,7 @@ __device__ __forceinline__ uint32_t tile_at(int rows, int r, int ch)
     return (uint32_t)((ch >> 3) * rows * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
 
-template <int D, int BITS, bool LO>
+template <int D, int BITS, bool P3>
 __global__ void __launch_bounds__(kThreads, 1)
 k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ codes,
              const uint8_t *__restrict__ khdr, const int32_t *__restrict__ len, int S, int T, int N, int G, int nq, int nb,
@@ -202,7 +202,7 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
              int32_t *place, int32_t *status)
 {
     using C = TreeCfg<D, BITS>;
-    constexpr int kBufs = LO ? 1 : 2;                      // buffers for a half's scores and P
+    constexpr int kBufs = P3 ? 1 : 2;                      // buffers for a half's scores and P
     extern __shared__ uint8_t smem_raw[];
     uint8_t *qs = smem_raw + ((1024u - (um::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *kt = qs + C::kQ, *vt = kt + 2 * C::kTile, *ring = vt + 2 * C::kTile;
@@ -353,10 +353,8 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
                     for (int k = 0; k < kStep / 16; ++k) {
                         const uint32_t ak = a + 32 * (k >> 1) + 8 * (k & 1);
                         mma_bf16_ta(tm, ak, v + 2 * k, id_o, (j | k) != 0);
-                        if (LO) {
-                            mma_bf16_ta(tm, ak + 16, v + 2 * k, id_o, 1);
-                            mma_bf16_ta(tm, a + kStep + 8 * k, v + 2 * k, id_o, 1);
-                        }
+                        mma_bf16_ta(tm, ak + 16, v + 2 * k, id_o, 1);
+                        if (P3) mma_bf16_ta(tm, a + kStep + 8 * k, v + 2 * k, id_o, 1);
                     }
                     um::mma_commit(o_done + 2 * t + buf);
                     if (leaves(g)) um::mma_commit(v_empty + b);
@@ -558,18 +556,14 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
                             sums[e & 1] = __fadd2_rn(sums[e & 1], pp);
                             const __nv_bfloat162 h2 = __floats2bfloat162_rn(pp.x, pp.y);
                             hi[e] = as_u32(h2);
-                            if (LO) {
-                                const float rx = pp.x - __low2float(h2), ry = pp.y - __high2float(h2);
-                                const __nv_bfloat162 l2 = __floats2bfloat162_rn(rx, ry);
-                                lo[e] = as_u32(l2);
-                                th[e] = as_u32(__floats2bfloat162_rn(rx - __low2float(l2), ry - __high2float(l2)));
-                            }
+                            const float rx = pp.x - __low2float(h2), ry = pp.y - __high2float(h2);
+                            const __nv_bfloat162 l2 = __floats2bfloat162_rn(rx, ry);
+                            lo[e] = as_u32(l2);
+                            if (P3) th[e] = as_u32(__floats2bfloat162_rn(rx - __low2float(l2), ry - __high2float(l2)));
                         }
                         tmem_st16(ts + 32 * k, hi);
-                        if (LO) {
-                            tmem_st16(ts + 32 * k + 16, lo);
-                            tmem_st16(ts + kStep + 16 * k, th);
-                        }
+                        tmem_st16(ts + 32 * k + 16, lo);
+                        if (P3) tmem_st16(ts + kStep + 16 * k, th);
                     }
                     l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
                     tmem_wait_st();
@@ -630,7 +624,7 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
     }
 }
 
-template <int D, int BITS, bool LO>
+template <int D, int BITS, bool P3>
 cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *c, const int32_t *len,
                 const DenseCut &cut, int ctas, float scale_log2, float *part, float2 *ml, int32_t *place, int32_t *status,
                 cudaStream_t s)
@@ -639,12 +633,12 @@ cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dens
     static PerDevice<int> setup;
     int unused = 0;
     cudaError_t e = per_device(setup, unused, [](int &) {
-        return cudaFuncSetAttribute(k_dense_tree<D, BITS, LO>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        return cudaFuncSetAttribute(k_dense_tree<D, BITS, P3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (e != cudaSuccess) return e;
     const int tiles = (nq * (H / g.N) + 255) / 256;
     ProfScope prof("dense_attention_tree", s);
-    k_dense_tree<D, BITS, LO><<<(unsigned)((size_t)ctas * g.N * tiles), kThreads, C::kSmem, s>>>(
+    k_dense_tree<D, BITS, P3><<<(unsigned)((size_t)ctas * g.N * tiles), kThreads, C::kSmem, s>>>(
         (const __nv_bfloat16 *)q, (const uint8_t *)c->codes, (const uint8_t *)c->khdr, len, g.S, g.T, g.N, H / g.N,
         nq, g.nb, cut, tiles, scale_log2, part, ml, place, status);
     return cudaGetLastError();
@@ -653,13 +647,13 @@ cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dens
 }  // namespace
 
 cudaError_t launch_dense_tree(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *c,
-                              const int32_t *len, const DenseCut &cut, int ctas, float scale_log2, bool p_lo, float *part,
+                              const int32_t *len, const DenseCut &cut, int ctas, float scale_log2, bool p3, float *part,
                               float2 *ml, int32_t *place, int32_t *status, cudaStream_t s)
 {
     auto go = [&](auto bits, auto d) -> cudaError_t {
         constexpr int B = decltype(bits)::value, D = decltype(d)::value;
         if constexpr (D <= 128)
-            return p_lo ? run<D, B, true>(g, H, q, nq, c, len, cut, ctas, scale_log2, part, ml, place, status, s)
+            return p3 ? run<D, B, true>(g, H, q, nq, c, len, cut, ctas, scale_log2, part, ml, place, status, s)
                         : run<D, B, false>(g, H, q, nq, c, len, cut, ctas, scale_log2, part, ml, place, status, s);
         else
             return cudaErrorInvalidValue;
