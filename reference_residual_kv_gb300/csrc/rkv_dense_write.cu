@@ -324,6 +324,7 @@ k_dense_write(const __grid_constant__ CUtensorMap map, int mapped, const TIN *__
             }
             __syncwarp();
             if (!__all_sync(0xffffffffu, um::mbar_wait(bars + warp, 0, kWaitCycles))) {
+                um::mbar_wait(bars + warp, 0, kWaitCycles);    // what is on its way gets as long again
                 set_status(status, RKV_ERR_DEVICE_TIMEOUT);
                 return;
             }
