@@ -427,14 +427,16 @@ k_dense_split(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ c
 // then drafted tokens 0..31, 32..63.  A group's scores for all rows are one product (two
 // warps, 16 tokens each); every row then takes its own, and adds p v for the tokens that it
 // sees alone.  The warps of a row deal tokens and partials among them.
+// part, ml and place are written while this kernel is already running: they are read behind the wait
+// and not declared as read-only.
 // With RPW = 2 a warp has two rows, 8 apart (wpr is 1 then), and a CTA's tokens serve 16 rows.
 template <int D, int RPW>
 __global__ void __launch_bounds__(32 * kFinWarps, D <= 128 ? 4 : 2)
 k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ tail,
                const int32_t *__restrict__ len, const int32_t *__restrict__ parent,
                const __nv_bfloat16 *__restrict__ draft, int S, int T, int N, int G, int nq, int listed, int slots,
-               int each_log, int wpr, int row_ctas, float scale_log2, const float *__restrict__ part,
-               const float2 *__restrict__ ml, const int32_t *place, void *__restrict__ out, int out_bf16,
+               int each_log, int wpr, int row_ctas, float scale_log2, const float *part,
+               const float2 *ml, const int32_t *place, void *__restrict__ out, int out_bf16,
                int32_t *status)
 {
     constexpr int kCh = D / 8, kPad = kCh + 1, kE = D / 32;   // 16-byte chunks of a row; channels of a lane
@@ -610,7 +612,8 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
             uint32_t todo = __ballot_sync(0xffffffffu, v.x > -INFINITY);
             constexpr int kU = RPW > 1 || kE > 4 ? 4 : 8;  // sums in flight
             while (todo) {
-                float x[kU][kE], w[kU];
+                alignas(16) float x[kU][kE];
+                float w[kU];
 #pragma unroll
                 for (int j = 0; j < kU; ++j) {
                     const int i = todo ? __ffs(todo) - 1 : 0;
@@ -620,8 +623,12 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
                     for (int e = 0; e < kE; ++e) x[j][e] = 0.0f;
                     if (todo) {
                         const float *pr = part + part_at(i0 + i * wpr) * D + lane * kE;
+                        if constexpr (kE == 2) {
+                            *(float2 *)x[j] = *(const float2 *)pr;
+                        } else {
 #pragma unroll
-                        for (int e = 0; e < kE; ++e) x[j][e] = pr[e];
+                            for (int e = 0; e < kE; e += 4) *(float4 *)(x[j] + e) = *(const float4 *)(pr + e);
+                        }
                     }
                     todo &= todo - 1u;
                 }

@@ -347,12 +347,13 @@ __device__ unsigned long long exact_score(const __nv_bfloat16 *q, const uint8_t 
 }
 
 // Workspace of a list beside the scores: keys (where they exceed shared memory), candidates
-// and their exact keys.
+// and their exact keys.  The scores are written while this kernel is already running: they are read
+// behind the wait, from L2, and not declared as read-only.
 template <int D>
 __global__ void __launch_bounds__(kPickThreads, 1)
 k_block_pick(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ khdr,
              const int32_t *__restrict__ len, int T, int N, int G, int nb, int lists, int want_all, int keep_first,
-             int keep_last, float qmax, const float2 *__restrict__ scores, uint32_t *keys_ws, int32_t *cand_ws,
+             int keep_last, float qmax, const float2 *scores, uint32_t *keys_ws, int32_t *cand_ws,
              unsigned long long *exact_ws, int32_t *__restrict__ blocks, int32_t *status)
 {
     extern __shared__ __align__(128) uint32_t smem_u[];
@@ -384,11 +385,11 @@ k_block_pick(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kh
     float e = 0.0f;
     for (int b = tid; b < have; b += kPickThreads) {
         const float2 *p = scores + ((size_t)s * N + n0) * nb + b;
-        float2 v = p[0];
+        float2 v = __ldcg(p);
         for (int n1 = 1; n1 < heads; n1 += 8) {            // eight loads in flight
             float2 x[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = p[(size_t)min(n1 + k, heads - 1) * nb];
+            for (int k = 0; k < 8; ++k) x[k] = __ldcg(p + (size_t)min(n1 + k, heads - 1) * nb);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 v.x = max_nan(v.x, x[k].x);
@@ -457,7 +458,7 @@ k_block_pick(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kh
                 bool needed = i < cands * heads;
                 if (needed && heads > 1) {
                     const int b = cand[i / heads];
-                    needed = !(scores[((size_t)s * N + n0 + i % heads) * nb + b].x < value32(keys[b]) - band);
+                    needed = !(__ldcg(scores + ((size_t)s * N + n0 + i % heads) * nb + b).x < value32(keys[b]) - band);
                 }
                 uint32_t todo = __ballot_sync(0xffffffffu, needed);
                 while (todo) {

@@ -33,3 +33,24 @@ def test_no_warp_leaves_with_a_copy_in_flight(name):
     assert given_up
     for b in given_up:
         assert "um::mbar_wait(" in b, b
+
+
+# a kernel that is launched while the one before it still runs must not take that one's outputs as
+# read-only: such loads may be moved before its wait, or come from a cache that does not follow writes
+@pytest.mark.parametrize("name,kernel,outputs", [
+    ("rkv_dense_attention.cu", "k_dense_finish", ("part", "ml", "place")),
+    ("rkv_dense_select.cu", "k_block_pick", ("scores",)),
+    ("rkv_attention.cu", "k_attn_combine", ("part",))])
+def test_outputs_of_the_kernel_before_are_not_read_only(name, kernel, outputs):
+    src = source(name)
+    at = src.index(kernel + "(")
+    args, body = src[at: src.index("{", at)], block_at(src, at)
+    assert "griddepcontrol.wait" in body
+    for x in outputs:
+        assert re.search(r"const \w+ \*%s\b" % x, args), x
+        assert not re.search(r"__ldg\([^,;]*\b%s\b" % x, body), x
+
+
+def test_every_kernel_that_waits_for_the_one_before_is_listed():
+    waiting = [f for f in os.listdir(CSRC) if f.endswith(".cu") for _ in re.findall(r"griddepcontrol\.wait", source(f))]
+    assert sorted(waiting) == ["rkv_attention.cu", "rkv_dense_attention.cu", "rkv_dense_select.cu"]
