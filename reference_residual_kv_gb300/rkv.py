@@ -469,6 +469,7 @@ class DenseCache:
     guard > 0 puts that many guard bytes behind every buffer, scratch included (test support)."""
 
     def __init__(self, p: rkv_dense_params, device="cuda", guard: int = 0):
+        p = rkv_dense_params.from_buffer_copy(p)           # the buffers' own: later changes to the caller's do not reach it
         codes, khdr, tail = rkv_dense_sizes(p)
         self.p = p
         self.S, self.T, self.N, self.D = p.S, p.T, p.N, p.D
