@@ -508,6 +508,8 @@ class DenseCache:
         dev = self.device.index
         if dev is None:
             raise ValueError("%s: the cache is on %s, not on a GPU" % (name, self.device))
+        if stream is not None and not isinstance(stream, int) and stream.device != self.device:
+            raise ValueError("%s: the stream is on %s, the cache on %s" % (name, stream.device, self.device))
         if stream is None and torch.cuda.current_device() == dev:
             st = self._enter(name, need, args, _raw_stream(dev))
         else:

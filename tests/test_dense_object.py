@@ -20,3 +20,14 @@ def test_a_cache_keeps_its_own_params():
     assert (d.p.S, d.p.T, d.p.bits) == (50, 4000, 2)
     assert c.codes.numel() == rkv.rkv_dense_sizes(c.p)[0] and d.codes.numel() == rkv.rkv_dense_sizes(d.p)[0]
     assert c._p_ref._obj is c.p
+
+
+def test_a_stream_of_another_device_is_refused():
+    # its launches would take this device's buffers to that one
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 1
+
+    c = rkv.DenseCache(rkv.make_dense_params(2, 100, 4, 128), device="cpu")
+    c.device = torch.device("cuda", 0)
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        c._call("rkv_dense_write", Stream(), None)
