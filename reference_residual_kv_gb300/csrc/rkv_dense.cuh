@@ -200,7 +200,7 @@ cudaError_t launch_block_select(const DenseGeom &g, int H, const void *q, const 
                                 const int32_t *len, int lists, int n_blocks, int keep_first, int keep_last,
                                 int32_t *blocks, void *ws, int32_t *status, cudaStream_t s);
 
-size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq);
+size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq, int out_dtype);
 // blocks may be NULL (all finished blocks); parent and draft are NULL for one token (nq = 1)
 cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int nq, const int32_t *parent,
                                    const void *draft, const rkv_dense_cache *cache, const int32_t *len,

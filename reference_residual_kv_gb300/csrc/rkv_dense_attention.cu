@@ -783,9 +783,9 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
-size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq)
+size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq, int out_dtype)
 {
-    const Plan p = plan_of(g, H, nq, true);                // the larger one
+    const Plan p = plan_of(g, H, nq, out_dtype == RKV_F32);
     const size_t rows = (size_t)p.slots * p.each * nq * H;
     return align256(rows * g.D * sizeof(float)) + align256(rows * sizeof(float2)) + ((size_t)g.S + 1) * 4;
 }
