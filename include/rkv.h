@@ -312,7 +312,9 @@ rkv_status rkv_dense_read(const rkv_dense_params *p, const rkv_dense_cache *cach
  * them, where there are fewer), ascending, then -1; the first keep_first and the last
  * keep_last finished blocks are always in it (keep_first + keep_last <= n_blocks).  The
  * ranking is that of the exact scores, equal ones by the lower index; a NaN ranks above
- * every number.
+ * every number.  (Scores of different blocks that differ by less than 2^-60 of the largest
+ * sum_d |q_d| max(|lo_d|, |hi_d|) of the list, or by less than 2^-52 of a score where such a
+ * sum is beyond the range of fp32, may be ranked either way.)
  * q: bf16 [S][H][D]; blocks (output): int32 [S][lists][n_blocks].
  * workspace: >= the bytes of rkv_block_select_workspace, 256-byte aligned.
  * Requires H a multiple of N, H/N <= 8.                                                  */

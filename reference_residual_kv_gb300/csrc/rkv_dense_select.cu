@@ -14,11 +14,13 @@
 //                   (counts only: nothing depends on an order of atomics); with E
 //                   the largest error bound, blocks above t + 2 E are in and those below
 //                   t - 2 E are out.  If the ones between are more than there is room for,
-//                   they are scored again in 70 bits and ranked by (score, lower index).
+//                   they are scored again in about 70 bits and ranked by (score, lower index).
 //                   512 of 4096 blocks in 17.5 us: a chain of passes over the keys with barriers
 //                   between them, by one CTA where there is one list (43 % of its SM's issue).
-// The fp32 sums of the tensor cores are taken to be within kErr A of the exact score: 512
-// terms at 2^-24 each would give 2^-15 A, even if every addition cut instead of rounding.
+// The fp32 sums of the tensor cores are taken to be within kErr A of the exact score: of a channel's
+// two products one is zero, and 256 additions that lose up to 2^-23 each, as they do if they cut
+// instead of rounding, give 2^-15 A.  kTiny stands for what products below fp32's range lose
+// (256 of at most 2^-126).
 #include "rkv_dense.cuh"
 
 namespace rkv {
@@ -27,7 +29,7 @@ namespace {
 constexpr int kScoreWarps = 4;
 constexpr int kPickThreads = 1024;
 constexpr int kPickWarps = kPickThreads / 32;
-constexpr float kErr = 1.0f / 16384.0f;
+constexpr float kErr = 1.0f / 16384.0f, kTiny = 0x1p-116f;
 constexpr int kSmallCand = 1024;             // candidates ranked by one thread each
 constexpr int kKeysSmem = 40960;             // scores kept in shared memory
 
@@ -113,7 +115,7 @@ k_block_scores(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ 
             e = max_nan(e, __shfl_xor_sync(0xffffffffu, e, o));
         }
         const int b = b0 + g + 8 * h;
-        if (c == 0 && b < have) scores[(size_t)sn * nb + b] = make_float2(v, e * kErr);
+        if (c == 0 && b < have) scores[(size_t)sn * nb + b] = make_float2(v, fmaf(e, kErr, kTiny));
     }
 }
 
@@ -243,12 +245,57 @@ struct Sum72 {
     }
 };
 
-// The exact score of block b for the query heads of KV head n, as an ordered key, by one warp.
+// The same in two doubles, for any product of bf16 numbers.
+struct Sum106 {
+    double a = 0.0, b = 0.0;
+    __device__ __forceinline__ void add(double x)
+    {
+        const double t = __dadd_rn(a, x), v = __dsub_rn(t, a);
+        b += __dadd_rn(__dsub_rn(a, __dsub_rn(t, v)), __dsub_rn(x, v));
+        a = t;
+    }
+};
+
+// How candidates' scores become keys: a candidate's largest is near the threshold t (its fp32 score
+// within 2.01 E, so less than 4 E), and 64 bits hold what lies between a score and t in units 2^-k
+// of 2^-58 E at most, that is, 2^-72 A, finer than the sums are.  Where t or E is infinite, the keys
+// are those of doubles.
+struct Scale { float t; int k; bool near; };
+__device__ __forceinline__ Scale scale_of(float t, float e)
+{
+    const bool near = fabsf(t) < INFINITY && e < INFINITY;
+    return Scale{t, near ? 58 - ilogbf(e) : 0, near};
+}
+// x in units of 2^-k, 2^61 at most (by shifts: fp64 takes 64 times as long)
+__device__ __forceinline__ long long fixed(float x, int k)
+{
+    const uint32_t u = __float_as_uint(x), e = (u >> 23) & 255u;
+    const unsigned long long m = (u & 0x7fffffu) | (e ? 0x800000u : 0u);
+    const int up = (int)max(e, 1u) - 150 + k;
+    unsigned long long v = up > 37 ? 1ull << 61 : m << max(up, 0);
+    if (up < 0) v = up > -26 ? (m + (1ull << (-up - 1))) >> -up : 0ull;
+    return (u >> 31) ? -(long long)v : (long long)v;
+}
+// Key of the score t + a + b + c, which is finite.  (Heads far below a candidate's largest are
+// never the maximum that is taken of the keys.)
+__device__ __forceinline__ unsigned long long near_key(const Scale &sc, float a, float b, float c)
+{
+    return (unsigned long long)(fixed(a, sc.k) + fixed(b, sc.k) + fixed(c, sc.k)) ^ (1ull << 63);
+}
+__device__ __forceinline__ unsigned long long near_key(const Scale &sc, double a, double b)
+{
+    const double x = scalbn(a, sc.k);
+    const long long v = fabs(x) < 0x1p61 ? __double2ll_rn(x) + __double2ll_rn(scalbn(b, sc.k)) : (x < 0.0 ? -1ll : 1ll) << 61;
+    return (unsigned long long)v ^ (1ull << 63);
+}
+
+// The score of block b for the query heads of KV head n as an ordered key, by one warp: exact but
+// for 2^-60 of its sum of magnitudes at most (the third float's roundings).
 // max(q lo, q hi) is q times hi or lo by the sign of q, a product that fp32 holds exactly
 // unless it is tiny; those, and sums that are not finite, go through fp64.
 template <int D>
 __device__ unsigned long long exact_score(const __nv_bfloat16 *q, const uint8_t *khdr, size_t sn, int G, int nb, int b,
-                                          float qmax, int lane)
+                                          float qmax, const Scale &sc, int lane)
 {
     constexpr int kI = (D / 4 + 31) / 32;                  // unit i / 4, c = i % 4 of i = lane + 32 k
     float lo[kI][4], hi[kI][4];
@@ -311,13 +358,19 @@ __device__ unsigned long long exact_score(const __nv_bfloat16 *q, const uint8_t 
         Sum72 t = swapped(b1 ? p1 : p0, b1 ? p0 : p1, 2);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) t = swapped(t, t, o);
-        double v = ((double)t.c + (double)t.b) + (double)t.a;
-        unsigned long long key = order64(v);
-        if (__any_sync(0xffffffffu, tiny || !(fabs(v) < 1e300))) {
+        const bool odd = tiny || !(fabsf(t.a) < INFINITY);
+        unsigned long long key;
+        if (sc.near) {
+            t.add(-sc.t);
+            key = near_key(sc, t.a, t.b, t.c);
+        } else {
+            key = order64(((double)t.c + (double)t.b) + (double)t.a);
+        }
+        if (__any_sync(0xffffffffu, odd)) {
             key = 0ull;
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {
-                v = 0.0;
+                Sum106 w;
                 const uint32_t *qr = (const uint32_t *)(q + (sn * G + min(j0 + j, G - 1)) * D);
 #pragma unroll
                 for (int k = 0; k < kI; ++k) {
@@ -326,12 +379,25 @@ __device__ unsigned long long exact_score(const __nv_bfloat16 *q, const uint8_t 
                     for (int e = 0; e < 4; ++e) {
                         const uint32_t qv = i < D / 4 ? __ldg(qr + (i >> 2) * 8 + (i & 3) + 4 * (e >> 1)) : 0u;
                         const float x = __uint_as_float((e & 1) ? qv & 0xffff0000u : qv << 16);
-                        v += (double)max_nan(x, 0.0f) * hi[k][e] + (double)-max_nan(-x, 0.0f) * lo[k][e];
+                        w.add((double)max_nan(x, 0.0f) * hi[k][e] + (double)-max_nan(-x, 0.0f) * lo[k][e]);
                     }
                 }
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                const unsigned long long kj = order64(v);
+                for (int o = 16; o > 0; o >>= 1) {
+                    const double oa = __shfl_xor_sync(0xffffffffu, w.a, o), ob = __shfl_xor_sync(0xffffffffu, w.b, o);
+                    w.add(oa);
+                    w.b += ob;
+                }
+                // numbers between the keys of -infinity and of infinity and NaN
+                unsigned long long kj = w.a != w.a ? ~0ull : (w.a > 0.0 ? ~0ull - 1ull : 0ull);
+                if (fabs(w.a) < INFINITY) {
+                    if (sc.near) {
+                        w.add(-(double)sc.t);
+                        kj = near_key(sc, w.a, w.b);
+                    } else {
+                        kj = order64(w.a + w.b);
+                    }
+                }
                 key = kj > key ? kj : key;
             }
         }
@@ -413,6 +479,7 @@ k_block_pick(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kh
         // every block a candidate
         const float t = value32(kt), band = 2.01f * e;
         const float above = t + band, below = t - band;
+        const Scale sc = scale_of(t, e);
         auto kind = [&](uint32_t k) -> int {               // 2: in, 1: candidate, 0: out
             if (k == 0u) return 0;
             const float v = value32(k);
@@ -465,7 +532,7 @@ k_block_pick(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kh
                     const int j = i0 + (__ffs(todo) - 1) * kPickWarps;
                     todo &= todo - 1u;
                     const unsigned long long k = exact_score<D>(q, khdr, (size_t)s * N + n0 + j % heads, G, nb,
-                                                                cand[j / heads], qmax, lane);
+                                                                cand[j / heads], qmax, sc, lane);
                     if (lane == 0) atomicMax(ex + j / heads, k);   // a maximum: in any order
                 }
             }
