@@ -45,6 +45,8 @@ def test_the_workspace_of_a_tree_is_that_of_its_output_type():
         need = {dt: rkv.rkv_tree_attention_workspace(p, H, n, dt) for dt in (rkv.RKV_F32, rkv.RKV_BF16)}
         assert rkv.rkv_dense_attention_workspace(p, H, n) == max(need.values()) == need[rkv.RKV_F32]
         if n * H // N > 32 and D <= 128:
+            # (what keeps a share's sums, in accumulators that cut, from growing long)
+            assert need[rkv.RKV_F32] >= S * (T // 32) / 96 * 2 * n * H * (4 * D + 8)
             # two partials and their {max, sum} for each share of a KV head and each sequence
             rows = (152 // N + S) * 2 * n * H
             assert need[rkv.RKV_BF16] <= 1.1 * (rows * (4 * D + 8) + 4 * (S + 1)) + 1024
