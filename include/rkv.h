@@ -353,12 +353,8 @@ rkv_status rkv_dense_attention(const rkv_dense_params *p, int32_t H, const void 
  * token does not see has no effect on it, NaN included.  Probabilities meet the values of
  * finished blocks as in rkv_dense_attention.
  * q: bf16 [S][n_draft][H][D]; out: [S][n_draft][H][D] in out_dtype.  1 <= n_draft <= 64.
- * workspace: >= the bytes of rkv_tree_attention_workspace for the call's out_dtype
- * (rkv_dense_attention_workspace(p, H, n_draft) is the larger one of both types), 256-byte
- * aligned.  With fp32 outputs and more than 32 query rows (n_draft H/N) of D <= 128 it grows with S T,
- * by a partial for every 96 blocks.  Requires H a multiple of N, H/N <= 8.               */
-rkv_status rkv_tree_attention_workspace(const rkv_dense_params *p, int32_t H, int32_t n_draft,
-                                        int32_t out_dtype, size_t *bytes);
+ * workspace: >= the bytes of rkv_dense_attention_workspace(p, H, n_draft), 256-byte
+ * aligned.  Requires H a multiple of N, H/N <= 8.                                        */
 rkv_status rkv_tree_attention(const rkv_dense_params *p, int32_t H, const void *q, int32_t n_draft,
                               const int32_t *parent, const void *draft_kv,
                               const rkv_dense_cache *cache, const int32_t *len, void *out,

@@ -76,7 +76,7 @@ __device__ __forceinline__ int value_slot(int g, int c) { return 8 * c + ((g + 2
 // run of sequence s has number i + s: the numbers of a sequence's runs follow one another, and
 // no two runs have the same (the next CTA's first sequence is this one's last, or a later one).
 struct DenseCut {
-    int ctas, unit, least, most;             // wanted CTAs; per: a multiple of unit, from least to most
+    int ctas, unit, least;                   // shares at most; per: a multiple of unit, least at least
 };
 struct DenseRun { int s, first, end, slot; };   // blocks first .. end - 1 of sequence s; s < 0: none
 struct DenseCursor { int at, end, s0, base; };  // block reached; the share's end; sequences s0 .. begin at block base
@@ -107,7 +107,7 @@ __device__ __forceinline__ int2 dense_shares(const int32_t *len, int S, int T, i
 #pragma unroll 8
     for (int s = lane; s < S; s += 32) all += blocks_of(len, s, S, T, listed, status);
     all = __reduce_add_sync(0xffffffffu, all);
-    const int per = min(c.most, max(c.least, (int)(((long long)all + c.ctas - 1) / c.ctas)));
+    const int per = max(c.least, (int)(((long long)all + c.ctas - 1) / c.ctas));
     return make_int2(all, (per + c.unit - 1) / c.unit * c.unit);
 }
 // CTA i's share.
@@ -200,7 +200,7 @@ cudaError_t launch_block_select(const DenseGeom &g, int H, const void *q, const 
                                 const int32_t *len, int lists, int n_blocks, int keep_first, int keep_last,
                                 int32_t *blocks, void *ws, int32_t *status, cudaStream_t s);
 
-size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq, int out_dtype);
+size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq);
 // blocks may be NULL (all finished blocks); parent and draft are NULL for one token (nq = 1)
 cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int nq, const int32_t *parent,
                                    const void *draft, const rkv_dense_cache *cache, const int32_t *len,
@@ -210,7 +210,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
 // The finished blocks against many query rows (rkv_dense_tree.cu), D <= 128: two partials for
 // each run and KV head.
 cudaError_t launch_dense_tree(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *cache,
-                              const int32_t *len, const DenseCut &cut, int ctas, float scale_log2, bool p3, float *part,
+                              const int32_t *len, const DenseCut &cut, float scale_log2, bool p3, float *part,
                               float2 *ml, int32_t *place, int32_t *status, cudaStream_t s);
 
 }  // namespace rkv

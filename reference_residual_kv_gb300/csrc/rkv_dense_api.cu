@@ -151,7 +151,7 @@ rkv_status rkv_dense_attention_workspace(const rkv_dense_params *p, int32_t H, i
     if (st != RKV_OK) return st;
     if (!bytes) return RKV_ERR_INVALID_ARG;
     const DenseGeom g = geom(p);
-    *bytes = dense_attention_workspace_bytes(g, H, n_query, RKV_F32);      // the larger one
+    *bytes = dense_attention_workspace_bytes(g, H, n_query);
     return RKV_OK;
 }
 
@@ -168,20 +168,10 @@ rkv_status rkv_dense_attention(const rkv_dense_params *p, int32_t H, const void 
     if ((st = check_dense_cache(cache, g)) != RKV_OK) return st;
     if (!q || !len || !out || !dev_status) return RKV_ERR_INVALID_ARG;
     if (!aligned16(q, len, blocks, out, dev_status)) return RKV_ERR_ALIGNMENT;
-    const size_t need = dense_attention_workspace_bytes(g, H, 1, out_dtype);
+    const size_t need = dense_attention_workspace_bytes(g, H, 1);
     if ((st = check_workspace(workspace, workspace_bytes, need)) != RKV_OK) return st;
     return done(launch_dense_attention(g, H, q, 1, nullptr, nullptr, cache, len, blocks, lists, n_blocks, out,
                                        out_dtype, workspace, dev_status, (cudaStream_t)stream));
-}
-
-rkv_status rkv_tree_attention_workspace(const rkv_dense_params *p, int32_t H, int32_t n_draft, int32_t out_dtype,
-                                        size_t *bytes)
-{
-    rkv_status st = check_attention_shape(p, H, n_draft, 0, 0);
-    if (st != RKV_OK) return st;
-    if (!bytes || (out_dtype != RKV_F32 && out_dtype != RKV_BF16)) return RKV_ERR_INVALID_ARG;
-    *bytes = dense_attention_workspace_bytes(geom(p), H, n_draft, out_dtype);
-    return RKV_OK;
 }
 
 rkv_status rkv_tree_attention(const rkv_dense_params *p, int32_t H, const void *q, int32_t n_draft,
@@ -196,7 +186,7 @@ rkv_status rkv_tree_attention(const rkv_dense_params *p, int32_t H, const void *
     if ((st = check_dense_cache(cache, g)) != RKV_OK) return st;
     if (!q || !parent || !draft_kv || !len || !out || !dev_status) return RKV_ERR_INVALID_ARG;
     if (!aligned16(q, parent, draft_kv, len, out, dev_status)) return RKV_ERR_ALIGNMENT;
-    const size_t need = dense_attention_workspace_bytes(g, H, n_draft, out_dtype);
+    const size_t need = dense_attention_workspace_bytes(g, H, n_draft);
     if ((st = check_workspace(workspace, workspace_bytes, need)) != RKV_OK) return st;
     return done(launch_dense_attention(g, H, q, n_draft, parent, draft_kv, cache, len, nullptr, 1, 0, out, out_dtype,
                                        workspace, dev_status, (cudaStream_t)stream));

@@ -23,7 +23,6 @@
 #include "rkv_dense.cuh"
 #include "umma.cuh"
 
-#include <limits.h>
 #include <math.h>
 
 namespace rkv {
@@ -683,27 +682,22 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
 // so that the workspace's size and the order of the sums do not either.
 struct Plan {
     bool tree;
-    int tiles, nt, each, ctas, slots;        // row tiles of a CTA's size; partials of a run; most shares and runs
+    int tiles, nt, each, slots;              // row tiles of a CTA's size; partials of a run; most runs
     DenseCut cut;
 };
 
-Plan plan_of(const DenseGeom &g, int H, int nq, bool f32)
+Plan plan_of(const DenseGeom &g, int H, int nq)
 {
     Plan p;
     const int R = nq * (H / g.N);
     p.tree = R > 32 && g.D <= 128;
     int ctas;
     p.cut.unit = 8;
-    p.cut.most = INT_MAX / 2;
     if (p.tree) {
         p.nt = 0;
         p.each = 2;
         p.tiles = (R + 255) / 256;
-        // one to an SM; for fp32 outputs no share above 96 blocks, since the products' accumulators
-        // cut what they add (64 drafts over 131072 tokens, error against 64 bits: 6.7e-6 at 216
-        // blocks and 289 us, 3.1e-6 at 96 blocks and 390 us; smaller work is not cut finer)
-        ctas = 152;
-        if (f32) p.cut.most = 96;
+        ctas = 152;                          // one to an SM
         p.cut.least = 16;
     } else {
         p.nt = R <= 4 ? 0 : (R <= 8 ? 1 : (R <= 16 || g.D == 256 ? 2 : 4));
@@ -713,8 +707,7 @@ Plan plan_of(const DenseGeom &g, int H, int nq, bool f32)
         p.cut.least = kWarps;
     }
     p.cut.ctas = max(1, ctas / (g.N * p.tiles));
-    p.ctas = (int)max((long long)p.cut.ctas, (long long)g.S * g.nb / p.cut.most + 1);
-    p.slots = p.ctas + g.S;
+    p.slots = p.cut.ctas + g.S;
     return p;
 }
 
@@ -731,7 +724,7 @@ cudaError_t run_split(const DenseGeom &g, const Plan &p, int H, const void *q, i
     });
     if (e != cudaSuccess) return e;
     ProfScope prof("dense_attention_split", s);
-    k_dense_split<D, BITS, NT0, P3><<<(unsigned)((size_t)p.ctas * g.N * p.tiles), 32 * kWarps, C::kSmem, s>>>(
+    k_dense_split<D, BITS, NT0, P3><<<(unsigned)((size_t)p.cut.ctas * g.N * p.tiles), 32 * kWarps, C::kSmem, s>>>(
         (const __nv_bfloat16 *)q, (const uint8_t *)c->codes, (const uint8_t *)c->khdr, len, blocks, lists, n_blocks,
         g.S, g.T, g.N, H / g.N, nq, g.nb, p.cut, p.tiles, scale_log2, part, ml, place, status);
     return cudaGetLastError();
@@ -783,9 +776,9 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
-size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq, int out_dtype)
+size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq)
 {
-    const Plan p = plan_of(g, H, nq, out_dtype == RKV_F32);
+    const Plan p = plan_of(g, H, nq);
     const size_t rows = (size_t)p.slots * p.each * nq * H;
     return align256(rows * g.D * sizeof(float)) + align256(rows * sizeof(float2)) + ((size_t)g.S + 1) * 4;
 }
@@ -795,7 +788,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
                                    const int32_t *blocks, int lists, int n_blocks, void *out, int out_dtype,
                                    void *ws, int32_t *status, cudaStream_t s)
 {
-    const Plan p = plan_of(g, H, nq, out_dtype == RKV_F32);
+    const Plan p = plan_of(g, H, nq);
     const size_t rows = (size_t)p.slots * p.each * nq * H;
     float *part = (float *)ws;
     float2 *ml = (float2 *)((uint8_t *)ws + align256(rows * g.D * sizeof(float)));
@@ -821,7 +814,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
             }
         };
         if (p.tree)
-            e = launch_dense_tree(g, H, q, nq, cache, len, p.cut, p.ctas, scale_log2, out_dtype == RKV_F32, part, ml, place,
+            e = launch_dense_tree(g, H, q, nq, cache, len, p.cut, scale_log2, out_dtype == RKV_F32, part, ml, place,
                                   status, s);
         else if (out_dtype == RKV_F32)
             e = split(std::true_type{});

@@ -42,6 +42,15 @@ constexpr int kTok = 128;                    // tokens of a tile: 4 blocks
 constexpr int kThreads = 640;
 constexpr int kStep = 64;                    // tokens of a step: 2 blocks
 constexpr int kColS = 256;                   // tensor memory: outputs at 0 and 128, scores at 256 + 128 t + 64 buffer
+// fp32 outputs: the products' accumulators cut what they add, and after this many steps of a half their
+// sums join those before, rounded, in the partial's own place in L2.  64 drafts and 16 over 131072
+// tokens, 16 x 8192 with 24, 24 x 4000 with 33 (fp32), error against 64 bits, us:
+//   16 steps   1.2e-6 311   1.4e-6 180   1.7e-6 128   1.4e-6 336
+//    8 steps   0.8e-6 321   1.0e-6 181   1.0e-6 128   0.8e-6 333
+//    4 steps   0.7e-6 359   0.9e-6 194   0.6e-6 136   0.5e-6 345
+// (plain fp32 sums are 2.4e-6, 2.8e-6, 0.8e-6, 0.5e-6 off; shares ended after 96 blocks 3.1e-6 392,
+// 2.1e-6 234, 2.9e-6 122, 2.7e-6 285, with partials of 3 GB for 32 such caches instead of 0.1 GB.)
+constexpr int kJoin = 4;
 
 // Registers of a thread, of the 96 that 640 threads are launched with: the shares of the five
 // groups of four warps (88 + 2 x 64 + 2 x 128 = 472) stay within the launch's 5 x 96 = 480.  The
@@ -352,7 +361,7 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
 #pragma unroll
                     for (int k = 0; k < kStep / 16; ++k) {
                         const uint32_t ak = a + 32 * (k >> 1) + 8 * (k & 1);
-                        mma_bf16_ta(tm, ak, v + 2 * k, id_o, (j | k) != 0);
+                        mma_bf16_ta(tm, ak, v + 2 * k, id_o, (P3 ? j % kJoin : j) != 0 || k != 0);
                         mma_bf16_ta(tm, ak + 16, v + 2 * k, id_o, 1);
                         if (P3) mma_bf16_ta(tm, a + kStep + 8 * k, v + 2 * k, id_o, 1);
                     }
@@ -495,6 +504,50 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
             __syncwarp();
             if (lane == 0 && ok) um::mbar_arrive(q_full + (runs0 & 3));
             float m_ref = -INFINITY, l = 0.0f;
+            const size_t base = (((size_t)run.slot * N + n) * 2 + (two ? 0 : t)) * R + row0;
+            const int r_warp = (two ? 128 * t : 0) + 32 * w;
+            // fp32 outputs: what the accumulator held before, against m_kept, lies where the warp's rows
+            // of the partial will go, four columns of them after four others.  Joins the accumulator with it,
+            // there or (at the end) in tensor memory
+            float m_kept = -INFINITY;
+            bool kept = false;
+            auto join = [&](bool last) {
+                const int there = min(32, rows - r_warp);
+                float4 *col = (float4 *)(part + (base + r_warp) * D) + lane;
+                const float f = m_kept == m_ref ? 1.0f : ex2(m_kept - m_ref);
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k, col += 8 * there) {
+                    float v[32];
+                    float4 x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x[e] = kept && lane < there ? col[e * there] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    tmem_ld32(to + 32 * k, v);
+                    tmem_wait_ld(v);
+                    if (kept)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            v[4 * e] = fmaf(x[e].x, f, v[4 * e]);
+                            v[4 * e + 1] = fmaf(x[e].y, f, v[4 * e + 1]);
+                            v[4 * e + 2] = fmaf(x[e].z, f, v[4 * e + 2]);
+                            v[4 * e + 3] = fmaf(x[e].w, f, v[4 * e + 3]);
+                        }
+                    if (last) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t u[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[16 * h + e]);
+                            tmem_st16(to + 32 * k + 16 * h, u);
+                        }
+                    } else if (lane < there) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) col[e * there] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    }
+                }
+                m_kept = m_ref;
+                kept = true;
+            };
             for (int j = 0; j < end; ++j) {
                 const int jj = steps0 + j, buf = jj % kBufs;
                 bool here = !*abort_flag && um::mbar_wait(s_full + 2 * t + buf, (uint32_t)(jj / kBufs) & 1u, kWaitCycles);
@@ -503,6 +556,9 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
                 if (busy) {
                     const uint32_t ts = tmem + lanes + kColS + t * 128 + buf * kStep;
                     const bool whole = blocks - 2 * step_of(t, j) >= 2;   // else the step's second block is not there
+                    // the output products begin anew: with one buffer, these scores came after the last one
+                    const bool anew = P3 && j > 0 && j % kJoin == 0;
+                    if (anew) join(false);
                     float v[2][32];
                     tmem_ld32(ts, v[0]);
                     tmem_ld32(ts + 32, v[1]);
@@ -522,7 +578,7 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
                     const bool move = top > m_ref + 8.0f || (m_ref == -INFINITY && top != -INFINITY);
                     if (__any_sync(0xffffffffu, move)) {
                         const float f = move ? (m_ref == -INFINITY ? 0.0f : ex2(m_ref - top)) : 1.0f;
-                        if (j > 0) {
+                        if (j > 0 && !anew) {
                             // the last step's output product may still be under way
                             here = um::mbar_wait(o_done + 2 * t + (jj - 1) % kBufs, (uint32_t)((jj - 1) / kBufs) & 1u, kWaitCycles);
                             if (!__all_sync(0xffffffffu, here)) { ok = false; break; }
@@ -586,9 +642,11 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
             // is free once both halves' products are complete
             um::bar_sync(1, 256);
             if (busy) {
-                const size_t base = (((size_t)run.slot * N + n) * 2 + (two ? 0 : t)) * R + row0;
-                const int r_warp = (two ? 128 * t : 0) + 32 * w;
                 if (end > 0 && ok) {
+                    if (P3 && kept) {
+                        join(true);
+                        tmem_wait_st();
+                    }
                     float *stage = (float *)qs + (size_t)(warp - 12) * 32 * 32;
 #pragma unroll 1
                     for (int k = 0; k < D / 32; ++k) {
@@ -626,7 +684,7 @@ k_dense_tree(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ co
 
 template <int D, int BITS, bool P3>
 cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *c, const int32_t *len,
-                const DenseCut &cut, int ctas, float scale_log2, float *part, float2 *ml, int32_t *place, int32_t *status,
+                const DenseCut &cut, float scale_log2, float *part, float2 *ml, int32_t *place, int32_t *status,
                 cudaStream_t s)
 {
     using C = TreeCfg<D, BITS>;
@@ -638,7 +696,7 @@ cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dens
     if (e != cudaSuccess) return e;
     const int tiles = (nq * (H / g.N) + 255) / 256;
     ProfScope prof("dense_attention_tree", s);
-    k_dense_tree<D, BITS, P3><<<(unsigned)((size_t)ctas * g.N * tiles), kThreads, C::kSmem, s>>>(
+    k_dense_tree<D, BITS, P3><<<(unsigned)((size_t)cut.ctas * g.N * tiles), kThreads, C::kSmem, s>>>(
         (const __nv_bfloat16 *)q, (const uint8_t *)c->codes, (const uint8_t *)c->khdr, len, g.S, g.T, g.N, H / g.N,
         nq, g.nb, cut, tiles, scale_log2, part, ml, place, status);
     return cudaGetLastError();
@@ -647,14 +705,14 @@ cudaError_t run(const DenseGeom &g, int H, const void *q, int nq, const rkv_dens
 }  // namespace
 
 cudaError_t launch_dense_tree(const DenseGeom &g, int H, const void *q, int nq, const rkv_dense_cache *c,
-                              const int32_t *len, const DenseCut &cut, int ctas, float scale_log2, bool p3, float *part,
+                              const int32_t *len, const DenseCut &cut, float scale_log2, bool p3, float *part,
                               float2 *ml, int32_t *place, int32_t *status, cudaStream_t s)
 {
     auto go = [&](auto bits, auto d) -> cudaError_t {
         constexpr int B = decltype(bits)::value, D = decltype(d)::value;
         if constexpr (D <= 128)
-            return p3 ? run<D, B, true>(g, H, q, nq, c, len, cut, ctas, scale_log2, part, ml, place, status, s)
-                        : run<D, B, false>(g, H, q, nq, c, len, cut, ctas, scale_log2, part, ml, place, status, s);
+            return p3 ? run<D, B, true>(g, H, q, nq, c, len, cut, scale_log2, part, ml, place, status, s)
+                        : run<D, B, false>(g, H, q, nq, c, len, cut, scale_log2, part, ml, place, status, s);
         else
             return cudaErrorInvalidValue;
     };

@@ -23,7 +23,7 @@ EXPORTED = ("rkv_n_ref", "rkv_query_sizes", "rkv_build_ref_pool", "rkv_compress"
             "rkv_debug_wait_fault", "rkv_status_string",
             "rkv_dense_sizes", "rkv_dense_write", "rkv_dense_read", "rkv_block_select_workspace",
             "rkv_block_select", "rkv_dense_attention_workspace", "rkv_dense_attention",
-            "rkv_tree_attention_workspace", "rkv_tree_attention")
+            "rkv_tree_attention")
 _DTYPES = {"f32": RKV_F32, "bf16": RKV_BF16, "fp8": RKV_FP8_E4M3}
 
 
@@ -105,7 +105,6 @@ def lib():
                 ("rkv_block_select", [DP, I32, V, DC, V, I32, I32, I32, I32, V, V, Z, V, V]),
                 ("rkv_dense_attention_workspace", [DP, I32, I32, sz]),
                 ("rkv_dense_attention", [DP, I32, V, DC, V, V, I32, I32, V, I32, V, Z, V, V]),
-                ("rkv_tree_attention_workspace", [DP, I32, I32, I32, sz]),
                 ("rkv_tree_attention", [DP, I32, V, I32, V, V, DC, V, V, I32, V, Z, V, V])):
             f = getattr(L, name)
             f.argtypes, f.restype = args, I32
@@ -303,14 +302,6 @@ def rkv_dense_attention(p: rkv_dense_params, H: int, q, cache: rkv_dense_cache, 
                                    workspace_bytes, _ptr(dev_status), _stream(stream))
     if st:
         raise RkvError(st, "rkv_dense_attention")
-
-
-def rkv_tree_attention_workspace(p: rkv_dense_params, H: int, n_draft: int, out_dtype: int) -> int:
-    b = ctypes.c_size_t()
-    st = lib().rkv_tree_attention_workspace(ctypes.byref(p), H, n_draft, out_dtype, ctypes.byref(b))
-    if st:
-        raise RkvError(st, "rkv_tree_attention_workspace")
-    return b.value
 
 
 def rkv_tree_attention(p: rkv_dense_params, H: int, q, n_draft: int, parent, draft_kv,
@@ -548,11 +539,10 @@ class DenseCache:
         return t
 
     def _size(self, *key):
-        """Bytes of scratch: ("select", lists), ("attend", H) or ("tree", H, n_draft, out_dtype)."""
+        """Bytes of scratch: ("select", lists) or ("attend", H, n_query)."""
         need = self._sizes.get(key)
         if need is None:
-            f = {"select": rkv_block_select_workspace, "attend": rkv_dense_attention_workspace,
-                 "tree": rkv_tree_attention_workspace}[key[0]]
+            f = rkv_block_select_workspace if key[0] == "select" else rkv_dense_attention_workspace
             need = self._sizes[key] = f(self.p, *key[1:])
         return need
 
@@ -602,7 +592,7 @@ class DenseCache:
                 raise ValueError("blocks: an empty list")
             listed = blocks.data_ptr()
         dt = RKV_F32 if out.dtype is _F32 else RKV_BF16
-        self._call("rkv_dense_attention", stream, self._size("attend", H), H, q.data_ptr(), self._cache_ref,
+        self._call("rkv_dense_attention", stream, self._size("attend", H, 1), H, q.data_ptr(), self._cache_ref,
                    length.data_ptr(), listed, lists, n, out.data_ptr(), dt)
 
     def tree_attend(self, H: int, q, parent, draft_kv, length, out, stream=None):
@@ -615,7 +605,7 @@ class DenseCache:
         self._check("length", length, (_I32,), (self.S,))
         self._check("out", out, (_F32, _BF16), (self.S, n, H, self.D))
         dt = RKV_F32 if out.dtype is _F32 else RKV_BF16
-        self._call("rkv_tree_attention", stream, self._size("tree", H, n, dt), H, q.data_ptr(), n, parent.data_ptr(),
+        self._call("rkv_tree_attention", stream, self._size("attend", H, n), H, q.data_ptr(), n, parent.data_ptr(),
                    draft_kv.data_ptr(), self._cache_ref, length.data_ptr(), out.data_ptr(), dt)
 
     def device_status(self) -> int:
