@@ -13,13 +13,14 @@
 //                   query rows its columns.  Probabilities go from one product to the
 //                   other by movmatrix, as bf16 in two or three parts.  Softmax: running
 //                   reference and sum for each warp, in base 2.  No masks: a finished block
-//                   is whole.  Bound by instruction issue, most of it codes to bf16 (issue 64 %,
+//                   is whole.  Most of its instructions turn codes into bf16 (issue 64 %,
 //                   integer pipe 60 %, products 24 %, DRAM 42 %): 8 uneven caches of up to
-//                   32768 tokens, 8 KV heads of 4 queries, 214 MB in 66-69 us, 3.2 TB/s.
+//                   32768 tokens, 8 KV heads of 4 queries, 214 MB in 62-72 us, 3.2 TB/s.
 //   k_dense_finish  the bf16 rows of the unfinished block and the drafted tokens that a row
-//                   sees (the values of a token that it does not see are not touched), while
-//                   the first kernel still runs, then the merge of the runs' partials (24 drafts
-//                   x 7 heads, 16 sequences of 4 KV heads: 26 us, issue 52 %).
+//                   sees (the values of a token that it does not see are not touched), then the
+//                   merge of the runs' partials (24 drafts x 7 heads, 16 sequences of 4 KV heads:
+//                   27 us, issue 50 %).  It may start before the first kernel ends, but finds room
+//                   only on SMs that the first kernel's CTAs have left.
 #include "rkv_dense.cuh"
 #include "umma.cuh"
 
@@ -680,6 +681,21 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
 
 // Which kernel takes the finished blocks, and how they are cut.  Does not depend on the device,
 // so that the workspace's size and the order of the sums do not either.
+//
+// R > 32: k_dense_tree, which has 128 rows at least and turns a block into bf16 once for all of them.
+// k_dense_split | k_dense_tree, us, 8 KV heads (4 of the 16 caches), D = 128 but for the fourth line:
+//   tokens         bf16 outputs, R = 16    32          36          128         fp32, 32    36          128
+//   131072         74 | 145    112 | 146   185 | 147   367 | 144   130 | 190   219 | 190   439 | 209
+//   16 x 8192      44 | 79     66 | 82     111 | 82    205 | 101   75 | 107    130 | 106   240 | 128
+//   4096           14 | 21     17 | 21     23 | 21     30 | 23     17 | 24     24 | 25     32 | 26
+//   131072, D 64   49 | 94     71 | 94     115 | 95    220 | 101   82 | 151    136 | 148   267 | 155
+// Row tiles of k_dense_split, us for 131072 tokens, D = 128, bf16 outputs: 4 rows twice in a tile 48, in
+// tiles of 8 52, of 16 69, of 32 102; 8 rows in tiles of 8 54, of 16 72; 16 rows in tiles of 8 91, of
+// 16 74, of 32 108; 32 rows in tiles of 8 172, of 16 123, of 32 112 (4096 tokens: all within 1.5 to 3).
+// D = 256, 65536 tokens: 4 rows twice 55, in tiles of 8 57; 16 rows in tiles of 8 93, of 16 78; tiles of
+// 32 rows do not fit the registers.
+// A share has 8 blocks at least (16 in k_dense_tree): 16 (8) are as fast, 32 take 16-22 us instead of
+// 13-17 for caches of 2048 to 16384 tokens (64 in k_dense_tree: 45-50 instead of 21-35).
 struct Plan {
     bool tree;
     int tiles, nt, each, slots;              // row tiles of a CTA's size; partials of a run; most runs

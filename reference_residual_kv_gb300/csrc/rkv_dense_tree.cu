@@ -13,21 +13,23 @@
 //   warps 1, 2   the products of a half each: outputs of step j, then scores of step j + 2, so
 //                that the scores of step j + 1 are there while step j's are at the softmax
 //                (one warp for both halves, issuing whatever was ready, spent half of its time
-//                on looking: 146 against 136 us for 64 drafts over 131072 tokens)
+//                on looking: 146 against 136 us for 64 drafts over 131072 tokens, P in one part)
 //   warps 4..11  codes to bf16, a block of the tile each: warps 4..7 K [token][channel], warps
 //                8..11 V^T [channel][token], in shared memory, K-major with 128-byte swizzle (a
 //                16 x 16 operand of rkv_dense.cuh is one stmatrix)
 //   warps 12..19 two halves of four warps, a thread per row: softmax in base 2 against a
 //                running reference m that lags the maximum by at most 8 (p <= 2^8 is harmless
 //                in fp32 sums and has the same relative error in bf16), so that the output
-//                accumulator is rescaled only where the maximum grows by more than that; P
-//                goes back to tensor memory, over the scores, as the first operand of P V.
+//                accumulator is rescaled only where the maximum grows by more than that (a
+//                published variant of the running softmax); P goes back to tensor memory, over
+//                the scores, as the first operand of P V.
 // P is bf16 in two parts (the scores' 64 columns hold both), as in the split pass, so that the
 // number of query rows does not change the outputs' precision; fp32 outputs have three, which take
 // the columns of both buffers, so that there is one.  In one part P put bf16 outputs 1.85e-3 off
 // instead of 1.6e-3, which is their own rounding.
-// 64 drafts x 4 heads over 131072 tokens, 8 KV heads: a call of 173 us (145 with one part).  The
-// chain scores, softmax, P, outputs of the two halves is what the time goes to.
+// 64 drafts x 4 heads over 131072 tokens, 8 KV heads, bf16 outputs: 163 us (134 with one part).  No
+// unit is full (issue 63 %, integer pipe 51 %, tensor pipe 55 %, its memory 60 %): the chain scores,
+// softmax, P, outputs of the two halves is what the time goes to.
 // All waits are bounded; a CTA whose wait runs out sets RKV_ERR_DEVICE_TIMEOUT and writes NaN
 // as its partials' maxima, so that its rows read NaN.
 #include "rkv_dense.cuh"
