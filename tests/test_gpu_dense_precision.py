@@ -163,3 +163,40 @@ def test_the_largest_trees(D, bits, S, G, n, dtype):
     for s in range(S):                             # no row hides behind the others' norm
         for j in np.nonzero(parent[s] > -2)[0]:
             assert off(got[s, j], want[s, j]) <= 4 * limit, (s, j)
+
+
+# sums that leave the accumulators several times in a share while the running maximum grows (one row
+# tile whose last warp has four rows, two tiles, the second one of four rows and of 32, and 64 rows
+# beyond 256)
+@pytest.mark.parametrize("D,bits,G,n", [(128, 4, 4, 9), (64, 2, 4, 33), (128, 2, 8, 20), (128, 4, 8, 40)])
+def test_joined_sums_follow_a_growing_maximum(D, bits, G, n):
+    T, N = 20005, 8
+    H = N * G
+    gen = torch.Generator("cuda").manual_seed(n)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    kv = rand(1, T, 2 * N * D)
+    kv[:, :, : N * D] *= 0.2 + 4.0 * torch.arange(T, device="cuda")[:, None] / T
+    c = rkv.DenseCache(rkv.make_dense_params(1, T, N, D, bits), guard=4096)
+    c.write(kv.bfloat16(), i32(0))
+    k, v = torch.empty(1, T, N * D, dtype=torch.bfloat16, device="cuda"), torch.empty(1, T, N * D, dtype=torch.bfloat16, device="cuda")
+    c.read(i32(T), torch.arange(T, dtype=torch.int32, device="cuda")[None], k, v)
+    q, draft = (rand(1, n, H, D) * 1.5).bfloat16(), rand(1, n, 2 * N * D).bfloat16()
+    parent = torch.full((1, n), -1, dtype=torch.int32, device="cuda")
+    out = torch.full((1, n, H, D), float("nan"), device="cuda")
+    c.tree_attend(H, q, parent, draft, i32(T), out)
+    d = draft.double().view(n, 2, N, D)
+    for h in range(H):
+        own_k, own_v = d[:, 0, h // G], d[:, 1, h // G]
+        K, V = k.view(T, N, D)[:, h // G].double(), v.view(T, N, D)[:, h // G].double()
+        Q = q[0, :, h].double()
+        x = torch.cat([Q @ K.T, (Q * own_k).sum(1, keepdim=True)], 1) / D ** 0.5
+        p = torch.softmax(x, 1)
+        want = p[:, :T] @ V + p[:, T:] * own_v
+        # the bound of _dense_oracle.attend
+        A = torch.maximum((Q.abs() @ K.abs().T).amax(1), (Q.abs() * own_k.abs()).sum(1)) / D ** 0.5
+        r = D * 2.0 ** -22 * A + 2.0 ** -23 * x.abs().amax(1) + 2.0 ** -20
+        tol = (2 * r + 2.0 ** -16)[:, None] * (p[:, :T] @ V.abs() + p[:, T:] * own_v.abs())
+        assert bool(((out[0, :, h].double() - want).abs() <= tol).all()), h
+    torch.cuda.synchronize()
+    assert c.device_status() == 0 and not c.guard_violations()
