@@ -305,10 +305,10 @@ k_attn_combine(const float *part, int H, int N, int splits, float *__restrict__ 
     const size_t ss = (size_t)G * (D + 2);                   // split stride
     // launched as a programmatic dependent of the split pass: wait for that grid to
     // complete and its partials to be visible (no effect after an ordinary launch).  They are not
-    // read-only for this kernel's whole life, and are read from L2
+    // read-only for this kernel's whole life
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float M = -INFINITY;
-    for (int s = threadIdx.x; s < splits; s += blockDim.x) M = fmaxf(M, __ldcg(base + s * ss + D));
+    for (int s = threadIdx.x; s < splits; s += blockDim.x) M = fmaxf(M, base[s * ss + D]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (lane == 0) red[warp] = M;
@@ -320,10 +320,10 @@ k_attn_combine(const float *part, int H, int N, int splits, float *__restrict__ 
 #pragma unroll
     for (int e = 0; e < EPL; ++e) acc[e] = 0.0f;
     for (int s = warp; s < splits; s += kWarps) {
-        const float f = M == -INFINITY ? 0.0f : __expf(__ldcg(base + s * ss + D) - M);
-        L = fmaf(__ldcg(base + s * ss + D + 1), f, L);
+        const float f = M == -INFINITY ? 0.0f : __expf(base[s * ss + D] - M);
+        L = fmaf(base[s * ss + D + 1], f, L);
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) acc[e] = fmaf(__ldcg(base + s * ss + lane * EPL + e), f, acc[e]);
+        for (int e = 0; e < EPL; ++e) acc[e] = fmaf(base[s * ss + lane * EPL + e], f, acc[e]);
     }
 #pragma unroll
     for (int e = 0; e < EPL; ++e) acc_s[warp][lane * EPL + e] = acc[e];
