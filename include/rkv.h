@@ -361,6 +361,104 @@ rkv_status rkv_tree_attention(const rkv_dense_params *p, int32_t H, const void *
                               int32_t out_dtype, void *workspace, size_t workspace_bytes,
                               int32_t *dev_status, void *stream);
 
+/* ---- a prompt's way through a full-attention layer -------------------------------
+ * H query heads over N KV heads of D channels (H a multiple of N; query head j reads KV head
+ * floor(j / (H/N))).  Rows are tokens; the heads of a row lie behind one another, and rows
+ * lie `stride` elements apart, so that q, k and v may be three matrices or the parts of one
+ * projection's rows.  Strides are multiples of 16 bytes and no smaller than a row's heads.  */
+typedef struct rkv_head_params {
+    int32_t H, N, D;        /* D 64, 128 or 256                                            */
+    int32_t reserved;       /* set to 0                                                    */
+} rkv_head_params;
+
+/* Which channels of a head a rotation pairs: (2i, 2i + 1), or (i, i + R/2).               */
+typedef enum rkv_rope_layout { RKV_ROPE_PAIRS = 0, RKV_ROPE_HALVES = 1 } rkv_rope_layout;
+
+/* Frequencies for contexts longer than the trained one; theta_i = base^(-2i/R).
+ *  LINEAR: theta_i / factor.
+ *  BANDS:  by wavelength 2 pi / theta_i: above original / low theta_i / factor, below
+ *          original / high theta_i, between them the mean of both weighted by
+ *          s = (original theta_i / 2 pi - low) / (high - low):  (1 - s) theta_i / factor + s theta_i.
+ *  YARN:   (1 - w) theta_i / factor + w theta_i with w = 1 - clip((i - a) / (b - a), 0, 1),
+ *          a = max(0, floor(d(low))), b = min(R - 1, ceil(d(high))), b - a at least 1e-3,
+ *          d(turns) = R ln(original / (2 pi turns)) / (2 ln base) (low and high are the turns over
+ *          the trained context that bound the ramp, 32 and 1 as published), and
+ *          gain = 0.1 ln(factor) + 1 (1 where factor <= 1).                               */
+typedef enum rkv_rope_scaling_kind {
+    RKV_ROPE_PLAIN = 0, RKV_ROPE_LINEAR = 1, RKV_ROPE_BANDS = 2, RKV_ROPE_YARN = 3
+} rkv_rope_scaling_kind;
+typedef struct rkv_rope_scaling {
+    int32_t kind;           /* rkv_rope_scaling_kind                                       */
+    int32_t reserved;       /* set to 0                                                    */
+    double factor, original, low, high;
+} rkv_rope_scaling;
+
+/* A rotation, in host memory: rkv_rope_init() fills it, a caller may change the frequencies. */
+typedef struct rkv_rope {
+    int32_t D, R;           /* head dim; its first R channels rotate, R a multiple of 16   */
+    int32_t layout;         /* rkv_rope_layout                                             */
+    float gain;             /* factor of cosines and sines                                 */
+    uint64_t turn[128];     /* turns per position of pair i < R/2, in units of 2^-64       */
+} rkv_rope;
+
+/* Host only.  scaling may be NULL (RKV_ROPE_PLAIN).  base > 1.                             */
+rkv_status rkv_rope_init(rkv_rope *rope, int32_t D, int32_t R, int32_t layout, double base,
+                         const rkv_rope_scaling *scaling);
+
+/* Norm by head (optional) and rotation of queries and keys, in one pass: for each head x of
+ * row i, with weight w (of D values; NULL: no norm for these heads)
+ *   y = x / sqrt(mean(x^2) + eps) * w
+ *   (y_a, y_b) -> gain (y_a cos - y_b sin, y_a sin + y_b cos) for each pair of the layout,
+ * the angle being pos[i] theta; channels R .. D - 1 are left as the norm gives them.  Sums,
+ * norms and the rotation in fp32, whole turns of the angle dropped in 64-bit integers (so that
+ * far positions lose nothing), one rounding to the rows' type at the end.  Keys that go to
+ * rkv_dense_write and queries of every attention here need it; rkv_restore_kv rotates restored
+ * keys by RKV_ROPE_PAIRS over all D channels, with gain 1.
+ * dtype: RKV_F32 or RKV_BF16, of rows and weights alike.  q (H heads) or k (N heads) may be
+ * NULL with its output: only the other is done.  pos: int32 [rows]; -1: padding, nothing of
+ * that row is written; below -1: RKV_ERR_INDEX and the same.  Outputs may be the inputs
+ * themselves (same pointer and stride); otherwise they must not overlap them.              */
+rkv_status rkv_qk_rotate(const rkv_head_params *p, const rkv_rope *rope, int32_t rows, int32_t dtype,
+                         const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const int32_t *pos, const void *q_weight, const void *k_weight, float eps,
+                         void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+                         int32_t *dev_status, void *stream);
+
+/* Causal attention of whole prompts, packed behind one another: sequence s has rows
+ * start[s] .. start[s + 1] - 1 (start: int32 [S + 1], device, ascending within [0, rows]; none
+ * for equal entries), and row i of a sequence
+ *   out[i][j] = softmax( q[i][j] K^T / sqrt(D) ) V
+ * over its own rows up to i.  Rows of no sequence are not written, and no row depends on what
+ * lies in rows that it does not see, NaN included.  Where start descends or leaves [0, rows],
+ * RKV_ERR_INDEX is set and nothing is written.
+ * q, k, v, out: bf16, rows of H, N, N and H heads.  Scores, softmax and sums in fp32;
+ * probabilities meet the values as bf16 (relative error 2^-9, as the output's own rounding).
+ * RKV_ERR_DEVICE_TIMEOUT (a wait ran out): the outputs are not to be used.
+ * workspace: >= the bytes of rkv_prompt_attention_workspace(p, S, rows), 256-byte aligned.
+ * Requires H/N <= 8.                                                                      */
+rkv_status rkv_prompt_attention_workspace(const rkv_head_params *p, int32_t S, int32_t rows, size_t *bytes);
+rkv_status rkv_prompt_attention(const rkv_head_params *p, int32_t S, const int32_t *start, int32_t rows,
+                                const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                const void *v, int64_t v_stride, void *out, int64_t out_stride,
+                                void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Attention of a piece of each sequence's text over the dense cache and over itself: rows
+ * 0 .. n_new[s] - 1 of sequence s follow the len[s] tokens that the cache holds, and row i
+ * attends to those and to rows 0 .. i.  The piece itself is written with rkv_dense_write
+ * afterwards (the call reads the unfinished block's rows, which that write replaces).
+ * q: bf16 [S][n][H][D]; kv: bf16 [S][n][2 N D], as for rkv_dense_write; out: bf16 [S][n][H][D],
+ * rows from n_new[s] on are not written.  n_new: int32 [S], device, or NULL (n rows for every
+ * sequence).  Where len < 0, n_new is outside [0, n] or len + n_new > T, RKV_ERR_INDEX is set
+ * and nothing of that sequence is written.  1 <= n <= T.  Precision as in rkv_prompt_attention.
+ * workspace: >= the bytes of rkv_chunk_attention_workspace(p, H, n), 256-byte aligned: for more
+ * rows than rkv_tree_attention takes it holds K and V of all S T tokens in bf16 (4 N D bytes
+ * each), and one layer's calls may follow another's in it.  Requires H/N <= 8.            */
+rkv_status rkv_chunk_attention_workspace(const rkv_dense_params *p, int32_t H, int32_t n, size_t *bytes);
+rkv_status rkv_chunk_attention(const rkv_dense_params *p, int32_t H, const void *q, int32_t n,
+                               const int32_t *n_new, const void *kv, const rkv_dense_cache *cache,
+                               const int32_t *len, void *out, void *workspace, size_t workspace_bytes,
+                               int32_t *dev_status, void *stream);
+
 /* Diagnostics: per-kernel device time.  rkv_profile_enable(1) clears the record
  * and brackets every later kernel launch of the library with two CUDA events on
  * the launch stream; rkv_profile_enable(0) stops recording.  rkv_profile_collect

@@ -201,11 +201,12 @@ cudaError_t launch_block_select(const DenseGeom &g, int H, const void *q, const 
                                 int32_t *blocks, void *ws, int32_t *status, cudaStream_t s);
 
 size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq);
-// blocks may be NULL (all finished blocks); parent and draft are NULL for one token (nq = 1)
+// blocks may be NULL (all finished blocks); parent and draft are NULL for one token (nq = 1);
+// leave: padding rows are not written (else they are zero)
 cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int nq, const int32_t *parent,
                                    const void *draft, const rkv_dense_cache *cache, const int32_t *len,
                                    const int32_t *blocks, int lists, int n_blocks, void *out, int out_dtype,
-                                   void *ws, int32_t *status, cudaStream_t s);
+                                   void *ws, int32_t *status, cudaStream_t s, bool leave = false);
 
 // The finished blocks against many query rows (rkv_dense_tree.cu), D <= 128: two partials for
 // each run and KV head.

@@ -436,7 +436,7 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
                const int32_t *__restrict__ len, const int32_t *__restrict__ parent,
                const __nv_bfloat16 *__restrict__ draft, int S, int T, int N, int G, int nq, int listed, int slots,
                int each_log, int wpr, int row_ctas, float scale_log2, const float *part,
-               const float2 *ml, const int32_t *place, void *__restrict__ out, int out_bf16,
+               const float2 *ml, const int32_t *place, void *__restrict__ out, int out_bf16, int leave,
                int32_t *status)
 {
     constexpr int kCh = D / 8, kPad = kCh + 1, kE = D / 32;   // 16-byte chunks of a row; channels of a lane
@@ -660,7 +660,7 @@ k_dense_finish(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restr
 #pragma unroll
     for (int k = 0; k < RPW; ++k) {
         const int r = r0 + slot + 8 * k;
-        if (r >= R) continue;
+        if (r >= R || (leave && padding[k])) continue;
         // l is 0 only where the row sees nothing (the largest p is 1); NaN stays NaN
         const bool none = padding[k] || l[k] == 0.0f;
         const float inv = none ? 0.0f : 1.0f / l[k];
@@ -749,8 +749,8 @@ cudaError_t run_split(const DenseGeom &g, const Plan &p, int H, const void *q, i
 template <int D>
 cudaError_t run_finish(const DenseGeom &g, const Plan &p, int H, const void *q, int nq, int listed, const int32_t *parent,
                        const void *draft, const rkv_dense_cache *c, const int32_t *len, float scale_log2,
-                       const float *part, const float2 *ml, const int32_t *place, void *out, int out_dtype, int32_t *status,
-                       cudaStream_t s)
+                       const float *part, const float2 *ml, const int32_t *place, void *out, int out_dtype, bool leave,
+                       int32_t *status, cudaStream_t s)
 {
     const int R = nq * (H / g.N);
     const int wpr = R <= 1 ? 8 : (R <= 2 ? 4 : (R <= 4 ? 2 : 1));
@@ -784,7 +784,7 @@ cudaError_t run_finish(const DenseGeom &g, const Plan &p, int H, const void *q, 
     e = cudaLaunchKernelEx(&cfg, twice ? k_dense_finish<D, 2> : k_dense_finish<D, 1>, (const __nv_bfloat16 *)q,
                            (const __nv_bfloat16 *)c->tail, len, parent, (const __nv_bfloat16 *)draft, g.S, g.T, g.N,
                            H / g.N, nq, listed, p.slots, p.each - 1, wpr, row_ctas, scale_log2, part, ml, place, out,
-                           (int)(out_dtype == RKV_BF16), status);
+                           (int)(out_dtype == RKV_BF16), (int)leave, status);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -802,7 +802,7 @@ size_t dense_attention_workspace_bytes(const DenseGeom &g, int H, int nq)
 cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int nq, const int32_t *parent,
                                    const void *draft, const rkv_dense_cache *cache, const int32_t *len,
                                    const int32_t *blocks, int lists, int n_blocks, void *out, int out_dtype,
-                                   void *ws, int32_t *status, cudaStream_t s)
+                                   void *ws, int32_t *status, cudaStream_t s, bool leave)
 {
     const Plan p = plan_of(g, H, nq);
     const size_t rows = (size_t)p.slots * p.each * nq * H;
@@ -838,7 +838,7 @@ cudaError_t launch_dense_attention(const DenseGeom &g, int H, const void *q, int
             e = split(std::false_type{});
         if (e != cudaSuccess) return e;
         return run_finish<D>(g, p, H, q, nq, blocks ? n_blocks : 0, parent, draft, cache, len, scale_log2, part, ml, place,
-                             out, out_dtype, status, s);
+                             out, out_dtype, leave, status, s);
     };
     return dense_dispatch(g, go);
 }

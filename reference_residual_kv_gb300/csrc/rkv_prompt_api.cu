@@ -1,0 +1,269 @@
+// rkv_prompt_api.cu -- the extern "C" entry points of the prompt's operators: argument checks
+// and dispatch.  No entry point allocates device memory.
+#include "rkv_prompt.cuh"
+
+#include <limits.h>
+#include <math.h>
+
+namespace rkv {
+namespace {
+
+constexpr int kMaxRotated = 256;
+
+template <class... P>
+bool aligned16(P... q)
+{
+    return ((((uintptr_t)q & 15u) == 0) && ...);
+}
+
+rkv_status check_head_params(const rkv_head_params *p, int most_per_kv)
+{
+    if (!p || p->H < 1 || p->N < 1 || p->D < 1 || p->reserved != 0) return RKV_ERR_INVALID_ARG;
+    if (p->D != 64 && p->D != 128 && p->D != 256) return RKV_ERR_UNSUPPORTED;
+    if (p->H % p->N != 0 || p->N > 1024 || p->H > 65536 || p->H / p->N > most_per_kv) return RKV_ERR_UNSUPPORTED;
+    return RKV_OK;
+}
+
+// rows of `heads` heads, `stride` elements of `item` bytes apart
+rkv_status check_stride(int64_t stride, int heads, int D, int item)
+{
+    if (stride < (int64_t)heads * D || stride > (1LL << 36)) return RKV_ERR_INVALID_ARG;
+    return stride * item % 16 == 0 ? RKV_OK : RKV_ERR_ALIGNMENT;
+}
+
+rkv_status check_rope(const rkv_rope *r)
+{
+    if (!r || r->R < 0 || r->R > r->D || r->R % 16 != 0) return RKV_ERR_INVALID_ARG;
+    if (r->layout != RKV_ROPE_PAIRS && r->layout != RKV_ROPE_HALVES) return RKV_ERR_INVALID_ARG;
+    return isfinite(r->gain) ? RKV_OK : RKV_ERR_INVALID_ARG;
+}
+
+PromptShape packed_shape(const rkv_head_params *p, int S, int rows, const int32_t *start)
+{
+    PromptShape x{};
+    x.S = S;
+    x.H = p->H;
+    x.N = p->N;
+    x.D = p->D;
+    x.rows = rows;
+    x.start = start;
+    return x;
+}
+
+rkv_status check_packed(const rkv_head_params *p, int32_t S, int32_t rows)
+{
+    rkv_status st = check_head_params(p, 8);
+    if (st != RKV_OK) return st;
+    if (S < 0 || rows < 0) return RKV_ERR_INVALID_ARG;
+    // items of all KV heads are counted in 32 bits
+    const long long per = 16 * (p->D == 256 ? 1 : 2);
+    return ((long long)rows / per + S) * p->N > (1LL << 30) ? RKV_ERR_UNSUPPORTED : RKV_OK;
+}
+
+rkv_status check_piece(const rkv_dense_params *p, int32_t H, int32_t n)
+{
+    size_t unused;
+    rkv_status st = rkv_dense_sizes(p, &unused, nullptr, nullptr);
+    if (st != RKV_OK) return st;
+    if (H < 1 || n < 1 || n > p->T) return RKV_ERR_INVALID_ARG;
+    if (H % p->N != 0 || H / p->N > 8) return RKV_ERR_UNSUPPORTED;
+    if ((long long)p->S * n * H > (long long)INT_MAX) return RKV_ERR_UNSUPPORTED;
+    return RKV_OK;
+}
+
+DenseGeom geom(const rkv_dense_params *p) { return DenseGeom{p->S, p->T, p->N, p->D, p->bits, p->T / kBlk}; }
+
+PromptShape piece_shape(const rkv_dense_params *p, int H, int n, const int32_t *len, const int32_t *n_new)
+{
+    PromptShape x{};
+    x.S = p->S;
+    x.H = H;
+    x.N = p->N;
+    x.D = p->D;
+    x.rows = (long long)p->S * n;
+    x.len = len;
+    x.n_new = n_new;
+    x.n = n;
+    x.T = p->T;
+    return x;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Up to kMaxDraft rows go the way of drafted trees, which read the cache as it is; more rows read
+// bf16 rows that k_dense_rows makes of it first.
+bool as_tree(int n) { return n <= kMaxDraft; }
+
+size_t piece_rows_bytes(const rkv_dense_params *p)
+{
+    return align256((size_t)p->S * p->T * 4 * p->N * p->D);
+}
+
+rkv_status done(cudaError_t e) { return e == cudaSuccess ? RKV_OK : RKV_ERR_CUDA; }
+
+}  // namespace
+}  // namespace rkv
+
+using namespace rkv;
+
+extern "C" {
+
+rkv_status rkv_rope_init(rkv_rope *r, int32_t D, int32_t R, int32_t layout, double base, const rkv_rope_scaling *sc)
+{
+    if (!r || D < 1 || R < 0 || R > D || R % 16 != 0 || !(base > 1.0) || !isfinite(base)) return RKV_ERR_INVALID_ARG;
+    if (layout != RKV_ROPE_PAIRS && layout != RKV_ROPE_HALVES) return RKV_ERR_INVALID_ARG;
+    if (D > kMaxRotated) return RKV_ERR_UNSUPPORTED;
+    const int kind = sc ? sc->kind : RKV_ROPE_PLAIN;
+    if (kind < RKV_ROPE_PLAIN || kind > RKV_ROPE_YARN || (sc && sc->reserved != 0)) return RKV_ERR_INVALID_ARG;
+    if (kind != RKV_ROPE_PLAIN && (!(sc->factor > 0.0) || !isfinite(sc->factor))) return RKV_ERR_INVALID_ARG;
+    if (kind >= RKV_ROPE_BANDS && (!(sc->original > 0.0) || !isfinite(sc->original) || !(sc->low > 0.0) ||
+                                   !(sc->high > 0.0) || !isfinite(sc->low) || !isfinite(sc->high)))
+        return RKV_ERR_INVALID_ARG;
+    if (kind == RKV_ROPE_BANDS && !(sc->high > sc->low)) return RKV_ERR_INVALID_ARG;
+    const double kTurn = 6.283185307179586476925;
+    rkv_rope x{};
+    x.D = D;
+    x.R = R;
+    x.layout = layout;
+    x.gain = 1.0f;
+    double a = 0.0, b = 0.0;
+    if (kind == RKV_ROPE_YARN) {
+        auto at = [&](double turns) { return R * log(sc->original / (turns * kTurn)) / (2.0 * log(base)); };
+        a = fmax(0.0, floor(at(sc->low)));
+        b = fmin(R - 1.0, ceil(at(sc->high)));
+        if (sc->factor > 1.0) x.gain = (float)(0.1 * log(sc->factor) + 1.0);
+    }
+    for (int i = 0; i < R / 2; ++i) {
+        const double th = pow(base, -2.0 * i / R);
+        double t = th;
+        if (kind == RKV_ROPE_LINEAR) t = th / sc->factor;
+        if (kind == RKV_ROPE_BANDS) {
+            const double s = fmin(1.0, fmax(0.0, (sc->original * th / kTurn - sc->low) / (sc->high - sc->low)));
+            t = th * s + th / sc->factor * (1.0 - s);
+        }
+        if (kind == RKV_ROPE_YARN) {
+            const double w = 1.0 - fmin(1.0, fmax(0.0, (i - a) / fmax(b - a, 1e-3)));
+            t = th * w + th / sc->factor * (1.0 - w);
+        }
+        double f = t / kTurn;
+        f -= floor(f);                                     // whole turns per position say nothing
+        x.turn[i] = (uint64_t)ldexp(f, 64);                // f has 53 bits at most: below 2^64
+    }
+    *r = x;
+    return RKV_OK;
+}
+
+rkv_status rkv_qk_rotate(const rkv_head_params *p, const rkv_rope *rope, int32_t rows, int32_t dtype, const void *q,
+                         int64_t q_stride, const void *k, int64_t k_stride, const int32_t *pos, const void *q_weight,
+                         const void *k_weight, float eps, void *q_out, int64_t q_out_stride, void *k_out,
+                         int64_t k_out_stride, int32_t *dev_status, void *stream)
+{
+    rkv_status st = check_head_params(p, 65536);
+    if (st == RKV_OK) st = check_rope(rope);
+    if (st != RKV_OK) return st;
+    if (rope->D != p->D || rows < 0 || (dtype != RKV_F32 && dtype != RKV_BF16) || !(eps >= 0.0f) || !isfinite(eps))
+        return RKV_ERR_INVALID_ARG;
+    const int item = dtype == RKV_F32 ? 4 : 2;
+    if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr)) return RKV_ERR_INVALID_ARG;
+    if (q && ((st = check_stride(q_stride, p->H, p->D, item)) != RKV_OK ||
+              (st = check_stride(q_out_stride, p->H, p->D, item)) != RKV_OK))
+        return st;
+    if (k && ((st = check_stride(k_stride, p->N, p->D, item)) != RKV_OK ||
+              (st = check_stride(k_out_stride, p->N, p->D, item)) != RKV_OK))
+        return st;
+    if (rows == 0) return RKV_OK;
+    if ((!q && !k) || !pos || !dev_status) return RKV_ERR_INVALID_ARG;
+    if ((q == q_out && q && q_stride != q_out_stride) || (k == k_out && k && k_stride != k_out_stride))
+        return RKV_ERR_INVALID_ARG;
+    if (!aligned16(q, k, q_out, k_out, q_weight, k_weight, pos, dev_status)) return RKV_ERR_ALIGNMENT;
+    RotateArgs a{};
+    a.q = q;
+    a.k = k;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.q_out_stride = q_out_stride;
+    a.k_out_stride = k_out_stride;
+    a.pos = pos;
+    a.status = dev_status;
+    a.rows = rows;
+    a.H = p->H;
+    a.N = p->N;
+    a.eps = eps;
+    return done(launch_rotate(a, *rope, dtype, (cudaStream_t)stream));
+}
+
+rkv_status rkv_prompt_attention_workspace(const rkv_head_params *p, int32_t S, int32_t rows, size_t *bytes)
+{
+    rkv_status st = check_packed(p, S, rows);
+    if (st != RKV_OK) return st;
+    if (!bytes) return RKV_ERR_INVALID_ARG;
+    static const int32_t some = 0;               // packed: any start
+    *bytes = S && rows ? prompt_workspace_bytes(packed_shape(p, S, rows, &some)) : 0;
+    return RKV_OK;
+}
+
+rkv_status rkv_prompt_attention(const rkv_head_params *p, int32_t S, const int32_t *start, int32_t rows, const void *q,
+                                int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                void *out, int64_t out_stride, void *workspace, size_t workspace_bytes,
+                                int32_t *dev_status, void *stream)
+{
+    rkv_status st = check_packed(p, S, rows);
+    if (st != RKV_OK) return st;
+    if ((st = check_stride(q_stride, p->H, p->D, 2)) != RKV_OK || (st = check_stride(k_stride, p->N, p->D, 2)) != RKV_OK ||
+        (st = check_stride(v_stride, p->N, p->D, 2)) != RKV_OK || (st = check_stride(out_stride, p->H, p->D, 2)) != RKV_OK)
+        return st;
+    if (S == 0 || rows == 0) return RKV_OK;
+    if (!start || !q || !k || !v || !out || !dev_status) return RKV_ERR_INVALID_ARG;
+    if (!aligned16(q, k, v, out, start, dev_status)) return RKV_ERR_ALIGNMENT;
+    const PromptShape x = packed_shape(p, S, rows, start);
+    if (!workspace || workspace_bytes < prompt_workspace_bytes(x)) return RKV_ERR_WORKSPACE;
+    if ((uintptr_t)workspace & 255u) return RKV_ERR_ALIGNMENT;
+    const PromptTensors t{q, k, v, out, q_stride, k_stride, v_stride, out_stride, rows};
+    return done(launch_prompt_attention(x, t, workspace, dev_status, (cudaStream_t)stream));
+}
+
+rkv_status rkv_chunk_attention_workspace(const rkv_dense_params *p, int32_t H, int32_t n, size_t *bytes)
+{
+    rkv_status st = check_piece(p, H, n);
+    if (st != RKV_OK) return st;
+    if (!bytes) return RKV_ERR_INVALID_ARG;
+    if (as_tree(n)) *bytes = align256((size_t)p->S * n * 4) + dense_attention_workspace_bytes(geom(p), H, n);
+    else *bytes = piece_rows_bytes(p) + prompt_workspace_bytes(piece_shape(p, H, n, nullptr, nullptr));
+    return RKV_OK;
+}
+
+rkv_status rkv_chunk_attention(const rkv_dense_params *p, int32_t H, const void *q, int32_t n, const int32_t *n_new,
+                               const void *kv, const rkv_dense_cache *cache, const int32_t *len, void *out,
+                               void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream)
+{
+    size_t need;
+    rkv_status st = rkv_chunk_attention_workspace(p, H, n, &need);
+    if (st != RKV_OK) return st;
+    const DenseGeom g = geom(p);
+    if (!cache || !cache->tail || (g.nb > 0 && (!cache->codes || !cache->khdr))) return RKV_ERR_INVALID_ARG;
+    if (!q || !kv || !len || !out || !dev_status) return RKV_ERR_INVALID_ARG;
+    if (!aligned16(cache->codes, cache->khdr, cache->tail, q, kv, len, n_new, out, dev_status)) return RKV_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < need) return RKV_ERR_WORKSPACE;
+    if ((uintptr_t)workspace & 255u) return RKV_ERR_ALIGNMENT;
+    cudaStream_t s = (cudaStream_t)stream;
+    uint8_t *ws = (uint8_t *)workspace;
+    if (as_tree(n)) {
+        int32_t *parent = (int32_t *)ws;
+        cudaError_t e = launch_chunk_parents(g, len, n, n_new, parent, dev_status, s);
+        if (e != cudaSuccess) return RKV_ERR_CUDA;
+        return done(launch_dense_attention(g, H, q, n, parent, kv, cache, len, nullptr, 1, 0, out, RKV_BF16,
+                                           ws + align256((size_t)p->S * n * 4), dev_status, s, true));
+    }
+    cudaError_t e = launch_dense_rows(g, cache, len, kv, n, n_new, ws, dev_status, s);
+    if (e != cudaSuccess) return RKV_ERR_CUDA;
+    const PromptShape x = piece_shape(p, H, n, len, n_new);
+    const int64_t row = 2LL * p->N * p->D, qrow = (int64_t)H * p->D;
+    const PromptTensors t{q, ws, ws + (size_t)p->N * p->D * 2, out, qrow, row, row, qrow, (long long)p->S * p->T};
+    return done(launch_prompt_attention(x, t, ws + piece_rows_bytes(p), dev_status, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,1028 @@
+// rkv_prompt_attention.cu -- causal attention of rows over bf16 K and V on the 5th-generation
+// tensor cores: packed prompts, and pieces of prompts behind their cached text.
+//
+// out = softmax(q K^T / sqrt(D)) V.  A tile is 128 rows: the G query heads of a KV head for
+// 128 / G (rounded down) neighbouring tokens, token by token, so that all rows of a tile read the
+// same K and V and a short text fills a tile with its heads.  A CTA takes an item (up to 256 rows,
+// two tiles, of one sequence and KV head, and a range of keys) and walks over the keys in tiles of
+// kTok; scores = Q K^T and out += P V are tcgen05 products with accumulators in tensor memory.
+//   warp 0       producer: takes items from a counter, Q, K and V by TMA, K and V into a ring
+//   warp 1       the products: while one row tile is at its softmax, the other one's are under way
+//   warps 2, 3   look through V, a tile in turn each, where rows see only a part of a key tile: 0 times a
+//                value that is not finite is not 0, so such values are taken out there and noted, and
+//                given back to the rows that do see them
+//   warps 4..    four warps to a row tile, a thread per row: softmax in base 2 against a running
+//                reference m that lags the maximum by at most 8 (p <= 2^8 is harmless in fp32 sums
+//                and has the same relative error in bf16), so that the accumulator is rescaled only where
+//                the maximum grows by more than that (a published variant of the running softmax);
+//                P goes back to tensor memory, over the scores, as the first operand of P V
+// D = 256 has one row tile (its outputs take 256 columns) and two buffers of scores instead.
+//
+// Items come from k_prompt_plan, one CTA that reads the lengths: sorted so that the last ones to
+// start are short, and split over the keys where there are few; the parts of a split item leave
+// {m, l, out} in fp32, which k_prompt_join puts together.
+// All waits are bounded: RKV_ERR_DEVICE_TIMEOUT is set, the copies and products under way are
+// waited for, and the outputs are incomplete.
+#include "rkv_prompt.cuh"
+#include "umma.cuh"
+
+#include <math.h>
+
+namespace rkv {
+namespace {
+
+// ---------------------------------------------------------------- items
+struct PromptItem {
+    int q_row, tokens;      // first row (token) of the item and its tokens
+    int k_row;              // row of K and V that holds key 0
+    int first;              // the key that the first token sees last
+    int kt0, kt1;           // key tiles
+    int slot;               // partial of this part for KV head 0; below 0: the item is whole (-1 - its
+                            // sequence's items, where items go by sequence)
+    int seq;                // index of its sequence's first item, where items go by sequence
+};
+static_assert(sizeof(PromptItem) == 32, "two 16-byte loads");
+struct PromptJoin { int q_row, tokens, slot, parts; };
+struct PromptHead {
+    int items;              // for each KV head
+    int by_seq;             // items of a sequence in a row for each KV head (else KV heads innermost)
+    int next;               // the item to take next
+    int joins, slots;
+    int pad[3];
+};
+
+constexpr int kCtas = 152;
+constexpr int kSlots = 4 * kCtas;            // partials at most
+constexpr int kPlanThreads = 1024;
+// K and V that stay in L2 beside what else is read: up to here items go by cost alone
+constexpr long long kInL2 = 48LL << 20;
+constexpr int kItemCost = 3;                 // of an item beside its keys, in key tiles of 128
+
+struct PlanArgs {
+    const int32_t *start;                    // packed prompts
+    const int32_t *len, *n_new;              // pieces: [S], n rows each at most
+    int S, rows, n, T;
+    int N, tile_tokens, tok, key_bytes, max_slots, max_items, max_joins, ctas;
+    PromptHead *head;
+    PromptItem *items;
+    PromptJoin *joins;
+    int32_t *status;
+};
+
+struct Text { int q_row, n, before, k_row; };
+__device__ __forceinline__ Text text_of(const PlanArgs &a, int s)
+{
+    if (a.start) {
+        const int b = __ldg(a.start + s), e = __ldg(a.start + s + 1);
+        if (b < 0 || e < b || e > a.rows) {
+            set_status(a.status, RKV_ERR_INDEX);
+            return Text{-1, 0, 0, 0};
+        }
+        return Text{b, e - b, 0, b};
+    }
+    const int before = __ldg(a.len + s), n = a.n_new ? __ldg(a.n_new + s) : a.n;
+    if (before < 0 || n < 0 || n > a.n || before > a.T - n) {
+        set_status(a.status, RKV_ERR_INDEX);
+        return Text{0, 0, 0, 0};
+    }
+    return Text{s * a.n, n, before, s * a.T};
+}
+
+__device__ __forceinline__ int block_scan(int v, int *warps, int &total)   // exclusive; warps: [32] shared
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int x = lane_scan(v);
+    __syncthreads();
+    if (lane == 31) warps[w] = x;
+    __syncthreads();
+    if (w == 0) warps[lane] = lane_scan(warps[lane]);
+    __syncthreads();
+    total = warps[31];
+    return x - v + (w ? warps[w - 1] : 0);
+}
+
+constexpr int kCands = 32;
+constexpr int kFull = 256, kBuckets = 2 * kFull;   // parts of full length by their place, others by cost
+
+__global__ void __launch_bounds__(kPlanThreads)
+k_prompt_plan(const PlanArgs a)
+{
+    __shared__ int warps[32], first_tile[kPlanThreads + 1], bucket[kBuckets];
+    __shared__ Text texts[kPlanThreads];
+    __shared__ int cand[kCands];
+    __shared__ long long sum_cost, sum_keys;
+    __shared__ int sum_tiles, max_cost, part_len, slots, n_items, n_joins, wrong;
+    const int tid = threadIdx.x;
+    if (tid == 0) {
+        sum_cost = sum_keys = 0;
+        sum_tiles = max_cost = slots = n_items = n_joins = wrong = 0;
+    }
+    if (tid < kCands) cand[tid] = 0;
+    for (int i = tid; i < kBuckets; i += kPlanThreads) bucket[i] = 0;
+    __syncthreads();
+
+    // Calls f(x, text, tile, cost, tiles of that text) for every tile x of 1024 texts at a time
+    auto each = [&](auto f) {
+        int before = 0;
+        for (int s0 = 0; s0 < a.S; s0 += kPlanThreads) {
+            const int s = s0 + tid;
+            Text t{0, 0, 0, 0};
+            if (s < a.S) t = text_of(a, s);
+            const int tiles = (t.n + a.tile_tokens - 1) / a.tile_tokens;
+            int total;
+            const int at = block_scan(tiles, warps, total);
+            texts[tid] = t;
+            first_tile[tid] = at;
+            if (tid == 0) first_tile[kPlanThreads] = total;
+            __syncthreads();
+            for (int x = tid; x < total; x += kPlanThreads) {
+                int lo = 0, hi = kPlanThreads;             // the last text that begins at or before x
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (first_tile[mid] <= x) lo = mid;
+                    else hi = mid;
+                }
+                const Text &w = texts[lo];
+                const int tile = x - first_tile[lo], last = min(w.n, (tile + 1) * a.tile_tokens);
+                f(before + x, w, tile, (w.before + last + a.tok - 1) / a.tok, first_tile[lo + 1] - first_tile[lo],
+                  before + first_tile[lo]);
+            }
+            before += total;
+            __syncthreads();
+        }
+    };
+    {
+        long long keys = 0;
+        for (int s = tid; s < a.S; s += kPlanThreads) {
+            const Text t = text_of(a, s);
+            if (t.n > 0) keys += t.before + t.n;
+            if (t.q_row < 0) wrong = 1;
+        }
+        long long cost = 0;
+        int n = 0, most = 0;
+        each([&](int, const Text &, int, int c, int, int) {
+            cost += c;
+            ++n;
+            most = max(most, c);
+        });
+        atomicAdd((unsigned long long *)&sum_keys, (unsigned long long)keys);
+        atomicAdd((unsigned long long *)&sum_cost, (unsigned long long)cost);
+        atomicAdd(&sum_tiles, n);
+        atomicMax(&max_cost, most);
+        __syncthreads();
+    }
+    // Packed rows that do not ascend may be more than the workspace is for: nothing attends
+    if (wrong) {
+        if (tid == 0) *a.head = PromptHead{0, 0, a.ctas, 0, 0, {0, 0, 0}};
+        return;
+    }
+    // Few items: parts of L key tiles each, L from max_cost / 1, / 2 .. so that the time, taken as
+    // (all costs) / CTAs + what the last round of parts leaves idle, is least
+    const bool few = (long long)sum_tiles * a.N < 8 * kCtas && sum_tiles > 0;
+    const int over = kItemCost * 128 / a.tok;
+    auto len_of = [&](int k) { return (max_cost + k) / (k + 1); };
+    auto parts_of = [](int c, int L) { return c <= L + L / 4 ? 1 : (c - L / 4 + L - 1) / L; };
+    if (few) {
+        each([&](int, const Text &, int, int c, int, int) {
+            for (int k = 0; k < kCands; ++k) atomicAdd(&cand[k], parts_of(c, len_of(k)));
+        });
+        if (tid < 32) {
+            const int L = len_of(tid);
+            const float P = (float)cand[tid] * a.N, W = (float)sum_cost * a.N + over * P * (tid ? 1.7f : 1.0f);
+            float t = W / kCtas + (ceilf(P / kCtas) - P / kCtas) * (L + over);
+            if (tid && (cand[tid] * a.N > a.max_slots || L < 4 * 128 / a.tok)) t = INFINITY;
+            int best = tid;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                const float y = __shfl_xor_sync(0xffffffffu, t, o);
+                const int b = __shfl_xor_sync(0xffffffffu, best, o);
+                if (y < t || (y == t && b < best)) { t = y; best = b; }
+            }
+            if (tid == 0) part_len = best ? len_of(best) : max_cost;
+        }
+        __syncthreads();
+    } else {
+        if (tid == 0) part_len = max(max_cost, 1);
+        __syncthreads();
+    }
+    const int L = part_len;
+    const bool split = few && L < max_cost;
+    const bool by_seq = !split && sum_keys * a.key_bytes > kInL2;
+    if (by_seq) {
+        each([&](int x, const Text &w, int tile, int c, int tiles, int seq) {
+            if (seq + tiles > a.max_items) return;         // lengths that changed under the call
+            a.items[seq + tiles - 1 - tile] = PromptItem{w.q_row + tile * a.tile_tokens, min(a.tile_tokens, w.n - tile * a.tile_tokens),
+                                                         w.k_row, w.before + tile * a.tile_tokens, 0, c, -1 - tiles, seq};
+        });
+        if (tid == 0) n_items = sum_tiles;
+    } else {
+        auto bucket_of = [&](int part, int c) {
+            return split && c >= L ? min(part, kFull - 1) : kFull + (kFull - 1) - (int)((long long)min(c, L) * (kFull - 1) / L);
+        };
+        each([&](int, const Text &, int, int c, int, int) {
+            const int parts = split ? parts_of(c, L) : 1;
+            for (int i = 0; i < parts; ++i) atomicAdd(&bucket[bucket_of(i, i + 1 < parts ? L : c - i * L)], 1);
+        });
+        __syncthreads();
+        int total;
+        const int have = tid < kBuckets ? bucket[tid] : 0;
+        const int at = block_scan(have, warps, total);
+        if (tid < kBuckets) bucket[tid] = at;
+        if (tid == 0) n_items = total;
+        __syncthreads();
+        each([&](int, const Text &w, int tile, int c, int, int) {
+            const int parts = split ? parts_of(c, L) : 1;
+            const int q_row = w.q_row + tile * a.tile_tokens, tokens = min(a.tile_tokens, w.n - tile * a.tile_tokens);
+            int slot = -1;
+            if (parts > 1) {
+                const int j = atomicAdd(&n_joins, 1);
+                slot = atomicAdd(&slots, parts * a.N);
+                if (j >= a.max_joins || slot + parts * a.N > a.max_slots) return;
+                a.joins[j] = PromptJoin{q_row, tokens, slot, parts};
+            }
+            for (int i = 0; i < parts; ++i) {
+                const int to = i + 1 < parts ? (i + 1) * L : c;
+                const int at = atomicAdd(&bucket[bucket_of(i, to - i * L)], 1);
+                if (at >= a.max_items) return;
+                a.items[at] = PromptItem{q_row, tokens, w.k_row, w.before + tile * a.tile_tokens, i * L, to,
+                               parts > 1 ? slot + i * a.N : -1, 0};
+            }
+        });
+    }
+    __syncthreads();
+    if (tid == 0)
+        *a.head = PromptHead{min(n_items, a.max_items), by_seq, a.ctas, min(n_joins, a.max_joins), slots, {0, 0, 0}};
+}
+
+// ---------------------------------------------------------------- attention
+template <int R>
+__device__ __forceinline__ void regs_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+// D[tmem] (+)= A[tmem] B[smem]^T, one M x N x 16 step: A holds two bf16 a column
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    __syncwarp();
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st()
+{
+    __syncwarp();
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// 32 columns of this warp's 32 lanes: the load is under way until tmem_wait_ld of its registers
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
+{
+    __syncwarp();
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(float (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :: "memory");
+    asm volatile("" : "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                      "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                      "+f"(v[30]), "+f"(v[31]) :: "memory");
+}
+
+template <int D>
+struct FlashCfg {
+    static constexpr int kHalves = D == 256 ? 1 : 2;       // row tiles
+    static constexpr int kBufs = D == 256 ? 2 : 1;         // score buffers of a row tile
+    static constexpr int kTok = D == 256 ? 64 : 128;       // keys of a tile
+    static constexpr int kStages = D == 64 ? 8 : 5;
+    static_assert(kStages <= 8, "four tiles of V at most are in the ring: v_issued and v_clean have as many barriers");
+    static constexpr int kScan = D == 256 ? 1 : 2;         // warps that look through V
+    static constexpr int kQ = 128 * D * 2, kTile = kTok * D * 2;
+    static constexpr int kThreads = 128 + 128 * kHalves;
+    static constexpr int kBars = 2 * kStages + 36;
+    static constexpr int kSmem = kHalves * kQ + kStages * kTile + kBars * 8 + 4 * 48 + kScan * D * 4 + 64 + 1024;
+    static constexpr int kColS = kHalves * (D < 128 ? 128 : D);   // tensor memory: outputs, then scores
+    static constexpr int kColsO = D < 128 ? 128 : D;
+    // registers: 384 threads begin with 168; 128 x 72 + 256 x 216 is what the launch has
+    static constexpr int kRegsFew = 72, kRegsRows = 216;
+    static_assert(kHalves == 1 || kRegsFew + 2 * kRegsRows <= 3 * 168, "registers of the launch");
+    static_assert(kSmem <= 227 * 1024, "shared memory of the attention");
+    static_assert(kColS + kHalves * kBufs * kTok <= 512, "tensor memory");
+};
+
+struct FlashMaps { CUtensorMap q, k, v; };
+struct FlashArgs {
+    PromptHead *head;
+    const PromptItem *items;
+    __nv_bfloat16 *out;
+    int64_t out_stride;
+    float *part;                    // [slots][128 kHalves][D]
+    float2 *ml;                     // [slots][128 kHalves]
+    int32_t *status;
+    int N, G;
+    float scale_log2;
+};
+
+// An item as the roles share it: its KV head, and how many key tiles each row tile has
+struct FlashWork { PromptItem it; int n, pad[3]; };
+
+constexpr int kNoValue = 0x3fffffff;            // three fields of ten bits: the first key in question
+// A word of the values that are not finite: bits 0..9 NaN, 10..19 +inf, 20..29 -inf, the first key
+// (counted from the item's first partly seen key tile) with one.
+__device__ __forceinline__ void note_value(int *word, int key, int kind)
+{
+    int old = *(volatile int *)word;
+    while (true) {
+        const int sh = 10 * kind, have = (old >> sh) & 1023;
+        if (have <= key) return;
+        const int now = (old & ~(1023 << sh)) | (key << sh), seen = atomicCAS(word, old, now);
+        if (seen == old) return;
+        old = seen;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(FlashCfg<D>::kThreads, 1)
+k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
+{
+    using C = FlashCfg<D>;
+    constexpr int kHalves = C::kHalves, kBufs = C::kBufs, kTok = C::kTok, kStages = C::kStages, kScan = C::kScan;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *qs = smem_raw + ((1024u - (um::smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *ring = qs + kHalves * C::kQ;
+    uint64_t *kv_full = (uint64_t *)(ring + kStages * C::kTile), *kv_empty = kv_full + kStages;
+    uint64_t *q_full = kv_empty + kStages, *q_empty = q_full + 2;
+    uint64_t *s_full = q_empty + 2, *p_full = s_full + 4, *pv_done = p_full + 4;   // [half * kBufs + buffer]
+    uint64_t *o_empty = pv_done + 4, *v_issued = o_empty + 2, *v_clean = v_issued + 4;
+    uint64_t *w_full = v_clean + 4, *w_empty = w_full + 4, *drain = w_empty + 4;
+    FlashWork *works = (FlashWork *)(kv_full + C::kBars);
+    int *odd = (int *)(works + 4);                         // [kScan][D] values that are not finite, as each warp found them
+    volatile int *done = odd + kScan * D;                      // items that each of the rows' warps is through with
+    volatile int *odd_item = done + 8;                     // the items that `odd` belongs to, + 1
+    volatile int *abort_flag = odd_item + 2;
+    uint32_t *tmem_slot = (uint32_t *)(odd_item + 3);
+    static_assert(2 * kStages + 2 + 2 + 4 + 4 + 4 + 2 + 4 + 4 + 4 + 4 + 1 <= C::kBars && sizeof(FlashWork) == 48, "shared memory");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.G, N = a.N, tile_tok = 128 / G;        // tokens of a row tile
+    if (threadIdx.x == 0) {
+        um::prefetch_tmap(&maps.q);
+        um::prefetch_tmap(&maps.k);
+        um::prefetch_tmap(&maps.v);
+        for (int i = 0; i < kStages; ++i) {
+            um::mbar_init(kv_full + i, 1);
+            um::mbar_init(kv_empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            um::mbar_init(q_full + i, 1);
+            um::mbar_init(q_empty + i, 1);
+            um::mbar_init(o_empty + i, 4);
+        }
+        for (int i = 0; i < 4; ++i) {
+            um::mbar_init(s_full + i, 1);
+            um::mbar_init(p_full + i, 4);
+            um::mbar_init(pv_done + i, 1);
+            um::mbar_init(v_issued + i, 1);
+            um::mbar_init(v_clean + i, 1);
+            um::mbar_init(w_full + i, 1);
+            um::mbar_init(w_empty + i, 1 + kScan + 4 * kHalves);
+        }
+        um::mbar_init(drain, 1);
+        for (int i = 0; i < 8; ++i) done[i] = 0;
+        odd_item[0] = odd_item[1] = *abort_flag = 0;
+        um::fence_mbar_init();
+    }
+    if (warp == 1) {
+        um::tmem_alloc(tmem_slot, 512);
+        um::tmem_relinquish();
+    }
+    um::tc_fence_before();
+    __syncthreads();
+    um::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (kHalves == 2 && warp < 4) regs_down<C::kRegsFew>();
+
+    // whole warps wait; false once a wait anywhere has run out
+    auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
+        bool ok = um::mbar_try_wait(bar, phase & 1u);
+        if (!__all_sync(0xffffffffu, ok)) {
+            const long long t0 = clock64();
+            while (!ok && !*abort_flag && clock64() - t0 <= kWaitCycles) ok = um::mbar_try_wait(bar, phase & 1u);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok && lane == 0) *abort_flag = 1;
+        }
+        return ok;
+    };
+    // key tiles of half h in an item: those that its last token reaches
+    auto tiles_of = [&](const PromptItem &it, int h) -> int {
+        const int last = min(it.tokens, (h + 1) * tile_tok);
+        if (last <= h * tile_tok) return 0;
+        return max(0, min(it.kt1, (it.first + last + kTok - 1) / kTok) - it.kt0);
+    };
+    // the first key tile that some row of the item does not see whole
+    auto partly = [&](const PromptItem &it) -> int { return (it.first + 1) / kTok; };
+    // item number i of this CTA; tokens = 0: there are no more
+    auto take = [&](int i, FlashWork &w) -> bool {
+        if (!wait(w_full + (i & 3), (uint32_t)(i >> 2))) return false;
+        w = works[i & 3];
+        __syncwarp();
+        if (lane == 0) um::mbar_arrive(w_empty + (i & 3));
+        return w.it.tokens > 0;
+    };
+
+    if (warp == 0) {
+        const int items = *(volatile int *)&a.head->items, by_seq = *(volatile int *)&a.head->by_seq;
+        const long long all = (long long)items * N;
+        int idx = blockIdx.x;
+        uint32_t loads = 0, uses[2] = {0, 0}, cleans = 0;
+        auto fetch = [&](long long at) -> FlashWork {
+            FlashWork w{};
+            if (at >= all) return w;
+            int e = (int)(at / N), n = (int)(at % N);
+            if (by_seq) {
+                // this sequence's items in a row, once for each KV head: item at / N is one of them
+                const int4 y = __ldcg((const int4 *)(a.items + e) + 1);
+                const int first = y.w, count = -1 - y.z, r = (int)(at - (long long)first * N);
+                n = r / count;
+                e = first + r % count;
+            }
+            const int4 *src = (const int4 *)(a.items + e);
+            const int4 x = __ldcg(src), y = __ldcg(src + 1);
+            w.it = PromptItem{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            w.n = n;
+            return w;
+        };
+        FlashWork w = fetch(idx);
+        for (int i = 0;; ++i) {
+            int next = 0;
+            if (lane == 0 && w.it.tokens > 0) next = atomicAdd(&a.head->next, 1);
+            if (!wait(w_empty + (i & 3), (uint32_t)(i >> 2) ^ 1u)) break;
+            if (lane == 0) {
+                works[i & 3] = w;
+                um::mbar_arrive(w_full + (i & 3));
+            }
+            __syncwarp();
+            if (w.it.tokens <= 0) break;
+            FlashWork coming{};
+            const int c[2] = {tiles_of(w.it, 0), kHalves == 2 ? tiles_of(w.it, 1) : 0}, count = max(c[0], c[1]);
+            bool ok = true;
+            auto load_q = [&](int h) {
+                if (!ok || c[h] == 0) return;
+                ok = wait(q_empty + h, uses[h] ^ 1u);
+                if (!ok) return;
+                ++uses[h];
+                if (lane == 0) {
+                    um::mbar_arrive_expect_tx(q_full + h, (uint32_t)(D / 64 * G * tile_tok * 128));
+#pragma unroll
+                    for (int k = 0; k < D / 64; ++k)
+                        um::tma_load_3d(qs + h * C::kQ + k * 128 * 128, &maps.q, q_full + h, 64 * k, w.n * G,
+                                        w.it.q_row + h * tile_tok);
+                }
+                __syncwarp();
+            };
+            const int base = partly(w.it);
+            // V that is to be looked through: the barrier of its stage says that it is there only once
+            // its load has been issued (before, it may still be at the load before)
+            auto load_kv = [&](int kt, const CUtensorMap *m, bool looked) {
+                if (!ok) return;
+                const uint32_t st = loads % kStages;
+                ok = wait(kv_empty + st, (loads / kStages) ^ 1u);
+                if (!ok) return;
+                ++loads;
+                if (lane == 0) {
+                    um::mbar_arrive_expect_tx(kv_full + st, C::kTile);
+#pragma unroll
+                    for (int k = 0; k < D / 64; ++k)
+                        um::tma_load_3d(ring + st * C::kTile + k * kTok * 128, m, kv_full + st, 64 * k, w.n,
+                                        w.it.k_row + kt * kTok);
+                    if (looked) um::mbar_arrive(v_issued + (cleans & 3));
+                }
+                cleans += looked;
+                __syncwarp();
+            };
+            for (int j = 0; j < count && ok; ++j) {
+                if (j == 0) load_q(0);
+                load_kv(w.it.kt0 + j, &maps.k, false);
+                if (j == 0 && kHalves == 2) load_q(1);
+                load_kv(w.it.kt0 + j, &maps.v, w.it.kt0 + j >= base);
+                if (j == 0) coming = fetch(__shfl_sync(0xffffffffu, next, 0));
+            }
+            if (!ok) break;
+            w = coming;
+        }
+        // no copy is in flight when the CTA leaves
+        if (lane == 0) {
+            for (uint32_t k = loads > kStages ? loads - kStages : 0; k < loads; ++k)
+                um::mbar_wait(kv_full + k % kStages, (k / kStages) & 1u, kWaitCycles);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (uses[h]) um::mbar_wait(q_full + h, (uses[h] - 1) & 1u, kWaitCycles);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // The whole warp walks through the loop with values that are the same for all lanes; one
+        // elected lane issues.  Products of one thread are carried out in the order of issue: the scores
+        // of the next key tile go over the probabilities that the product before them reads.
+        const uint32_t tm = __reduce_or_sync(0xffffffffu, tmem);
+        const uint32_t id_s = um::idesc_bf16_f32(128, kTok), id_o = um::idesc_bf16_f32(128, D) | (1u << 16);   // V: N-major
+        const uint64_t qd = um::sdesc_sw128(um::smem_u32(qs));
+        const uint64_t kd = um::sdesc_sw128(um::smem_u32(ring));
+        const uint64_t vd = um::sdesc_sw128_mn(um::smem_u32(ring), kTok * 128, 1024);
+        uint32_t loads = 0, turns[2] = {0, 0}, cleans = 0;    // turns: items in which a half has had keys
+        uint32_t steps[2] = {0, 0};                        // key tiles that each half is through with
+        bool ok = true;
+        FlashWork w;
+        for (int i = 0; ok && take(i, w); ++i) {
+            const int c[2] = {tiles_of(w.it, 0), kHalves == 2 ? tiles_of(w.it, 1) : 0}, count = max(c[0], c[1]);
+            const int part0 = max(0, partly(w.it) - w.it.kt0);   // first tile that is looked through
+            auto last_user = [&](int h, int j) { return h == kHalves - 1 || j >= c[1]; };
+            auto scores = [&](int h, int j) {
+                const uint32_t ld = loads + 2 * j, st = ld % kStages, t = steps[h] + j, buf = t % kBufs;
+                if (j == 0) ok = ok && wait(q_full + h, turns[h]);
+                ok = ok && wait(kv_full + st, ld / kStages);
+                if (!ok) return;
+                um::tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t q0 = qd + h * (C::kQ / 16), k0 = kd + st * (C::kTile / 16);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        um::mma_bf16(tm + C::kColS + (h * kBufs + buf) * kTok, q0 + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
+                                     k0 + (k >> 2) * (kTok * 128 / 16) + 2 * (k & 3), id_s, k != 0);
+                    um::mma_commit(s_full + h * kBufs + buf);
+                    if (last_user(h, j)) um::mma_commit(kv_empty + st);
+                    if (j == c[h] - 1) um::mma_commit(q_empty + h);
+                }
+                __syncwarp();
+            };
+            auto outputs = [&](int h, int j) {
+                const uint32_t ld = loads + 2 * j + 1, st = ld % kStages, t = steps[h] + j, buf = t % kBufs;
+                ok = ok && wait(kv_full + st, ld / kStages);
+                if (j >= part0) {
+                    const uint32_t cl = cleans + (j - part0);
+                    ok = ok && wait(v_clean + (cl & 3), cl >> 2);
+                }
+                if (j == 0) ok = ok && wait(o_empty + h, turns[h] ^ 1u);
+                ok = ok && wait(p_full + h * kBufs + buf, t / kBufs);
+                if (!ok) return;
+                um::tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t v0 = vd + st * (C::kTile / 16);
+                    const uint32_t p0 = tm + C::kColS + (h * kBufs + buf) * kTok;
+#pragma unroll
+                    for (int k = 0; k < kTok / 16; ++k)
+                        mma_bf16_ta(tm + h * C::kColsO, p0 + 8 * k, v0 + k * (2048 / 16), id_o, j != 0 || k != 0);
+                    um::mma_commit(pv_done + h * kBufs + buf);
+                    if (last_user(h, j)) um::mma_commit(kv_empty + st);
+                }
+                __syncwarp();
+            };
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                for (int j = 0; j < kBufs; ++j)
+                    if (j < c[h] && ok) scores(h, j);
+            for (int j = 0; j < count && ok; ++j)
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+                    if (j >= c[h] || !ok) continue;
+                    outputs(h, j);
+                    if (j + kBufs < c[h] && ok) scores(h, j + kBufs);
+                }
+            loads += 2 * count;
+            cleans += max(0, count - part0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                steps[h] += c[h];
+                turns[h] += c[h] > 0;
+            }
+        }
+        // every issued product completes before tensor memory is released
+        if (elect_one()) um::mma_commit(drain);
+        __syncwarp();
+        um::mbar_wait(drain, 0, kWaitCycles);
+        __syncwarp();
+    } else if (warp < 2 + kScan) {
+        uint32_t loads = 0, cleans = 0;
+        FlashWork w;
+        bool ok = true;
+        for (int i = 0; ok && take(i, w); ++i) {
+            const int count = max(tiles_of(w.it, 0), kHalves == 2 ? tiles_of(w.it, 1) : 0);
+            const int base = partly(w.it), part0 = max(0, base - w.it.kt0), kv_len = w.it.first + w.it.tokens;
+            for (int j = part0; j < count && ok; ++j, ++cleans) {
+                if (cleans % kScan != (uint32_t)(warp - 2)) continue;
+                const uint32_t ld = loads + 2 * j + 1, st = ld % kStages;
+                ok = wait(v_issued + (cleans & 3), cleans >> 2) && wait(kv_full + st, ld / kStages);
+                if (!ok) break;
+                uint8_t *v = ring + st * C::kTile;
+                uint32_t bad = 0;
+#pragma unroll 8
+                for (int x = lane; x < C::kTile / 16; x += 32) {
+                    const uint4 y = *(const uint4 *)(v + 16 * x);
+                    const uint32_t e[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) bad |= (e[k] & 0x7f807f80u) + 0x00800080u;
+                }
+                if (__any_sync(0xffffffffu, bad & 0x80008000u)) {
+                    int *words = odd + (warp - 2) * D;
+                    if (odd_item[warp - 2] != i + 1) {
+                        // the rows are through with the values of the items before
+                        const long long t0 = clock64();
+                        bool here = false;
+                        while (!here && !*abort_flag && clock64() - t0 <= kWaitCycles)
+                            here = lane >= 4 * kHalves || done[lane] >= i;
+                        ok = __all_sync(0xffffffffu, here);
+                        if (!ok) {
+                            if (lane == 0) *abort_flag = 1;
+                            break;
+                        }
+                        for (int d = lane; d < D; d += 32) words[d] = kNoValue;
+                        __syncwarp();
+                        if (lane == 0) odd_item[warp - 2] = i + 1;
+                    }
+                    for (int x = lane; x < C::kTile / 16; x += 32) {
+                        const int box = x / (kTok * 8), r = x / 8 % kTok, ch = (x & 7) ^ (r & 7);
+                        const int key = (w.it.kt0 + j) * kTok + r;
+                        uint16_t *e = (uint16_t *)(v + 16 * x);
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t y = e[k];
+                            if ((y & 0x7f80u) != 0x7f80u) continue;
+                            e[k] = 0;
+                            if (key < kv_len) note_value(words + 64 * box + 8 * ch + k, key - base * kTok, (y & 0x7fu) ? 0 : 1 + (int)(y >> 15));
+                        }
+                    }
+                    um::fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) um::mbar_arrive(v_clean + (cleans & 3));
+            }
+            loads += 2 * count;
+        }
+    } else if (warp >= 4) {
+        if (kHalves == 2) regs_up<C::kRegsRows>();
+        const int h = (warp - 4) >> 2, w4 = warp & 3, r = 32 * w4 + lane;
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+        const uint32_t to = tmem + lanes + h * C::kColsO;
+        const int tok = h * tile_tok + r / G;              // token of the item
+        const bool in_tile = r / G < tile_tok;
+        uint32_t steps = 0;
+        FlashWork w;
+        bool ok = true;
+        for (int i = 0; ok && take(i, w); ++i) {
+            const int count = tiles_of(w.it, h);
+            const int sees = w.it.first + min(tok, w.it.tokens - 1);          // last key of this row
+            const int whole = (w.it.first + h * tile_tok + 1) / kTok - w.it.kt0;   // tiles that every row sees
+            float m_ref = -INFINITY, l = 0.0f;
+            for (int j = 0; j < count && ok; ++j) {
+                const uint32_t t = steps + j, buf = t % kBufs;
+                ok = wait(s_full + h * kBufs + buf, t / kBufs);
+                if (!ok) break;
+                um::tc_fence_after();
+                const uint32_t ts = tmem + lanes + C::kColS + (h * kBufs + buf) * kTok;
+                float v[kTok / 32][32];
+#pragma unroll
+                for (int k = 0; k < kTok / 32; ++k) tmem_ld32(ts + 32 * k, v[k]);
+#pragma unroll
+                for (int k = 0; k < kTok / 32; ++k) tmem_wait_ld(v[k]);
+                if (j >= whole) {
+                    const int left = sees - (w.it.kt0 + j) * kTok;            // columns up to this one are seen
+#pragma unroll
+                    for (int k = 0; k < kTok / 32; ++k)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * k + e > left) v[k][e] = -INFINITY;
+                }
+                float top[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) top[x] = v[x * (kTok / 128)][x * 8 % 32];
+#pragma unroll
+                for (int k = 0; k < kTok / 32; ++k)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) top[x] = max3f(top[x], v[k][e + 2 * x], v[k][e + 2 * x + 1]);
+                const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+                // the reference moves where the maximum is more than 8 above it, and at the start
+                const bool move = most > m_ref + 8.0f || (m_ref == -INFINITY && most != -INFINITY);
+                if (__any_sync(0xffffffffu, move)) {
+                    const float f = move ? (m_ref == -INFINITY ? 0.0f : ex2(m_ref - most)) : 1.0f;
+                    if (j > 0) {
+                        // with one buffer, these scores came after the last output product
+                        if (kBufs > 1) {
+                            ok = wait(pv_done + h * kBufs + (t - 1) % kBufs, (t - 1) / kBufs);
+                            if (!ok) break;
+                            um::tc_fence_after();
+                        }
+#pragma unroll 1
+                        for (int k = 0; k < D / 32; ++k) {
+                            float o[32];
+                            tmem_ld32(to + 32 * k, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                uint32_t x[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[16 * y + e] * f);
+                                tmem_st16(to + 32 * k + 16 * y, x);
+                            }
+                        }
+                    }
+                    l *= f;
+                    if (move) m_ref = most;
+                }
+                const float mu = m_ref == -INFINITY ? 0.0f : m_ref;
+                const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), mu2 = make_float2(-mu, -mu);
+                float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                for (int k = 0; k < kTok / 32; ++k) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x = __ffma2_rn(make_float2(v[k][2 * e], v[k][2 * e + 1]), sc2, mu2);
+                        const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+                        sums[e & 1] = __fadd2_rn(sums[e & 1], pp);
+                        p[e] = as_u32(__floats2bfloat162_rn(pp.x, pp.y));
+                    }
+                    tmem_st16(ts + 16 * k, p);
+                }
+                l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+                tmem_wait_st();
+                um::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) um::mbar_arrive(p_full + h * kBufs + buf);
+            }
+            if (!ok) break;
+            if (count > 0) {
+                const uint32_t t = steps + count - 1;
+                ok = wait(pv_done + h * kBufs + t % kBufs, t / kBufs);
+                if (!ok) break;
+                um::tc_fence_after();
+            }
+            steps += count;
+            const bool live = in_tile && tok < w.it.tokens, whole_item = w.it.slot < 0;
+            const size_t prow = whole_item ? 0 : (size_t)(w.it.slot + w.n) * (128 * kHalves) + 128 * h + r;
+            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays
+            const bool odd_here[2] = {odd_item[0] == i + 1, kScan == 2 && odd_item[1] == i + 1};
+            const int seen_to = min(1022, sees - partly(w.it) * kTok);
+            if (count > 0) {
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k) {
+                    float o[32];
+                    tmem_ld32(to + 32 * k, o);
+                    tmem_wait_ld(o);
+                    if (k == D / 32 - 1) {
+                        um::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) um::mbar_arrive(o_empty + h);
+                    }
+                    if (odd_here[0] || odd_here[1])
+#pragma unroll 1
+                        for (int e = 0; e < 32 * kScan; ++e) {
+                            if (!odd_here[e >> 5]) continue;
+                            const int word = odd[(e >> 5) * D + 32 * k + (e & 31)];
+                            const bool nan = (word & 1023) <= seen_to, up = ((word >> 10) & 1023) <= seen_to,
+                                       down = ((word >> 20) & 1023) <= seen_to;
+                            const float add = nan || (up && down) ? __uint_as_float(0x7fffffffu) : up ? INFINITY : down ? -INFINITY : 0.0f;
+#pragma unroll
+                            for (int y = 0; y < 32; ++y)
+                                if (y == (e & 31)) o[y] += add;
+                        }
+                    if (!live) continue;
+                    if (whole_item) {
+                        uint4 *dst = (uint4 *)(a.out + (w.it.q_row + tok) * a.out_stride + (w.n * G + r % G) * D + 32 * k);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                x[y] = as_u32(__floats2bfloat162_rn(o[8 * e + 2 * y] * inv, o[8 * e + 2 * y + 1] * inv));
+                            dst[e] = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                    } else {
+                        float4 *dst = (float4 *)(a.part + prow * D + 32 * k);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                }
+            }
+            if (live && !whole_item) a.ml[prow] = make_float2(m_ref, l);
+            // through with this item's values that are not finite
+            __syncwarp();
+            if (lane == 0) done[4 * h + w4] = i + 1;
+        }
+    }
+    um::tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) set_status(a.status, RKV_ERR_DEVICE_TIMEOUT);
+    if (warp == 1) {
+        um::tc_fence_after();
+        um::tmem_dealloc(tmem, 512);
+    }
+}
+
+// The parts of split items: a warp per row.  out = sum_i 2^(m_i - m) out_i / sum_i 2^(m_i - m) l_i
+// in the order of the keys.
+template <int D>
+__global__ void __launch_bounds__(256)
+k_prompt_join(const FlashArgs a, const PromptJoin *joins)
+{
+    constexpr int kRows = 128 * FlashCfg<D>::kHalves, kPer = D / 32;
+    const int lane = threadIdx.x & 31, n_joins = *(volatile int *)&a.head->joins;
+    const int tile_tok = 128 / a.G;
+    const long long rows = (long long)n_joins * a.N * kRows, warps = (long long)gridDim.x * 8;
+    for (long long x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); x < rows; x += warps) {
+        const int r = (int)(x % kRows), n = (int)(x / kRows % a.N);
+        const PromptJoin j = joins[x / kRows / a.N];
+        const int h = r >> 7, tok = h * tile_tok + (r & 127) / a.G;
+        if ((r & 127) / a.G >= tile_tok || tok >= j.tokens) continue;
+        auto at = [&](int i) { return (size_t)(j.slot + i * a.N + n) * kRows + r; };
+        float m = -INFINITY;
+        bool nan = false;
+        for (int i = 0; i < j.parts; ++i) {
+            const float2 y = __ldcg(a.ml + at(i));
+            m = fmaxf(m, y.x);
+            nan |= y.y != y.y;
+        }
+        float l = 0.0f, o[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] = 0.0f;
+        for (int i = 0; i < j.parts; ++i) {
+            const float2 y = __ldcg(a.ml + at(i));
+            if (y.x == -INFINITY) continue;                // no key of this part is seen
+            const float f = ex2(y.x - m);
+            l = fmaf(y.y, f, l);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) o[e] = fmaf(__ldcg(a.part + at(i) * D + 32 * e + lane), f, o[e]);
+        }
+        const float inv = nan ? __uint_as_float(0x7fffffffu) : l > 0.0f ? 1.0f / l : 0.0f;
+        __nv_bfloat16 *dst = a.out + (j.q_row + tok) * a.out_stride + (n * a.G + (r & 127) % a.G) * D;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) dst[32 * e + lane] = __float2bfloat16_rn(o[e] * inv);
+    }
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// What a call's sizes say about its items, and where its scratch lies.
+struct Layout {
+    int tile_tokens, tok, max_slots, ctas;
+    long long max_items, max_joins;            // for each KV head
+    size_t items, joins, ml, part, total;
+};
+Layout layout_of(const PromptShape &p)
+{
+    Layout y;
+    const int halves = p.D == 256 ? 1 : 2, rows = 128 * halves;
+    y.tile_tokens = halves * (128 / (p.H / p.N));
+    y.tok = p.D == 256 ? 64 : 128;
+    const long long tiles = p.start ? p.rows / y.tile_tokens + (long long)p.S
+                                    : (long long)p.S * ((p.n + y.tile_tokens - 1) / y.tile_tokens);
+    // no part is shorter than 4 x 128 keys
+    const long long keys = p.start ? p.rows : p.T;
+    y.max_slots = (int)min((long long)kSlots, tiles * p.N * (keys / (4 * 128)));
+    y.max_items = tiles + y.max_slots / p.N;
+    y.ctas = (int)min((long long)kCtas, y.max_items * p.N);
+    y.items = 256;
+    y.max_joins = y.max_slots ? tiles : 0;
+    y.joins = y.items + align256((size_t)y.max_items * sizeof(PromptItem));
+    y.ml = y.joins + align256((size_t)y.max_joins * sizeof(PromptJoin));
+    y.part = y.ml + align256((size_t)y.max_slots * rows * sizeof(float2));
+    y.total = y.part + (size_t)y.max_slots * rows * p.D * sizeof(float);
+    return y;
+}
+
+// Rows of G heads of one KV head (q) or one head (k, v), 64 channels of them
+bool make_rows_map(CUtensorMap *m, const void *base, int D, int heads, long long rows, int64_t stride, int box_heads, int box_rows)
+{
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)heads, (uint64_t)rows};
+    const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)stride * 2};
+    const uint32_t box[3] = {64, (uint32_t)box_heads, (uint32_t)box_rows};
+    return make_map_strided(m, base, dims, strides, box);
+}
+
+template <int D>
+cudaError_t run(const PromptShape &p, const Layout &y, const PromptTensors &t, uint8_t *ws, int32_t *status, cudaStream_t s)
+{
+    using C = FlashCfg<D>;
+    const int G = p.H / p.N;
+    FlashMaps maps;
+    if (!make_rows_map(&maps.q, t.q, D, p.H, p.rows, t.q_stride, G, 128 / G) ||
+        !make_rows_map(&maps.k, t.k, D, p.N, t.kv_rows, t.k_stride, 1, C::kTok) ||
+        !make_rows_map(&maps.v, t.v, D, p.N, t.kv_rows, t.v_stride, 1, C::kTok))
+        return cudaErrorInvalidValue;
+    static PerDevice<int> setup;
+    int unused = 0;
+    cudaError_t e = per_device(setup, unused, [](int &) {
+        return cudaFuncSetAttribute(k_prompt_attention<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    });
+    if (e != cudaSuccess) return e;
+    FlashArgs a{};
+    a.head = (PromptHead *)ws;
+    a.items = (const PromptItem *)(ws + y.items);
+    a.out = (__nv_bfloat16 *)t.out;
+    a.out_stride = t.out_stride;
+    a.part = (float *)(ws + y.part);
+    a.ml = (float2 *)(ws + y.ml);
+    a.status = status;
+    a.N = p.N;
+    a.G = G;
+    a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
+    {
+        ProfScope prof("prompt_attention", s);
+        k_prompt_attention<D><<<(unsigned)y.ctas, C::kThreads, C::kSmem, s>>>(maps, a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (y.max_slots) {
+        ProfScope prof("prompt_attention_join", s);
+        k_prompt_join<D><<<8 * kCtas, 256, 0, s>>>(a, (const PromptJoin *)(ws + y.joins));
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace
+
+size_t prompt_workspace_bytes(const PromptShape &p) { return layout_of(p).total; }
+
+cudaError_t launch_prompt_attention(const PromptShape &p, const PromptTensors &t, void *workspace, int32_t *status,
+                                    cudaStream_t s)
+{
+    const Layout y = layout_of(p);
+    uint8_t *ws = (uint8_t *)workspace;
+    PlanArgs a{};
+    a.start = p.start;
+    a.len = p.len;
+    a.n_new = p.n_new;
+    a.S = p.S;
+    a.rows = (int)p.rows;
+    a.n = p.n;
+    a.T = p.T;
+    a.N = p.N;
+    a.tile_tokens = y.tile_tokens;
+    a.tok = y.tok;
+    a.key_bytes = 4 * p.N * p.D;
+    a.max_slots = y.max_slots;
+    a.max_items = (int)y.max_items;
+    a.max_joins = (int)y.max_joins;
+    a.ctas = y.ctas;
+    a.head = (PromptHead *)ws;
+    a.items = (PromptItem *)(ws + y.items);
+    a.joins = (PromptJoin *)(ws + y.joins);
+    a.status = status;
+    {
+        ProfScope prof("prompt_plan", s);
+        k_prompt_plan<<<1, kPlanThreads, 0, s>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    switch (p.D) {
+    case 64: return run<64>(p, y, t, ws, status, s);
+    case 128: return run<128>(p, y, t, ws, status, s);
+    case 256: return run<256>(p, y, t, ws, status, s);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace rkv

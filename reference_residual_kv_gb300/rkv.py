@@ -23,7 +23,8 @@ EXPORTED = ("rkv_n_ref", "rkv_query_sizes", "rkv_build_ref_pool", "rkv_compress"
             "rkv_debug_wait_fault", "rkv_status_string",
             "rkv_dense_sizes", "rkv_dense_write", "rkv_dense_read", "rkv_block_select_workspace",
             "rkv_block_select", "rkv_dense_attention_workspace", "rkv_dense_attention",
-            "rkv_tree_attention")
+            "rkv_tree_attention", "rkv_rope_init", "rkv_qk_rotate", "rkv_prompt_attention_workspace",
+            "rkv_prompt_attention", "rkv_chunk_attention_workspace", "rkv_chunk_attention")
 _DTYPES = {"f32": RKV_F32, "bf16": RKV_BF16, "fp8": RKV_FP8_E4M3}
 
 
@@ -49,6 +50,20 @@ class rkv_dense_params(ctypes.Structure):
 
 class rkv_dense_cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "khdr", "tail")]
+
+
+class rkv_head_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("H", "N", "D", "reserved")]
+
+
+class rkv_rope_scaling(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("kind", "reserved")] + [
+        (n, ctypes.c_double) for n in ("factor", "original", "low", "high")]
+
+
+class rkv_rope(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("D", "R", "layout")] + [("gain", ctypes.c_float),
+                                                                      ("turn", ctypes.c_uint64 * 128)]
 
 
 class RkvError(RuntimeError):
@@ -97,6 +112,7 @@ def lib():
         L.rkv_sparse_attention.argtypes = [P, I32, V, V, V, V, I32, V, V, ctypes.c_size_t, V]
         L.rkv_sparse_attention.restype = I32
         DP, DC, Z = ctypes.POINTER(rkv_dense_params), ctypes.POINTER(rkv_dense_cache), ctypes.c_size_t
+        HP, RP, I64 = ctypes.POINTER(rkv_head_params), ctypes.POINTER(rkv_rope), ctypes.c_int64
         for name, args in (
                 ("rkv_dense_sizes", [DP, sz, sz, sz]),
                 ("rkv_dense_write", [DP, V, I32, I32, V, V, DC, V, V]),
@@ -105,7 +121,13 @@ def lib():
                 ("rkv_block_select", [DP, I32, V, DC, V, I32, I32, I32, I32, V, V, Z, V, V]),
                 ("rkv_dense_attention_workspace", [DP, I32, I32, sz]),
                 ("rkv_dense_attention", [DP, I32, V, DC, V, V, I32, I32, V, I32, V, Z, V, V]),
-                ("rkv_tree_attention", [DP, I32, V, I32, V, V, DC, V, V, I32, V, Z, V, V])):
+                ("rkv_tree_attention", [DP, I32, V, I32, V, V, DC, V, V, I32, V, Z, V, V]),
+                ("rkv_rope_init", [RP, I32, I32, I32, ctypes.c_double, ctypes.POINTER(rkv_rope_scaling)]),
+                ("rkv_qk_rotate", [HP, RP, I32, I32, V, I64, V, I64, V, V, V, ctypes.c_float, V, I64, V, I64, V, V]),
+                ("rkv_prompt_attention_workspace", [HP, I32, I32, sz]),
+                ("rkv_prompt_attention", [HP, I32, V, I32, V, I64, V, I64, V, I64, V, I64, V, Z, V, V]),
+                ("rkv_chunk_attention_workspace", [DP, I32, I32, sz]),
+                ("rkv_chunk_attention", [DP, I32, V, I32, V, V, DC, V, V, V, Z, V, V])):
             f = getattr(L, name)
             f.argtypes, f.restype = args, I32
         L.rkv_profile_enable.argtypes = [I32]
@@ -314,6 +336,73 @@ def rkv_tree_attention(p: rkv_dense_params, H: int, q, n_draft: int, parent, dra
         raise RkvError(st, "rkv_tree_attention")
 
 
+_LAYOUTS = {"pairs": 0, "halves": 1}
+_SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}
+
+
+def rkv_rope_init(D: int, R: int, layout: int, base: float, scaling: rkv_rope_scaling | None = None) -> rkv_rope:
+    r = rkv_rope()
+    st = lib().rkv_rope_init(ctypes.byref(r), D, R, layout, base, None if scaling is None else ctypes.byref(scaling))
+    if st:
+        raise RkvError(st, "rkv_rope_init")
+    return r
+
+
+def make_rope(D: int, R: int | None = None, layout: str = "pairs", base: float = 10000.0, scaling=None) -> rkv_rope:
+    """A rotation of the first R of D channels of a head (all of them by default).  layout: "pairs"
+    (2i, 2i + 1) or "halves" (i, i + R/2).  scaling: None, ("linear", factor), ("bands", factor, original,
+    low, high) or ("yarn", factor, original, fast, slow), as rkv.h gives them."""
+    sc = None
+    if scaling is not None:
+        sc = rkv_rope_scaling(_SCALINGS[scaling[0]], 0, *[float(x) for x in scaling[1:]])
+    return rkv_rope_init(D, D if R is None else R, _LAYOUTS[layout], float(base), sc)
+
+
+def rkv_qk_rotate(p: rkv_head_params, rope: rkv_rope, rows: int, dtype: int, q, q_stride: int, k, k_stride: int, pos,
+                  q_weight, k_weight, eps: float, q_out, q_out_stride: int, k_out, k_out_stride: int, dev_status,
+                  stream=None) -> None:
+    st = lib().rkv_qk_rotate(ctypes.byref(p), ctypes.byref(rope), rows, dtype, _ptr(q), q_stride, _ptr(k), k_stride,
+                             _ptr(pos), _ptr(q_weight), _ptr(k_weight), eps, _ptr(q_out), q_out_stride, _ptr(k_out),
+                             k_out_stride, _ptr(dev_status), _stream(stream))
+    if st:
+        raise RkvError(st, "rkv_qk_rotate")
+
+
+def rkv_prompt_attention_workspace(p: rkv_head_params, S: int, rows: int) -> int:
+    b = ctypes.c_size_t()
+    st = lib().rkv_prompt_attention_workspace(ctypes.byref(p), S, rows, ctypes.byref(b))
+    if st:
+        raise RkvError(st, "rkv_prompt_attention_workspace")
+    return b.value
+
+
+def rkv_prompt_attention(p: rkv_head_params, S: int, start, rows: int, q, q_stride: int, k, k_stride: int, v,
+                         v_stride: int, out, out_stride: int, workspace, workspace_bytes: int, dev_status,
+                         stream=None) -> None:
+    st = lib().rkv_prompt_attention(ctypes.byref(p), S, _ptr(start), rows, _ptr(q), q_stride, _ptr(k), k_stride,
+                                    _ptr(v), v_stride, _ptr(out), out_stride, _ptr(workspace), workspace_bytes,
+                                    _ptr(dev_status), _stream(stream))
+    if st:
+        raise RkvError(st, "rkv_prompt_attention")
+
+
+def rkv_chunk_attention_workspace(p: rkv_dense_params, H: int, n: int) -> int:
+    b = ctypes.c_size_t()
+    st = lib().rkv_chunk_attention_workspace(ctypes.byref(p), H, n, ctypes.byref(b))
+    if st:
+        raise RkvError(st, "rkv_chunk_attention_workspace")
+    return b.value
+
+
+def rkv_chunk_attention(p: rkv_dense_params, H: int, q, n: int, n_new, kv, cache: rkv_dense_cache, length, out,
+                        workspace, workspace_bytes: int, dev_status, stream=None) -> None:
+    st = lib().rkv_chunk_attention(ctypes.byref(p), H, _ptr(q), n, _ptr(n_new), _ptr(kv), ctypes.byref(cache),
+                                   _ptr(length), _ptr(out), _ptr(workspace), workspace_bytes, _ptr(dev_status),
+                                   _stream(stream))
+    if st:
+        raise RkvError(st, "rkv_chunk_attention")
+
+
 def rkv_debug_wait_fault(wait_cycles: int, skip_use: int) -> None:
     st = lib().rkv_debug_wait_fault(int(wait_cycles), int(skip_use))
     if st:
@@ -460,31 +549,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-class DenseCache:
-    """The dense cache of one rkv_dense_params on one device: its three buffers, the device
-    status, and its operators with their tensors checked (type, shape, contiguity, device).
-    Scratch is taken from torch's allocator for each call, on the stream that the call runs on,
-    so that calls on several streams, and captured graphs, share none of it.  Calls that write
-    the cache and calls that read it are ordered by the caller, as for any tensor.
-    guard > 0 puts that many guard bytes behind every buffer, scratch included (test support)."""
+class _DeviceOps:
+    """What DenseCache and PromptHeads share: tensors checked, the object's device made current,
+    scratch from torch's allocator for each call, on the stream that the call runs on."""
 
-    def __init__(self, p: rkv_dense_params, device="cuda", guard: int = 0):
-        p = rkv_dense_params.from_buffer_copy(p)           # the buffers' own: later changes to the caller's do not reach it
-        codes, khdr, tail = rkv_dense_sizes(p)
-        self.p = p
-        self.S, self.T, self.N, self.D = p.S, p.T, p.N, p.D
-        self.guard = guard
-        self._raw = {}
-        for name, n, fill in (("codes", codes, None), ("khdr", khdr, None), ("tail", tail, None), ("status", 16, 0)):
-            t, raw = guarded_empty((n,), torch.uint8, device, guard, fill)
-            setattr(self, name, t)
-            self._raw[name] = (t, raw)
-        self.status = self.status.view(torch.int32)
-        self.device = self.status.device
-        self.cache = rkv_dense_cache(_ptr(self.codes), _ptr(self.khdr), _ptr(self.tail))
-        self._sizes = {}
-        self._p_ref, self._cache_ref = ctypes.byref(self.p), ctypes.byref(self.cache)
-        self._status_ptr = self.status.data_ptr()
+    _what = "object"
 
     def _refuse(self, name, t, dtypes, shape):
         """Says what is wrong with an argument, if anything is."""
@@ -495,7 +564,7 @@ class DenseCache:
         if not t.is_contiguous():
             raise ValueError("%s is not contiguous" % name)
         if t.device != self.device:
-            raise ValueError("%s is on %s, the cache on %s" % (name, t.device, self.device))
+            raise ValueError("%s is on %s, the %s on %s" % (name, t.device, self._what, self.device))
 
     def _check(self, name, t, dtypes, shape):
         if not (t.dtype in dtypes and t.shape == shape and t.device == self.device and t.is_contiguous()):
@@ -503,13 +572,13 @@ class DenseCache:
 
     def _call(self, name, stream, need, *args):
         """The entry point `name` with (params, *args, [workspace, bytes,] status, stream): the
-        cache's device current, scratch of `need` bytes (None: it takes none) from the pool of the
+        object's device current, scratch of `need` bytes (None: it takes none) from the pool of the
         stream that the call runs on."""
         dev = self.device.index
         if dev is None:
-            raise ValueError("%s: the cache is on %s, not on a GPU" % (name, self.device))
+            raise ValueError("%s: the %s is on %s, not on a GPU" % (name, self._what, self.device))
         if stream is not None and not isinstance(stream, int) and stream.device != self.device:
-            raise ValueError("%s: the stream is on %s, the cache on %s" % (name, stream.device, self.device))
+            raise ValueError("%s: the stream is on %s, the %s on %s" % (name, stream.device, self._what, self.device))
         if stream is None and torch.cuda.current_device() == dev:
             st = self._enter(name, need, args, _raw_stream(dev))
         else:
@@ -538,11 +607,48 @@ class DenseCache:
         self._raw["scratch %d" % len(self._raw)] = (t, raw)
         return t
 
+    def device_status(self) -> int:
+        return int(self.status[0].item())
+
+    def guard_violations(self):
+        """Names of the buffers whose guard bytes changed (empty without guards)."""
+        return [k for k, (t, raw) in self._raw.items() if raw is not None and not guard_intact(t, raw)]
+
+
+class DenseCache(_DeviceOps):
+    """The dense cache of one rkv_dense_params on one device: its three buffers, the device
+    status, and its operators with their tensors checked (type, shape, contiguity, device).
+    Scratch is taken from torch's allocator for each call, on the stream that the call runs on,
+    so that calls on several streams, and captured graphs, share none of it.  Calls that write
+    the cache and calls that read it are ordered by the caller, as for any tensor.
+    guard > 0 puts that many guard bytes behind every buffer, scratch included (test support)."""
+
+    _what = "cache"
+
+    def __init__(self, p: rkv_dense_params, device="cuda", guard: int = 0):
+        p = rkv_dense_params.from_buffer_copy(p)           # the buffers' own: later changes to the caller's do not reach it
+        codes, khdr, tail = rkv_dense_sizes(p)
+        self.p = p
+        self.S, self.T, self.N, self.D = p.S, p.T, p.N, p.D
+        self.guard = guard
+        self._raw = {}
+        for name, n, fill in (("codes", codes, None), ("khdr", khdr, None), ("tail", tail, None), ("status", 16, 0)):
+            t, raw = guarded_empty((n,), torch.uint8, device, guard, fill)
+            setattr(self, name, t)
+            self._raw[name] = (t, raw)
+        self.status = self.status.view(torch.int32)
+        self.device = self.status.device
+        self.cache = rkv_dense_cache(_ptr(self.codes), _ptr(self.khdr), _ptr(self.tail))
+        self._sizes = {}
+        self._p_ref, self._cache_ref = ctypes.byref(self.p), ctypes.byref(self.cache)
+        self._status_ptr = self.status.data_ptr()
+
     def _size(self, *key):
-        """Bytes of scratch: ("select", lists) or ("attend", H, n_query)."""
+        """Bytes of scratch: ("select", lists), ("attend", H, n_query) or ("chunk", H, n)."""
         need = self._sizes.get(key)
         if need is None:
-            f = rkv_block_select_workspace if key[0] == "select" else rkv_dense_attention_workspace
+            f = {"select": rkv_block_select_workspace, "attend": rkv_dense_attention_workspace,
+                 "chunk": rkv_chunk_attention_workspace}[key[0]]
             need = self._sizes[key] = f(self.p, *key[1:])
         return need
 
@@ -608,9 +714,103 @@ class DenseCache:
         self._call("rkv_tree_attention", stream, self._size("attend", H, n), H, q.data_ptr(), n, parent.data_ptr(),
                    draft_kv.data_ptr(), self._cache_ref, length.data_ptr(), out.data_ptr(), dt)
 
-    def device_status(self) -> int:
-        return int(self.status[0].item())
+    def chunk_attend(self, H: int, q, kv, length, out, n_new=None, stream=None):
+        """out [S][n][H][D] (bf16): attention of the rows q [S][n][H][D] that follow the cached
+        tokens, over those and over their own kv bf16 [S][n][2ND] up to themselves; n_new[s] of the n
+        rows (all of them where n_new is None), the others are not written.  The rows are written to
+        the cache afterwards (write(kv, length, n_new))."""
+        n = q.shape[1] if q.dim() == 4 else -1
+        self._check("q", q, (_BF16,), (self.S, n, H, self.D))
+        self._check("kv", kv, (_BF16,), (self.S, n, 2 * self.N * self.D))
+        self._check("length", length, (_I32,), (self.S,))
+        self._check("out", out, (_BF16,), (self.S, n, H, self.D))
+        if n_new is not None:
+            self._check("n_new", n_new, (_I32,), (self.S,))
+        self._call("rkv_chunk_attention", stream, self._size("chunk", H, n), H, q.data_ptr(), n,
+                   None if n_new is None else n_new.data_ptr(), kv.data_ptr(), self._cache_ref, length.data_ptr(),
+                   out.data_ptr())
 
-    def guard_violations(self):
-        """Names of the buffers whose guard bytes changed (empty without guards)."""
-        return [k for k, (t, raw) in self._raw.items() if raw is not None and not guard_intact(t, raw)]
+
+class PromptHeads(_DeviceOps):
+    """H query heads over N KV heads of D channels on one device, and what a prompt's rows go
+    through: norm and rotation of queries and keys, causal attention of packed prompts.  Rows are
+    tensors [rows][heads][D] whose heads lie behind one another; rows may lie further apart (parts
+    of one projection's rows).  Keeps a device status; scratch as in DenseCache.
+    guard > 0 puts that many guard bytes behind the status and scratch (test support)."""
+
+    _what = "heads"
+
+    def __init__(self, H: int, N: int, D: int, device="cuda", guard: int = 0):
+        self.H, self.N, self.D = H, N, D
+        self.p = rkv_head_params(H, N, D, 0)
+        rkv_prompt_attention_workspace(rkv_head_params(N, N, D, 0), 1, 1)      # refuses what no operator takes
+        if H < 1 or H % N:
+            raise RkvError(RKV_ERR_UNSUPPORTED, "PromptHeads")
+        self.guard = guard
+        self._raw = {}
+        t, raw = guarded_empty((16,), torch.uint8, device, guard, 0)
+        self._raw["status"] = (t, raw)
+        self.status = t.view(torch.int32)
+        self.device = self.status.device
+        self._p_ref = ctypes.byref(self.p)
+        self._status_ptr = self.status.data_ptr()
+
+    def _rows(self, name, t, dtypes, heads, rows=None):
+        """Distance of a tensor's rows, in elements."""
+        if t.dtype not in dtypes:
+            raise ValueError("%s: %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.D or (rows is not None and t.shape[0] != rows):
+            raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), ("rows" if rows is None else rows, heads, self.D)))
+        if t.device != self.device:
+            raise ValueError("%s is on %s, the %s on %s" % (name, t.device, self._what, self.device))
+        stride, wide = t.stride(), heads * self.D
+        if stride[2] != 1 or (heads > 1 and stride[1] != self.D):
+            raise ValueError("%s: the heads of a row do not lie behind one another" % name)
+        if t.shape[0] <= 1:
+            return wide
+        if stride[0] < wide or stride[0] * t.element_size() % 16:
+            raise ValueError("%s: rows %d elements apart" % (name, stride[0]))
+        return stride[0]
+
+    def rotate(self, rope: rkv_rope, q, k, pos, q_out, k_out, q_weight=None, k_weight=None, eps: float = 1e-6,
+               stream=None):
+        """Queries q [rows][H][D] and keys k [rows][N][D] (bf16 or fp32; either may be None with its
+        output), normed by head where a weight [D] is given and rotated to positions pos [rows]
+        (-1: nothing is written), to q_out and k_out, which may be q and k themselves."""
+        some = q if q is not None else k
+        if some is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
+            raise ValueError("q or k, each with its output")
+        dt = (some.dtype,) if some.dtype in (_BF16, _F32) else (_BF16, _F32)
+        rows = some.shape[0] if some.dim() == 3 else -1
+        args = []
+        for name, x, x_out, w, heads in (("q", q, q_out, q_weight, self.H), ("k", k, k_out, k_weight, self.N)):
+            if x is None:
+                args.append((None, 0, None, None, 0))
+                if w is not None:
+                    raise ValueError("%s_weight without %s" % (name, name))
+                continue
+            sx, so = self._rows(name, x, dt, heads, rows), self._rows(name + "_out", x_out, dt, heads, rows)
+            if w is not None:
+                self._check(name + "_weight", w, dt, (self.D,))
+            args.append((x.data_ptr(), sx, None if w is None else w.data_ptr(), x_out.data_ptr(), so))
+        self._check("pos", pos, (_I32,), (rows,))
+        if rope.D != self.D:
+            raise ValueError("rope: heads of %d channels, expected %d" % (rope.D, self.D))
+        (qp, qs, qw, qo, qos), (kp, ks, kw, ko, kos) = args
+        wide = self.H * self.D
+        self._call("rkv_qk_rotate", stream, None, ctypes.byref(rope), rows, RKV_F32 if dt[0] is _F32 else RKV_BF16, qp,
+                   qs or wide, kp, ks or wide, pos.data_ptr(), qw, kw, eps, qo, qos or wide, ko, kos or wide)
+
+    def attend(self, q, k, v, start, out, stream=None):
+        """out [rows][H][D] (bf16): causal attention of packed prompts, q [rows][H][D] over k, v
+        [rows][N][D]; prompt s has rows start[s] .. start[s + 1] - 1.  Rows of none are not written."""
+        sq = self._rows("q", q, (_BF16,), self.H)
+        rows = q.shape[0]
+        sk, sv = self._rows("k", k, (_BF16,), self.N, rows), self._rows("v", v, (_BF16,), self.N, rows)
+        so = self._rows("out", out, (_BF16,), self.H, rows)
+        S = start.shape[0] - 1 if start.dim() == 1 else -1
+        if S < 0:
+            raise ValueError("start: shape %s, expected one more than prompts" % (tuple(start.shape),))
+        self._check("start", start, (_I32,), (S + 1,))
+        self._call("rkv_prompt_attention", stream, rkv_prompt_attention_workspace(self.p, S, rows), S, start.data_ptr(),
+                   rows, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, out.data_ptr(), so)
