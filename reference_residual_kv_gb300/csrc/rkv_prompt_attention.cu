@@ -7,10 +7,11 @@
 // two tiles, of one sequence and KV head, and a range of keys) and walks over the keys in tiles of
 // kTok; scores = Q K^T and out += P V are tcgen05 products with accumulators in tensor memory.
 //   warp 0       producer: takes items from a counter, Q, K and V by TMA, K and V into a ring
-//   warp 1       the products: while one row tile is at its softmax, the other one's are under way
-//   warps 2, 3   look through V, a tile in turn each, where rows see only a part of a key tile: 0 times a
-//                value that is not finite is not 0, so such values are taken out there and noted, and
-//                given back to the rows that do see them
+//   warps 1, 2   the products of a row tile each: while one tile is at its softmax, the other one's are
+//                under way
+//   warp 3       looks through V where rows see only a part of a key tile: 0 times a value that is not
+//                finite is not 0, so such values are taken out there and noted, and given back to the
+//                rows that do see them
 //   warps 4..    four warps to a row tile, a thread per row: softmax in base 2 against a running
 //                reference m that lags the maximum by at most 8 (p <= 2^8 is harmless in fp32 sums
 //                and has the same relative error in bf16), so that the accumulator is rescaled only where
@@ -331,18 +332,38 @@ __device__ __forceinline__ void tmem_wait_ld(float (&v)[32])
                       "+f"(v[30]), "+f"(v[31]) :: "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
+{
+    __syncwarp();
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(float (&v)[16])
+{
+    __syncwarp();
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :: "memory");
+}
+
 template <int D>
 struct FlashCfg {
     static constexpr int kHalves = D == 256 ? 1 : 2;       // row tiles
-    static constexpr int kBufs = D == 256 ? 2 : 1;         // score buffers of a row tile
-    static constexpr int kTok = D == 256 ? 64 : 128;       // keys of a tile
+    static constexpr int kBufs = D == 128 ? 1 : 2;         // score buffers of a row tile
+    static constexpr int kTok = D == 128 ? 128 : 64;       // keys of a tile
+    static constexpr int kParts = D == 128 ? 2 : 1, kPart = kTok / kParts;   // P goes to the products so many keys at a time
+    static constexpr bool kTurns = D == 128;               // the row tiles' products go in turns
     static constexpr int kStages = D == 64 ? 8 : 5;
     static_assert(kStages <= 8, "four tiles of V at most are in the ring: v_issued and v_clean have as many barriers");
-    static constexpr int kScan = D == 256 ? 1 : 2;         // warps that look through V
     static constexpr int kQ = 128 * D * 2, kTile = kTok * D * 2;
     static constexpr int kThreads = 128 + 128 * kHalves;
-    static constexpr int kBars = 2 * kStages + 36;
-    static constexpr int kSmem = kHalves * kQ + kStages * kTile + kBars * 8 + 4 * 48 + kScan * D * 4 + 64 + 1024;
+    static constexpr int kBars = 2 * kStages + 38;
+    static constexpr int kSmem = kHalves * kQ + kStages * kTile + kBars * 8 + 4 * 48 + D * 4 + 64 + 1024;
     static constexpr int kColS = kHalves * (D < 128 ? 128 : D);   // tensor memory: outputs, then scores
     static constexpr int kColsO = D < 128 ? 128 : D;
     // registers: 384 threads begin with 168; 128 x 72 + 256 x 216 is what the launch has
@@ -368,6 +389,10 @@ struct FlashArgs {
 // An item as the roles share it: its KV head, and how many key tiles each row tile has
 struct FlashWork { PromptItem it; int n, pad[3]; };
 
+// Sums of a tile's probabilities up to here need no other reference: p <= 2^10 is harmless in fp32
+// sums and has the same relative error in bf16 as p <= 1.
+constexpr float kMost = 1024.0f;
+
 constexpr int kNoValue = 0x3fffffff;            // three fields of ten bits: the first key in question
 // A word of the values that are not finite: bits 0..9 NaN, 10..19 +inf, 20..29 -inf, the first key
 // (counted from the item's first partly seen key tile) with one.
@@ -388,22 +413,22 @@ __global__ void __launch_bounds__(FlashCfg<D>::kThreads, 1)
 k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
 {
     using C = FlashCfg<D>;
-    constexpr int kHalves = C::kHalves, kBufs = C::kBufs, kTok = C::kTok, kStages = C::kStages, kScan = C::kScan;
+    constexpr int kHalves = C::kHalves, kBufs = C::kBufs, kTok = C::kTok, kStages = C::kStages, kParts = C::kParts;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *qs = smem_raw + ((1024u - (um::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *ring = qs + kHalves * C::kQ;
     uint64_t *kv_full = (uint64_t *)(ring + kStages * C::kTile), *kv_empty = kv_full + kStages;
     uint64_t *q_full = kv_empty + kStages, *q_empty = q_full + 2;
-    uint64_t *s_full = q_empty + 2, *p_full = s_full + 4, *pv_done = p_full + 4;   // [half * kBufs + buffer]
+    uint64_t *s_full = q_empty + 2, *p_full = s_full + 4, *pv_done = p_full + 4;   // s_full: [half * kBufs + buffer], others: [2 half + buffer]
     uint64_t *o_empty = pv_done + 4, *v_issued = o_empty + 2, *v_clean = v_issued + 4;
-    uint64_t *w_full = v_clean + 4, *w_empty = w_full + 4, *drain = w_empty + 4;
+    uint64_t *w_full = v_clean + 4, *w_empty = w_full + 4, *drain = w_empty + 4, *turn = drain + 2;
     FlashWork *works = (FlashWork *)(kv_full + C::kBars);
-    int *odd = (int *)(works + 4);                         // [kScan][D] values that are not finite, as each warp found them
-    volatile int *done = odd + kScan * D;                      // items that each of the rows' warps is through with
-    volatile int *odd_item = done + 8;                     // the items that `odd` belongs to, + 1
-    volatile int *abort_flag = odd_item + 2;
-    uint32_t *tmem_slot = (uint32_t *)(odd_item + 3);
-    static_assert(2 * kStages + 2 + 2 + 4 + 4 + 4 + 2 + 4 + 4 + 4 + 4 + 1 <= C::kBars && sizeof(FlashWork) == 48, "shared memory");
+    int *odd = (int *)(works + 4);                         // [D] values that are not finite
+    volatile int *done = odd + D;                      // items that each of the rows' warps is through with
+    volatile int *odd_item = done + 8;                     // the item that `odd` belongs to, + 1
+    volatile int *abort_flag = odd_item + 1;
+    uint32_t *tmem_slot = (uint32_t *)(odd_item + 2);
+    static_assert(2 * kStages + 2 + 2 + 4 + 4 + 4 + 2 + 4 + 4 + 4 + 4 + 2 + 2 <= C::kBars && sizeof(FlashWork) == 48, "shared memory");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.G, N = a.N, tile_tok = 128 / G;        // tokens of a row tile
@@ -413,7 +438,7 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
         um::prefetch_tmap(&maps.v);
         for (int i = 0; i < kStages; ++i) {
             um::mbar_init(kv_full + i, 1);
-            um::mbar_init(kv_empty + i, 1);
+            um::mbar_init(kv_empty + i, kHalves);
         }
         for (int i = 0; i < 2; ++i) {
             um::mbar_init(q_full + i, 1);
@@ -427,11 +452,14 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
             um::mbar_init(v_issued + i, 1);
             um::mbar_init(v_clean + i, 1);
             um::mbar_init(w_full + i, 1);
-            um::mbar_init(w_empty + i, 1 + kScan + 4 * kHalves);
+            um::mbar_init(w_empty + i, 1 + 5 * kHalves);
         }
         um::mbar_init(drain, 1);
+        um::mbar_init(drain + 1, 1);
+        um::mbar_init(turn, 1);
+        um::mbar_init(turn + 1, 1);
         for (int i = 0; i < 8; ++i) done[i] = 0;
-        odd_item[0] = odd_item[1] = *abort_flag = 0;
+        *odd_item = *abort_flag = 0;
         um::fence_mbar_init();
     }
     if (warp == 1) {
@@ -561,89 +589,115 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                 if (uses[h]) um::mbar_wait(q_full + h, (uses[h] - 1) & 1u, kWaitCycles);
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // The whole warp walks through the loop with values that are the same for all lanes; one
-        // elected lane issues.  Products of one thread are carried out in the order of issue: the scores
-        // of the next key tile go over the probabilities that the product before them reads.
+    } else if (warp == 1 || (kHalves == 2 && warp == 2)) {
+        // The products of a row tile, a warp each, so that those of one go on while the other warp looks
+        // whether its next operands are there.  The whole warp walks through the loop with values that
+        // are the same for all lanes; one elected lane issues.  Products of one thread are carried out in
+        // the order of issue: the scores of the next key tile go over the probabilities that the
+        // product before them reads.
+        // The two warps issue in turns, outputs of a tile and scores of the next one: mixed, both row tiles'
+        // scores would be ready, and both at their softmax, at the same time.
+        const int h = kHalves == 2 ? __reduce_or_sync(0xffffffffu, warp - 1) : 0;
         const uint32_t tm = __reduce_or_sync(0xffffffffu, tmem);
         const uint32_t id_s = um::idesc_bf16_f32(128, kTok), id_o = um::idesc_bf16_f32(128, D) | (1u << 16);   // V: N-major
-        const uint64_t qd = um::sdesc_sw128(um::smem_u32(qs));
+        const uint64_t qd = um::sdesc_sw128(um::smem_u32(qs)) + h * (C::kQ / 16);
         const uint64_t kd = um::sdesc_sw128(um::smem_u32(ring));
         const uint64_t vd = um::sdesc_sw128_mn(um::smem_u32(ring), kTok * 128, 1024);
-        uint32_t loads = 0, turns[2] = {0, 0}, cleans = 0;    // turns: items in which a half has had keys
-        uint32_t steps[2] = {0, 0};                        // key tiles that each half is through with
+        // loads: stage and phase of the next load that this warp comes to
+        uint32_t k_st = 0, k_ph = 0, turns = 0, cleans = 0, steps = 0, rounds = 0;   // turns: items in which this half has had keys
+        auto step_on = [&](uint32_t &st, uint32_t &ph, uint32_t n) {
+            st += n;
+            if (st >= kStages) { st -= kStages; ph ^= 1u; }
+        };
         bool ok = true;
         FlashWork w;
         for (int i = 0; ok && take(i, w); ++i) {
-            const int c[2] = {tiles_of(w.it, 0), kHalves == 2 ? tiles_of(w.it, 1) : 0}, count = max(c[0], c[1]);
-            const int part0 = max(0, partly(w.it) - w.it.kt0);   // first tile that is looked through
-            auto last_user = [&](int h, int j) { return h == kHalves - 1 || j >= c[1]; };
-            auto scores = [&](int h, int j) {
-                const uint32_t ld = loads + 2 * j, st = ld % kStages, t = steps[h] + j, buf = t % kBufs;
-                if (j == 0) ok = ok && wait(q_full + h, turns[h]);
-                ok = ok && wait(kv_full + st, ld / kStages);
+            const int mine = __reduce_max_sync(0xffffffffu, tiles_of(w.it, h));
+            const int count = kHalves == 2 ? __reduce_max_sync(0xffffffffu, max(mine, tiles_of(w.it, 1 - h))) : mine;
+            const int part0 = __reduce_max_sync(0xffffffffu, max(0, partly(w.it) - w.it.kt0));   // first tile that is looked through
+            uint32_t v_st = k_st, v_ph = k_ph;
+            step_on(v_st, v_ph, 1);
+            auto scores = [&](int j, bool waited) {
+                const uint32_t buf = (steps + j) % kBufs;
+                if (!waited) ok = ok && wait(kv_full + k_st, k_ph);
                 if (!ok) return;
                 um::tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t q0 = qd + h * (C::kQ / 16), k0 = kd + st * (C::kTile / 16);
+                    const uint64_t k0 = kd + k_st * (C::kTile / 16);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        um::mma_bf16(tm + C::kColS + (h * kBufs + buf) * kTok, q0 + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
+                    for (int k = 0; k < D / 16; ++k) {
+                        um::mma_bf16(tm + C::kColS + (h * kBufs + buf) * kTok, qd + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
                                      k0 + (k >> 2) * (kTok * 128 / 16) + 2 * (k & 3), id_s, k != 0);
+                    }
                     um::mma_commit(s_full + h * kBufs + buf);
-                    if (last_user(h, j)) um::mma_commit(kv_empty + st);
-                    if (j == c[h] - 1) um::mma_commit(q_empty + h);
+                    um::mma_commit(kv_empty + k_st);
+                    if (j == mine - 1) um::mma_commit(q_empty + h);
                 }
                 __syncwarp();
+                step_on(k_st, k_ph, 2);
             };
-            auto outputs = [&](int h, int j) {
-                const uint32_t ld = loads + 2 * j + 1, st = ld % kStages, t = steps[h] + j, buf = t % kBufs;
-                ok = ok && wait(kv_full + st, ld / kStages);
+            if (mine > 0) ok = ok && wait(q_full + h, turns);
+#pragma unroll
+            for (int j = 0; j < kBufs; ++j)
+                if (j < mine && ok) scores(j, false);
+            for (int j = 0; j < mine && ok; ++j, ++rounds) {
+                const uint32_t t = steps + j, buf = t % kBufs;
+                if (j + kBufs < mine) ok = ok && wait(kv_full + k_st, k_ph);
+                ok = ok && wait(kv_full + v_st, v_ph);
                 if (j >= part0) {
                     const uint32_t cl = cleans + (j - part0);
                     ok = ok && wait(v_clean + (cl & 3), cl >> 2);
                 }
-                if (j == 0) ok = ok && wait(o_empty + h, turns[h] ^ 1u);
-                ok = ok && wait(p_full + h * kBufs + buf, t / kBufs);
-                if (!ok) return;
-                um::tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t v0 = vd + st * (C::kTile / 16);
-                    const uint32_t p0 = tm + C::kColS + (h * kBufs + buf) * kTok;
+                if (j == 0) ok = ok && wait(o_empty + h, turns ^ 1u);
 #pragma unroll
-                    for (int k = 0; k < kTok / 16; ++k)
-                        mma_bf16_ta(tm + h * C::kColsO, p0 + 8 * k, v0 + k * (2048 / 16), id_o, j != 0 || k != 0);
-                    um::mma_commit(pv_done + h * kBufs + buf);
-                    if (last_user(h, j)) um::mma_commit(kv_empty + st);
+                for (int part = 0; part < kParts; ++part) {
+                    const int b = 2 * h + (kBufs > 1 ? buf : part);
+                    ok = ok && wait(p_full + b, t / kBufs);
+                    if (C::kTurns && part == 0) ok = ok && wait(turn + h, h ? rounds : rounds ^ 1u);
+                    if (!ok) break;
+                    um::tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t v0 = vd + v_st * (C::kTile / 16) + part * (C::kPart * 128 / 16);
+                        const uint32_t p0 = tm + C::kColS + (h * kBufs + buf) * kTok + C::kPart / 2 * part;
+#pragma unroll
+                        for (int k = 0; k < C::kPart / 16; ++k)
+                            mma_bf16_ta(tm + h * C::kColsO, p0 + 8 * k, v0 + k * (2048 / 16), id_o, j != 0 || part != 0 || k != 0);
+                        um::mma_commit(pv_done + b);
+                        if (part == kParts - 1) um::mma_commit(kv_empty + v_st);
+                    }
+                    __syncwarp();
                 }
+                step_on(v_st, v_ph, 2);
+                if (j + kBufs < mine && ok) scores(j + kBufs, true);
+                if (C::kTurns && ok && elect_one()) um::mbar_arrive(turn + 1 - h);
                 __syncwarp();
-            };
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-                for (int j = 0; j < kBufs; ++j)
-                    if (j < c[h] && ok) scores(h, j);
-            for (int j = 0; j < count && ok; ++j)
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
-                    if (j >= c[h] || !ok) continue;
-                    outputs(h, j);
-                    if (j + kBufs < c[h] && ok) scores(h, j + kBufs);
-                }
-            loads += 2 * count;
-            cleans += max(0, count - part0);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                steps[h] += c[h];
-                turns[h] += c[h] > 0;
             }
+            // key tiles that only the other half needs: they have to be there before they can be let go
+            for (int j = mine; j < count && ok; ++j, ++rounds) {
+                ok = wait(kv_full + k_st, k_ph);
+                if (ok && elect_one()) um::mbar_arrive(kv_empty + k_st);
+                __syncwarp();
+                step_on(k_st, k_ph, 1);
+                ok = ok && wait(kv_full + k_st, k_ph);
+                if (ok && elect_one()) um::mbar_arrive(kv_empty + k_st);
+                __syncwarp();
+                step_on(k_st, k_ph, 1);
+                if (C::kTurns) {
+                    ok = ok && wait(turn + h, h ? rounds : rounds ^ 1u);
+                    if (ok && elect_one()) um::mbar_arrive(turn + 1 - h);
+                    __syncwarp();
+                }
+            }
+            cleans += max(0, count - part0);
+            steps += mine;
+            turns += mine > 0;
         }
         // every issued product completes before tensor memory is released
-        if (elect_one()) um::mma_commit(drain);
+        if (elect_one()) um::mma_commit(drain + h);
         __syncwarp();
-        um::mbar_wait(drain, 0, kWaitCycles);
+        um::mbar_wait(drain + h, 0, kWaitCycles);
         __syncwarp();
-    } else if (warp < 2 + kScan) {
+    } else if (warp == 3) {
         uint32_t loads = 0, cleans = 0;
         FlashWork w;
         bool ok = true;
@@ -651,7 +705,6 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
             const int count = max(tiles_of(w.it, 0), kHalves == 2 ? tiles_of(w.it, 1) : 0);
             const int base = partly(w.it), part0 = max(0, base - w.it.kt0), kv_len = w.it.first + w.it.tokens;
             for (int j = part0; j < count && ok; ++j, ++cleans) {
-                if (cleans % kScan != (uint32_t)(warp - 2)) continue;
                 const uint32_t ld = loads + 2 * j + 1, st = ld % kStages;
                 ok = wait(v_issued + (cleans & 3), cleans >> 2) && wait(kv_full + st, ld / kStages);
                 if (!ok) break;
@@ -665,8 +718,8 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                     for (int k = 0; k < 4; ++k) bad |= (e[k] & 0x7f807f80u) + 0x00800080u;
                 }
                 if (__any_sync(0xffffffffu, bad & 0x80008000u)) {
-                    int *words = odd + (warp - 2) * D;
-                    if (odd_item[warp - 2] != i + 1) {
+                    int *words = odd;
+                    if (*odd_item != i + 1) {
                         // the rows are through with the values of the items before
                         const long long t0 = clock64();
                         bool here = false;
@@ -679,7 +732,7 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                         }
                         for (int d = lane; d < D; d += 32) words[d] = kNoValue;
                         __syncwarp();
-                        if (lane == 0) odd_item[warp - 2] = i + 1;
+                        if (lane == 0) *odd_item = i + 1;
                     }
                     for (int x = lane; x < C::kTile / 16; x += 32) {
                         const int box = x / (kTok * 8), r = x / 8 % kTok, ch = (x & 7) ^ (r & 7);
@@ -720,82 +773,93 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                 if (!ok) break;
                 um::tc_fence_after();
                 const uint32_t ts = tmem + lanes + C::kColS + (h * kBufs + buf) * kTok;
+                const int left = j >= whole ? sees - (w.it.kt0 + j) * kTok : kTok;   // columns up to this one are seen
+                // The exponentials take the reference as it is; where that turns out to be too low (rarely,
+                // but for the first keys) they are taken again.
                 float v[kTok / 32][32];
 #pragma unroll
-                for (int k = 0; k < kTok / 32; ++k) tmem_ld32(ts + 32 * k, v[k]);
+                for (int c = 0; c < kTok / 32; ++c) tmem_ld32(ts + 32 * c, v[c]);
 #pragma unroll
-                for (int k = 0; k < kTok / 32; ++k) tmem_wait_ld(v[k]);
-                if (j >= whole) {
-                    const int left = sees - (w.it.kt0 + j) * kTok;            // columns up to this one are seen
+                for (int c = 0; c < kTok / 32; ++c) tmem_wait_ld(v[c]);
+                if (left < kTok - 1)
 #pragma unroll
-                    for (int k = 0; k < kTok / 32; ++k)
+                    for (int c = 0; c < kTok / 32; ++c)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (32 * k + e > left) v[k][e] = -INFINITY;
-                }
-                float top[4];
+                            if (32 * c + e > left) v[c][e] = -INFINITY;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) top[x] = v[x * (kTok / 128)][x * 8 % 32];
+                for (int part = 0; part < kParts; ++part) {
+                    constexpr int kC = C::kPart / 32;
+                    const int pb = 2 * h + (kBufs > 1 ? (int)buf : part);
+                    float2 sums[2];
+                    auto exps = [&]() {
+                        const float mu = m_ref == -INFINITY ? 0.0f : m_ref;
+                        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), mu2 = make_float2(-mu, -mu);
+                        sums[0] = sums[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int k = 0; k < kTok / 32; ++k)
+                        for (int c = kC * part; c < kC * (part + 1); ++c) {
+                            uint32_t p[16];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
+                            for (int e = 0; e < 16; ++e) {
+                                const float2 y = __ffma2_rn(make_float2(v[c][2 * e], v[c][2 * e + 1]), sc2, mu2);
+                                const float2 pp = make_float2(ex2(y.x), ex2(y.y));
+                                sums[e & 1] = __fadd2_rn(sums[e & 1], pp);
+                                p[e] = as_u32(__floats2bfloat162_rn(pp.x, pp.y));
+                            }
+                            tmem_st16(ts + 16 * c, p);
+                        }
+                    };
+                    exps();
+                    // As long as the sum stays small, so does every probability: no maximum is taken.
+                    // The reference moves to the maximum where it does not, and at the start
+                    const float sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+                    float add = sum;
+                    const bool look = in_tile && (!(sum <= kMost) || m_ref == -INFINITY);
+                    if (__any_sync(0xffffffffu, look)) {
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) top[x] = max3f(top[x], v[k][e + 2 * x], v[k][e + 2 * x + 1]);
-                const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-                // the reference moves where the maximum is more than 8 above it, and at the start
-                const bool move = most > m_ref + 8.0f || (m_ref == -INFINITY && most != -INFINITY);
-                if (__any_sync(0xffffffffu, move)) {
-                    const float f = move ? (m_ref == -INFINITY ? 0.0f : ex2(m_ref - most)) : 1.0f;
-                    if (j > 0) {
-                        // with one buffer, these scores came after the last output product
-                        if (kBufs > 1) {
-                            ok = wait(pv_done + h * kBufs + (t - 1) % kBufs, (t - 1) / kBufs);
+                        for (int c = kC * part; c < kC * (part + 1); ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) top[z] = max3f(top[z], v[c][e + 2 * z], v[c][e + 2 * z + 1]);
+                        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+                        const bool move = look && most > m_ref;
+                        const float f = move ? (m_ref == -INFINITY ? 0.0f : ex2(m_ref - most)) : 1.0f;
+                        if (j > 0 || part > 0) {
+                            // the output products so far: with one buffer, those of earlier tiles came before
+                            // these scores
+                            if (kBufs > 1) ok = wait(pv_done + 2 * h + (t - 1) % kBufs, (t - 1) / kBufs);
+                            else if (part > 0) ok = wait(pv_done + 2 * h, t);
                             if (!ok) break;
                             um::tc_fence_after();
-                        }
 #pragma unroll 1
-                        for (int k = 0; k < D / 32; ++k) {
-                            float o[32];
-                            tmem_ld32(to + 32 * k, o);
-                            tmem_wait_ld(o);
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
+                            for (int k = 0; k < D / 16; ++k) {
+                                float o[16];
+                                tmem_ld16(to + 16 * k, o);
+                                tmem_wait_ld16(o);
                                 uint32_t x[16];
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[16 * y + e] * f);
-                                tmem_st16(to + 32 * k + 16 * y, x);
+                                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[e] * f);
+                                tmem_st16(to + 16 * k, x);
                             }
                         }
+                        l *= f;
+                        if (move) m_ref = most;
+                        exps();
+                        add = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
                     }
-                    l *= f;
-                    if (move) m_ref = most;
+                    l += add;
+                    tmem_wait_st();
+                    um::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) um::mbar_arrive(p_full + pb);
                 }
-                const float mu = m_ref == -INFINITY ? 0.0f : m_ref;
-                const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), mu2 = make_float2(-mu, -mu);
-                float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                for (int k = 0; k < kTok / 32; ++k) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 x = __ffma2_rn(make_float2(v[k][2 * e], v[k][2 * e + 1]), sc2, mu2);
-                        const float2 pp = make_float2(ex2(x.x), ex2(x.y));
-                        sums[e & 1] = __fadd2_rn(sums[e & 1], pp);
-                        p[e] = as_u32(__floats2bfloat162_rn(pp.x, pp.y));
-                    }
-                    tmem_st16(ts + 16 * k, p);
-                }
-                l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
-                tmem_wait_st();
-                um::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) um::mbar_arrive(p_full + h * kBufs + buf);
             }
             if (!ok) break;
             if (count > 0) {
                 const uint32_t t = steps + count - 1;
-                ok = wait(pv_done + h * kBufs + t % kBufs, t / kBufs);
+                ok = wait(pv_done + 2 * h + (kBufs > 1 ? t % kBufs : kParts - 1), t / kBufs);
                 if (!ok) break;
                 um::tc_fence_after();
             }
@@ -803,7 +867,7 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
             const bool live = in_tile && tok < w.it.tokens, whole_item = w.it.slot < 0;
             const size_t prow = whole_item ? 0 : (size_t)(w.it.slot + w.n) * (128 * kHalves) + 128 * h + r;
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays
-            const bool odd_here[2] = {odd_item[0] == i + 1, kScan == 2 && odd_item[1] == i + 1};
+            const bool odd_here = *odd_item == i + 1;
             const int seen_to = min(1022, sees - partly(w.it) * kTok);
             if (count > 0) {
 #pragma unroll 1
@@ -816,17 +880,16 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                         __syncwarp();
                         if (lane == 0) um::mbar_arrive(o_empty + h);
                     }
-                    if (odd_here[0] || odd_here[1])
+                    if (odd_here)
 #pragma unroll 1
-                        for (int e = 0; e < 32 * kScan; ++e) {
-                            if (!odd_here[e >> 5]) continue;
-                            const int word = odd[(e >> 5) * D + 32 * k + (e & 31)];
+                        for (int e = 0; e < 32; ++e) {
+                            const int word = odd[32 * k + e];
                             const bool nan = (word & 1023) <= seen_to, up = ((word >> 10) & 1023) <= seen_to,
                                        down = ((word >> 20) & 1023) <= seen_to;
                             const float add = nan || (up && down) ? __uint_as_float(0x7fffffffu) : up ? INFINITY : down ? -INFINITY : 0.0f;
 #pragma unroll
                             for (int y = 0; y < 32; ++y)
-                                if (y == (e & 31)) o[y] += add;
+                                if (y == e) o[y] += add;
                         }
                     if (!live) continue;
                     if (whole_item) {
@@ -916,7 +979,7 @@ Layout layout_of(const PromptShape &p)
     Layout y;
     const int halves = p.D == 256 ? 1 : 2, rows = 128 * halves;
     y.tile_tokens = halves * (128 / (p.H / p.N));
-    y.tok = p.D == 256 ? 64 : 128;
+    y.tok = p.D == 128 ? 128 : 64;
     const long long tiles = p.start ? p.rows / y.tile_tokens + (long long)p.S
                                     : (long long)p.S * ((p.n + y.tile_tokens - 1) / y.tile_tokens);
     // no part is shorter than 4 x 128 keys
