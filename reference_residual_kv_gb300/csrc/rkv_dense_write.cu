@@ -19,7 +19,7 @@
 //                  kTogether of the entries ask for is read for that token alone (4 x 131072
 //                  tokens, 1 / 6 / 12 % of them: 65 / 120 / 150 us; all by blocks 74 / 131 / 153,
 //                  blocks from 4 entries on 66 / 138 / 163).
-#include "rkv_prompt.cuh"
+#include "rkv_prompt_plan.cuh"
 #include "umma.cuh"
 
 namespace rkv {
@@ -676,63 +676,70 @@ k_dense_read(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
     }
 }
 
-// K and V of a sequence's cached tokens, and of the rows behind them, as bf16 rows [T][2 N D]: what
-// attention over many query rows reads.  A warp takes kRowBlocks blocks of 32 tokens of a KV head's
-// keys or values, the next record on its way while one becomes bf16.
-constexpr int kRowBlocks = 4;
+// K and V of a sequence's cached tokens, and of the rows behind them, in bf16 as [N][2][T][D]: what
+// attention over many query rows reads.  The first CTA works out the items of that attention meanwhile.
+// A warp takes a block of 32 tokens of a KV head's keys or values at a time, every n-th of them, n
+// the warps of the grid, so that a capacity far beyond the lengths costs a look at them only.  Many
+// warps to an SM with a record each on its way: 131072 tokens of 8 heads of 128 at 4 bits 114 us (6.2 TB/s of
+// codes and rows), with four blocks to a warp and the next record on its way 137.
+template <int D, int BITS>
+struct RowsCfg {
+    using C = ReadCfg<D, BITS>;
+    static constexpr int kWarp = C::kRows + C::kStage + 128;   // 32 rows of 64 channels, a record, a barrier
+    static_assert(kWarp % 128 == 0, "the rows' places are flipped bits of their addresses");
+    static constexpr int kPlan = (int)sizeof(PlanShared<32 * kReadWarps>);
+    static constexpr int kSmem = kReadWarps * kWarp > kPlan ? kReadWarps * kWarp : kPlan;
+};
 
 template <int D, int BITS>
 __global__ void __launch_bounds__(32 * kReadWarps)
 k_dense_rows(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr, const __nv_bfloat16 *__restrict__ tail,
              const int32_t *__restrict__ len, const __nv_bfloat16 *__restrict__ kv, int n, const int32_t *__restrict__ n_new,
-             int S, int N, int T, int nb, int groups, __nv_bfloat16 *__restrict__ out, int32_t *status)
+             int S, int N, int T, int nb, __nv_bfloat16 *__restrict__ out, const PlanArgs plan, int32_t *status)
 {
     using C = ReadCfg<D, BITS>;
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kCh = D / 8;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint4 *buf = (uint4 *)(smem + (size_t)warp * C::kWarp);
-    uint8_t *stage = (uint8_t *)buf + C::kRows;
-    uint64_t *bars = (uint64_t *)(smem + (size_t)kReadWarps * C::kWarp) + warp * C::kStages;
-    const long long id = (long long)blockIdx.x * kReadWarps + warp;
-    const bool is_v = id & 1;
-    const int h = (int)((id >> 1) % N), grp = (int)((id >> 1) / N % groups), s = (int)((id >> 1) / N / groups);
-    if (s >= S) return;
-    const int length = __ldg(len + s), more = n_new ? __ldg(n_new + s) : n;
-    if (length < 0 || more < 0 || more > n || length > T - more) {
-        set_status(status, RKV_ERR_INDEX);
+    if (blockIdx.x == 0) {
+        prompt_plan<32 * kReadWarps>(plan, *(PlanShared<32 * kReadWarps> *)smem);
         return;
     }
-    const int full = length / kBlk, first = grp * kRowBlocks;
-    const int last = min(first + kRowBlocks, (length + more + kBlk - 1) / kBlk);
-    if (more == 0 || first >= last) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint4 *buf = (uint4 *)(smem + (size_t)warp * RowsCfg<D, BITS>::kWarp);
+    uint8_t *rec = (uint8_t *)buf + C::kRows;
+    uint64_t *bar = (uint64_t *)(rec + C::kStage);
     if (lane == 0) {
-        for (int k = 0; k < C::kStages; ++k) um::mbar_init(bars + k, 1);
+        um::mbar_init(bar, 1);
         um::fence_mbar_init();
     }
     __syncwarp();
-    const size_t sh = (size_t)s * N + h;
-    auto fetch = [&](int b) {
-        if (lane == 0 && b < last && b < full) {
-            const int st = (b - first) % C::kStages;
-            const uint8_t *rec = codes + (sh * nb + b) * C::kRec;
-            um::mbar_arrive_expect_tx(bars + st, C::kStage);
-            bulk_load(stage + st * C::kStage, rec + (is_v ? C::kUnit : 0), C::kUnit, bars + st);
-            bulk_load(stage + st * C::kStage + C::kUnit, is_v ? rec + 2 * C::kUnit : khdr + (sh * nb + b) * C::kHdr, C::kHdr, bars + st);
+    const int groups = (T + kBlk - 1) / kBlk;
+    const long long units = (long long)S * N * 2 * groups, step = (long long)(gridDim.x - 1) * kReadWarps;
+    uint32_t uses = 0;
+    for (long long id = (long long)(blockIdx.x - 1) * kReadWarps + warp; id < units; id += step) {
+        const int b = (int)(id % groups);
+        const long long shv = id / groups;
+        const bool is_v = shv & 1;
+        const size_t sh = (size_t)(shv >> 1);
+        const int s = (int)(sh / N), h = (int)(sh % N);
+        const int length = __ldg(len + s), more = n_new ? __ldg(n_new + s) : n;
+        if (length < 0 || more < 0 || more > n || length > T - more) {
+            if (b == 0) set_status(status, RKV_ERR_INDEX);
+            continue;
         }
-    };
-    auto row_of = [&](int t) { return (uint4 *)(out + (((size_t)s * T + t) * 2 + is_v) * N * D + (size_t)h * D); };
-    fetch(first);
-    for (int b = first; b < last; ++b) {
-        fetch(b + 1);
-        if (b < full) {
-            const int st = (b - first) % C::kStages;
-            const uint8_t *rec = stage + st * C::kStage;
-            const bool here = um::mbar_wait(bars + st, (uint32_t)((b - first) / C::kStages) & 1u, kWaitCycles);
+        if (more == 0 || b * kBlk >= length + more) continue;
+        uint4 *dst = (uint4 *)(out + ((sh * 2 + is_v) * T + b * kBlk) * D);
+        if (b < length / kBlk) {
+            if (lane == 0) {
+                const uint8_t *r = codes + (sh * nb + b) * C::kRec;
+                um::mbar_arrive_expect_tx(bar, C::kStage);
+                bulk_load(rec, r + (is_v ? C::kUnit : 0), C::kUnit, bar);
+                bulk_load(rec + C::kUnit, is_v ? r + 2 * C::kUnit : khdr + (sh * nb + b) * C::kHdr, C::kHdr, bar);
+            }
+            const bool here = um::mbar_wait(bar, uses++ & 1u, kWaitCycles);
             if (!__all_sync(0xffffffffu, here)) {
                 // what is on its way gets as long again
-                for (int i = b; i <= b + 1 && i < last && i < full; ++i)
-                    um::mbar_wait(bars + (i - first) % C::kStages, (uint32_t)((i - first) / C::kStages) & 1u, kWaitCycles);
+                um::mbar_wait(bar, (uses - 1) & 1u, kWaitCycles);
                 set_status(status, RKV_ERR_DEVICE_TIMEOUT);
                 return;
             }
@@ -743,8 +750,7 @@ k_dense_rows(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
                 else read_block<BITS, false>(rec, rec + C::kUnit, part, lane, buf);
                 __syncwarp();
 #pragma unroll
-                for (int r = lane >> 3; r < kBlk; r += 4)
-                    row_of(b * kBlk + r)[8 * part + (lane & 7)] = buf[tile_chunk(r, lane & 7)];
+                for (int r = lane >> 3; r < kBlk; r += 4) dst[r * kCh + 8 * part + (lane & 7)] = buf[tile_chunk(r, lane & 7)];
             }
             __syncwarp();
         } else {
@@ -755,7 +761,7 @@ k_dense_rows(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
                 if (t >= length + more) continue;
                 const __nv_bfloat16 *src = t < length ? tail + ((sh * 2 + is_v) * kBlk + t % kBlk) * D
                                                       : kv + (((size_t)s * n + t - length) * 2 + is_v) * N * D + (size_t)h * D;
-                row_of(t)[x % kCh] = __ldg((const uint4 *)src + x % kCh);
+                dst[x] = __ldg((const uint4 *)src + x % kCh);
             }
         }
     }
@@ -774,11 +780,11 @@ __global__ void k_chunk_parents(const int32_t *__restrict__ len, int n, const in
 
 template <int D, int BITS>
 cudaError_t run_rows(const DenseGeom &g, const rkv_dense_cache *c, const int32_t *len, const void *kv, int n,
-                     const int32_t *n_new, void *out, int32_t *status, cudaStream_t s)
+                     const int32_t *n_new, void *out, const PlanArgs &plan, int32_t *status, cudaStream_t s)
 {
-    const int groups = ((g.T + kBlk - 1) / kBlk + kRowBlocks - 1) / kRowBlocks;
-    const long long warps = (long long)g.S * groups * g.N * 2;
-    constexpr int kSmem = ReadCfg<D, BITS>::kSmem;
+    constexpr int kSmem = RowsCfg<D, BITS>::kSmem;
+    const long long units = (long long)g.S * g.N * 2 * ((g.T + kBlk - 1) / kBlk);
+    const long long ctas = min((units + kReadWarps - 1) / kReadWarps, 152LL * 64);
     static PerDevice<int> setup;
     int unused = 0;
     cudaError_t e = per_device(setup, unused, [](int &) {
@@ -786,9 +792,9 @@ cudaError_t run_rows(const DenseGeom &g, const rkv_dense_cache *c, const int32_t
     });
     if (e != cudaSuccess) return e;
     ProfScope prof("dense_rows", s);
-    k_dense_rows<D, BITS><<<(unsigned)((warps + kReadWarps - 1) / kReadWarps), 32 * kReadWarps, kSmem, s>>>(
+    k_dense_rows<D, BITS><<<(unsigned)ctas + 1, 32 * kReadWarps, kSmem, s>>>(
         (const uint8_t *)c->codes, (const uint8_t *)c->khdr, (const __nv_bfloat16 *)c->tail, len, (const __nv_bfloat16 *)kv,
-        n, n_new, g.S, g.N, g.T, g.nb, groups, (__nv_bfloat16 *)out, status);
+        n, n_new, g.S, g.N, g.T, g.nb, (__nv_bfloat16 *)out, plan, status);
     return cudaGetLastError();
 }
 
@@ -859,10 +865,10 @@ cudaError_t launch_dense_read(const DenseGeom &g, const rkv_dense_cache *c, cons
 }
 
 cudaError_t launch_dense_rows(const DenseGeom &g, const rkv_dense_cache *c, const int32_t *len, const void *kv, int n,
-                              const int32_t *n_new, void *out, int32_t *status, cudaStream_t s)
+                              const int32_t *n_new, void *out, const PlanArgs &plan, int32_t *status, cudaStream_t s)
 {
     auto go = [&](auto bits, auto d) -> cudaError_t {
-        return run_rows<decltype(d)::value, decltype(bits)::value>(g, c, len, kv, n, n_new, out, status, s);
+        return run_rows<decltype(d)::value, decltype(bits)::value>(g, c, len, kv, n, n_new, out, plan, status, s);
     };
     return dense_dispatch(g, go);
 }

@@ -130,8 +130,8 @@ cudaError_t per_device(PerDevice<T> &pd, T &value, F setup)
 // (rkv_umma.cu); false if the driver rejects it.
 bool make_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows,
               uint64_t batch, uint32_t box_rows);
-bool make_map_strided(CUtensorMap *m, const void *base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
-                      const uint32_t (&box)[3]);
+bool make_map_strided(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                      const uint32_t *box);
 bool make_map_store(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows, uint64_t batch,
                     uint32_t box_inner, uint32_t box_rows);
 

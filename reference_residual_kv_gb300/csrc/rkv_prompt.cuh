@@ -26,16 +26,19 @@ struct PromptShape {
 struct PromptTensors {
     const void *q, *k, *v;
     void *out;
-    int64_t q_stride, k_stride, v_stride, out_stride;
-    long long kv_rows;
+    int64_t q_stride, k_stride, v_stride, out_stride;      // between rows
+    int64_t kv_head, kv_seq;                               // between heads and sequences of k and v
 };
+struct PlanArgs;
+PlanArgs prompt_plan_args(const PromptShape &p, void *workspace, int32_t *status);
 size_t prompt_workspace_bytes(const PromptShape &p);
 cudaError_t launch_prompt_attention(const PromptShape &p, const PromptTensors &t, void *workspace, int32_t *status,
                                     cudaStream_t s);
 
-// K and V of cached text and the rows behind it as bf16 rows [S][T][2 N D] (rkv_dense_write.cu)
+// K and V of cached text and the rows behind it in bf16, [S][N][2 (K, V)][T][D], and the items of the
+// attention that reads them (rkv_dense_write.cu)
 cudaError_t launch_dense_rows(const DenseGeom &g, const rkv_dense_cache *cache, const int32_t *len, const void *kv, int n,
-                              const int32_t *n_new, void *out, int32_t *status, cudaStream_t s);
+                              const int32_t *n_new, void *out, const PlanArgs &plan, int32_t *status, cudaStream_t s);
 // Each row's parent in a piece of text, for launch_dense_attention: the row before it
 cudaError_t launch_chunk_parents(const DenseGeom &g, const int32_t *len, int n, const int32_t *n_new, int32_t *parent,
                                  int32_t *status, cudaStream_t s);

@@ -1,6 +1,6 @@
 // rkv_prompt_api.cu -- the extern "C" entry points of the prompt's operators: argument checks
 // and dispatch.  No entry point allocates device memory.
-#include "rkv_prompt.cuh"
+#include "rkv_prompt_plan.cuh"
 
 #include <limits.h>
 #include <math.h>
@@ -90,9 +90,27 @@ PromptShape piece_shape(const rkv_dense_params *p, int H, int n, const int32_t *
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Up to kMaxDraft rows go the way of drafted trees, which read the cache as it is; more rows read
-// bf16 rows that k_dense_rows makes of it first.
-bool as_tree(int n) { return n <= kMaxDraft; }
+// Short pieces go the way of drafted trees, which read the cache as it is, but whose last pass takes a
+// row at a time; others read bf16 rows that k_dense_rows makes of the cache first.  R = n H / N rows to a
+// KV head.  As a tree | from bf16 rows, us (D = 128 but where stated, 4 bits, T tokens of each sequence):
+//   8 KV heads, H = 32                  n = 8       16          32          48          64
+//     1 x 131072                        112 | 221   152 | 223   145 | 224   171 | 226   173 | 228
+//     4 x 8192                          49 | 70     53 | 71     56 | 72     80 | 76     91 | 80
+//     16 x 8192                         107 | 198   151 | 198   168 | 199   227 | 207   267 | 208
+//     64 x 1024                         95 | 105    139 | 107   219 | 109   381 | 117   524 | 120
+//     1 x 4096                          19 | 34     22 | 35     24 | 36     26 | 38     27 | 40
+//   4 KV heads, H = 28, 16 x 8192       78 | 115    92 | 118    120 | 131   211 | 153   250 | 154
+//   4 KV heads, H = 16, D = 256
+//     1 x 131072                        125 | 253   217 | 254   423 | 258   625 | 297   924 | 298
+//     4 x 8192                          52 | 83     74 | 86     129 | 88    187 | 105   269 | 105
+//     1 x 4096                          21 | 39     25 | 41     32 | 44     44 | 44     56 | 44
+bool as_tree(const rkv_dense_params *p, int H, int n)
+{
+    const long long R = (long long)n * (H / p->N);
+    if (n > kMaxDraft) return false;
+    if (44 * R >= p->T && (long long)p->S * n * H >= 4096) return false;
+    return p->D < 256 || R <= 64 || (long long)p->S * p->T < 8192;
+}
 
 size_t piece_rows_bytes(const rkv_dense_params *p)
 {
@@ -222,7 +240,7 @@ rkv_status rkv_prompt_attention(const rkv_head_params *p, int32_t S, const int32
     const PromptShape x = packed_shape(p, S, rows, start);
     if (!workspace || workspace_bytes < prompt_workspace_bytes(x)) return RKV_ERR_WORKSPACE;
     if ((uintptr_t)workspace & 255u) return RKV_ERR_ALIGNMENT;
-    const PromptTensors t{q, k, v, out, q_stride, k_stride, v_stride, out_stride, rows};
+    const PromptTensors t{q, k, v, out, q_stride, k_stride, v_stride, out_stride, p->D, p->D};
     return done(launch_prompt_attention(x, t, workspace, dev_status, (cudaStream_t)stream));
 }
 
@@ -231,7 +249,7 @@ rkv_status rkv_chunk_attention_workspace(const rkv_dense_params *p, int32_t H, i
     rkv_status st = check_piece(p, H, n);
     if (st != RKV_OK) return st;
     if (!bytes) return RKV_ERR_INVALID_ARG;
-    if (as_tree(n)) *bytes = align256((size_t)p->S * n * 4) + dense_attention_workspace_bytes(geom(p), H, n);
+    if (as_tree(p, H, n)) *bytes = align256((size_t)p->S * n * 4) + dense_attention_workspace_bytes(geom(p), H, n);
     else *bytes = piece_rows_bytes(p) + prompt_workspace_bytes(piece_shape(p, H, n, nullptr, nullptr));
     return RKV_OK;
 }
@@ -251,19 +269,20 @@ rkv_status rkv_chunk_attention(const rkv_dense_params *p, int32_t H, const void 
     if ((uintptr_t)workspace & 255u) return RKV_ERR_ALIGNMENT;
     cudaStream_t s = (cudaStream_t)stream;
     uint8_t *ws = (uint8_t *)workspace;
-    if (as_tree(n)) {
+    if (as_tree(p, H, n)) {
         int32_t *parent = (int32_t *)ws;
         cudaError_t e = launch_chunk_parents(g, len, n, n_new, parent, dev_status, s);
         if (e != cudaSuccess) return RKV_ERR_CUDA;
         return done(launch_dense_attention(g, H, q, n, parent, kv, cache, len, nullptr, 1, 0, out, RKV_BF16,
                                            ws + align256((size_t)p->S * n * 4), dev_status, s, true));
     }
-    cudaError_t e = launch_dense_rows(g, cache, len, kv, n, n_new, ws, dev_status, s);
-    if (e != cudaSuccess) return RKV_ERR_CUDA;
     const PromptShape x = piece_shape(p, H, n, len, n_new);
-    const int64_t row = 2LL * p->N * p->D, qrow = (int64_t)H * p->D;
-    const PromptTensors t{q, ws, ws + (size_t)p->N * p->D * 2, out, qrow, row, row, qrow, (long long)p->S * p->T};
-    return done(launch_prompt_attention(x, t, ws + piece_rows_bytes(p), dev_status, s));
+    uint8_t *rest = ws + piece_rows_bytes(p);
+    const cudaError_t e = launch_dense_rows(g, cache, len, kv, n, n_new, ws, prompt_plan_args(x, rest, dev_status), dev_status, s);
+    if (e != cudaSuccess) return RKV_ERR_CUDA;
+    const int64_t head = 2LL * p->T * p->D, qrow = (int64_t)H * p->D;
+    const PromptTensors t{q, ws, ws + (size_t)p->T * p->D * 2, out, qrow, p->D, p->D, qrow, head, head * p->N};
+    return done(launch_prompt_attention(x, t, rest, dev_status, s));
 }
 
 }  // extern "C"

@@ -19,12 +19,13 @@
 //                P goes back to tensor memory, over the scores, as the first operand of P V
 // D = 256 has one row tile (its outputs take 256 columns) and two buffers of scores instead.
 //
-// Items come from k_prompt_plan, one CTA that reads the lengths: sorted so that the last ones to
-// start are short, and split over the keys where there are few; the parts of a split item leave
-// {m, l, out} in fp32, which k_prompt_join puts together.
+// Items come from one CTA that reads the lengths (rkv_prompt_plan.cuh), split over the keys where there
+// are few; the parts of a split item leave {m, l, out} in fp32, which k_prompt_join puts together.
+// A few sequences whose items are one round, and one sequence whose items are many, need neither: there
+// the producers work out their items by themselves, from the last tile to the first.
 // All waits are bounded: RKV_ERR_DEVICE_TIMEOUT is set, the copies and products under way are
 // waited for, and the outputs are incomplete.
-#include "rkv_prompt.cuh"
+#include "rkv_prompt_plan.cuh"
 #include "umma.cuh"
 
 #include <math.h>
@@ -32,227 +33,13 @@
 namespace rkv {
 namespace {
 
-// ---------------------------------------------------------------- items
-struct PromptItem {
-    int q_row, tokens;      // first row (token) of the item and its tokens
-    int k_row;              // row of K and V that holds key 0
-    int first;              // the key that the first token sees last
-    int kt0, kt1;           // key tiles
-    int slot;               // partial of this part for KV head 0; below 0: the item is whole (-1 - its
-                            // sequence's items, where items go by sequence)
-    int seq;                // index of its sequence's first item, where items go by sequence
-};
-static_assert(sizeof(PromptItem) == 32, "two 16-byte loads");
-struct PromptJoin { int q_row, tokens, slot, parts; };
-struct PromptHead {
-    int items;              // for each KV head
-    int by_seq;             // items of a sequence in a row for each KV head (else KV heads innermost)
-    int next;               // the item to take next
-    int joins, slots;
-    int pad[3];
-};
-
-constexpr int kCtas = 152;
-constexpr int kSlots = 4 * kCtas;            // partials at most
 constexpr int kPlanThreads = 1024;
-// K and V that stay in L2 beside what else is read: up to here items go by cost alone
-constexpr long long kInL2 = 48LL << 20;
-constexpr int kItemCost = 3;                 // of an item beside its keys, in key tiles of 128
-
-struct PlanArgs {
-    const int32_t *start;                    // packed prompts
-    const int32_t *len, *n_new;              // pieces: [S], n rows each at most
-    int S, rows, n, T;
-    int N, tile_tokens, tok, key_bytes, max_slots, max_items, max_joins, ctas;
-    PromptHead *head;
-    PromptItem *items;
-    PromptJoin *joins;
-    int32_t *status;
-};
-
-struct Text { int q_row, n, before, k_row; };
-__device__ __forceinline__ Text text_of(const PlanArgs &a, int s)
-{
-    if (a.start) {
-        const int b = __ldg(a.start + s), e = __ldg(a.start + s + 1);
-        if (b < 0 || e < b || e > a.rows) {
-            set_status(a.status, RKV_ERR_INDEX);
-            return Text{-1, 0, 0, 0};
-        }
-        return Text{b, e - b, 0, b};
-    }
-    const int before = __ldg(a.len + s), n = a.n_new ? __ldg(a.n_new + s) : a.n;
-    if (before < 0 || n < 0 || n > a.n || before > a.T - n) {
-        set_status(a.status, RKV_ERR_INDEX);
-        return Text{0, 0, 0, 0};
-    }
-    return Text{s * a.n, n, before, s * a.T};
-}
-
-__device__ __forceinline__ int block_scan(int v, int *warps, int &total)   // exclusive; warps: [32] shared
-{
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int x = lane_scan(v);
-    __syncthreads();
-    if (lane == 31) warps[w] = x;
-    __syncthreads();
-    if (w == 0) warps[lane] = lane_scan(warps[lane]);
-    __syncthreads();
-    total = warps[31];
-    return x - v + (w ? warps[w - 1] : 0);
-}
-
-constexpr int kCands = 32;
-constexpr int kFull = 256, kBuckets = 2 * kFull;   // parts of full length by their place, others by cost
 
 __global__ void __launch_bounds__(kPlanThreads)
 k_prompt_plan(const PlanArgs a)
 {
-    __shared__ int warps[32], first_tile[kPlanThreads + 1], bucket[kBuckets];
-    __shared__ Text texts[kPlanThreads];
-    __shared__ int cand[kCands];
-    __shared__ long long sum_cost, sum_keys;
-    __shared__ int sum_tiles, max_cost, part_len, slots, n_items, n_joins, wrong;
-    const int tid = threadIdx.x;
-    if (tid == 0) {
-        sum_cost = sum_keys = 0;
-        sum_tiles = max_cost = slots = n_items = n_joins = wrong = 0;
-    }
-    if (tid < kCands) cand[tid] = 0;
-    for (int i = tid; i < kBuckets; i += kPlanThreads) bucket[i] = 0;
-    __syncthreads();
-
-    // Calls f(x, text, tile, cost, tiles of that text) for every tile x of 1024 texts at a time
-    auto each = [&](auto f) {
-        int before = 0;
-        for (int s0 = 0; s0 < a.S; s0 += kPlanThreads) {
-            const int s = s0 + tid;
-            Text t{0, 0, 0, 0};
-            if (s < a.S) t = text_of(a, s);
-            const int tiles = (t.n + a.tile_tokens - 1) / a.tile_tokens;
-            int total;
-            const int at = block_scan(tiles, warps, total);
-            texts[tid] = t;
-            first_tile[tid] = at;
-            if (tid == 0) first_tile[kPlanThreads] = total;
-            __syncthreads();
-            for (int x = tid; x < total; x += kPlanThreads) {
-                int lo = 0, hi = kPlanThreads;             // the last text that begins at or before x
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (first_tile[mid] <= x) lo = mid;
-                    else hi = mid;
-                }
-                const Text &w = texts[lo];
-                const int tile = x - first_tile[lo], last = min(w.n, (tile + 1) * a.tile_tokens);
-                f(before + x, w, tile, (w.before + last + a.tok - 1) / a.tok, first_tile[lo + 1] - first_tile[lo],
-                  before + first_tile[lo]);
-            }
-            before += total;
-            __syncthreads();
-        }
-    };
-    {
-        long long keys = 0;
-        for (int s = tid; s < a.S; s += kPlanThreads) {
-            const Text t = text_of(a, s);
-            if (t.n > 0) keys += t.before + t.n;
-            if (t.q_row < 0) wrong = 1;
-        }
-        long long cost = 0;
-        int n = 0, most = 0;
-        each([&](int, const Text &, int, int c, int, int) {
-            cost += c;
-            ++n;
-            most = max(most, c);
-        });
-        atomicAdd((unsigned long long *)&sum_keys, (unsigned long long)keys);
-        atomicAdd((unsigned long long *)&sum_cost, (unsigned long long)cost);
-        atomicAdd(&sum_tiles, n);
-        atomicMax(&max_cost, most);
-        __syncthreads();
-    }
-    // Packed rows that do not ascend may be more than the workspace is for: nothing attends
-    if (wrong) {
-        if (tid == 0) *a.head = PromptHead{0, 0, a.ctas, 0, 0, {0, 0, 0}};
-        return;
-    }
-    // Few items: parts of L key tiles each, L from max_cost / 1, / 2 .. so that the time, taken as
-    // (all costs) / CTAs + what the last round of parts leaves idle, is least
-    const bool few = (long long)sum_tiles * a.N < 8 * kCtas && sum_tiles > 0;
-    const int over = kItemCost * 128 / a.tok;
-    auto len_of = [&](int k) { return (max_cost + k) / (k + 1); };
-    auto parts_of = [](int c, int L) { return c <= L + L / 4 ? 1 : (c - L / 4 + L - 1) / L; };
-    if (few) {
-        each([&](int, const Text &, int, int c, int, int) {
-            for (int k = 0; k < kCands; ++k) atomicAdd(&cand[k], parts_of(c, len_of(k)));
-        });
-        if (tid < 32) {
-            const int L = len_of(tid);
-            const float P = (float)cand[tid] * a.N, W = (float)sum_cost * a.N + over * P * (tid ? 1.7f : 1.0f);
-            float t = W / kCtas + (ceilf(P / kCtas) - P / kCtas) * (L + over);
-            if (tid && (cand[tid] * a.N > a.max_slots || L < 4 * 128 / a.tok)) t = INFINITY;
-            int best = tid;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                const float y = __shfl_xor_sync(0xffffffffu, t, o);
-                const int b = __shfl_xor_sync(0xffffffffu, best, o);
-                if (y < t || (y == t && b < best)) { t = y; best = b; }
-            }
-            if (tid == 0) part_len = best ? len_of(best) : max_cost;
-        }
-        __syncthreads();
-    } else {
-        if (tid == 0) part_len = max(max_cost, 1);
-        __syncthreads();
-    }
-    const int L = part_len;
-    const bool split = few && L < max_cost;
-    const bool by_seq = !split && sum_keys * a.key_bytes > kInL2;
-    if (by_seq) {
-        each([&](int x, const Text &w, int tile, int c, int tiles, int seq) {
-            if (seq + tiles > a.max_items) return;         // lengths that changed under the call
-            a.items[seq + tiles - 1 - tile] = PromptItem{w.q_row + tile * a.tile_tokens, min(a.tile_tokens, w.n - tile * a.tile_tokens),
-                                                         w.k_row, w.before + tile * a.tile_tokens, 0, c, -1 - tiles, seq};
-        });
-        if (tid == 0) n_items = sum_tiles;
-    } else {
-        auto bucket_of = [&](int part, int c) {
-            return split && c >= L ? min(part, kFull - 1) : kFull + (kFull - 1) - (int)((long long)min(c, L) * (kFull - 1) / L);
-        };
-        each([&](int, const Text &, int, int c, int, int) {
-            const int parts = split ? parts_of(c, L) : 1;
-            for (int i = 0; i < parts; ++i) atomicAdd(&bucket[bucket_of(i, i + 1 < parts ? L : c - i * L)], 1);
-        });
-        __syncthreads();
-        int total;
-        const int have = tid < kBuckets ? bucket[tid] : 0;
-        const int at = block_scan(have, warps, total);
-        if (tid < kBuckets) bucket[tid] = at;
-        if (tid == 0) n_items = total;
-        __syncthreads();
-        each([&](int, const Text &w, int tile, int c, int, int) {
-            const int parts = split ? parts_of(c, L) : 1;
-            const int q_row = w.q_row + tile * a.tile_tokens, tokens = min(a.tile_tokens, w.n - tile * a.tile_tokens);
-            int slot = -1;
-            if (parts > 1) {
-                const int j = atomicAdd(&n_joins, 1);
-                slot = atomicAdd(&slots, parts * a.N);
-                if (j >= a.max_joins || slot + parts * a.N > a.max_slots) return;
-                a.joins[j] = PromptJoin{q_row, tokens, slot, parts};
-            }
-            for (int i = 0; i < parts; ++i) {
-                const int to = i + 1 < parts ? (i + 1) * L : c;
-                const int at = atomicAdd(&bucket[bucket_of(i, to - i * L)], 1);
-                if (at >= a.max_items) return;
-                a.items[at] = PromptItem{q_row, tokens, w.k_row, w.before + tile * a.tile_tokens, i * L, to,
-                               parts > 1 ? slot + i * a.N : -1, 0};
-            }
-        });
-    }
-    __syncthreads();
-    if (tid == 0)
-        *a.head = PromptHead{min(n_items, a.max_items), by_seq, a.ctas, min(n_joins, a.max_joins), slots, {0, 0, 0}};
+    __shared__ PlanShared<kPlanThreads> z;
+    prompt_plan<kPlanThreads>(a, z);
 }
 
 // ---------------------------------------------------------------- attention
@@ -265,6 +52,14 @@ template <int R>
 __device__ __forceinline__ void regs_up()
 {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *m, uint64_t *bar, int x, int y, int z, int w)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(um::smem_u32(dst)),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(um::smem_u32(bar))
+        : "memory");
 }
 __device__ __forceinline__ float ex2(float x)
 {
@@ -382,7 +177,9 @@ struct FlashArgs {
     float *part;                    // [slots][128 kHalves][D]
     float2 *ml;                     // [slots][128 kHalves]
     int32_t *status;
-    int N, G;
+    const int32_t *start;           // packed prompts whose items the producers work out; else NULL
+    int S, rows;
+    int N, G, packed;
     float scale_log2;
 };
 
@@ -501,14 +298,41 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
     };
 
     if (warp == 0) {
-        const int items = *(volatile int *)&a.head->items, by_seq = *(volatile int *)&a.head->by_seq;
-        const long long all = (long long)items * N;
-        int idx = blockIdx.x;
         uint32_t loads = 0, uses[2] = {0, 0}, cleans = 0;
+        const int item_tok = kHalves * tile_tok;
+        // items worked out here: lane s holds sequence s
+        int begin = 0, n_tok = 0, upto = 0, by_seq = 0;
+        long long all;
+        if (a.start) {
+            if (lane < a.S) {
+                begin = __ldg(a.start + lane);
+                n_tok = __ldg(a.start + lane + 1) - begin;
+            }
+            const bool wrong = begin < 0 || n_tok < 0 || begin > a.rows - n_tok;
+            upto = lane_scan((n_tok + item_tok - 1) / item_tok);
+            all = (long long)__shfl_sync(0xffffffffu, upto, 31) * N;
+            if (__any_sync(0xffffffffu, wrong)) {
+                if (lane == 0) set_status(a.status, RKV_ERR_INDEX);
+                all = 0;
+            }
+        } else {
+            all = (long long)*(volatile int *)&a.head->items * N;
+            by_seq = *(volatile int *)&a.head->by_seq;
+        }
         auto fetch = [&](long long at) -> FlashWork {
             FlashWork w{};
             if (at >= all) return w;
             int e = (int)(at / N), n = (int)(at % N);
+            if (a.start) {
+                e = (int)(all / N) - 1 - e;
+                const int s = __ffs(__ballot_sync(0xffffffffu, e < upto)) - 1;
+                const int b = __shfl_sync(0xffffffffu, begin, s), m = __shfl_sync(0xffffffffu, n_tok, s);
+                const int t0 = (e - __shfl_sync(0xffffffffu, upto - (n_tok + item_tok - 1) / item_tok, s)) * item_tok;
+                const int tokens = min(item_tok, m - t0);
+                w.it = PromptItem{b + t0, tokens, b, t0, 0, (t0 + tokens + kTok - 1) / kTok, -1, 0};
+                w.n = n;
+                return w;
+            }
             if (by_seq) {
                 // this sequence's items in a row, once for each KV head: item at / N is one of them
                 const int4 y = __ldcg((const int4 *)(a.items + e) + 1);
@@ -522,10 +346,12 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
             w.n = n;
             return w;
         };
-        FlashWork w = fetch(idx);
+        FlashWork w = fetch(blockIdx.x);
         for (int i = 0;; ++i) {
             int next = 0;
-            if (lane == 0 && w.it.tokens > 0) next = atomicAdd(&a.head->next, 1);
+            // the first item is the CTA's own; the others by a counter, or to and fro
+            if (a.start) next = (i + 1) * gridDim.x + (i & 1 ? blockIdx.x : gridDim.x - 1 - blockIdx.x);
+            else if (lane == 0 && w.it.tokens > 0) next = atomicAdd(&a.head->next, 1);
             if (!wait(w_empty + (i & 3), (uint32_t)(i >> 2) ^ 1u)) break;
             if (lane == 0) {
                 works[i & 3] = w;
@@ -563,8 +389,8 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                     um::mbar_arrive_expect_tx(kv_full + st, C::kTile);
 #pragma unroll
                     for (int k = 0; k < D / 64; ++k)
-                        um::tma_load_3d(ring + st * C::kTile + k * kTok * 128, m, kv_full + st, 64 * k, w.n,
-                                        w.it.k_row + kt * kTok);
+                        tma_load_4d(ring + st * C::kTile + k * kTok * 128, m, kv_full + st, 64 * k,
+                                    (a.packed ? w.it.k_row : 0) + kt * kTok, w.n, a.packed ? 0 : w.it.k_row);
                     if (looked) um::mbar_arrive(v_issued + (cleans & 3));
                 }
                 cleans += looked;
@@ -971,38 +797,59 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 // What a call's sizes say about its items, and where its scratch lies.
 struct Layout {
     int tile_tokens, tok, max_slots, ctas;
+    bool direct;                               // the producers work out their items
     long long max_items, max_joins;            // for each KV head
     size_t items, joins, ml, part, total;
 };
 Layout layout_of(const PromptShape &p)
 {
-    Layout y;
+    Layout y{};
     const int halves = p.D == 256 ? 1 : 2, rows = 128 * halves;
     y.tile_tokens = halves * (128 / (p.H / p.N));
     y.tok = p.D == 128 ? 128 : 64;
     const long long tiles = p.start ? p.rows / y.tile_tokens + (long long)p.S
                                     : (long long)p.S * ((p.n + y.tile_tokens - 1) / y.tile_tokens);
-    // no part is shorter than 4 x 128 keys
     const long long keys = p.start ? p.rows : p.T;
-    y.max_slots = (int)min((long long)kSlots, tiles * p.N * (keys / (4 * 128)));
+    // no part is shorter than 4 x 128 keys
+    y.max_slots = (int)min((long long)kPromptSlots, tiles * p.N * (keys / (4 * 128)));
+    if (p.start) {
+        // one round of short items, or one prompt: as good as without parts where the longest item is no
+        // more than its share of all of them, or short
+        const double all = 0.5 * (double)(p.rows / (double)y.tile_tokens) * (p.rows / 128.0 + 2 * kItemCost) * p.N / kPromptCtas;
+        const double longest = p.rows / 128.0 + kItemCost;
+        y.direct = p.S == 1 ? longest <= 16 + kItemCost || longest <= 1.1 * all
+                            : p.S <= 32 && tiles * p.N <= kPromptCtas && longest <= 16 + kItemCost;
+    }
+    if (y.direct) y.max_slots = 0;
+    if (y.max_slots < 2 * p.N) y.max_slots = 0;
     y.max_items = tiles + y.max_slots / p.N;
-    y.ctas = (int)min((long long)kCtas, y.max_items * p.N);
-    y.items = 256;
     y.max_joins = y.max_slots ? tiles : 0;
-    y.joins = y.items + align256((size_t)y.max_items * sizeof(PromptItem));
+    y.ctas = (int)min((long long)kPromptCtas, y.max_items * p.N);
+    y.items = 256;
+    y.joins = y.items + (y.direct ? 0 : align256((size_t)y.max_items * sizeof(PromptItem)));
     y.ml = y.joins + align256((size_t)y.max_joins * sizeof(PromptJoin));
     y.part = y.ml + align256((size_t)y.max_slots * rows * sizeof(float2));
     y.total = y.part + (size_t)y.max_slots * rows * p.D * sizeof(float);
     return y;
 }
 
-// Rows of G heads of one KV head (q) or one head (k, v), 64 channels of them
-bool make_rows_map(CUtensorMap *m, const void *base, int D, int heads, long long rows, int64_t stride, int box_heads, int box_rows)
+// G heads of some rows of Q, 64 channels of them
+bool make_q_map(CUtensorMap *m, const PromptShape &p, const PromptTensors &t)
 {
-    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)heads, (uint64_t)rows};
-    const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)stride * 2};
-    const uint32_t box[3] = {64, (uint32_t)box_heads, (uint32_t)box_rows};
-    return make_map_strided(m, base, dims, strides, box);
+    const int G = p.H / p.N;
+    const uint64_t dims[3] = {(uint64_t)p.D, (uint64_t)p.H, (uint64_t)p.rows};
+    const uint64_t strides[2] = {(uint64_t)p.D * 2, (uint64_t)t.q_stride * 2};
+    const uint32_t box[3] = {64, (uint32_t)G, (uint32_t)(128 / G)};
+    return make_map_strided(m, t.q, 3, dims, strides, box);
+}
+// One head of some rows of K or V of a sequence (packed: of all of them), 64 channels of them
+bool make_kv_map(CUtensorMap *m, const PromptShape &p, const void *base, int64_t row, int64_t head, int64_t seq, int tok)
+{
+    const bool packed = p.start != nullptr;
+    const uint64_t dims[4] = {(uint64_t)p.D, (uint64_t)(packed ? p.rows : p.T), (uint64_t)p.N, (uint64_t)(packed ? 1 : p.S)};
+    const uint64_t strides[3] = {(uint64_t)row * 2, (uint64_t)head * 2, (uint64_t)seq * 2};
+    const uint32_t box[4] = {64, (uint32_t)tok, 1, 1};
+    return make_map_strided(m, base, 4, dims, strides, box);
 }
 
 template <int D>
@@ -1011,9 +858,8 @@ cudaError_t run(const PromptShape &p, const Layout &y, const PromptTensors &t, u
     using C = FlashCfg<D>;
     const int G = p.H / p.N;
     FlashMaps maps;
-    if (!make_rows_map(&maps.q, t.q, D, p.H, p.rows, t.q_stride, G, 128 / G) ||
-        !make_rows_map(&maps.k, t.k, D, p.N, t.kv_rows, t.k_stride, 1, C::kTok) ||
-        !make_rows_map(&maps.v, t.v, D, p.N, t.kv_rows, t.v_stride, 1, C::kTok))
+    if (!make_q_map(&maps.q, p, t) || !make_kv_map(&maps.k, p, t.k, t.k_stride, t.kv_head, t.kv_seq, C::kTok) ||
+        !make_kv_map(&maps.v, p, t.v, t.v_stride, t.kv_head, t.kv_seq, C::kTok))
         return cudaErrorInvalidValue;
     static PerDevice<int> setup;
     int unused = 0;
@@ -1029,6 +875,10 @@ cudaError_t run(const PromptShape &p, const Layout &y, const PromptTensors &t, u
     a.part = (float *)(ws + y.part);
     a.ml = (float2 *)(ws + y.ml);
     a.status = status;
+    a.start = y.direct ? p.start : nullptr;
+    a.S = p.S;
+    a.rows = (int)p.rows;
+    a.packed = p.start != nullptr;
     a.N = p.N;
     a.G = G;
     a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
@@ -1039,7 +889,7 @@ cudaError_t run(const PromptShape &p, const Layout &y, const PromptTensors &t, u
     }
     if (y.max_slots) {
         ProfScope prof("prompt_attention_join", s);
-        k_prompt_join<D><<<8 * kCtas, 256, 0, s>>>(a, (const PromptJoin *)(ws + y.joins));
+        k_prompt_join<D><<<8 * kPromptCtas, 256, 0, s>>>(a, (const PromptJoin *)(ws + y.joins));
         e = cudaGetLastError();
     }
     return e;
@@ -1049,8 +899,7 @@ cudaError_t run(const PromptShape &p, const Layout &y, const PromptTensors &t, u
 
 size_t prompt_workspace_bytes(const PromptShape &p) { return layout_of(p).total; }
 
-cudaError_t launch_prompt_attention(const PromptShape &p, const PromptTensors &t, void *workspace, int32_t *status,
-                                    cudaStream_t s)
+PlanArgs prompt_plan_args(const PromptShape &p, void *workspace, int32_t *status)
 {
     const Layout y = layout_of(p);
     uint8_t *ws = (uint8_t *)workspace;
@@ -1074,9 +923,18 @@ cudaError_t launch_prompt_attention(const PromptShape &p, const PromptTensors &t
     a.items = (PromptItem *)(ws + y.items);
     a.joins = (PromptJoin *)(ws + y.joins);
     a.status = status;
-    {
+    return a;
+}
+
+cudaError_t launch_prompt_attention(const PromptShape &p, const PromptTensors &t, void *workspace, int32_t *status,
+                                    cudaStream_t s)
+{
+    const Layout y = layout_of(p);
+    uint8_t *ws = (uint8_t *)workspace;
+    // pieces' items come from k_dense_rows
+    if (p.start && !y.direct) {
         ProfScope prof("prompt_plan", s);
-        k_prompt_plan<<<1, kPlanThreads, 0, s>>>(a);
+        k_prompt_plan<<<1, kPlanThreads, 0, s>>>(prompt_plan_args(p, workspace, status));
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }

@@ -831,17 +831,20 @@ bool make_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows,
     return r == CUDA_SUCCESS;
 }
 
-// bf16 of three dimensions, byte strides of the outer two, a box 64 wide, 128-byte swizzle.
-bool make_map_strided(CUtensorMap *m, const void *base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
-                      const uint32_t (&box)[3])
+// bf16 of `rank` dimensions, byte strides of all but the innermost, a box 64 wide, 128-byte swizzle.
+bool make_map_strided(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides, const uint32_t *box)
 {
     auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
-    const cuuint64_t st[2] = {strides[0], strides[1]};
-    const cuuint32_t b[3] = {box[0], box[1], box[2]};
-    const cuuint32_t es[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), d, st, b, es,
+    if (!fn || rank < 2 || rank > 5) return false;
+    cuuint64_t d[5], st[5];
+    cuuint32_t b[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        es[i] = 1;
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), d, st, b, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

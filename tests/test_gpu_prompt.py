@@ -308,7 +308,7 @@ def check_piece(c, H, q, kv, lens, new, out):
 @pytest.mark.parametrize("H,N,D", [(8, 2, 128), (7, 1, 64), (3, 3, 128), (8, 1, 256)])
 @pytest.mark.parametrize("n", [1, 33, 64, 65, 200])
 def test_pieces(bits, H, N, D, n):
-    # n up to 64 goes as drafted trees do
+    # short pieces go as drafted trees do
     gen = torch.Generator(device="cuda").manual_seed(n + D)
     lens = [0, 1, 31, 32, 33, 64, 500, 777]
     new = [n, max(1, n - 1), n, 0, n // 2, 1, n, max(1, n - 7)]
