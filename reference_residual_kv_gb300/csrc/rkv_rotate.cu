@@ -13,7 +13,9 @@
 namespace rkv {
 namespace {
 
-constexpr int kRotateThreads = 256;
+constexpr int kRotateThreads = 128;
+template <typename T>
+constexpr int kMostPasses = sizeof(T) == 2 ? 4 : 2;     // of a warp, their loads in flight together
 
 template <typename T>
 struct Run8;                                   // 8 values as they lie in memory
@@ -58,123 +60,121 @@ struct Run8<float> {
     }
 };
 
-// `parts` warps share a row's passes (512/D heads each).
+// How a row's heads are dealt out: passes of 512/D heads each, `per` of them to a warp, queries and
+// keys apart.
+struct RotatePasses {
+    int q_passes, k_passes, per, q_units, units;         // units: of a row
+};
+
 template <typename T, int D, bool PAIRS>
 __global__ void __launch_bounds__(kRotateThreads)
-k_qk_rotate(const RotateArgs a, const __grid_constant__ rkv_rope rope, int parts)
+k_qk_rotate(const RotateArgs a, const __grid_constant__ rkv_rope rope, const RotatePasses z)
 {
-    constexpr int kLanes = D / 16, kHeads = 32 / kLanes, kOwn = 8 / kHeads > 0 ? 8 / kHeads : 1;
-    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;         // passes with their loads in flight together
+    constexpr int kLanes = D / 16, kHeads = 32 / kLanes, kOwn = 8 / kHeads;
+    constexpr int kPer = kMostPasses<T>;
     const int lane = threadIdx.x & 31, j = lane % kLanes, hl = lane / kLanes;
-    const int R = rope.R, rl = R / 16;
-    const bool turns = j < rl;
+    const long long u = (long long)blockIdx.x * (kRotateThreads / 32) + (threadIdx.x >> 5);
+    const int row = (int)(u / z.units), part = (int)(u % z.units);
+    if (row >= a.rows) return;
+    const bool is_q = part < z.q_units;
+    const int heads = is_q ? a.H : a.N, h0 = (is_q ? part : part - z.q_units) * z.per * kHeads + hl;
+    const int n = min(z.per, (is_q ? z.q_passes : z.k_passes) - (is_q ? part : part - z.q_units) * z.per);   // passes of this warp
+    const T *src = is_q ? (const T *)a.q + row * a.q_stride : (const T *)a.k + row * a.k_stride;
+    T *dst = is_q ? (T *)a.q_out + row * a.q_out_stride : (T *)a.k_out + row * a.k_out_stride;
+    const T *weight = (const T *)(is_q ? a.q_weight : a.k_weight);
+    const int R = rope.R;
+    const bool turns = j < R / 16;
     // this lane's two runs of channels
     const int c0 = PAIRS || !turns ? 16 * j : 8 * j, c1 = PAIRS || !turns ? 16 * j + 8 : 8 * j + R / 2;
-    // the pairs whose angles this lane works out: pair 8 j + kOwn hl + o (D = 64: all of 8 lanes one)
-    uint64_t turn[kOwn];
+    const int pos = __ldg(a.pos + row);
+    Run8<T> x0[kPer], x1[kPer], w0, w1;
 #pragma unroll
-    for (int o = 0; o < kOwn; ++o) turn[o] = turns ? rope.turn[8 * j + (kOwn * hl + o) % 8] : 0;
-    const int q_passes = a.q ? (a.H + kHeads - 1) / kHeads : 0, k_passes = a.k ? (a.N + kHeads - 1) / kHeads : 0;
-    const int passes = q_passes + k_passes, per = (passes + parts - 1) / parts;
-    const long long warps = (long long)gridDim.x * (kRotateThreads / 32);
-    const long long units = (long long)a.rows * parts;
-    for (long long u = (long long)blockIdx.x * (kRotateThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
-        const int row = (int)(u / parts), p0 = (int)(u % parts) * per, p1 = min(passes, p0 + per);
-        const int pos = __ldg(a.pos + row);
-        if (pos < 0) {
-            if (pos < -1) set_status(a.status, RKV_ERR_INDEX);
-            continue;
+    for (int i = 0; i < kPer; ++i)
+        if (i < n && h0 + i * kHeads < heads) {
+            const T *p = src + (size_t)(h0 + i * kHeads) * D;
+            x0[i].load(p + c0);
+            x1[i].load(p + c1);
         }
-        Run8<T> x0[kAhead], x1[kAhead];
-        auto src = [&](int p, int &h, bool &is_q) -> const T * {
-            is_q = p < q_passes;
-            h = (is_q ? p : p - q_passes) * kHeads + hl;
-            if (p >= p1 || h >= (is_q ? a.H : a.N)) return nullptr;
-            return is_q ? (const T *)a.q + row * a.q_stride + h * D : (const T *)a.k + row * a.k_stride + h * D;
-        };
-        auto fetch = [&](int p) {
+    if (weight) {
+        w0.load(weight + c0);
+        w1.load(weight + c1);
+    }
+    if (pos < 0) {
+        if (pos < -1) set_status(a.status, RKV_ERR_INDEX);
+        return;
+    }
+    // cosines and sines of pairs 8 j .. 8 j + 7: kOwn of them worked out here, the others by the lanes
+    // that hold the same channels of other heads
+    float co[8], si[8];
+    {
+        float oc[kOwn], os[kOwn];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                int h;
-                bool is_q;
-                const T *s = src(p + i, h, is_q);
-                if (s) {
-                    x0[i].load(s + c0);
-                    x1[i].load(s + c1);
-                }
-            }
-        };
-        fetch(p0);
-        float co[8], si[8];
-        {
-            float oc[kOwn], os[kOwn];
-#pragma unroll
-            for (int o = 0; o < kOwn; ++o) {
-                const int frac = (int)(uint32_t)((turn[o] * (uint64_t)pos) >> 32);
-                sincospif((float)frac * 0x1p-31f, &os[o], &oc[o]);
+        for (int o = 0; o < kOwn; ++o) {
+            const uint64_t turn = turns ? rope.turn[8 * j + kOwn * hl + o] : 0;
+            const int frac = (int)(uint32_t)((turn * (uint64_t)pos) >> 32);
+            sincospif((float)frac * 0x1p-31f, &os[o], &oc[o]);
+            if (turns) {
                 oc[o] *= rope.gain;
                 os[o] *= rope.gain;
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int from = (e / kOwn) % kHeads * kLanes + j;
-                co[e] = __shfl_sync(0xffffffffu, oc[e % kOwn], from);
-                si[e] = __shfl_sync(0xffffffffu, os[e % kOwn], from);
-            }
         }
-        for (int p = p0; p < p1; p += kAhead) {
-            if (p > p0) fetch(p);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                int h;
-                bool is_q;
-                const bool there = src(p + i, h, is_q) != nullptr;
-                if (p + i >= p1) break;                    // the same for the whole warp
-                const T *w = (const T *)(is_q ? a.q_weight : a.k_weight);
-                float v0[8], v1[8];
-                x0[i].get(v0);
-                x1[i].get(v1);
-                if (w) {
-                    float ss = 0.0f;
+        for (int e = 0; e < 8; ++e) {
+            const int from = e / kOwn * kLanes + j;
+            co[e] = __shfl_sync(0xffffffffu, oc[e % kOwn], from);
+            si[e] = __shfl_sync(0xffffffffu, os[e % kOwn], from);
+        }
+    }
+    // The weights go with the cosines and sines: pair e's first channel becomes x_a ca - x_b sb, its
+    // second one x_a sa + x_b cb
+    float ca[8], cb[8], sa[8], sb[8];
+    auto first = [](auto &v0, auto &v1, int e) -> float & { return PAIRS ? (e < 4 ? v0[2 * e & 7] : v1[2 * e & 7]) : v0[e]; };
+    auto second = [](auto &v0, auto &v1, int e) -> float & { return PAIRS ? (e < 4 ? v0[2 * e + 1 & 7] : v1[2 * e + 1 & 7]) : v1[e]; };
+    if (weight) {
+        float f0[8], f1[8];
+        w0.get(f0);
+        w1.get(f1);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(v0[e], v0[e], fmaf(v1[e], v1[e], ss));
+        for (int e = 0; e < 8; ++e) {
+            const float wa = first(f0, f1, e), wb = second(f0, f1, e);
+            ca[e] = co[e] * wa;
+            sa[e] = si[e] * wa;
+            cb[e] = co[e] * wb;
+            sb[e] = si[e] * wb;
+        }
+    } else {
 #pragma unroll
-                    for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
-                    Run8<T> w0, w1;
-                    w0.load(w + c0);
-                    w1.load(w + c1);
-                    float f0[8], f1[8];
-                    w0.get(f0);
-                    w1.get(f1);
+        for (int e = 0; e < 8; ++e) {
+            ca[e] = cb[e] = co[e];
+            sa[e] = sb[e] = si[e];
+        }
+    }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        v0[e] = v0[e] * inv * f0[e];
-                        v1[e] = v1[e] * inv * f1[e];
-                    }
-                }
-                if (turns) {
+    for (int i = 0; i < kPer; ++i) {
+        if (i >= n) break;                                 // the same for the whole warp
+        float v0[8], v1[8];
+        x0[i].get(v0);
+        x1[i].get(v1);
+        float inv = 1.0f;
+        if (weight) {
+            float ss = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        if (PAIRS) {
-                            // pair e of the lane's 16 neighbouring channels
-                            float &x = e < 4 ? v0[2 * e & 7] : v1[2 * e & 7], &y = e < 4 ? v0[(2 * e + 1) & 7] : v1[(2 * e + 1) & 7];
-                            const float xa = x, xb = y;
-                            x = xa * co[e] - xb * si[e];
-                            y = xa * si[e] + xb * co[e];
-                        } else {
-                            const float xa = v0[e], xb = v1[e];
-                            v0[e] = xa * co[e] - xb * si[e];
-                            v1[e] = xa * si[e] + xb * co[e];
-                        }
-                    }
-                }
-                if (there) {
-                    T *d = is_q ? (T *)a.q_out + row * a.q_out_stride + h * D : (T *)a.k_out + row * a.k_out_stride + h * D;
-                    Run8<T>::store(d + c0, v0);
-                    Run8<T>::store(d + c1, v1);
-                }
-            }
+            for (int e = 0; e < 8; ++e) ss = fmaf(v0[e], v0[e], fmaf(v1[e], v1[e], ss));
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            inv = rsqrtf(ss * (1.0f / D) + a.eps);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float &xa = first(v0, v1, e), &xb = second(v0, v1, e);
+            const float p = xa * inv, q = xb * inv;
+            xa = turns ? p * ca[e] - q * sb[e] : p * ca[e];
+            xb = turns ? p * sa[e] + q * cb[e] : q * cb[e];
+        }
+        if (h0 + i * kHeads < heads) {
+            T *d = dst + (size_t)(h0 + i * kHeads) * D;
+            Run8<T>::store(d + c0, v0);
+            Run8<T>::store(d + c1, v1);
         }
     }
 }
@@ -183,15 +183,19 @@ template <typename T, int D>
 cudaError_t run(const RotateArgs &a, const rkv_rope &rope, cudaStream_t s)
 {
     constexpr int kHeads = 512 / D, kWarps = kRotateThreads / 32;
-    const int passes = (a.q ? (a.H + kHeads - 1) / kHeads : 0) + (a.k ? (a.N + kHeads - 1) / kHeads : 0);
-    // few rows: their heads go to as many warps as fill the GPU's SMs with eight CTAs
-    const long long fill = 152LL * 8 * kWarps;
-    const int parts = (int)max(1LL, min((long long)passes, fill / max(1, a.rows)));
-    const long long units = (long long)a.rows * parts;
-    const unsigned grid = (unsigned)min(fill / kWarps, (units + kWarps - 1) / kWarps);
+    RotatePasses z;
+    z.q_passes = a.q ? (a.H + kHeads - 1) / kHeads : 0;
+    z.k_passes = a.k ? (a.N + kHeads - 1) / kHeads : 0;
+    // few rows: their heads go to as many warps as the GPU holds at 16 to an SM
+    z.per = kMostPasses<T>;
+    while (z.per > 1 && (long long)a.rows * ((z.q_passes + z.per - 1) / z.per + (z.k_passes + z.per - 1) / z.per) < 152LL * 16) z.per /= 2;
+    z.q_units = (z.q_passes + z.per - 1) / z.per;
+    z.units = z.q_units + (z.k_passes + z.per - 1) / z.per;
+    const long long ctas = ((long long)a.rows * z.units + kWarps - 1) / kWarps;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     ProfScope prof("qk_rotate", s);
-    if (rope.layout == RKV_ROPE_PAIRS) k_qk_rotate<T, D, true><<<grid, kRotateThreads, 0, s>>>(a, rope, parts);
-    else k_qk_rotate<T, D, false><<<grid, kRotateThreads, 0, s>>>(a, rope, parts);
+    if (rope.layout == RKV_ROPE_PAIRS) k_qk_rotate<T, D, true><<<(unsigned)ctas, kRotateThreads, 0, s>>>(a, rope, z);
+    else k_qk_rotate<T, D, false><<<(unsigned)ctas, kRotateThreads, 0, s>>>(a, rope, z);
     return cudaGetLastError();
 }
 

@@ -544,6 +544,7 @@ class Buffers:
 
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_BF16S, _F32S, _I32S = (_BF16,), (_F32,), (_I32,)
 # the raw handle of a device's current stream, without a Stream object around it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -752,25 +753,30 @@ class PromptHeads(_DeviceOps):
         self._raw["status"] = (t, raw)
         self.status = t.view(torch.int32)
         self.device = self.status.device
+        self._dev = t.get_device()
+        self._sizes = {}
         self._p_ref = ctypes.byref(self.p)
         self._status_ptr = self.status.data_ptr()
 
-    def _rows(self, name, t, dtypes, heads, rows=None):
-        """Distance of a tensor's rows, in elements."""
+    def _rows(self, name, t, dtypes, heads, rows):
+        """Distance of a tensor's rows [rows][heads][D], in elements."""
+        s, wide = t.stride(), heads * self.D
+        if (t.dtype in dtypes and t.shape == (rows, heads, self.D) and s[2] == 1 and s[1] == self.D and s[0] >= wide
+                and s[0] % 8 == 0 and t.get_device() == self._dev):
+            return s[0]
         if t.dtype not in dtypes:
             raise ValueError("%s: %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.D or (rows is not None and t.shape[0] != rows):
-            raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), ("rows" if rows is None else rows, heads, self.D)))
+        if t.shape != (rows, heads, self.D):
+            raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), (rows, heads, self.D)))
         if t.device != self.device:
             raise ValueError("%s is on %s, the %s on %s" % (name, t.device, self._what, self.device))
-        stride, wide = t.stride(), heads * self.D
-        if stride[2] != 1 or (heads > 1 and stride[1] != self.D):
+        if s[2] != 1 or (heads > 1 and s[1] != self.D):
             raise ValueError("%s: the heads of a row do not lie behind one another" % name)
-        if t.shape[0] <= 1:
+        if rows <= 1:
             return wide
-        if stride[0] < wide or stride[0] * t.element_size() % 16:
-            raise ValueError("%s: rows %d elements apart" % (name, stride[0]))
-        return stride[0]
+        if s[0] < wide or s[0] * t.element_size() % 16:
+            raise ValueError("%s: rows %d elements apart" % (name, s[0]))
+        return s[0]
 
     def rotate(self, rope: rkv_rope, q, k, pos, q_out, k_out, q_weight=None, k_weight=None, eps: float = 1e-6,
                stream=None):
@@ -780,37 +786,48 @@ class PromptHeads(_DeviceOps):
         some = q if q is not None else k
         if some is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
             raise ValueError("q or k, each with its output")
-        dt = (some.dtype,) if some.dtype in (_BF16, _F32) else (_BF16, _F32)
-        rows = some.shape[0] if some.dim() == 3 else -1
-        args = []
-        for name, x, x_out, w, heads in (("q", q, q_out, q_weight, self.H), ("k", k, k_out, k_weight, self.N)):
-            if x is None:
-                args.append((None, 0, None, None, 0))
-                if w is not None:
-                    raise ValueError("%s_weight without %s" % (name, name))
-                continue
-            sx, so = self._rows(name, x, dt, heads, rows), self._rows(name + "_out", x_out, dt, heads, rows)
-            if w is not None:
-                self._check(name + "_weight", w, dt, (self.D,))
-            args.append((x.data_ptr(), sx, None if w is None else w.data_ptr(), x_out.data_ptr(), so))
-        self._check("pos", pos, (_I32,), (rows,))
+        if (q is None and q_weight is not None) or (k is None and k_weight is not None):
+            raise ValueError("a weight without its heads")
         if rope.D != self.D:
             raise ValueError("rope: heads of %d channels, expected %d" % (rope.D, self.D))
-        (qp, qs, qw, qo, qos), (kp, ks, kw, ko, kos) = args
-        wide = self.H * self.D
-        self._call("rkv_qk_rotate", stream, None, ctypes.byref(rope), rows, RKV_F32 if dt[0] is _F32 else RKV_BF16, qp,
-                   qs or wide, kp, ks or wide, pos.data_ptr(), qw, kw, eps, qo, qos or wide, ko, kos or wide)
+        dt = _F32S if some.dtype is _F32 else _BF16S
+        rows = some.shape[0] if some.dim() == 3 else -1
+        qp = kp = qw = kw = qo = ko = None
+        qs = ks = qos = kos = self.H * self.D              # of no account where there are no heads
+        if q is not None:
+            qs, qos = self._rows("q", q, dt, self.H, rows), self._rows("q_out", q_out, dt, self.H, rows)
+            qp, qo = q.data_ptr(), q_out.data_ptr()
+            if q_weight is not None:
+                self._check("q_weight", q_weight, dt, (self.D,))
+                qw = q_weight.data_ptr()
+        if k is not None:
+            ks, kos = self._rows("k", k, dt, self.N, rows), self._rows("k_out", k_out, dt, self.N, rows)
+            kp, ko = k.data_ptr(), k_out.data_ptr()
+            if k_weight is not None:
+                self._check("k_weight", k_weight, dt, (self.D,))
+                kw = k_weight.data_ptr()
+        self._check("pos", pos, _I32S, (rows,))
+        self._call("rkv_qk_rotate", stream, None, ctypes.byref(rope), rows, RKV_F32 if dt is _F32S else RKV_BF16, qp, qs,
+                   kp, ks, pos.data_ptr(), qw, kw, eps, qo, qos, ko, kos)
 
     def attend(self, q, k, v, start, out, stream=None):
         """out [rows][H][D] (bf16): causal attention of packed prompts, q [rows][H][D] over k, v
         [rows][N][D]; prompt s has rows start[s] .. start[s + 1] - 1.  Rows of none are not written."""
-        sq = self._rows("q", q, (_BF16,), self.H)
-        rows = q.shape[0]
-        sk, sv = self._rows("k", k, (_BF16,), self.N, rows), self._rows("v", v, (_BF16,), self.N, rows)
-        so = self._rows("out", out, (_BF16,), self.H, rows)
+        rows = q.shape[0] if q.dim() == 3 else -1
+        sq, so = self._rows("q", q, _BF16S, self.H, rows), self._rows("out", out, _BF16S, self.H, rows)
+        sk, sv = self._rows("k", k, _BF16S, self.N, rows), self._rows("v", v, _BF16S, self.N, rows)
         S = start.shape[0] - 1 if start.dim() == 1 else -1
         if S < 0:
             raise ValueError("start: shape %s, expected one more than prompts" % (tuple(start.shape),))
-        self._check("start", start, (_I32,), (S + 1,))
-        self._call("rkv_prompt_attention", stream, rkv_prompt_attention_workspace(self.p, S, rows), S, start.data_ptr(),
-                   rows, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, out.data_ptr(), so)
+        self._check("start", start, _I32S, (S + 1,))
+        self._call("rkv_prompt_attention", stream, self._size(S, rows), S, start.data_ptr(), rows, q.data_ptr(), sq,
+                   k.data_ptr(), sk, v.data_ptr(), sv, out.data_ptr(), so)
+
+    def _size(self, S, rows):
+        """Bytes of scratch (kept for the sizes that come again)."""
+        need = self._sizes.get((S, rows))
+        if need is None:
+            if len(self._sizes) >= 4096:
+                self._sizes.clear()
+            need = self._sizes[S, rows] = rkv_prompt_attention_workspace(self.p, S, rows)
+        return need
