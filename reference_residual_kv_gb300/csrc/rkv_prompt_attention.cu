@@ -150,7 +150,7 @@ template <int D>
 struct FlashCfg {
     static constexpr int kHalves = D == 256 ? 1 : 2;       // row tiles
     static constexpr int kBufs = D == 128 ? 1 : 2;         // score buffers of a row tile
-    static constexpr int kTok = D == 128 ? 128 : 64;       // keys of a tile
+    static constexpr int kTok = D == 128 ? 128 : D == 64 ? 96 : 64;   // keys of a tile
     static constexpr int kParts = D == 128 ? 2 : 1, kPart = kTok / kParts;   // P goes to the products so many keys at a time
     static constexpr bool kTurns = D == 128;               // the row tiles' products go in turns
     static constexpr int kStages = D == 64 ? 8 : 5;
@@ -159,8 +159,8 @@ struct FlashCfg {
     static constexpr int kThreads = 128 + 128 * kHalves;
     static constexpr int kBars = 2 * kStages + 38;
     static constexpr int kSmem = kHalves * kQ + kStages * kTile + kBars * 8 + 4 * 48 + D * 4 + 64 + 1024;
-    static constexpr int kColS = kHalves * (D < 128 ? 128 : D);   // tensor memory: outputs, then scores
-    static constexpr int kColsO = D < 128 ? 128 : D;
+    static constexpr int kColS = kHalves * D;   // tensor memory: outputs, then scores
+    static constexpr int kColsO = D;
     // registers: 384 threads begin with 168; 128 x 72 + 256 x 216 is what the launch has
     static constexpr int kRegsFew = 72, kRegsRows = 216;
     static_assert(kHalves == 1 || kRegsFew + 2 * kRegsRows <= 3 * 168, "registers of the launch");
@@ -635,12 +635,15 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                             tmem_st16(ts + 16 * c, p);
                         }
                     };
-                    exps();
                     // As long as the sum stays small, so does every probability: no maximum is taken.
                     // The reference moves to the maximum where it does not, and at the start
-                    const float sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
-                    float add = sum;
-                    const bool look = in_tile && (!(sum <= kMost) || m_ref == -INFINITY);
+                    float add = 0.0f;
+                    const bool anew = __any_sync(0xffffffffu, in_tile && m_ref == -INFINITY);
+                    if (!anew) {
+                        exps();
+                        add = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+                    }
+                    const bool look = in_tile && (anew || !(add <= kMost));
                     if (__any_sync(0xffffffffu, look)) {
                         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -650,7 +653,7 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
 #pragma unroll
                                 for (int z = 0; z < 4; ++z) top[z] = max3f(top[z], v[c][e + 2 * z], v[c][e + 2 * z + 1]);
                         const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-                        const bool move = look && most > m_ref;
+                        const bool move = look && most > m_ref + (anew && m_ref != -INFINITY ? 8.0f : 0.0f);
                         const float f = move ? (m_ref == -INFINITY ? 0.0f : ex2(m_ref - most)) : 1.0f;
                         if (j > 0 || part > 0) {
                             // the output products so far: with one buffer, those of earlier tiles came before
@@ -806,7 +809,7 @@ Layout layout_of(const PromptShape &p)
     Layout y{};
     const int halves = p.D == 256 ? 1 : 2, rows = 128 * halves;
     y.tile_tokens = halves * (128 / (p.H / p.N));
-    y.tok = p.D == 128 ? 128 : 64;
+    y.tok = p.D == 128 ? 128 : p.D == 64 ? 96 : 64;
     const long long tiles = p.start ? p.rows / y.tile_tokens + (long long)p.S
                                     : (long long)p.S * ((p.n + y.tile_tokens - 1) / y.tile_tokens);
     const long long keys = p.start ? p.rows : p.T;

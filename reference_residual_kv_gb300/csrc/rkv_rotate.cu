@@ -13,7 +13,7 @@
 namespace rkv {
 namespace {
 
-constexpr int kRotateThreads = 128;
+constexpr int kRotateThreads = 32;             // a warp of its own: its place is taken anew as soon as it ends
 template <typename T>
 constexpr int kMostPasses = sizeof(T) == 2 ? 4 : 2;     // of a warp, their loads in flight together
 
