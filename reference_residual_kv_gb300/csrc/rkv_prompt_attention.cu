@@ -21,8 +21,9 @@
 //
 // Items come from one CTA that reads the lengths (rkv_prompt_plan.cuh), split over the keys where there
 // are few; the parts of a split item leave {m, l, out} in fp32, which k_prompt_join puts together.
-// A few sequences whose items are one round, and one sequence whose items are many, need neither: there
-// the producers work out their items by themselves, from the last tile to the first.
+// Up to 32 prompts whose K and V stay in L2, where no item is longer than the others leave time for, need
+// neither: there the producers work out their items by themselves, the last tiles of the longest
+// prompts first.
 // All waits are bounded: RKV_ERR_DEVICE_TIMEOUT is set, the copies and products under way are
 // waited for, and the outputs are incomplete.
 #include "rkv_prompt_plan.cuh"
@@ -301,7 +302,7 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
         uint32_t loads = 0, uses[2] = {0, 0}, cleans = 0;
         const int item_tok = kHalves * tile_tok;
         // items worked out here: lane s holds sequence s
-        int begin = 0, n_tok = 0, upto = 0, by_seq = 0;
+        int begin = 0, n_tok = 0, tiles = 0, most = 0, by_seq = 0;
         long long all;
         if (a.start) {
             if (lane < a.S) {
@@ -309,8 +310,9 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                 n_tok = __ldg(a.start + lane + 1) - begin;
             }
             const bool wrong = begin < 0 || n_tok < 0 || begin > a.rows - n_tok;
-            upto = lane_scan((n_tok + item_tok - 1) / item_tok);
-            all = (long long)__shfl_sync(0xffffffffu, upto, 31) * N;
+            tiles = (n_tok + item_tok - 1) / item_tok;
+            most = __reduce_max_sync(0xffffffffu, tiles);
+            all = (long long)__reduce_add_sync(0xffffffffu, tiles) * N;
             if (__any_sync(0xffffffffu, wrong)) {
                 if (lane == 0) set_status(a.status, RKV_ERR_INDEX);
                 all = 0;
@@ -324,10 +326,17 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
             if (at >= all) return w;
             int e = (int)(at / N), n = (int)(at % N);
             if (a.start) {
-                e = (int)(all / N) - 1 - e;
-                const int s = __ffs(__ballot_sync(0xffffffffu, e < upto)) - 1;
-                const int b = __shfl_sync(0xffffffffu, begin, s), m = __shfl_sync(0xffffffffu, n_tok, s);
-                const int t0 = (e - __shfl_sync(0xffffffffu, upto - (n_tok + item_tok - 1) / item_tok, s)) * item_tok;
+                // the e-th of all tiles, the last ones of the longest sequences first: its number t in its
+                // sequence is the least of which no more than e tiles have a higher one
+                int lo = 0, hi = most;
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if ((int)__reduce_add_sync(0xffffffffu, max(0, tiles - mid - 1)) <= e) hi = mid;
+                    else lo = mid + 1;
+                }
+                const int t = lo, r = e - (int)__reduce_add_sync(0xffffffffu, max(0, tiles - t - 1));
+                const int s = (int)__fns(__ballot_sync(0xffffffffu, tiles > t), 0, r + 1);
+                const int b = __shfl_sync(0xffffffffu, begin, s), m = __shfl_sync(0xffffffffu, n_tok, s), t0 = t * item_tok;
                 const int tokens = min(item_tok, m - t0);
                 w.it = PromptItem{b + t0, tokens, b, t0, 0, (t0 + tokens + kTok - 1) / kTok, -1, 0};
                 w.n = n;
@@ -816,12 +825,16 @@ Layout layout_of(const PromptShape &p)
     // no part is shorter than 4 x 128 keys
     y.max_slots = (int)min((long long)kPromptSlots, tiles * p.N * (keys / (4 * 128)));
     if (p.start) {
-        // one round of short items, or one prompt: as good as without parts where the longest item is no
-        // more than its share of all of them, or short
-        const double all = 0.5 * (double)(p.rows / (double)y.tile_tokens) * (p.rows / 128.0 + 2 * kItemCost) * p.N / kPromptCtas;
-        const double longest = p.rows / 128.0 + kItemCost;
-        y.direct = p.S == 1 ? longest <= 16 + kItemCost || longest <= 1.1 * all
-                            : p.S <= 32 && tiles * p.N <= kPromptCtas && longest <= 16 + kItemCost;
+        // Without parts the longest item should be no longer than its CTA's share of all items, or short.
+        // A prompt of 2 CTAs tile_tokens / N rows has items of that share at its end, whatever the others'
+        // lengths.  With and without (us, 4 prompts of 50 .. 2000 rows, 8 of 1024; 32 heads): 54 | 42, 92 | 80.
+        const double longest = p.rows / 128.0;
+        const double share = 0.5 * (double)(p.rows / (double)y.tile_tokens) * (longest + 2 * kItemCost) * p.N / kPromptCtas;
+        const bool even = longest <= 16 || 2.0 * kPromptCtas * y.tile_tokens / p.N <= 24 * 128 ||
+                          (p.S == 1 && longest + kItemCost <= 1.1 * share);
+        // by sequence, where K and V are more than stays in L2 and a KV head would have less than 4 CTAs
+        const bool mixed = p.S == 1 || p.rows * 4 * p.N * p.D <= kInL2 || 4LL * p.S * p.N <= kPromptCtas;
+        y.direct = p.S <= 32 && even && mixed;
     }
     if (y.direct) y.max_slots = 0;
     if (y.max_slots < 2 * p.N) y.max_slots = 0;

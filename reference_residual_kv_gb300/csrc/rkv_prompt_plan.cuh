@@ -42,7 +42,7 @@ struct PromptHead {
 constexpr int kPromptCtas = 152;
 constexpr int kPromptSlots = 4 * kPromptCtas;        // partials at most
 // K and V that stay in L2 beside what else is read
-constexpr long long kInL2 = 48LL << 20;
+constexpr long long kInL2 = 80LL << 20;
 constexpr int kItemCost = 2, kPartCost = 4;      // of an item or a part beside its keys, in key tiles of 128
 constexpr int kFewItems = 512, kFewRounds = 8;       // parts are considered up to here
 
