@@ -677,7 +677,8 @@ k_dense_read(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
 }
 
 // K and V of a sequence's cached tokens, and of the rows behind them, in bf16 as [N][2][T][D]: what
-// attention over many query rows reads.  The first CTA works out the items of that attention meanwhile.
+// attention over many query rows reads.  The first CTA works out the items of that attention
+// meanwhile, where the sequences are few.
 // A warp takes a block of 32 tokens of a KV head's keys or values at a time, every n-th of them, n
 // the warps of the grid, so that a capacity far beyond the lengths costs a look at them only.  Many
 // warps to an SM with a record each on its way: 131072 tokens of 8 heads of 128 at 4 bits 114 us (6.2 TB/s of
@@ -701,7 +702,7 @@ k_dense_rows(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kCh = D / 8;
     if (blockIdx.x == 0) {
-        prompt_plan<32 * kReadWarps>(plan, *(PlanShared<32 * kReadWarps> *)smem);
+        if (plan.S <= kPlanBeside) prompt_plan<32 * kReadWarps>(plan, *(PlanShared<32 * kReadWarps> *)smem);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

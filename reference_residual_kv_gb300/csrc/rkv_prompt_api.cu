@@ -55,6 +55,7 @@ rkv_status check_packed(const rkv_head_params *p, int32_t S, int32_t rows)
     rkv_status st = check_head_params(p, 8);
     if (st != RKV_OK) return st;
     if (S < 0 || rows < 0) return RKV_ERR_INVALID_ARG;
+    if (rows > 1 << 30) return RKV_ERR_UNSUPPORTED;        // a tile's last row is counted in 32 bits
     // items of all KV heads are counted in 32 bits
     const long long per = 16 * (p->D == 256 ? 1 : 2);
     return ((long long)rows / per + S) * p->N > (1LL << 30) ? RKV_ERR_UNSUPPORTED : RKV_OK;
@@ -189,6 +190,7 @@ rkv_status rkv_qk_rotate(const rkv_head_params *p, const rkv_rope *rope, int32_t
     if (k && ((st = check_stride(k_stride, p->N, p->D, item)) != RKV_OK ||
               (st = check_stride(k_out_stride, p->N, p->D, item)) != RKV_OK))
         return st;
+    if ((long long)rows * (p->H + p->N) > (long long)INT_MAX) return RKV_ERR_UNSUPPORTED;   // a warp to some heads
     if (rows == 0) return RKV_OK;
     if ((!q && !k) || !pos || !dev_status) return RKV_ERR_INVALID_ARG;
     if ((q == q_out && q && q_stride != q_out_stride) || (k == k_out && k && k_stride != k_out_stride))

@@ -947,8 +947,9 @@ cudaError_t launch_prompt_attention(const PromptShape &p, const PromptTensors &t
 {
     const Layout y = layout_of(p);
     uint8_t *ws = (uint8_t *)workspace;
-    // pieces' items come from k_dense_rows
-    if (p.start && !y.direct) {
+    // pieces' items come from k_dense_rows, but those of many sequences, which its 64 threads would take
+    // longer for than its rows
+    if (p.start ? !y.direct : p.S > kPlanBeside) {
         ProfScope prof("prompt_plan", s);
         k_prompt_plan<<<1, kPlanThreads, 0, s>>>(prompt_plan_args(p, workspace, status));
         const cudaError_t e = cudaGetLastError();

@@ -46,6 +46,8 @@ constexpr long long kInL2 = 80LL << 20;
 constexpr int kItemCost = 2, kPartCost = 4;      // of an item or a part beside its keys, in key tiles of 128
 constexpr int kFewItems = 512, kFewRounds = 8;       // parts are considered up to here
 
+constexpr int kPlanBeside = 256;               // sequences whose items k_dense_rows works out
+
 struct PlanArgs {
     const int32_t *start;                      // packed prompts
     const int32_t *len, *n_new;                // pieces: [S], n rows each at most

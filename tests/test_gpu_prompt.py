@@ -105,6 +105,29 @@ def test_more_keys_than_stay_in_l2():
     assert bool(((out[start[1]: start[2]].double() - alone.double()).abs() <= 2 * HALF * alone.double().abs() + 1e-3).all())
 
 
+def test_many_heads_of_more_keys_than_stay_in_l2():
+    # items by sequence and KV head
+    gen = torch.Generator(device="cuda").manual_seed(19)
+    q, k, v, start = packed(gen, [9000, 4, 8000, 0, 700, 5000, 3000], 32, 8, 128, behind=5)
+    out = attend(q, k, v, start)
+    for a, b in zip(start[:-1], start[1:]):
+        for h in (0, 13, 31):
+            if b > a:
+                want, mag = po.causal(q[a:b, h: h + 1].double(), k[a:b, h // 4: h // 4 + 1].double(), v[a:b, h // 4: h // 4 + 1].double())
+                near(out[a:b, h: h + 1], want, mag)
+    assert bool((out[start[-1]:] == MARK).all()) and not bool((out[: start[-1]] == MARK).all(-1).any())
+
+
+@pytest.mark.parametrize("S", [2, 31, 32, 33])
+def test_items_worked_out_by_the_producers(S):
+    # up to 32 sequences whatever their lengths, the empty ones among them; one more goes by the plan
+    gen = torch.Generator(device="cuda").manual_seed(S)
+    rng = np.random.default_rng(S)
+    lens = [int(x) for x in rng.integers(0, 150, size=S - 1)] + [700]
+    q, k, v, start = packed(gen, lens, 8, 2, 128, behind=2)
+    check(q, k, v, start, attend(q, k, v, start))
+
+
 def test_thousands_of_short_prompts():
     gen = torch.Generator(device="cuda").manual_seed(12)
     rng = np.random.default_rng(12)
@@ -341,6 +364,17 @@ def test_a_sequence_alone_and_in_a_batch():
     lens = [(37 * s) % 310 for s in range(S)]
     new = [(53 * s) % 91 for s in range(S)]
     c = cache_with(rows_kv(gen, S, 310, N, D), lens, T, N, D, 4)
+    q, kv = randn(gen, S, n, H, D).to(BF16), rows_kv(gen, S, n, N, D)
+    check_piece(c, H, q, kv, lens, new, piece(c, H, q, kv, lens, new))
+
+
+def test_hundreds_of_sequences_pieces():
+    # more than the cache's way to bf16 works the items out for
+    gen = torch.Generator(device="cuda").manual_seed(25)
+    S, n, T, H, N, D = 300, 70, 200, 4, 2, 64
+    lens = [(29 * s) % 131 for s in range(S)]
+    new = [(31 * s) % 71 for s in range(S)]
+    c = cache_with(rows_kv(gen, S, 130, N, D), lens, T, N, D, 2)
     q, kv = randn(gen, S, n, H, D).to(BF16), rows_kv(gen, S, n, N, D)
     check_piece(c, H, q, kv, lens, new, piece(c, H, q, kv, lens, new))
 

@@ -70,7 +70,7 @@ def test_rotate_refuses(lib):
     loud.gain = math.inf
     for kw, code in ((dict(p=(0, 2, 128, 0)), INVALID), (dict(p=(8, 3, 128, 0)), UNSUPPORTED), (dict(p=(8, 2, 96, 0)), UNSUPPORTED),
                      (dict(p=(8, 2, 128, 1)), INVALID), (dict(rope=None), INVALID), (dict(rope=rkv.make_rope(64)), INVALID),
-                     (dict(rope=bent), INVALID), (dict(rope=loud), INVALID), (dict(rows=-1), INVALID), (dict(dt=2), INVALID),
+                     (dict(rope=bent), INVALID), (dict(rope=loud), INVALID), (dict(rows=-1), INVALID), (dict(rows=1 << 28), UNSUPPORTED), (dict(dt=2), INVALID),
                      (dict(q=None), INVALID), (dict(qo=None), INVALID), (dict(q=None, qo=None, k=None, ko=None), INVALID),
                      (dict(qs=1023), INVALID), (dict(qs=1028), ALIGN), (dict(kos=260), ALIGN), (dict(pos=None), INVALID),
                      (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(st=None), INVALID),
@@ -86,7 +86,7 @@ def test_prompt_attention_refuses(lib):
 
     assert attend(S=0) == 0 and attend(rows=0) == 0
     for kw, code in ((dict(p=(9, 1, 128, 0)), UNSUPPORTED), (dict(p=(8, 2, 32, 0)), UNSUPPORTED), (dict(p=(8, 0, 128, 0)), INVALID),
-                     (dict(S=-1), INVALID), (dict(rows=-1), INVALID), (dict(S=1 << 30), UNSUPPORTED), (dict(start=None), INVALID),
+                     (dict(S=-1), INVALID), (dict(rows=-1), INVALID), (dict(S=1 << 30), UNSUPPORTED), (dict(rows=(1 << 30) + 1), UNSUPPORTED), (dict(start=None), INVALID),
                      (dict(q=None), INVALID), (dict(v=None), INVALID), (dict(o=None), INVALID), (dict(st=None), INVALID),
                      (dict(qs=1000), INVALID), (dict(ks=260), ALIGN), (dict(os=1028), ALIGN), (dict(k=24), ALIGN),
                      (dict(nb=64), WORKSPACE), (dict(ws=None), WORKSPACE), (dict(ws=128), ALIGN)):
