@@ -679,6 +679,8 @@ k_dense_read(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
 // K and V of a sequence's cached tokens, and of the rows behind them, in bf16 as [N][2][T][D]: what
 // attention over many query rows reads.  The first CTA works out the items of that attention
 // meanwhile, where the sequences are few.
+// Behind the last row zeros follow to the end of any key tile (128 rows at most), so that what was there is
+// not taken for values that are not finite.
 // A warp takes a block of 32 tokens of a KV head's keys or values at a time, every n-th of them, n
 // the warps of the grid, so that a capacity far beyond the lengths costs a look at them only.  Many
 // warps to an SM with a record each on its way: 131072 tokens of 8 heads of 128 at 4 bits 114 us (6.2 TB/s of
@@ -728,7 +730,7 @@ k_dense_rows(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
             if (b == 0) set_status(status, RKV_ERR_INDEX);
             continue;
         }
-        if (more == 0 || b * kBlk >= length + more) continue;
+        if (more == 0 || b * kBlk >= length + more + 127) continue;
         uint4 *dst = (uint4 *)(out + ((sh * 2 + is_v) * T + b * kBlk) * D);
         if (b < length / kBlk) {
             if (lane == 0) {
@@ -755,11 +757,15 @@ k_dense_rows(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ khdr
             }
             __syncwarp();
         } else {
-            // the unfinished block's rows, then the new ones, four loads in flight
+            // the unfinished block's rows, then the new ones, four loads in flight, then zeros
 #pragma unroll 4
             for (int x = lane; x < kBlk * kCh; x += 32) {
                 const int t = b * kBlk + x / kCh;
-                if (t >= length + more) continue;
+                if (t >= T) continue;
+                if (t >= length + more) {
+                    dst[x] = make_uint4(0u, 0u, 0u, 0u);
+                    continue;
+                }
                 const __nv_bfloat16 *src = t < length ? tail + ((sh * 2 + is_v) * kBlk + t % kBlk) * D
                                                       : kv + (((size_t)s * n + t - length) * 2 + is_v) * N * D + (size_t)h * D;
                 dst[x] = __ldg((const uint4 *)src + x % kCh);

@@ -544,40 +544,54 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                 ok = wait(v_issued + (cleans & 3), cleans >> 2) && wait(kv_full + st, ld / kStages);
                 if (!ok) break;
                 uint8_t *v = ring + st * C::kTile;
-                uint32_t bad = 0;
-#pragma unroll 8
-                for (int x = lane; x < C::kTile / 16; x += 32) {
-                    const uint4 y = *(const uint4 *)(v + 16 * x);
+                // whether one of eight values has an exponent of all ones
+                auto odd_in = [](const uint4 &y) -> uint32_t {
                     const uint32_t e[4] = {y.x, y.y, y.z, y.w};
+                    uint32_t bad = 0;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) bad |= (e[k] & 0x7f807f80u) + 0x00800080u;
-                }
-                if (__any_sync(0xffffffffu, bad & 0x80008000u)) {
-                    int *words = odd;
-                    if (*odd_item != i + 1) {
-                        // the rows are through with the values of the items before
-                        const long long t0 = clock64();
-                        bool here = false;
-                        while (!here && !*abort_flag && clock64() - t0 <= kWaitCycles)
-                            here = lane >= 4 * kHalves || done[lane] >= i;
-                        ok = __all_sync(0xffffffffu, here);
-                        if (!ok) {
-                            if (lane == 0) *abort_flag = 1;
-                            break;
-                        }
-                        for (int d = lane; d < D; d += 32) words[d] = kNoValue;
-                        __syncwarp();
-                        if (lane == 0) *odd_item = i + 1;
-                    }
+                    return bad & 0x80008000u;
+                };
+                auto key_of = [&](int x) { return (w.it.kt0 + j) * kTok + x / 8 % kTok; };
+                uint32_t bad = 0;
+#pragma unroll 8
+                for (int x = lane; x < C::kTile / 16; x += 32) bad |= odd_in(*(const uint4 *)(v + 16 * x));
+                if (__any_sync(0xffffffffu, bad)) {
+                    // rows behind the text: nobody sees them
+                    bool seen = false;
+#pragma unroll 4
                     for (int x = lane; x < C::kTile / 16; x += 32) {
-                        const int box = x / (kTok * 8), r = x / 8 % kTok, ch = (x & 7) ^ (r & 7);
-                        const int key = (w.it.kt0 + j) * kTok + r;
-                        uint16_t *e = (uint16_t *)(v + 16 * x);
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t y = e[k];
-                            if ((y & 0x7f80u) != 0x7f80u) continue;
-                            e[k] = 0;
-                            if (key < kv_len) note_value(words + 64 * box + 8 * ch + k, key - base * kTok, (y & 0x7fu) ? 0 : 1 + (int)(y >> 15));
+                        uint4 *y = (uint4 *)(v + 16 * x);
+                        if (!odd_in(*y)) continue;
+                        if (key_of(x) < kv_len) seen = true;
+                        else *y = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    if (__any_sync(0xffffffffu, seen)) {
+                        if (*odd_item != i + 1) {
+                            // the rows are through with the values of the items before
+                            const long long t0 = clock64();
+                            bool here = false;
+                            while (!here && !*abort_flag && clock64() - t0 <= kWaitCycles)
+                                here = lane >= 4 * kHalves || done[lane] >= i;
+                            ok = __all_sync(0xffffffffu, here);
+                            if (!ok) {
+                                if (lane == 0) *abort_flag = 1;
+                                break;
+                            }
+                            for (int d = lane; d < D; d += 32) odd[d] = kNoValue;
+                            __syncwarp();
+                            if (lane == 0) *odd_item = i + 1;
+                        }
+                        for (int x = lane; x < C::kTile / 16; x += 32) {
+                            if (!odd_in(*(const uint4 *)(v + 16 * x))) continue;
+                            const int box = x / (kTok * 8), ch = (x & 7) ^ (x / 8 & 7);
+                            uint16_t *e = (uint16_t *)(v + 16 * x);
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t y = e[k];
+                                if ((y & 0x7f80u) != 0x7f80u) continue;
+                                e[k] = 0;
+                                note_value(odd + 64 * box + 8 * ch + k, key_of(x) - base * kTok, (y & 0x7fu) ? 0 : 1 + (int)(y >> 15));
+                            }
                         }
                     }
                     um::fence_proxy_async_smem();
