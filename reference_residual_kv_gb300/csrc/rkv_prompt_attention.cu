@@ -230,6 +230,24 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.G, N = a.N, tile_tok = 128 / G;        // tokens of a row tile
+    // The producer's view of the items, on its way while the CTA is set up: where they are worked out here
+    // lane s holds sequence s, else the first one
+    const int item_tok = kHalves * tile_tok;
+    int begin = 0, n_tok = 0;
+    int4 head4 = make_int4(0, 0, 0, 0), item0 = head4, item1 = head4;
+    if (warp == 0) {
+        if (a.start) {
+            if (lane < a.S) {
+                begin = __ldg(a.start + lane);
+                n_tok = __ldg(a.start + lane + 1);
+            }
+        } else {
+            const int4 *src = (const int4 *)(a.items + blockIdx.x / N);      // there is room for as many
+            head4 = __ldcg((const int4 *)a.head);
+            item0 = __ldcg(src);
+            item1 = __ldcg(src + 1);
+        }
+    }
     if (threadIdx.x == 0) {
         um::prefetch_tmap(&maps.q);
         um::prefetch_tmap(&maps.k);
@@ -300,15 +318,10 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
 
     if (warp == 0) {
         uint32_t loads = 0, uses[2] = {0, 0}, cleans = 0;
-        const int item_tok = kHalves * tile_tok;
-        // items worked out here: lane s holds sequence s
-        int begin = 0, n_tok = 0, tiles = 0, most = 0, by_seq = 0;
+        int tiles = 0, most = 0, by_seq = 0;
         long long all;
         if (a.start) {
-            if (lane < a.S) {
-                begin = __ldg(a.start + lane);
-                n_tok = __ldg(a.start + lane + 1) - begin;
-            }
+            n_tok -= begin;
             const bool wrong = begin < 0 || n_tok < 0 || begin > a.rows - n_tok;
             tiles = (n_tok + item_tok - 1) / item_tok;
             most = __reduce_max_sync(0xffffffffu, tiles);
@@ -318,8 +331,8 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                 all = 0;
             }
         } else {
-            all = (long long)*(volatile int *)&a.head->items * N;
-            by_seq = *(volatile int *)&a.head->by_seq;
+            all = (long long)head4.x * N;
+            by_seq = head4.y;
         }
         auto fetch = [&](long long at) -> FlashWork {
             FlashWork w{};
@@ -350,7 +363,8 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                 e = first + r % count;
             }
             const int4 *src = (const int4 *)(a.items + e);
-            const int4 x = __ldcg(src), y = __ldcg(src + 1);
+            const bool here = at == blockIdx.x && !by_seq;
+            const int4 x = here ? item0 : __ldcg(src), y = here ? item1 : __ldcg(src + 1);
             w.it = PromptItem{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
             w.n = n;
             return w;
