@@ -17,7 +17,8 @@
 //                and has the same relative error in bf16), so that the accumulator is rescaled only where
 //                the maximum grows by more than that (a published variant of the running softmax);
 //                P goes back to tensor memory, over the scores, as the first operand of P V
-// D = 256 has one row tile (its outputs take 256 columns) and two buffers of scores instead.
+// D = 256 has one row tile (its outputs take 256 columns) and two buffers of scores instead, and its query
+// rows lie in tensor memory: from shared memory both operands of Q K^T for 64 keys take twice the product's time.
 //
 // Items come from one CTA that reads the lengths (rkv_prompt_plan.cuh), split over the keys where there
 // are few; the parts of a split item leave {m, l, out} in fp32, which k_prompt_join puts together.
@@ -153,12 +154,14 @@ struct FlashCfg {
     static constexpr int kBufs = D == 128 ? 1 : 2;         // score buffers of a row tile
     static constexpr int kTok = D == 128 ? 128 : D == 64 ? 96 : 64;   // keys of a tile
     static constexpr int kParts = D == 128 ? 2 : 1, kPart = kTok / kParts;   // P goes to the products so many keys at a time
+    static constexpr bool kQInTmem = D == 256;             // the query rows, at kColQ
+    static constexpr int kColQ = 384;
     static constexpr bool kTurns = D == 128;               // the row tiles' products go in turns
     static constexpr int kStages = D == 64 ? 8 : 5;
     static_assert(kStages <= 8, "four tiles of V at most are in the ring: v_issued and v_clean have as many barriers");
     static constexpr int kQ = 128 * D * 2, kTile = kTok * D * 2;
     static constexpr int kThreads = 128 + 128 * kHalves;
-    static constexpr int kBars = 2 * kStages + 38;
+    static constexpr int kBars = 2 * kStages + 40;
     static constexpr int kSmem = kHalves * kQ + kStages * kTile + kBars * 8 + 4 * 48 + D * 4 + 64 + 1024;
     static constexpr int kColS = kHalves * D;   // tensor memory: outputs, then scores
     static constexpr int kColsO = D;
@@ -166,7 +169,7 @@ struct FlashCfg {
     static constexpr int kRegsFew = 72, kRegsRows = 216;
     static_assert(kHalves == 1 || kRegsFew + 2 * kRegsRows <= 3 * 168, "registers of the launch");
     static_assert(kSmem <= 227 * 1024, "shared memory of the attention");
-    static_assert(kColS + kHalves * kBufs * kTok <= 512, "tensor memory");
+    static_assert(kColS + kHalves * kBufs * kTok <= (kQInTmem ? kColQ : 512) && kColQ + D / 2 <= 512, "tensor memory");
 };
 
 struct FlashMaps { CUtensorMap q, k, v; };
@@ -219,14 +222,14 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
     uint64_t *q_full = kv_empty + kStages, *q_empty = q_full + 2;
     uint64_t *s_full = q_empty + 2, *p_full = s_full + 4, *pv_done = p_full + 4;   // s_full: [half * kBufs + buffer], others: [2 half + buffer]
     uint64_t *o_empty = pv_done + 4, *v_issued = o_empty + 2, *v_clean = v_issued + 4;
-    uint64_t *w_full = v_clean + 4, *w_empty = w_full + 4, *drain = w_empty + 4, *turn = drain + 2;
+    uint64_t *w_full = v_clean + 4, *w_empty = w_full + 4, *drain = w_empty + 4, *turn = drain + 2, *q_there = turn + 2;
     FlashWork *works = (FlashWork *)(kv_full + C::kBars);
     int *odd = (int *)(works + 4);                         // [D] values that are not finite
     volatile int *done = odd + D;                      // items that each of the rows' warps is through with
     volatile int *odd_item = done + 8;                     // the item that `odd` belongs to, + 1
     volatile int *abort_flag = odd_item + 1;
     uint32_t *tmem_slot = (uint32_t *)(odd_item + 2);
-    static_assert(2 * kStages + 2 + 2 + 4 + 4 + 4 + 2 + 4 + 4 + 4 + 4 + 2 + 2 <= C::kBars && sizeof(FlashWork) == 48, "shared memory");
+    static_assert(2 * kStages + 2 + 2 + 4 + 4 + 4 + 2 + 4 + 4 + 4 + 4 + 2 + 2 + 1 <= C::kBars && sizeof(FlashWork) == 48, "shared memory");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.G, N = a.N, tile_tok = 128 / G;        // tokens of a row tile
@@ -258,7 +261,7 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
         }
         for (int i = 0; i < 2; ++i) {
             um::mbar_init(q_full + i, 1);
-            um::mbar_init(q_empty + i, 1);
+            um::mbar_init(q_empty + i, C::kQInTmem ? 4 : 1);
             um::mbar_init(o_empty + i, 4);
         }
         for (int i = 0; i < 4; ++i) {
@@ -272,6 +275,7 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
         }
         um::mbar_init(drain, 1);
         um::mbar_init(drain + 1, 1);
+        um::mbar_init(q_there, 4);
         um::mbar_init(turn, 1);
         um::mbar_init(turn + 1, 1);
         for (int i = 0; i < 8; ++i) done[i] = 0;
@@ -475,17 +479,19 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                     const uint64_t k0 = kd + k_st * (C::kTile / 16);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        um::mma_bf16(tm + C::kColS + (h * kBufs + buf) * kTok, qd + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
-                                     k0 + (k >> 2) * (kTok * 128 / 16) + 2 * (k & 3), id_s, k != 0);
+                        const uint32_t d0 = tm + C::kColS + (h * kBufs + buf) * kTok;
+                        const uint64_t kk = k0 + (k >> 2) * (kTok * 128 / 16) + 2 * (k & 3);
+                        if (C::kQInTmem) mma_bf16_ta(d0, tm + C::kColQ + 8 * k, kk, id_s, k != 0);
+                        else um::mma_bf16(d0, qd + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3), kk, id_s, k != 0);
                     }
                     um::mma_commit(s_full + h * kBufs + buf);
                     um::mma_commit(kv_empty + k_st);
-                    if (j == mine - 1) um::mma_commit(q_empty + h);
+                    if (!C::kQInTmem && j == mine - 1) um::mma_commit(q_empty + h);
                 }
                 __syncwarp();
                 step_on(k_st, k_ph, 2);
             };
-            if (mine > 0) ok = ok && wait(q_full + h, turns);
+            if (mine > 0) ok = ok && wait(C::kQInTmem ? q_there : q_full + h, turns);
 #pragma unroll
             for (int j = 0; j < kBufs; ++j)
                 if (j < mine && ok) scores(j, false);
@@ -622,7 +628,7 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
         const uint32_t to = tmem + lanes + h * C::kColsO;
         const int tok = h * tile_tok + r / G;              // token of the item
         const bool in_tile = r / G < tile_tok;
-        uint32_t steps = 0;
+        uint32_t steps = 0, turns = 0;
         FlashWork w;
         bool ok = true;
         for (int i = 0; ok && take(i, w); ++i) {
@@ -630,6 +636,31 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
             const int sees = w.it.first + min(tok, w.it.tokens - 1);          // last key of this row
             const int whole = (w.it.first + h * tile_tok + 1) / kTok - w.it.kt0;   // tiles that every row sees
             float m_ref = -INFINITY, l = 0.0f;
+            if (C::kQInTmem && count > 0) {
+                // the query row, from shared memory; the products before are through with the last one
+                ok = wait(q_full + h, turns++);
+                if (!ok) break;
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y) {
+                    uint32_t x[16];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint4 v = *(const uint4 *)(qs + (y >> 1) * 128 * 128 + r * 128 + ((((y & 1) * 4 + c) ^ (r & 7)) << 4));
+                        x[4 * c] = v.x;
+                        x[4 * c + 1] = v.y;
+                        x[4 * c + 2] = v.z;
+                        x[4 * c + 3] = v.w;
+                    }
+                    tmem_st16(tmem + lanes + C::kColQ + 16 * y, x);
+                }
+                tmem_wait_st();
+                um::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    um::mbar_arrive(q_empty + h);
+                    um::mbar_arrive(q_there);
+                }
+            }
             for (int j = 0; j < count && ok; ++j) {
                 const uint32_t t = steps + j, buf = t % kBufs;
                 ok = wait(s_full + h * kBufs + buf, t / kBufs);

@@ -42,11 +42,12 @@ def bars(name, count, n):
 class Cta:
     """items: (key tiles of half 0, of half 1, first key tile that is looked through)."""
 
-    def __init__(self, items, halves, bufs, parts, stages, turns, rng, issued=True, order=True):
+    def __init__(self, items, halves, bufs, parts, stages, turns, rng, q_copied=False, issued=True, order=True):
         self.items, self.halves, self.bufs, self.parts, self.stages = items, halves, bufs, parts, stages
         self.turns, self.rng, self.issued, self.order = turns, rng, issued, order
+        self.q_copied, self.q_there, self.rows_q = q_copied, Bar("q_there", 4), [None] * 4     # queries in tensor memory
         self.kv_full, self.kv_empty = bars("kv_full", 1, stages), bars("kv_empty", halves, stages)
-        self.q_full, self.q_empty = bars("q_full", 1, 2), bars("q_empty", 1, 2)
+        self.q_full, self.q_empty = bars("q_full", 1, 2), bars("q_empty", 4 if q_copied else 1, 2)
         self.s_full = [bars("s_full%d" % h, 1, bufs) for h in range(halves)]
         self.p_full = [bars("p_full%d" % h, 4, max(bufs, parts)) for h in range(halves)]
         self.pv_done = [bars("pv_done%d" % h, 1, max(bufs, parts)) for h in range(halves)]
@@ -142,12 +143,12 @@ class Cta:
                 if ld != loads + 2 * j:
                     raise Fault("scores of tile %d from load %d" % (j, ld))
                 done = [self.s_full[h][t % self.bufs], self.kv_empty[ld % self.stages]]
-                if j == mine - 1:
+                if j == mine - 1 and not self.q_copied:
                     done.append(self.q_empty[h])
                 self.queues[h].append(("scores", i, t, ld, 0, False, done))
 
             if mine:
-                yield self.q_full[h], had
+                yield self.q_there if self.q_copied else self.q_full[h], had
             for j in range(min(self.bufs, mine)):
                 yield self.kv_full[(loads + 2 * j) % self.stages], (loads + 2 * j) // self.stages
                 scores(j)
@@ -195,10 +196,21 @@ class Cta:
             yield None
 
     def rows(self, h, w):
-        steps = 0
+        steps = had = 0
         for i in range(len(self.items)):
             yield from self.take(i)
             mine = self.items[i][h]
+            if self.q_copied and mine:
+                yield self.q_full[h], had
+                had += 1
+                yield None
+                if self.query[h] != i:
+                    raise Fault("query rows of %s for item %d" % (self.query[h], i))
+                if any(q[0] == "scores" for q in self.queues[h]):
+                    raise Fault("query rows written under a product")
+                self.rows_q[w] = i
+                self.q_empty[h].arrive()
+                self.q_there.arrive()
             for j in range(mine):
                 t = steps + j
                 buf = t % self.bufs
@@ -248,8 +260,8 @@ class Cta:
             raise Fault("%s of step %d read load %s for %d" % (kind, t, self.ring[ld % self.stages], ld))
         buf = t % self.bufs
         if kind == "scores":
-            if self.query[h] != i:
-                raise Fault("scores of item %d with the query of %s" % (i, self.query[h]))
+            if (self.rows_q != [i] * 4) if self.q_copied else (self.query[h] != i):
+                raise Fault("scores of item %d with the query of %s, %s" % (i, self.query[h], self.rows_q))
             if t >= self.bufs and any(self.p[h][buf * self.parts + x] != [t - self.bufs, "done"] for x in range(self.parts)):
                 raise Fault("scores of step %d over probabilities that are still needed" % t)
             self.s[h][buf] = t
@@ -301,7 +313,7 @@ class Cta:
 
 
 KINDS = {64: dict(halves=2, bufs=2, parts=1, stages=8, turns=False), 128: dict(halves=2, bufs=1, parts=2, stages=5, turns=True),
-         256: dict(halves=1, bufs=2, parts=1, stages=5, turns=False)}
+         256: dict(halves=1, bufs=2, parts=1, stages=5, turns=False, q_copied=True)}
 
 
 def random_items(rng, halves):
