@@ -434,8 +434,8 @@ rkv_status rkv_qk_rotate(const rkv_head_params *p, const rkv_rope *rope, int32_t
  * q, k, v, out: bf16, rows of H, N, N and H heads.  Scores, softmax and sums in fp32;
  * probabilities meet the values as bf16 (relative error 2^-9, as the output's own rounding).
  * RKV_ERR_DEVICE_TIMEOUT (a wait ran out): the outputs are not to be used.
- * workspace: >= the bytes of rkv_prompt_attention_workspace(p, S, rows), 256-byte aligned.
- * Requires H/N <= 8.                                                                      */
+ * workspace: >= the bytes of rkv_prompt_attention_workspace(p, S, rows), 256-byte aligned (0 bytes for
+ * some sizes: NULL will do).  Requires H/N <= 8.                                          */
 rkv_status rkv_prompt_attention_workspace(const rkv_head_params *p, int32_t S, int32_t rows, size_t *bytes);
 rkv_status rkv_prompt_attention(const rkv_head_params *p, int32_t S, const int32_t *start, int32_t rows,
                                 const void *q, int64_t q_stride, const void *k, int64_t k_stride,

@@ -240,7 +240,8 @@ rkv_status rkv_prompt_attention(const rkv_head_params *p, int32_t S, const int32
     if (!start || !q || !k || !v || !out || !dev_status) return RKV_ERR_INVALID_ARG;
     if (!aligned16(q, k, v, out, start, dev_status)) return RKV_ERR_ALIGNMENT;
     const PromptShape x = packed_shape(p, S, rows, start);
-    if (!workspace || workspace_bytes < prompt_workspace_bytes(x)) return RKV_ERR_WORKSPACE;
+    const size_t need = prompt_workspace_bytes(x);         // none where the producers work out the items
+    if (need > 0 && (!workspace || workspace_bytes < need)) return RKV_ERR_WORKSPACE;
     if ((uintptr_t)workspace & 255u) return RKV_ERR_ALIGNMENT;
     const PromptTensors t{q, k, v, out, q_stride, k_stride, v_stride, out_stride, p->D, p->D};
     return done(launch_prompt_attention(x, t, workspace, dev_status, (cudaStream_t)stream));

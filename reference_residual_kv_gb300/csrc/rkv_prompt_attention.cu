@@ -13,12 +13,36 @@
 //                finite is not 0, so such values are taken out there and noted, and given back to the
 //                rows that do see them
 //   warps 4..    four warps to a row tile, a thread per row: softmax in base 2 against a running
-//                reference m that lags the maximum by at most 8 (p <= 2^8 is harmless in fp32 sums
-//                and has the same relative error in bf16), so that the accumulator is rescaled only where
-//                the maximum grows by more than that (a published variant of the running softmax);
-//                P goes back to tensor memory, over the scores, as the first operand of P V
+//                reference m (a published variant: the reference lags the maximum, and the accumulator is
+//                rescaled only where it moves).  p = 2^(s - m) is worked out before anything is known of
+//                its maximum; while a row's p of 64 keys or more add up to 2^10 at most it is kept (any p up to there
+//                is harmless in fp32 sums and has the same relative error in bf16 as p <= 1), else, and for the
+//                first keys, the maximum is looked for and m moves there.  P goes back to tensor
+//                memory, over the scores, as the first operand of P V
 // D = 256 has one row tile (its outputs take 256 columns) and two buffers of scores instead, and its query
 // rows lie in tensor memory: from shared memory both operands of Q K^T for 64 keys take twice the product's time.
+//
+// P is bf16 (half a step of 2^-8, as the output's own rounding): outputs are 2.0-2.3e-3 off the exact ones
+// (relative norm), their rounding alone 1.5-1.7e-3.  A second part of P would take the products from 16 to 24 a
+// tile, half as long again.
+//
+// What bounds it, and what was measured (D = 128, 8192 tokens of 32 heads unless stated; 352 us, 1560
+// TFLOP/s of the 1900 that a large library product reaches; tensor pipe 65 %, L2 26 %, DRAM 5 %):
+//   - products read shared memory at about 93 bytes a cycle: P V of 128 x 128 x 16 takes 65 cycles, Q K^T 86
+//     alone and 64 among others, of 128 x 64 x 16 still 69.  So 64 keys at a time with two buffers of scores,
+//     which leave the softmax out of the way, take 366 us;
+//   - with one buffer a row tile's scores wait for its probabilities: the two tiles have to be at different
+//     places.  Their products go in turns, outputs and next scores of one tile, then of the other; without
+//     turns 395 us, with the turn given away between the two 392;
+//   - P in two parts of 64 keys, the first one's product during the other's softmax; in one part 415 us, 96 and
+//     32 keys 365;
+//   - maxima before the exponentials 402 us; an arrival on a barrier between products and their commit costs
+//     more than it gains (387);
+//   - an item takes about 2.4 us beside its keys, from the last product to the next softmax's first one.
+// D = 64 has half the products to the same exponentials and is bound by the softmax: two buffers of 96 keys, no
+// turns; 2 prompts of 4096 and 2048 tokens of 32 heads 96 us (64 keys 107, one buffer of 128 with turns 116).
+// D = 256: 8192 tokens of 16 heads 458 us (1200 TFLOP/s; query rows from shared memory 486), by its one
+// row tile's softmax.
 //
 // Items come from one CTA that reads the lengths (rkv_prompt_plan.cuh), split over the keys where there
 // are few; the parts of a split item leave {m, l, out} in fp32, which k_prompt_join puts together.
@@ -156,7 +180,7 @@ struct FlashCfg {
     static constexpr int kParts = D == 128 ? 2 : 1, kPart = kTok / kParts;   // P goes to the products so many keys at a time
     static constexpr bool kQInTmem = D == 256;             // the query rows, at kColQ
     static constexpr int kColQ = 384;
-    static constexpr bool kTurns = D == 128;               // the row tiles' products go in turns
+    static constexpr bool kTurns = D == 128;               // the row tiles' products go in turns (above)
     static constexpr int kStages = D == 64 ? 8 : 5;
     static_assert(kStages <= 8, "four tiles of V at most are in the ring: v_issued and v_clean have as many barriers");
     static constexpr int kQ = 128 * D * 2, kTile = kTok * D * 2;
@@ -900,8 +924,9 @@ Layout layout_of(const PromptShape &p)
     y.max_items = tiles + y.max_slots / p.N;
     y.max_joins = y.max_slots ? tiles : 0;
     y.ctas = (int)min((long long)kPromptCtas, y.max_items * p.N);
+    if (y.direct) return y;                    // no scratch
     y.items = 256;
-    y.joins = y.items + (y.direct ? 0 : align256((size_t)y.max_items * sizeof(PromptItem)));
+    y.joins = y.items + align256((size_t)y.max_items * sizeof(PromptItem));
     y.ml = y.joins + align256((size_t)y.max_joins * sizeof(PromptJoin));
     y.part = y.ml + align256((size_t)y.max_slots * rows * sizeof(float2));
     y.total = y.part + (size_t)y.max_slots * rows * p.D * sizeof(float);

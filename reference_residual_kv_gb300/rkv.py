@@ -598,6 +598,8 @@ class _DeviceOps:
         f = getattr(lib(), name)
         if need is None:
             return f(self._p_ref, *args, self._status_ptr, stream)
+        if need == 0:
+            return f(self._p_ref, *args, None, 0, self._status_ptr, stream)
         ws = self._scratch(need)
         return f(self._p_ref, *args, ws.data_ptr(), need, self._status_ptr, stream)
 

@@ -89,10 +89,12 @@ def test_prompt_attention_refuses(lib):
                      (dict(S=-1), INVALID), (dict(rows=-1), INVALID), (dict(S=1 << 30), UNSUPPORTED), (dict(rows=(1 << 30) + 1), UNSUPPORTED), (dict(start=None), INVALID),
                      (dict(q=None), INVALID), (dict(v=None), INVALID), (dict(o=None), INVALID), (dict(st=None), INVALID),
                      (dict(qs=1000), INVALID), (dict(ks=260), ALIGN), (dict(os=1028), ALIGN), (dict(k=24), ALIGN),
-                     (dict(nb=64), WORKSPACE), (dict(ws=None), WORKSPACE), (dict(ws=128), ALIGN)):
+                     (dict(S=40, nb=64), WORKSPACE), (dict(S=40, ws=None), WORKSPACE), (dict(S=40, ws=128), ALIGN),
+                     (dict(ws=128), ALIGN)):
         assert attend(**kw) == code, kw
     p = rkv.rkv_head_params(8, 2, 128, 0)
-    assert rkv.rkv_prompt_attention_workspace(p, 0, 40) == 0
+    assert rkv.rkv_prompt_attention_workspace(p, 0, 40) == 0 and rkv.rkv_prompt_attention_workspace(p, 40, 0) == 0
+    assert rkv.rkv_prompt_attention_workspace(p, 2, 40) == 0 and rkv.rkv_prompt_attention_workspace(p, 40, 40) > 64
     with pytest.raises(rkv.RkvError):
         rkv.rkv_prompt_attention_workspace(p, -1, 40)
 
