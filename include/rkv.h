@@ -433,6 +433,7 @@ rkv_status rkv_qk_rotate(const rkv_head_params *p, const rkv_rope *rope, int32_t
  * RKV_ERR_INDEX is set and nothing is written.
  * q, k, v, out: bf16, rows of H, N, N and H heads.  Scores, softmax and sums in fp32;
  * probabilities meet the values as bf16 (relative error 2^-9, as the output's own rounding).
+ * out may be q itself (same pointer and stride); otherwise it must not overlap q, k or v.
  * RKV_ERR_DEVICE_TIMEOUT (a wait ran out): the outputs are not to be used.
  * workspace: >= the bytes of rkv_prompt_attention_workspace(p, S, rows), 256-byte aligned (0 bytes for
  * some sizes: NULL will do).  Requires H/N <= 8.                                          */
@@ -447,9 +448,10 @@ rkv_status rkv_prompt_attention(const rkv_head_params *p, int32_t S, const int32
  * attends to those and to rows 0 .. i.  The piece itself is written with rkv_dense_write
  * afterwards (the call reads the unfinished block's rows, which that write replaces).
  * q: bf16 [S][n][H][D]; kv: bf16 [S][n][2 N D], as for rkv_dense_write; out: bf16 [S][n][H][D],
- * rows from n_new[s] on are not written.  n_new: int32 [S], device, or NULL (n rows for every
- * sequence).  Where len < 0, n_new is outside [0, n] or len + n_new > T, RKV_ERR_INDEX is set
- * and nothing of that sequence is written.  1 <= n <= T.  Precision as in rkv_prompt_attention.
+ * rows from n_new[s] on are not written; it must not overlap q or kv.  n_new: int32 [S], device,
+ * or NULL (n rows for every sequence).  Where len < 0, n_new is outside [0, n] or len + n_new > T,
+ * RKV_ERR_INDEX is set and nothing of that sequence is written.  1 <= n <= T.  Precision as in
+ * rkv_prompt_attention.
  * workspace: >= the bytes of rkv_chunk_attention_workspace(p, H, n), 256-byte aligned: for long
  * pieces (always for n > 64) it holds K and V of all S T tokens in bf16 (4 N D bytes each), and one
  * layer's calls may follow another's in it.  Requires H/N <= 8.                            */

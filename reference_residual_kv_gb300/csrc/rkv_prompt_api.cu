@@ -165,6 +165,7 @@ rkv_status rkv_rope_init(rkv_rope *r, int32_t D, int32_t R, int32_t layout, doub
             t = th * w + th / sc->factor * (1.0 - w);
         }
         double f = t / kTurn;
+        if (!isfinite(f)) return RKV_ERR_INVALID_ARG;      // a factor next to 0
         f -= floor(f);                                     // whole turns per position say nothing
         x.turn[i] = (uint64_t)ldexp(f, 64);                // f has 53 bits at most: below 2^64
     }

@@ -728,14 +728,15 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                         }
                     };
                     // As long as the sum stays small, so does every probability: no maximum is taken.
-                    // The reference moves to the maximum where it does not, and at the start
+                    // The reference moves to the maximum where it does not, and at the start.  A row decides
+                    // for itself: what lies in its neighbours' rows leaves its bits alone
                     float add = 0.0f;
-                    const bool anew = __any_sync(0xffffffffu, in_tile && m_ref == -INFINITY);
-                    if (!anew) {
+                    const bool none = !in_tile || m_ref == -INFINITY;
+                    if (!__all_sync(0xffffffffu, none)) {
                         exps();
                         add = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
                     }
-                    const bool look = in_tile && (anew || !(add <= kMost));
+                    const bool look = in_tile && (none || !(add <= kMost));
                     if (__any_sync(0xffffffffu, look)) {
                         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -745,7 +746,7 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
 #pragma unroll
                                 for (int z = 0; z < 4; ++z) top[z] = max3f(top[z], v[c][e + 2 * z], v[c][e + 2 * z + 1]);
                         const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-                        const bool move = look && most > m_ref + (anew && m_ref != -INFINITY ? 8.0f : 0.0f);
+                        const bool move = look && most > m_ref;
                         const float f = move ? (m_ref == -INFINITY ? 0.0f : ex2(m_ref - most)) : 1.0f;
                         if (j > 0 || part > 0) {
                             // the output products so far: with one buffer, those of earlier tiles came before

@@ -814,7 +814,8 @@ class PromptHeads(_DeviceOps):
 
     def attend(self, q, k, v, start, out, stream=None):
         """out [rows][H][D] (bf16): causal attention of packed prompts, q [rows][H][D] over k, v
-        [rows][N][D]; prompt s has rows start[s] .. start[s + 1] - 1.  Rows of none are not written."""
+        [rows][N][D]; prompt s has rows start[s] .. start[s + 1] - 1.  Rows of none are not written.
+        out may be q itself."""
         rows = q.shape[0] if q.dim() == 3 else -1
         sq, so = self._rows("q", q, _BF16S, self.H, rows), self._rows("out", out, _BF16S, self.H, rows)
         sk, sv = self._rows("k", k, _BF16S, self.N, rows), self._rows("v", v, _BF16S, self.N, rows)

@@ -211,6 +211,41 @@ def test_values_that_are_not_finite_are_seen_by_later_rows(D, H, N, n):
         assert torch.equal(o[~fine].nan_to_num(1.0), want[~fine].nan_to_num(1.0))
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [300, 3000])
+def test_a_row_leaves_its_neighbours_bits_alone(D, n):
+    # maxima that grow along the keys: each row moves its reference by its own scores, whatever the rows beside it hold
+    gen = torch.Generator(device="cuda").manual_seed(26)
+    q, k, v, start = packed(gen, [n], 4, 1, D, behind=10)
+    q = q.clone()
+    q[:, :, 0] = 8.0
+    k[:, 0, 0] = torch.linspace(-60, 60, n + 10, device="cuda").to(BF16)
+    clean = attend(q, k, v, start).clone()
+    q2 = q.clone()
+    q2[77, 1] = float("nan")
+    q2[n - 3, 2] = float("inf")
+    q2[n:] = float("nan")
+    out = attend(q2, k, v, start)
+    others = torch.ones(n, 4, dtype=torch.bool, device="cuda")
+    others[77, 1] = others[n - 3, 2] = False
+    assert torch.equal(out[:n][others], clean[:n][others])
+    assert bool(out[77, 1].isnan().all()) and bool(out[n - 3, 2].isnan().all())
+    assert bool((out[n:] == MARK).all())
+
+
+@pytest.mark.parametrize("lens,H,N,D,fused", [([1], 8, 2, 128, True), ([1], 1, 1, 64, False), ([300, 5, 1000], 8, 2, 128, True),
+                                              ([2500], 1, 1, 256, False), ([100] * 40, 7, 1, 64, True), ([3500], 2, 1, 128, True)])
+def test_outputs_over_the_queries(lens, H, N, D, fused):
+    # one row; whole items, items split over the keys, items of the plan
+    gen = torch.Generator(device="cuda").manual_seed(27)
+    q, k, v, start = packed(gen, lens, H, N, D, fused=fused)
+    want = attend(q, k, v, start).clone()
+    check(q, k, v, start, want)
+    before = k.clone(), v.clone()
+    assert attend(q, k, v, start, out=q).data_ptr() == q.data_ptr()
+    assert torch.equal(q, want) and torch.equal(k, before[0]) and torch.equal(v, before[1])
+
+
 def test_bad_starts_write_nothing():
     ensure_lib()
     gen = torch.Generator(device="cuda").manual_seed(16)
@@ -366,6 +401,25 @@ def test_a_sequence_alone_and_in_a_batch():
     c = cache_with(rows_kv(gen, S, 310, N, D), lens, T, N, D, 4)
     q, kv = randn(gen, S, n, H, D).to(BF16), rows_kv(gen, S, n, N, D)
     check_piece(c, H, q, kv, lens, new, piece(c, H, q, kv, lens, new))
+
+
+def test_pieces_of_more_keys_than_stay_in_l2():
+    # items by sequence and KV head
+    gen = torch.Generator(device="cuda").manual_seed(28)
+    S, n, T, H, N, D = 12, 1100, 5000, 32, 4, 128
+    lens = [3900 - 100 * s for s in range(S)]
+    new = [n - 7 * s for s in range(S)]
+    c = cache_with(rows_kv(gen, S, 3900, N, D), lens, T, N, D, 4)
+    q, kv = randn(gen, S, n, H, D).to(BF16), rows_kv(gen, S, n, N, D)
+    out = piece(c, H, q, kv, lens, new)
+    k0, v0 = held(c, lens)
+    x = kv.double().view(S, n, 2, N, D)
+    for s in range(S):
+        m, a, h = lens[s], new[s], (5 * s) % H
+        want, mag = po.causal(q[s, :a, h: h + 1].double(), torch.cat([k0[s, :m], x[s, :a, 0]])[:, h // 8: h // 8 + 1],
+                              torch.cat([v0[s, :m], x[s, :a, 1]])[:, h // 8: h // 8 + 1], m)
+        near(out[s, :a, h: h + 1], want, mag)
+        assert bool((out[s, a:] == MARK).all()) and not bool((out[s, :a] == MARK).all(-1).any())
 
 
 def test_hundreds_of_sequences_pieces():

@@ -48,6 +48,7 @@ def test_rope_refuses(lib):
     for kw, code in ((dict(r=None), INVALID), (dict(R=130), INVALID), (dict(R=24), INVALID), (dict(R=-16), INVALID),
                      (dict(R=144), INVALID), (dict(layout=2), INVALID), (dict(base=1.0), INVALID), (dict(base=nan), INVALID),
                      (dict(base=math.inf), INVALID), (dict(D=512), UNSUPPORTED), (dict(s=sc(4, 0, 2, 8192, 1, 4)), INVALID),
+                     (dict(s=sc(1, 0, 5e-324, 0, 0, 0)), INVALID),
                      (dict(s=sc(1, 1, 2, 0, 0, 0)), INVALID), (dict(s=sc(1, 0, 0, 0, 0, 0)), INVALID),
                      (dict(s=sc(2, 0, 8, 0, 1, 4)), INVALID), (dict(s=sc(2, 0, 8, 8192, 4, 4)), INVALID),
                      (dict(s=sc(3, 0, nan, 8192, 32, 1)), INVALID), (dict(s=sc(3, 0, 8, 8192, 32, 0)), INVALID)):
