@@ -35,14 +35,17 @@
 //     places.  Their products go in turns, outputs and next scores of one tile, then of the other; without
 //     turns 395 us, with the turn given away between the two 392;
 //   - P in two parts of 64 keys, the first one's product during the other's softmax; in one part 415 us, 96 and
-//     32 keys 365;
+//     32 keys 365, in four parts 373 where two take 332; two warps to 32 rows, 64 keys each and one part, 417: what a
+//     tile takes beside its products is the way from one role to the next, not the exponentials (waits that poll
+//     instead of suspending: 357, in the products' warps alone 350, where this takes 327);
 //   - maxima before the exponentials 402 us; an arrival on a barrier between products and their commit costs
 //     more than it gains (387);
 //   - an item takes about 2.4 us beside its keys, from the last product to the next softmax's first one.
 // D = 64 has half the products to the same exponentials and is bound by the softmax: two buffers of 96 keys, no
 // turns; 2 prompts of 4096 and 2048 tokens of 32 heads 96 us (64 keys 107, one buffer of 128 with turns 116).
-// D = 256: 8192 tokens of 16 heads 458 us (1200 TFLOP/s; query rows from shared memory 486), by its one
-// row tile's softmax.
+// D = 256: 8192 tokens of 16 heads 457 us (1200 TFLOP/s; query rows from shared memory 486; tensor pipe 48 %, L2
+// 27 %). Its scores are products of 64 keys, which take as long as those of 128, and there is no tensor memory for
+// 128; two warps to 32 rows, half the keys each, change nothing (458).
 //
 // Items come from one CTA that reads the lengths (rkv_prompt_plan.cuh), split over the keys where there
 // are few; the parts of a split item leave {m, l, out} in fp32, which k_prompt_join puts together.

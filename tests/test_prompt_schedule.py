@@ -122,7 +122,11 @@ class Cta:
                         raise Fault("looks through load %s for %d" % (self.ring[st], ld))
                     yield None
                 if self.rng.random() < 0.2:                  # values that are not finite
+                    spins = 0
                     while min(self.done) < i:
+                        spins += 1
+                        if spins > 20000:
+                            raise Fault("nothing goes on but the look through V")
                         yield None
                 self.cleaned[ld] = True
                 self.v_clean[cleans & 3].arrive()
