@@ -38,6 +38,9 @@
 //     32 keys 365, in four parts 373 where two take 332; two warps to 32 rows, 64 keys each and one part, 417: what a
 //     tile takes beside its products is the way from one role to the next, not the exponentials (waits that poll
 //     instead of suspending: 357, in the products' warps alone 350, where this takes 327);
+//   - by clock counters a turn issues outputs for 560 cycles and scores for 680, and takes 1560 with the way to the
+//     other warp and the wait for the second part of P; handing the turn on before the last two products of the
+//     scores changes nothing, before the last four 345 us, where this takes 327;
 //   - maxima before the exponentials 402 us; an arrival on a barrier between products and their commit costs
 //     more than it gains (387);
 //   - an item takes about 2.4 us beside its keys, from the last product to the next softmax's first one.
