@@ -45,7 +45,8 @@
 //     more than it gains (387);
 //   - an item takes about 2.4 us beside its keys, from the last product to the next softmax's first one.
 // D = 64 has half the products to the same exponentials and is bound by the softmax: two buffers of 96 keys, no
-// turns; 2 prompts of 4096 and 2048 tokens of 32 heads 96 us (64 keys 107, one buffer of 128 with turns 116).
+// turns; 2 prompts of 4096 and 2048 tokens of 32 heads 96 us (64 keys 107, one buffer of 128 with turns 116, two warps to 32
+// rows, 48 keys each, 107 where this takes 90).
 // D = 256: 8192 tokens of 16 heads 457 us (1200 TFLOP/s; query rows from shared memory 486; tensor pipe 48 %, L2
 // 27 %). Its scores are products of 64 keys, which take as long as those of 128, and there is no tensor memory for
 // 128; two warps to 32 rows, half the keys each, change nothing (458).
