@@ -432,7 +432,7 @@ rkv_status rkv_qk_rotate(const rkv_head_params *p, const rkv_rope *rope, int32_t
  * lies in rows that it does not see, NaN included.  Where start descends or leaves [0, rows],
  * RKV_ERR_INDEX is set and nothing is written.
  * q, k, v, out: bf16, rows of H, N, N and H heads.  Scores, softmax and sums in fp32;
- * probabilities meet the values as bf16 (relative error 2^-9, as the output's own rounding).
+ * probabilities meet the values as bf16 in two parts (relative error 2^-16).
  * out may be q itself (same pointer and stride); otherwise it must not overlap q, k or v.
  * RKV_ERR_DEVICE_TIMEOUT (a wait ran out): the outputs are not to be used.
  * workspace: >= the bytes of rkv_prompt_attention_workspace(p, S, rows), 256-byte aligned (0 bytes for

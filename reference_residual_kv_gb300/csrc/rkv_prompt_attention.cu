@@ -18,13 +18,16 @@
 //                its maximum; while a row's p of 64 keys or more add up to 2^10 at most it is kept (any p up to there
 //                is harmless in fp32 sums and has the same relative error in bf16 as p <= 1), else, and for the
 //                first keys, the maximum is looked for and m moves there.  P goes back to tensor
-//                memory, over the scores, as the first operand of P V
+//                memory, over the scores (its first part over their first half, its second part over
+//                the other), as the first operand of P V
 // D = 256 has one row tile (its outputs take 256 columns) and two buffers of scores instead, and its query
 // rows lie in tensor memory: from shared memory both operands of Q K^T for 64 keys take twice the product's time.
 //
-// P is bf16 (half a step of 2^-8, as the output's own rounding): outputs are 2.0-2.3e-3 off the exact ones
-// (relative norm), their rounding alone 1.5-1.7e-3.  A second part of P would take the products from 16 to 24 a
-// tile, half as long again.
+// P meets V as two bf16 parts, p cut off and the rest rounded (2^-16 of p is left out at most): outputs are as far
+// off the exact ones as their own rounding puts them, 1.55-1.66e-3 (relative norm; over 129024 keys 1.665e-3, the
+// rounding alone 1.659e-3: the accumulators cut what they add).  That takes 24 instead of 16 products a tile.  With the
+// first part alone outputs are 1.9-2.3e-3 off: 8192 tokens 355 us where two parts take 489, 6144 of heads of 64
+// 99 | 136, 8192 of 16 heads of 256 466 | 607, 2048 behind 129024 2725 | 3800 (calls from a graph, one run).
 //
 // What bounds it, and what was measured (D = 128, 8192 tokens of 32 heads unless stated; 352 us, 1560
 // TFLOP/s of the 1900 that a large library product reaches; tensor pipe 65 %, L2 26 %, DRAM 5 %):
@@ -546,8 +549,10 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                         const uint64_t v0 = vd + v_st * (C::kTile / 16) + part * (C::kPart * 128 / 16);
                         const uint32_t p0 = tm + C::kColS + (h * kBufs + buf) * kTok + C::kPart / 2 * part;
 #pragma unroll
-                        for (int k = 0; k < C::kPart / 16; ++k)
+                        for (int k = 0; k < C::kPart / 16; ++k) {
                             mma_bf16_ta(tm + h * C::kColsO, p0 + 8 * k, v0 + k * (2048 / 16), id_o, j != 0 || part != 0 || k != 0);
+                            mma_bf16_ta(tm + h * C::kColsO, p0 + kTok / 2 + 8 * k, v0 + k * (2048 / 16), id_o, 1);
+                        }
                         um::mma_commit(pv_done + b);
                         if (part == kParts - 1) um::mma_commit(kv_empty + v_st);
                     }
@@ -720,18 +725,24 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                     auto exps = [&]() {
                         const float mu = m_ref == -INFINITY ? 0.0f : m_ref;
                         const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), mu2 = make_float2(-mu, -mu);
+                        // what the first part leaves of p, and 2^-24 of the first part: above 0 where p is, so that an
+                        // infinite value stays infinite in the sum of both products
+                        const float2 rest = make_float2(-0x1.fffffep-1f, -0x1.fffffep-1f);
                         sums[0] = sums[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
                         for (int c = kC * part; c < kC * (part + 1); ++c) {
-                            uint32_t p[16];
+                            uint32_t hi[16], lo[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 const float2 y = __ffma2_rn(make_float2(v[c][2 * e], v[c][2 * e + 1]), sc2, mu2);
                                 const float2 pp = make_float2(ex2(y.x), ex2(y.y));
                                 sums[e & 1] = __fadd2_rn(sums[e & 1], pp);
-                                p[e] = as_u32(__floats2bfloat162_rn(pp.x, pp.y));
+                                hi[e] = __byte_perm(__float_as_uint(pp.x), __float_as_uint(pp.y), 0x7632);
+                                const float2 r = __ffma2_rn(make_float2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xffff0000u)), rest, pp);
+                                lo[e] = as_u32(__floats2bfloat162_rn(r.x, r.y));
                             }
-                            tmem_st16(ts + 16 * c, p);
+                            tmem_st16(ts + 16 * c, hi);
+                            tmem_st16(ts + kTok / 2 + 16 * c, lo);
                         }
                     };
                     // As long as the sum stays small, so does every probability: no maximum is taken.
