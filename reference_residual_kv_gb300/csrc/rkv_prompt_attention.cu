@@ -854,6 +854,8 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
             __syncwarp();
             if (lane == 0) done[4 * h + w4] = i + 1;
         }
+        // a wait that ran out may have left probabilities on their way to tensor memory
+        tmem_wait_st();
     }
     um::tc_fence_before();
     __syncwarp();
