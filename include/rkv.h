@@ -473,13 +473,16 @@ int32_t rkv_profile_collect(char *names, int32_t name_len, float *total_ms, int3
                             int32_t max_entries);
 
 /* Test hook of the device-side timeout path (failure handling; the paper has no
- * counterpart).  Arms a one-shot fault that the next rkv_compress call with bf16 kv,
- * from any host thread, takes in its W_c3 kernel: every barrier wait of that kernel
- * gives up after wait_cycles SM clock cycles instead of about 2e9, and the second CTA
- * of every CTA pair skips its tile loads for its stage use number skip_use, so that a
- * wait runs out.  The kernel then sets RKV_ERR_DEVICE_TIMEOUT in *dev_status, lets the
- * copies and MMAs it issued finish, frees its tensor memory and returns: nothing
- * traps, and the context stays usable for later calls.  The records of that call are
+ * counterpart).  Arms a one-shot fault that the next call, from any host thread, of one of
+ * these takes:
+ *  rkv_compress with bf16 kv, in its W_c3 kernel: the second CTA of every CTA pair skips its
+ *  tile loads for its stage use number skip_use;
+ *  rkv_prompt_attention, or rkv_chunk_attention for pieces that go through the same kernel:
+ *  every CTA skips its load number skip_use of a tile of K (even numbers) or V (odd ones).
+ * Every barrier wait of that kernel gives up after wait_cycles SM clock cycles instead of about
+ * 2e9, so that a wait runs out.  The kernel then sets RKV_ERR_DEVICE_TIMEOUT in *dev_status,
+ * lets the copies and MMAs it issued finish, frees its tensor memory and returns: nothing
+ * traps, and the context stays usable for later calls.  The outputs of that call are
  * incomplete.  For tests of the error path only.  Returns RKV_ERR_INVALID_ARG unless
  * 1e4 <= wait_cycles <= 2e9 and skip_use >= 0.                                      */
 rkv_status rkv_debug_wait_fault(int64_t wait_cycles, int32_t skip_use);

@@ -135,6 +135,9 @@ bool make_map_strided(CUtensorMap *m, const void *base, int rank, const uint64_t
 bool make_map_store(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows, uint64_t batch,
                     uint32_t box_inner, uint32_t box_rows);
 
+// The fault that rkv_debug_wait_fault armed, if any: both are set, and it is armed no longer (rkv_umma.cu)
+void take_wait_fault(long long &wait_cycles, int &skip);
+
 // single-token write (rkv_pool.cu: the pool entry; rkv_append.cu: the record)
 cudaError_t launch_append_ref(const Geometry &g, const void *kv_new, int t, const rkv_ref_pool *pool,
                               cudaStream_t s);

@@ -219,6 +219,8 @@ struct FlashArgs {
     int S, rows;
     int N, G, packed;
     float scale_log2;
+    int skip_load;                  // test hook: every CTA leaves this load of K or V out; else -1
+    uint32_t wait_cycles;           // limit of every wait
 };
 
 // An item as the roles share it: its KV head, and how many key tiles each row tile has
@@ -330,8 +332,8 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
     auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
         bool ok = um::mbar_try_wait(bar, phase & 1u);
         if (!__all_sync(0xffffffffu, ok)) {
-            const long long t0 = clock64();
-            while (!ok && !*abort_flag && clock64() - t0 <= kWaitCycles) ok = um::mbar_try_wait(bar, phase & 1u);
+            const uint32_t t0 = (uint32_t)clock();         // limits are below 2^31
+            while (!ok && !*abort_flag && (uint32_t)clock() - t0 <= a.wait_cycles) ok = um::mbar_try_wait(bar, phase & 1u);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok && lane == 0) *abort_flag = 1;
         }
@@ -447,11 +449,13 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                 if (!ok) return;
                 ++loads;
                 if (lane == 0) {
-                    um::mbar_arrive_expect_tx(kv_full + st, C::kTile);
+                    if ((int)loads - 1 != a.skip_load) {
+                        um::mbar_arrive_expect_tx(kv_full + st, C::kTile);
 #pragma unroll
-                    for (int k = 0; k < D / 64; ++k)
-                        tma_load_4d(ring + st * C::kTile + k * kTok * 128, m, kv_full + st, 64 * k,
-                                    (a.packed ? w.it.k_row : 0) + kt * kTok, w.n, a.packed ? 0 : w.it.k_row);
+                        for (int k = 0; k < D / 64; ++k)
+                            tma_load_4d(ring + st * C::kTile + k * kTok * 128, m, kv_full + st, 64 * k,
+                                        (a.packed ? w.it.k_row : 0) + kt * kTok, w.n, a.packed ? 0 : w.it.k_row);
+                    }
                     if (looked) um::mbar_arrive(v_issued + (cleans & 3));
                 }
                 cleans += looked;
@@ -470,10 +474,10 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
         // no copy is in flight when the CTA leaves
         if (lane == 0) {
             for (uint32_t k = loads > kStages ? loads - kStages : 0; k < loads; ++k)
-                um::mbar_wait(kv_full + k % kStages, (k / kStages) & 1u, kWaitCycles);
+                um::mbar_wait(kv_full + k % kStages, (k / kStages) & 1u, a.wait_cycles);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (uses[h]) um::mbar_wait(q_full + h, (uses[h] - 1) & 1u, kWaitCycles);
+                if (uses[h]) um::mbar_wait(q_full + h, (uses[h] - 1) & 1u, a.wait_cycles);
         }
         __syncwarp();
     } else if (warp == 1 || (kHalves == 2 && warp == 2)) {
@@ -586,7 +590,7 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
         // every issued product completes before tensor memory is released
         if (elect_one()) um::mma_commit(drain + h);
         __syncwarp();
-        um::mbar_wait(drain + h, 0, kWaitCycles);
+        um::mbar_wait(drain + h, 0, a.wait_cycles);
         __syncwarp();
     } else if (warp == 3) {
         uint32_t loads = 0, cleans = 0;
@@ -625,9 +629,9 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                     if (__any_sync(0xffffffffu, seen)) {
                         if (*odd_item != i + 1) {
                             // the rows are through with the values of the items before
-                            const long long t0 = clock64();
+                            const uint32_t t0 = (uint32_t)clock();
                             bool here = false;
-                            while (!here && !*abort_flag && clock64() - t0 <= kWaitCycles)
+                            while (!here && !*abort_flag && (uint32_t)clock() - t0 <= a.wait_cycles)
                                 here = lane >= 4 * kHalves || done[lane] >= i;
                             ok = __all_sync(0xffffffffu, here);
                             if (!ok) {
@@ -1003,6 +1007,10 @@ cudaError_t run(const PromptShape &p, const Layout &y, const PromptTensors &t, u
     a.N = p.N;
     a.G = G;
     a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
+    a.skip_load = -1;
+    long long limit = kWaitCycles;
+    take_wait_fault(limit, a.skip_load);
+    a.wait_cycles = (uint32_t)limit;
     {
         ProfScope prof("prompt_attention", s);
         k_prompt_attention<D><<<(unsigned)y.ctas, C::kThreads, C::kSmem, s>>>(maps, a);

@@ -796,10 +796,20 @@ k_umma(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
 }
 
 // ---------------------------------------------------------------------------- host
-// One-shot fault of the timeout path, armed by rkv_debug_wait_fault and taken by the
-// next W_c3 launch of the write path.
+// One-shot fault of the timeout path, armed by rkv_debug_wait_fault and taken by the next launch of
+// the write path's W_c3 kernel or of the prompt attention.
 static std::atomic<long long> g_fault_cycles{0};
 static std::atomic<int> g_fault_skip{-1};
+
+void take_wait_fault(long long &wait_cycles, int &skip)
+{
+    const long long fc = g_fault_cycles.exchange(0);
+    const int fs = g_fault_skip.exchange(-1);
+    if (fc > 0 && fs >= 0) {
+        wait_cycles = fc;
+        skip = fs;
+    }
+}
 
 static PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 {
@@ -1077,12 +1087,7 @@ cudaError_t launch_umma_compress(const Geometry &g, const void *kv, const rkv_re
         p.tiles_t = (p.rows + kTileM - 1) / kTileM;
         p.tiles_n = (g.d_c + kBN - 1) / kBN;
         p.k_chunks = (g.d_ff + kBK - 1) / kBK; p.a_sources = 2;
-        const long long fc = g_fault_cycles.exchange(0);
-        const int fs = g_fault_skip.exchange(-1);
-        if (fc > 0 && fs >= 0) {
-            p.wait_cycles = fc;
-            p.skip_use = fs;
-        }
+        take_wait_fault(p.wait_cycles, p.skip_use);
         if (compact) {
             if ((e = run<M_S2, 8>(mHc, mLc, mW3, p, s)) != cudaSuccess) return e;
         } else if ((e = run<M_S2>(mHi, mLo, mW3, p, s)) != cudaSuccess) {
