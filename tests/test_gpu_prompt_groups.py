@@ -70,3 +70,12 @@ def test_a_wrong_one_in_a_later_group(S, wrong):
         if a:
             near(out[s, :a], *po.causal(q[s, :a].double(), torch.cat([k0[s, :m], x[s, :a, 0]]), torch.cat([v0[s, :m], x[s, :a, 1]]), m))
         assert bool((out[s, a:] == MARK).all()), s
+
+
+# rows that the capacity has room for, though not for as many as the call allows
+@pytest.mark.parametrize("n", [40, 64, 65, 200])
+def test_the_last_rows_of_the_capacity(n):
+    S, T, H, N, D = 3, 500, 8, 2, 128
+    lens, new = [T - 3, T - n + 1, T], [3, n - 1, 0]
+    c, q, kv = make(S, n, T, H, N, D, lens, n)
+    check_piece(c, H, q, kv, lens, new, piece(c, H, q, kv, lens, new))
