@@ -430,7 +430,7 @@ rkv_status rkv_qk_rotate(const rkv_head_params *p, const rkv_rope *rope, int32_t
  *   out[i][j] = softmax( q[i][j] K^T / sqrt(D) ) V
  * over its own rows up to i.  Rows of no sequence are not written, and no row depends on what
  * lies in rows that it does not see, NaN included.  Where start descends or leaves [0, rows],
- * RKV_ERR_INDEX is set and nothing is written.
+ * RKV_ERR_INDEX is set and nothing is written.  A row all of whose scores are -inf gives zeros.
  * q, k, v, out: bf16, rows of H, N, N and H heads.  Scores, softmax and sums in fp32;
  * probabilities meet the values as bf16 in two parts (relative error 2^-16).
  * out may be q itself (same pointer and stride); otherwise it must not overlap q, k or v.
@@ -450,8 +450,8 @@ rkv_status rkv_prompt_attention(const rkv_head_params *p, int32_t S, const int32
  * q: bf16 [S][n][H][D]; kv: bf16 [S][n][2 N D], as for rkv_dense_write; out: bf16 [S][n][H][D],
  * rows from n_new[s] on are not written; it must not overlap q or kv.  n_new: int32 [S], device,
  * or NULL (n rows for every sequence).  Where len < 0, n_new is outside [0, n] or len + n_new > T,
- * RKV_ERR_INDEX is set and nothing of that sequence is written.  1 <= n <= T.  Precision as in
- * rkv_prompt_attention.
+ * RKV_ERR_INDEX is set and nothing of that sequence is written.  1 <= n <= T.  Precision, and rows
+ * all of whose scores are -inf, as in rkv_prompt_attention.
  * workspace: >= the bytes of rkv_chunk_attention_workspace(p, H, n), 256-byte aligned: for long
  * pieces (always for n > 64) it holds K and V of all S T tokens in bf16 (4 N D bytes each), and one
  * layer's calls may follow another's in it.  Requires H/N <= 8.                            */

@@ -810,7 +810,8 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
             steps += count;
             const bool live = in_tile && tok < w.it.tokens, whole_item = w.it.slot < 0;
             const size_t prow = whole_item ? 0 : (size_t)(w.it.slot + w.n) * (128 * kHalves) + 128 * h + r;
-            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays
+            // l is 0 only where all scores are -inf (the largest p is 1 at least once): zeros.  NaN stays
+            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
             const bool odd_here = *odd_item == i + 1;
             const int seen_to = min(1022, sees - partly(w.it) * kTok);
             if (count > 0) {
