@@ -453,8 +453,9 @@ rkv_status rkv_prompt_attention(const rkv_head_params *p, int32_t S, const int32
  * RKV_ERR_INDEX is set and nothing of that sequence is written.  1 <= n <= T.  Precision, and rows
  * all of whose scores are -inf, as in rkv_prompt_attention.
  * workspace: >= the bytes of rkv_chunk_attention_workspace(p, H, n), 256-byte aligned: for long
- * pieces (always for n > 64) it holds K and V of all S T tokens in bf16 (4 N D bytes each), and one
- * layer's calls may follow another's in it.  Requires H/N <= 8.                            */
+ * pieces (always for n > 64) it holds K and V of the sequences' T tokens in bf16 (4 N D bytes each),
+ * of as many sequences at a time as 4 GiB hold and of one at least, and some 80 MB at most for
+ * partial sums; one layer's calls may follow another's in it.  Requires H/N <= 8.         */
 rkv_status rkv_chunk_attention_workspace(const rkv_dense_params *p, int32_t H, int32_t n, size_t *bytes);
 rkv_status rkv_chunk_attention(const rkv_dense_params *p, int32_t H, const void *q, int32_t n,
                                const int32_t *n_new, const void *kv, const rkv_dense_cache *cache,

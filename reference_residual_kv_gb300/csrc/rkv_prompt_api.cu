@@ -72,16 +72,18 @@ rkv_status check_piece(const rkv_dense_params *p, int32_t H, int32_t n)
     return RKV_OK;
 }
 
-DenseGeom geom(const rkv_dense_params *p) { return DenseGeom{p->S, p->T, p->N, p->D, p->bits, p->T / kBlk}; }
+DenseGeom geom(const rkv_dense_params *p, int S) { return DenseGeom{S, p->T, p->N, p->D, p->bits, p->T / kBlk}; }
+DenseGeom geom(const rkv_dense_params *p) { return geom(p, p->S); }
 
-PromptShape piece_shape(const rkv_dense_params *p, int H, int n, const int32_t *len, const int32_t *n_new)
+// S of the sequences
+PromptShape piece_shape(const rkv_dense_params *p, int S, int H, int n, const int32_t *len, const int32_t *n_new)
 {
     PromptShape x{};
-    x.S = p->S;
+    x.S = S;
     x.H = H;
     x.N = p->N;
     x.D = p->D;
-    x.rows = (long long)p->S * n;
+    x.rows = (long long)S * n;
     x.len = len;
     x.n_new = n_new;
     x.n = n;
@@ -113,9 +115,24 @@ bool as_tree(const rkv_dense_params *p, int H, int n)
     return p->D < 256 || R <= 64 || (long long)p->S * p->T < 8192;
 }
 
-size_t piece_rows_bytes(const rkv_dense_params *p)
+// K and V of a sequence in bf16
+size_t piece_rows_bytes(const rkv_dense_params *p) { return align256((size_t)p->T * 4 * p->N * p->D); }
+
+// Sequences whose rows lie in the workspace at a time, so that a capacity far beyond the lengths, or many
+// sequences of which few have new rows, take 4 GiB at most (or one sequence's rows); even groups, one after
+// another.  All at a time | groups of 4 GiB | of 2 GiB, us, 131072 tokens of capacity, 32 heads over 8, D = 128:
+//   16 sequences (8 GiB), 512 rows behind 130560    14630 | 14660 | 15130
+//     128 rows behind 130944                        5184 | 5657 | 5279
+//     128 rows behind 1000                          313 | 316 | 413
+//   64 sequences (32 GiB), 512 rows behind 8000     4513 | 4870 | 5613
+//     128 rows behind 1000                          1155 | 1311 | 1684
+//     128 rows of one of them                       490 | 599 | 723
+constexpr size_t kMostRows = 4ull << 30;
+int piece_group(const rkv_dense_params *p)
 {
-    return align256((size_t)p->S * p->T * 4 * p->N * p->D);
+    const long long most = max(1LL, (long long)(kMostRows / piece_rows_bytes(p)));
+    const long long groups = (p->S + most - 1) / most;
+    return (int)((p->S + groups - 1) / groups);
 }
 
 rkv_status done(cudaError_t e) { return e == cudaSuccess ? RKV_OK : RKV_ERR_CUDA; }
@@ -254,7 +271,7 @@ rkv_status rkv_chunk_attention_workspace(const rkv_dense_params *p, int32_t H, i
     if (st != RKV_OK) return st;
     if (!bytes) return RKV_ERR_INVALID_ARG;
     if (as_tree(p, H, n)) *bytes = align256((size_t)p->S * n * 4) + dense_attention_workspace_bytes(geom(p), H, n);
-    else *bytes = piece_rows_bytes(p) + prompt_workspace_bytes(piece_shape(p, H, n, nullptr, nullptr));
+    else *bytes = piece_group(p) * piece_rows_bytes(p) + prompt_workspace_bytes(piece_shape(p, piece_group(p), H, n, nullptr, nullptr));
     return RKV_OK;
 }
 
@@ -280,13 +297,24 @@ rkv_status rkv_chunk_attention(const rkv_dense_params *p, int32_t H, const void 
         return done(launch_dense_attention(g, H, q, n, parent, kv, cache, len, nullptr, 1, 0, out, RKV_BF16,
                                            ws + align256((size_t)p->S * n * 4), dev_status, s, true));
     }
-    const PromptShape x = piece_shape(p, H, n, len, n_new);
-    uint8_t *rest = ws + piece_rows_bytes(p);
-    const cudaError_t e = launch_dense_rows(g, cache, len, kv, n, n_new, ws, prompt_plan_args(x, rest, dev_status), dev_status, s);
-    if (e != cudaSuccess) return RKV_ERR_CUDA;
+    const int group = piece_group(p);
+    const size_t heads = (size_t)p->N, rec = heads * g.nb * g.rec_bytes(), hdr = heads * g.nb * g.hdr_bytes();
     const int64_t head = 2LL * p->T * p->D, qrow = (int64_t)H * p->D;
-    const PromptTensors t{q, ws, ws + (size_t)p->T * p->D * 2, out, qrow, p->D, p->D, qrow, head, head * p->N};
-    return done(launch_prompt_attention(x, t, rest, dev_status, s));
+    uint8_t *rest = ws + group * piece_rows_bytes(p);
+    for (int s0 = 0; s0 < p->S; s0 += group) {
+        const int m = min(group, p->S - s0);
+        const PromptShape x = piece_shape(p, m, H, n, len + s0, n_new ? n_new + s0 : nullptr);
+        const rkv_dense_cache c{g.nb ? (uint8_t *)cache->codes + s0 * rec : nullptr, g.nb ? (uint8_t *)cache->khdr + s0 * hdr : nullptr,
+                                (uint8_t *)cache->tail + s0 * heads * 2 * kBlk * p->D * 2};
+        const size_t row = (size_t)s0 * n;                 // the group's first
+        cudaError_t e = launch_dense_rows(geom(p, m), &c, len + s0, (const uint8_t *)kv + row * 2 * heads * p->D * 2, n, x.n_new, ws,
+                                          prompt_plan_args(x, rest, dev_status), dev_status, s);
+        const PromptTensors t{(const uint8_t *)q + row * qrow * 2, ws, ws + (size_t)p->T * p->D * 2, (uint8_t *)out + row * qrow * 2,
+                              qrow, p->D, p->D, qrow, head, head * p->N};
+        if (e == cudaSuccess) e = launch_prompt_attention(x, t, rest, dev_status, s);
+        if (e != cudaSuccess) return RKV_ERR_CUDA;
+    }
+    return RKV_OK;
 }
 
 }  // extern "C"
