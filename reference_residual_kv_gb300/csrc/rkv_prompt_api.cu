@@ -94,25 +94,41 @@ PromptShape piece_shape(const rkv_dense_params *p, int S, int H, int n, const in
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Short pieces go the way of drafted trees, which read the cache as it is, but whose last pass takes a
-// row at a time; others read bf16 rows that k_dense_rows makes of the cache first.  R = n H / N rows to a
-// KV head.  As a tree | from bf16 rows, us (D = 128 but where stated, 4 bits, T tokens of each sequence):
-//   8 KV heads, H = 32                  n = 8       16          32          48          64
-//     1 x 131072                        112 | 221   152 | 223   145 | 224   171 | 226   173 | 228
-//     4 x 8192                          49 | 70     53 | 71     56 | 72     80 | 76     91 | 80
-//     16 x 8192                         107 | 198   151 | 198   168 | 199   227 | 207   267 | 208
-//     64 x 1024                         95 | 105    139 | 107   219 | 109   381 | 117   524 | 120
-//     1 x 4096                          19 | 34     22 | 35     24 | 36     26 | 38     27 | 40
-//   4 KV heads, H = 28, 16 x 8192       78 | 115    92 | 118    120 | 131   211 | 153   250 | 154
-//   4 KV heads, H = 16, D = 256
-//     1 x 131072                        125 | 253   217 | 254   423 | 258   625 | 297   924 | 298
-//     4 x 8192                          52 | 83     74 | 86     129 | 88    187 | 105   269 | 105
-//     1 x 4096                          21 | 39     25 | 41     32 | 44     44 | 44     56 | 44
+// row of a head at a time; others read bf16 rows that k_dense_rows makes of the cache first.  As a tree | from
+// bf16 rows, us (4 bits, S x T tokens, all but 64 of them cached, H heads over N, calls from a graph):
+//                                     n = 8       16          24          32          48          64
+//   D = 128
+//     1 x 131072, 32 over 8           114 | 220   149 | 222   147 | 225   144 | 229   169 | 248   174 | 253
+//     16 x 8192, 32 over 8            119 | 228   158 | 235   166 | 242   170 | 250   227 | 271   262 | 272
+//     4 x 8192, 32 over 8             50 | 70     52 | 73     52 | 76     54 | 79     75 | 85     89 | 88
+//     64 x 1024, 32 over 8            97 | 131    135 | 137   165 | 142   199 | 149   338 | 162   465 | 168
+//     1 x 4096, 32 over 8             18 | 37     22 | 37     24 | 38     25 | 39     27 | 41     29 | 42
+//     16 x 8192, 28 over 4            86 | 124    95 | 129    114 | 145   123 | 151   214 | 200   248 | 201
+//     4 x 8192, 28 over 4             40 | 51     42 | 52     47 | 56     49 | 57     76 | 71     87 | 72
+//     16 x 8192, 64 over 8            156 | 228   163 | 236   202 | 264   221 | 271   438 | 380   504 | 401
+//     256 x 512, 16 over 4            137 | 143   201 | 143   259 | 149   323 | 156   584 | 166   829 | 173
+//   D = 64, 16 x 8192, 32 over 8      74 | 140    103 | 143   110 | 148   119 | 151   182 | 171   208 | 172
+//     4 x 8192, 32 over 8             35 | 53     38 | 54     39 | 54     41 | 55     65 | 63     73 | 64
+//   D = 256, 1 x 131072, 16 over 4    125 | 256   213 | 262   323 | 267   424 | 273   622 | 326   924 | 327
+//     4 x 8192, 16 over 4             53 | 78     73 | 83     101 | 89    135 | 94    196 | 115   270 | 116
+//     16 x 2048, 16 over 4            56 | 75     87 | 81     126 | 87    158 | 94    240 | 110   340 | 111
+//     1 x 4096, 16 over 4             19 | 42     25 | 43     31 | 45     32 | 46     42 | 46     57 | 47
+//                                     n = 1       2           4           8
+//   D = 128, 500 x 100, 8 over 1      40 | 40     44 | 40     63 | 40     114 | 42
+//     2048 x 128, 8 over 1            100 | 120   137 | 121   240 | 123   369 | 127
+//   D = 64, 500 x 100, 8 over 1       29 | 35     37 | 34     51 | 34     88 | 34
+//   D = 256, 500 x 100, 8 over 1      58 | 57     63 | 58     116 | 60    230 | 65
+// A row of a head in a tree's last pass takes as long as the way of 32 tokens of a head of 128 channels to
+// bf16 and through memory, and that way's launches as long as 32768 more.  With 256 channels a tree also turns the cache
+// into bf16 anew for every 16 rows of a KV head: four times are as long as the way through memory, and its launches
+// as 131072 tokens of a head once.  (The rule is off by 8 % at most for n >= 8, by 20 % for hundreds of sequences
+// of about 100 tokens with one new row each.)
 bool as_tree(const rkv_dense_params *p, int H, int n)
 {
-    const long long R = (long long)n * (H / p->N);
     if (n > kMaxDraft) return false;
-    if (44 * R >= p->T && (long long)p->S * n * H >= 4096) return false;
-    return p->D < 256 || R <= 64 || (long long)p->S * p->T < 8192;
+    const double tokens = (double)p->S * p->T * p->N, rows = (double)p->S * n * H, R = (double)n * (H / p->N);
+    if (32.0 * rows > tokens * p->D / 128 + 32768.0) return false;
+    return p->D < 256 || (R / 16 - 4) * tokens <= 131072.0;
 }
 
 // K and V of a sequence in bf16

@@ -40,7 +40,7 @@ def test_prompts_are_as_far_off_as_their_own_rounding(lens, H, N, D):
 
 
 # as drafted trees, and from bf16 rows
-@pytest.mark.parametrize("n", [3, 64, 65, 300])
+@pytest.mark.parametrize("n", [3, 33, 64, 65, 300])
 @pytest.mark.parametrize("H,N,D,bits", [(8, 2, 128, 4), (7, 1, 64, 2), (4, 1, 256, 4)])
 def test_pieces_are_as_far_off_as_their_own_rounding(n, H, N, D, bits):
     gen = torch.Generator(device="cuda").manual_seed(n + D)
