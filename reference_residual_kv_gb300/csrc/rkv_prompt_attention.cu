@@ -27,32 +27,29 @@
 // off the exact ones as their own rounding puts them, 1.55-1.66e-3 (relative norm; over 129024 keys 1.665e-3, the
 // rounding alone 1.659e-3: the accumulators cut what they add).  That takes 24 instead of 16 products a tile.  With the
 // first part alone outputs are 1.9-2.3e-3 off: 8192 tokens 355 us where two parts take 489, 6144 of heads of 64
-// 99 | 136, 8192 of 16 heads of 256 466 | 607, 2048 behind 129024 2725 | 3800 (calls from a graph, one run).
+// 99 | 136, 8192 of 16 heads of 256 466 | 607, 2048 behind 129024 2725 | 3800.
 //
-// What bounds it, and what was measured (D = 128, 8192 tokens of 32 heads unless stated; 352 us, 1560
-// TFLOP/s of the 1900 that a large library product reaches; tensor pipe 65 %, L2 26 %, DRAM 5 %):
-//   - products read shared memory at about 93 bytes a cycle: P V of 128 x 128 x 16 takes 65 cycles, Q K^T 86
-//     alone and 64 among others, of 128 x 64 x 16 still 69.  So 64 keys at a time with two buffers of scores,
-//     which leave the softmax out of the way, take 366 us;
+// What bounds it, and what was measured.  Times in us are of calls one after another from a graph, over inputs that
+// stay, and each line's are of one run; ratios are those of a variant's time to the product's in the same run.  Those
+// marked * were taken with one part of P, the others as it is.
+// D = 128, 8192 tokens of 32 heads, 485 us: the tensor pipe, 77 % busy (1700 TFLOP/s with both parts of P; 79 % and 1900 in a
+// large library product); instructions issued 42 %, exponentials (XU pipe) 26 %, L2 19 %, DRAM 3 %.
 //   - with one buffer a row tile's scores wait for its probabilities: the two tiles have to be at different
-//     places.  Their products go in turns, outputs and next scores of one tile, then of the other; without
-//     turns 395 us, with the turn given away between the two 392;
-//   - P in two parts of 64 keys, the first one's product during the other's softmax; in one part 415 us, 96 and
-//     32 keys 365, in four parts 373 where two take 332; two warps to 32 rows, 64 keys each and one part, 417: what a
-//     tile takes beside its products is the way from one role to the next, not the exponentials (waits that poll
-//     instead of suspending: 357, in the products' warps alone 350, where this takes 327);
-//   - by clock counters a turn issues outputs for 560 cycles and scores for 680, and takes 1560 with the way to the
-//     other warp and the wait for the second part of P; handing the turn on before the last two products of the
-//     scores changes nothing, before the last four 345 us, where this takes 327;
-//   - maxima before the exponentials 402 us; an arrival on a barrier between products and their commit costs
-//     more than it gains (387);
-//   - an item takes about 2.4 us beside its keys, from the last product to the next softmax's first one.
-// D = 64 has half the products to the same exponentials and is bound by the softmax: two buffers of 96 keys, no
-// turns; 2 prompts of 4096 and 2048 tokens of 32 heads 96 us (64 keys 107, one buffer of 128 with turns 116, two warps to 32
-// rows, 48 keys each, 107 where this takes 90).
-// D = 256: 8192 tokens of 16 heads 457 us (1200 TFLOP/s; query rows from shared memory 486; tensor pipe 48 %, L2
-// 27 %). Its scores are products of 64 keys, which take as long as those of 128, and there is no tensor memory for
-// 128; two warps to 32 rows, half the keys each, change nothing (458).
+//     places.  Their products go in turns, outputs and next scores of one tile, then of the other: 484, without
+//     turns 536, two buffers of 64 keys and no turns 532; the turn handed on before the last two products of the
+//     scores * 1.00, before the last four * 1.06;
+//   - P goes over in two pieces of 64 keys, the first one's products during the other's softmax: 484, in one piece
+//     530, in four * 1.12; two warps to 32 rows, 64 keys each, and one piece * 1.19;
+//   - waits that poll instead of suspending * 1.09, in the products' warps alone * 1.07;
+//   - what the second part of P is made of: first part cut off by a permute 491, rounded 494 (which breaks infinities);
+//   - an item takes about 2.4 us * beside its keys, from the last product to the next softmax's first one.
+// D = 64, 4096 and 2048 tokens of 32 heads, 135 us: no unit is full (tensor pipe 42 %, instructions issued 47 %, ALU 33 %, XU
+// 28 %); products of half the work leave the way from role to role in sight.  Two buffers of 96 keys and no turns 135, of 64 keys
+// 140, one buffer of 128 with turns 144; two warps to 32 rows, 48 keys each, * 1.19.
+// D = 256, 8192 tokens of 16 heads, 611 us: tensor pipe 55 %, instructions issued 17 %, L2 22 %.  Its scores are products
+// of 64 keys, which alone take as long as those of 128 (69 cycles of 128 x 64 x 16; of 128 x 128 x 16 86 from shared
+// memory alone, 64 among P V's), and there is no tensor memory for 128; query rows from shared memory 634; two
+// warps to 32 rows, half the keys each, * 1.00.
 //
 // Items come from one CTA that reads the lengths (rkv_prompt_plan.cuh), split over the keys where there
 // are few; the parts of a split item leave {m, l, out} in fp32, which k_prompt_join puts together.
@@ -936,7 +933,7 @@ Layout layout_of(const PromptShape &p)
     if (p.start) {
         // Without parts the longest item should be no longer than its CTA's share of all items, or short.
         // A prompt of 2 CTAs tile_tokens / N rows has items of that share at its end, whatever the others'
-        // lengths.  With and without (us, 4 prompts of 50 .. 2000 rows, 8 of 1024; 32 heads): 54 | 42, 92 | 80.
+        // lengths.  With and without (us, 4 prompts of 50 .. 2000 rows, 8 of 1024; 32 heads): 78 | 65, 109 | 96.
         const double longest = p.rows / 128.0;
         const double share = 0.5 * (double)(p.rows / (double)y.tile_tokens) * (longest + 2 * kItemCost) * p.N / kPromptCtas;
         const bool even = longest <= 16 || 2.0 * kPromptCtas * y.tile_tokens / p.N <= 24 * 128 ||
