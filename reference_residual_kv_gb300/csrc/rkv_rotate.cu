@@ -10,10 +10,10 @@
 // a norm 7.35e-8 instead of 6.69e-8; they take no time.
 // A warp has up to four passes of a row's queries or keys, their loads all in flight before anything is
 // worked out, and a CTA to itself (with four warps to a CTA, which waits for its slowest one: 31.5 and
-// 182 us instead of 28 and 173).  A norm's weights are multiplied into the cosines and sines once for
+// 182 us for the first two cases below where one took 28 and 173).  A norm's weights are multiplied into the cosines and sines once for
 // all heads (applied by themselves the errors are the same, and 65536 rows take 3 % longer).
 // Bound by memory: reads and writes every value once.  8192 rows of 32 + 8 heads of 128 in bf16, with norm: 28 us
-// (6.0 TB/s); 65536 rows of 28 + 4, without: 173 us (6.2 TB/s); 4001 fp32 rows with norm: 21 us (6.1 TB/s); 32
+// (6.0 TB/s); 65536 rows of 28 + 4, without: 168 us (6.4 TB/s); 4001 fp32 rows with norm: 21 us (6.1 TB/s); 32
 // rows: 2.3 us, a launch.  Each from memory; the copy rate is 6.8 TB/s.
 #include "rkv_prompt.cuh"
 
