@@ -726,8 +726,8 @@ k_prompt_attention(const __grid_constant__ FlashMaps maps, const FlashArgs a)
                     auto exps = [&]() {
                         const float mu = m_ref == -INFINITY ? 0.0f : m_ref;
                         const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), mu2 = make_float2(-mu, -mu);
-                        // what the first part leaves of p, and 2^-24 of the first part: above 0 where p is, so that an
-                        // infinite value stays infinite in the sum of both products
+                        // what the first part leaves of p, and 2^-24 of the first part: above 0 where p is (down to
+                        // 2^-100), so that an infinite value stays infinite in the sum of both products
                         const float2 rest = make_float2(-0x1.fffffep-1f, -0x1.fffffep-1f);
                         sums[0] = sums[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
